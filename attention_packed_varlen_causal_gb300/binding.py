@@ -26,6 +26,8 @@ BG_DEVSTAT_PARENT = 0x04
 BG_DEVSTAT_CU_PROMPT = 0x08
 BG_DEVSTAT_EMPTY_ROW = 0x10
 BG_DEVSTAT_PLAN = 0x20
+BG_DEVSTAT_GROUP = 0x40
+BG_DEVSTAT_TOKEN = 0x80
 BG_DEVSTAT_TIMEOUT = 0x100
 BG_MAX_SUFFIX = 16
 BG_MAX_SEQLEN = 65536
@@ -35,6 +37,9 @@ BG_MAX_VOCAB = 1 << 22
 
 # Every symbol include/bg_attn.h declares, with its ctypes signature.
 _P, _I32, _F32, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
+_SHARED_PLAN = [_P, _I32, _I32, _I32, _P, _I32, _I32, _P, _I32, _I32, _I32, _I32, _P, _SZ, _P, _P]
+_SHARED_RUN = [_P, _P, _P, _P, _I32, _I32, _I32, _P, _P, _P, _I32, _I32, _P, _I32, _I32, _I32, _I32, _F32, _F32, _P, _P,
+               _P, _SZ, _P, _P]
 SIGNATURES = {
     "bg_status_string": ([ctypes.c_int], ctypes.c_char_p),
     "bg_packed_prefill_workspace_size": ([_I32] * 6, _SZ),
@@ -56,6 +61,13 @@ SIGNATURES = {
     "bg_beam_decode_step": ([_P, _P, _P, _P, _I32, _I32, _P, _P, _P, _P, _P, _P, _P, _I32, _I32, _I32, _I32, _I32,
                              _I32, _I32, _F32, _P, _P, _P], ctypes.c_int),
     "bg_beam_select_workspace_size": ([_I32] * 3, _SZ),
+    "bg_shared_attn_workspace_size": ([_I32] * 8, _SZ),
+    "bg_shared_prefill_plan": (_SHARED_PLAN, ctypes.c_int),
+    "bg_shared_last_token_plan": (_SHARED_PLAN, ctypes.c_int),
+    "bg_shared_prefill_attn": (_SHARED_RUN, ctypes.c_int),
+    "bg_shared_prefill_attn_planned": (_SHARED_RUN, ctypes.c_int),
+    "bg_shared_last_token_attn": (_SHARED_RUN, ctypes.c_int),
+    "bg_shared_last_token_attn_planned": (_SHARED_RUN, ctypes.c_int),
     "bg_selftest_wait_timeout": ([_P, _P, _P], ctypes.c_int),
     "bg_beam_select": ([_P, _P, _I32, _I32, _I32, _P, _P, _P, _P, _SZ, _P], ctypes.c_int),
 }
@@ -304,3 +316,133 @@ def bg_beam_select(logits, cum, token_out, parent_out, score_out, *, workspace=N
                                _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
     _check("bg_beam_select", st)
     return token_out, parent_out, score_out
+
+
+def _expect(fn: str, device, **tensors):
+    """Each of ``tensors`` is (tensor or None, dtype name, shape): a contiguous CUDA tensor on ``device``."""
+    for name, (t, dtype, shape) in tensors.items():
+        if t is None:
+            continue
+        if t.device != device or str(t.dtype) != f"torch.{dtype}" or tuple(t.shape) != tuple(shape) or \
+                not t.is_contiguous():
+            raise ValueError(f"{fn}: {name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, "
+                             f"got {str(t.dtype)[6:]} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
+
+
+def _on(device, stream):
+    """The context of ``device`` and the stream to use there: the given one, or its current one."""
+    import torch
+    if device.type != "cuda":
+        raise ValueError(f"CUDA tensors expected, got {device}")
+    return torch.cuda.device(device), _stream(torch.cuda.current_stream(device) if stream is None else stream)
+
+
+def bg_shared_attn_workspace_size(num_groups: int, num_seqs: int, total_tokens: int, max_seqlen: int,
+                                  max_prefix_len: int, Hq: int, Hkv: int, head_dim: int) -> int:
+    return int(load().bg_shared_attn_workspace_size(num_groups, num_seqs, total_tokens, max_seqlen, max_prefix_len, Hq,
+                                                    Hkv, head_dim))
+
+
+def _workspace(fn: str, workspace, need: int, device):
+    if workspace is None:
+        raise ValueError(f"{fn}: workspace of {need} bytes required (the library never allocates)")
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"{fn}: workspace must be contiguous on {device}")
+    return _ptr(workspace), workspace.numel() * workspace.element_size()
+
+
+def _shared_run(fn: str, last: bool, q, k, v, cu_seqlens, max_seqlen, prefix_k, prefix_v, cu_prefix, max_prefix_len,
+                cu_group, out, lse, scale, softcap, workspace, dev_status, stream):
+    rows, Hq, d = q.shape
+    T, Hkv = k.shape[0], k.shape[1]
+    P = 0 if prefix_k is None else prefix_k.shape[0]
+    S, R = cu_seqlens.numel() - 1, cu_group.numel() - 1
+    dev = q.device
+    if (prefix_k is None) != (prefix_v is None):
+        raise ValueError(f"{fn}: prefix_k and prefix_v come together")
+    _expect(fn, dev, q=(q, "bfloat16", (S if last else T, Hq, d)), k=(k, "bfloat16", (T, Hkv, d)),
+            v=(v, "bfloat16", (T, Hkv, d)), cu_seqlens=(cu_seqlens, "int32", (S + 1,)),
+            prefix_k=(prefix_k, "bfloat16", (P, Hkv, d)), prefix_v=(prefix_v, "bfloat16", (P, Hkv, d)),
+            cu_prefix=(cu_prefix, "int32", (R + 1,)), cu_group=(cu_group, "int32", (R + 1,)),
+            out=(out, "bfloat16", (rows, Hq, d)), lse=(lse, "float32", (rows, Hq)),
+            dev_status=(dev_status, "int32", () if dev_status is None else dev_status.shape))
+    ws, ws_bytes = _workspace(fn, workspace, bg_shared_attn_workspace_size(R, S, T, int(max_seqlen),
+                                                                           int(max_prefix_len), Hq, Hkv, d), dev)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    ctx, st = _on(dev, stream)
+    with ctx:
+        _check(fn, getattr(load(), fn)(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens), S, T, int(max_seqlen), _ptr(prefix_k), _ptr(prefix_v),
+            _ptr(cu_prefix), P, int(max_prefix_len), _ptr(cu_group), R, Hq, Hkv, d, float(scale), float(softcap),
+            _ptr(out), _ptr(lse), ws, ws_bytes, _ptr(dev_status), st))
+    return out
+
+
+def bg_shared_prefill_attn(q, k, v, cu_seqlens, max_seqlen: int, prefix_k, prefix_v, cu_prefix, max_prefix_len: int,
+                           cu_group, out, *, lse=None, scale: Optional[float] = None, softcap: float = 0.0,
+                           workspace=None, dev_status=None, stream=None):
+    """Causal attention of the samples' tokens over their request's prefix and their own sample.
+    q [T,Hq,d], k/v [T,Hkv,d] bf16, packed by cu_seqlens int32 [S+1]; prefix_k/prefix_v [P,Hkv,d] (or
+    None) packed by cu_prefix int32 [R+1]; samples cu_group[r] .. cu_group[r+1]-1 belong to request r
+    (int32 [R+1]); out [T,Hq,d] (written); lse fp32 [T,Hq] or None; scores capped by softcap * tanh(x /
+    softcap) if softcap > 0; workspace a uint8 CUDA tensor of bg_shared_attn_workspace_size bytes."""
+    return _shared_run("bg_shared_prefill_attn", False, q, k, v, cu_seqlens, max_seqlen, prefix_k, prefix_v, cu_prefix,
+                       max_prefix_len, cu_group, out, lse, scale, softcap, workspace, dev_status, stream)
+
+
+def bg_shared_last_token_attn(q, k, v, cu_seqlens, max_seqlen: int, prefix_k, prefix_v, cu_prefix, max_prefix_len: int,
+                              cu_group, out, *, lse=None, scale: Optional[float] = None, softcap: float = 0.0,
+                              workspace=None, dev_status=None, stream=None):
+    """As bg_shared_prefill_attn with one query per sample, over the prefix and the whole sample:
+    q and out [S,Hq,d], lse fp32 [S,Hq] or None."""
+    return _shared_run("bg_shared_last_token_attn", True, q, k, v, cu_seqlens, max_seqlen, prefix_k, prefix_v,
+                       cu_prefix, max_prefix_len, cu_group, out, lse, scale, softcap, workspace, dev_status, stream)
+
+
+def bg_shared_prefill_attn_planned(q, k, v, cu_seqlens, max_seqlen: int, prefix_k, prefix_v, cu_prefix,
+                                   max_prefix_len: int, cu_group, out, *, lse=None, scale: Optional[float] = None,
+                                   softcap: float = 0.0, workspace=None, dev_status=None, stream=None):
+    """bg_shared_prefill_attn with the work list that bg_shared_prefill_plan left in workspace."""
+    return _shared_run("bg_shared_prefill_attn_planned", False, q, k, v, cu_seqlens, max_seqlen, prefix_k, prefix_v,
+                       cu_prefix, max_prefix_len, cu_group, out, lse, scale, softcap, workspace, dev_status, stream)
+
+
+def bg_shared_last_token_attn_planned(q, k, v, cu_seqlens, max_seqlen: int, prefix_k, prefix_v, cu_prefix,
+                                      max_prefix_len: int, cu_group, out, *, lse=None, scale: Optional[float] = None,
+                                      softcap: float = 0.0, workspace=None, dev_status=None, stream=None):
+    """bg_shared_last_token_attn with the work list that bg_shared_last_token_plan left in workspace."""
+    return _shared_run("bg_shared_last_token_attn_planned", True, q, k, v, cu_seqlens, max_seqlen, prefix_k, prefix_v,
+                       cu_prefix, max_prefix_len, cu_group, out, lse, scale, softcap, workspace, dev_status, stream)
+
+
+def _shared_plan(fn: str, cu_seqlens, total_tokens, max_seqlen, cu_prefix, total_prefix, max_prefix_len, cu_group, Hq,
+                 Hkv, head_dim, workspace, dev_status, stream):
+    S, R = cu_seqlens.numel() - 1, cu_group.numel() - 1
+    dev = cu_seqlens.device
+    _expect(fn, dev, cu_seqlens=(cu_seqlens, "int32", (S + 1,)), cu_prefix=(cu_prefix, "int32", (R + 1,)),
+            cu_group=(cu_group, "int32", (R + 1,)),
+            dev_status=(dev_status, "int32", () if dev_status is None else dev_status.shape))
+    ws, ws_bytes = _workspace(fn, workspace, bg_shared_attn_workspace_size(
+        R, S, int(total_tokens), int(max_seqlen), int(max_prefix_len), Hq, Hkv, head_dim), dev)
+    ctx, st = _on(dev, stream)
+    with ctx:
+        _check(fn, getattr(load(), fn)(_ptr(cu_seqlens), S, int(total_tokens), int(max_seqlen), _ptr(cu_prefix),
+                                       int(total_prefix), int(max_prefix_len), _ptr(cu_group), R, Hq, Hkv, head_dim,
+                                       ws, ws_bytes, _ptr(dev_status), st))
+
+
+def bg_shared_prefill_plan(cu_seqlens, total_tokens: int, max_seqlen: int, cu_prefix, total_prefix: int,
+                           max_prefix_len: int, cu_group, Hq: int, Hkv: int, head_dim: int, *, workspace=None,
+                           dev_status=None, stream=None):
+    """The work list of a packing into workspace, for bg_shared_prefill_attn_planned calls with it."""
+    _shared_plan("bg_shared_prefill_plan", cu_seqlens, total_tokens, max_seqlen, cu_prefix, total_prefix,
+                 max_prefix_len, cu_group, Hq, Hkv, head_dim, workspace, dev_status, stream)
+
+
+def bg_shared_last_token_plan(cu_seqlens, total_tokens: int, max_seqlen: int, cu_prefix, total_prefix: int,
+                              max_prefix_len: int, cu_group, Hq: int, Hkv: int, head_dim: int, *, workspace=None,
+                              dev_status=None, stream=None):
+    """The work list of a packing into workspace, for bg_shared_last_token_attn_planned calls with it."""
+    _shared_plan("bg_shared_last_token_plan", cu_seqlens, total_tokens, max_seqlen, cu_prefix, total_prefix,
+                 max_prefix_len, cu_group, Hq, Hkv, head_dim, workspace, dev_status, stream)

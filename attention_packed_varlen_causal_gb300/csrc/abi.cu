@@ -12,6 +12,7 @@
 #include "bg_attn.h"
 #include "bg_attn_kernel.cuh"
 #include "bg_internal.h"
+#include "shared_attn.h"
 
 using namespace bg;
 
@@ -581,5 +582,201 @@ bg_status_t bg_selftest_wait_timeout(int32_t *dev_status, unsigned long long *wa
     if (launch_wait_timeout_selftest(dev_status, waited_ns, stream) != cudaSuccess) return BG_ERR_CUDA;
     return BG_OK;
 }
+
+}  // extern "C"
+
+namespace {
+
+// Sizes and supported shapes of the shared-prefix calls (checked before any pointer).
+bg_status_t shared_check_sizes(const ShProblem &pb)
+{
+    if (pb.num_seqs < 0 || pb.total_tokens < 0 || pb.max_seqlen < 0 || pb.num_groups < 0 || pb.total_prefix < 0 ||
+        pb.max_prefix_len < 0 || pb.Hq <= 0 || pb.Hkv <= 0 || pb.head_dim <= 0 || pb.Hq % pb.Hkv != 0)
+        return BG_ERR_INVALID_ARG;
+    if (pb.num_groups == 0 && (pb.num_seqs > 0 || pb.total_prefix > 0)) return BG_ERR_INVALID_ARG;
+    if (!supported_head_dim(pb.head_dim) || pb.Hq / pb.Hkv > kShRows || pb.max_seqlen > BG_MAX_SEQLEN ||
+        pb.max_prefix_len > BG_MAX_SEQLEN)
+        return BG_ERR_UNSUPPORTED;
+    const ShLayout lay = shared_layout(pb);
+    if ((lay.max_entries + kShSlots) * pb.Hkv >= (int64_t(1) << 31)) return BG_ERR_UNSUPPORTED;
+    return BG_OK;
+}
+
+bool shared_is_noop(const ShProblem &pb) { return pb.last ? pb.num_seqs == 0 : pb.total_tokens == 0; }
+
+bg_status_t shared_check_plan(const ShProblem &pb, const void *workspace, size_t workspace_bytes,
+                              const int32_t *dev_status)
+{
+    if (!pb.cu_seqlens || !pb.cu_prefix || !pb.cu_group || !aligned(pb.cu_seqlens, 4) || !aligned(pb.cu_prefix, 4) ||
+        !aligned(pb.cu_group, 4) || (dev_status && !aligned(dev_status, 4)))
+        return BG_ERR_INVALID_ARG;
+    if (!workspace || !aligned(workspace, 256) || workspace_bytes < shared_layout(pb).total) return BG_ERR_INVALID_ARG;
+    if (overlap(pb.cu_seqlens, (static_cast<size_t>(pb.num_seqs) + 1) * 4, workspace, workspace_bytes) ||
+        overlap(pb.cu_prefix, (static_cast<size_t>(pb.num_groups) + 1) * 4, workspace, workspace_bytes) ||
+        overlap(pb.cu_group, (static_cast<size_t>(pb.num_groups) + 1) * 4, workspace, workspace_bytes))
+        return BG_ERR_INVALID_ARG;
+    return BG_OK;
+}
+
+bg_status_t shared_plan_impl(const ShProblem &pb, void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                             cudaStream_t stream)
+{
+    bg_status_t st = shared_check_sizes(pb);
+    if (st != BG_OK || shared_is_noop(pb)) return st;
+    st = shared_check_plan(pb, workspace, workspace_bytes, dev_status);
+    if (st != BG_OK) return st;
+    return launch_shared_plan(pb, shared_layout(pb), workspace, dev_status, stream) == cudaSuccess ? BG_OK
+                                                                                                   : BG_ERR_CUDA;
+}
+
+bg_status_t shared_impl(const ShProblem &pb, const void *q, const void *k, const void *v, const void *prefix_k,
+                        const void *prefix_v, float scale, float softcap, void *out, float *lse, void *workspace,
+                        size_t workspace_bytes, int32_t *dev_status, cudaStream_t stream, bool with_plan)
+{
+    if (!std::isfinite(scale) || !(scale > 0.f) || !std::isfinite(softcap) || softcap < 0.f) return BG_ERR_INVALID_ARG;
+    // scale / cap and cap * log2(e) have to be ordinary numbers
+    const bool capped = softcap > 0.f;
+    if (capped && (!std::isnormal(scale / softcap) || !std::isnormal(softcap * 1.4426950408889634f)))
+        return BG_ERR_INVALID_ARG;
+    bg_status_t st = shared_check_sizes(pb);
+    if (st != BG_OK || shared_is_noop(pb)) return st;
+    st = shared_check_plan(pb, workspace, workspace_bytes, dev_status);
+    if (st != BG_OK) return st;
+    if (!q || !out || (pb.total_tokens > 0 && (!k || !v)) || (pb.total_prefix > 0 && (!prefix_k || !prefix_v)))
+        return BG_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(prefix_k, 16) ||
+        !aligned(prefix_v, 16) || !aligned(lse, 4))
+        return BG_ERR_INVALID_ARG;
+    const size_t rows = static_cast<size_t>(pb.last ? pb.num_seqs : pb.total_tokens);
+    const size_t qbytes = rows * pb.Hq * pb.head_dim * 2;
+    const size_t kvbytes = static_cast<size_t>(pb.total_tokens) * pb.Hkv * pb.head_dim * 2;
+    const size_t pbytes = static_cast<size_t>(pb.total_prefix) * pb.Hkv * pb.head_dim * 2;
+    const size_t lsebytes = lse ? rows * pb.Hq * 4 : 0;
+    const void *in[8] = {q, k, v, prefix_k, prefix_v, pb.cu_seqlens, pb.cu_prefix, pb.cu_group};
+    const size_t inb[8] = {qbytes, kvbytes, kvbytes, pbytes, pbytes, (static_cast<size_t>(pb.num_seqs) + 1) * 4,
+                           (static_cast<size_t>(pb.num_groups) + 1) * 4, (static_cast<size_t>(pb.num_groups) + 1) * 4};
+    for (int i = 0; i < 8; ++i)
+        if (overlap(out, qbytes, in[i], inb[i]) || overlap(lse, lsebytes, in[i], inb[i]) ||
+            overlap(workspace, workspace_bytes, in[i], inb[i]))
+            return BG_ERR_INVALID_ARG;
+    if (overlap(out, qbytes, lse, lsebytes) || overlap(out, qbytes, workspace, workspace_bytes) ||
+        overlap(lse, lsebytes, workspace, workspace_bytes))
+        return BG_ERR_INVALID_ARG;
+
+    const int nsm = sm_count();
+    if (nsm <= 0) return BG_ERR_CUDA;
+    const int32_t g = pb.Hq / pb.Hkv;
+    const int32_t bt = kShRows / g;
+    CUtensorMap tm_q, tm_k, tm_v, tm_pk, tm_pv;
+    const uint64_t D = static_cast<uint64_t>(pb.head_dim);
+    const uint64_t dq[4] = {D, static_cast<uint64_t>(g), static_cast<uint64_t>(pb.Hkv), rows};
+    const uint64_t sq[3] = {D * 2, static_cast<uint64_t>(g) * D * 2, static_cast<uint64_t>(pb.Hq) * D * 2};
+    const uint32_t boxq[4] = {64, static_cast<uint32_t>(g), 1, static_cast<uint32_t>(bt)};
+    const uint64_t skv[2] = {D * 2, static_cast<uint64_t>(pb.Hkv) * D * 2};
+    const uint32_t boxkv[3] = {64, 1, static_cast<uint32_t>(kShKeys)};
+    // With no rows of a kind no tile of it is ever loaded; the maps only need a valid base.
+    auto kv_map = [&](CUtensorMap *m, const void *base, int32_t n) {
+        const uint64_t dims[3] = {D, static_cast<uint64_t>(pb.Hkv), static_cast<uint64_t>(n > 0 ? n : 1)};
+        return encode_map(m, n > 0 ? base : q, 3, dims, skv, boxkv);
+    };
+    if (!encode_map(&tm_q, q, 4, dq, sq, boxq) || !kv_map(&tm_k, k, pb.total_tokens) ||
+        !kv_map(&tm_v, v, pb.total_tokens) || !kv_map(&tm_pk, prefix_k, pb.total_prefix) ||
+        !kv_map(&tm_pv, prefix_v, pb.total_prefix))
+        return BG_ERR_CUDA;
+
+    const ShLayout lay = shared_layout(pb);
+    if (with_plan && launch_shared_plan(pb, lay, workspace, dev_status, stream) != cudaSuccess) return BG_ERR_CUDA;
+
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    ShParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.Hq = pb.Hq;
+    p.Hkv = pb.Hkv;
+    p.g = g;
+    p.bt = bt;
+    p.last = pb.last;
+    p.num_seqs = pb.num_seqs;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.cap_in = capped ? scale / softcap : 0.f;
+    p.cap_log2 = softcap * 1.4426950408889634f;
+    p.out = static_cast<__nv_bfloat16 *>(out);
+    p.lse = lse;
+    p.dev_status = dev_status;
+    p.key = shared_key(pb);
+    p.cu_seqlens = pb.cu_seqlens;
+    p.hdr = reinterpret_cast<const int32_t *>(ws);
+    p.entries = reinterpret_cast<const ShEntry *>(ws + lay.entries);
+    p.splits = reinterpret_cast<const ShSplit *>(ws + lay.splits);
+    p.part_o = reinterpret_cast<float *>(ws + lay.part_o);
+    p.part_l = reinterpret_cast<float *>(ws + lay.part_l);
+    p.part_fix = lay.slots * kShTiles * kShRows;
+    const int64_t items = (lay.max_entries + (lay.slots > 0 ? kShSlots : 0)) * pb.Hkv;
+    const int grid = static_cast<int>(items < nsm ? items : nsm);
+    return launch_shared_attn(pb.head_dim, capped, tm_q, tm_k, tm_v, tm_pk, tm_pv, p, grid, lay.slots > 0, stream) ==
+                   cudaSuccess
+               ? BG_OK
+               : BG_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t bg_shared_attn_workspace_size(int32_t num_groups, int32_t num_seqs, int32_t total_tokens, int32_t max_seqlen,
+                                     int32_t max_prefix_len, int32_t Hq, int32_t Hkv, int32_t head_dim)
+{
+    size_t most = 0;
+    for (int32_t last = 0; last < 2; ++last) {
+        const ShProblem pb{nullptr, nullptr, nullptr, num_seqs, total_tokens, max_seqlen, num_groups, 0,
+                           max_prefix_len, Hq, Hkv, head_dim, last};
+        if (shared_check_sizes(pb) != BG_OK) return 0;
+        const size_t n = shared_layout(pb).total;
+        if (n > most) most = n;
+    }
+    return most;
+}
+
+#define BG_SHARED_PROBLEM(LAST)                                                                                       \
+    const ShProblem pb{cu_seqlens, cu_prefix, cu_group, num_seqs, total_tokens, max_seqlen, num_groups, total_prefix, \
+                       max_prefix_len, Hq, Hkv, head_dim, LAST}
+
+bg_status_t bg_shared_prefill_plan(const int32_t *cu_seqlens, int32_t num_seqs, int32_t total_tokens,
+                                   int32_t max_seqlen, const int32_t *cu_prefix, int32_t total_prefix,
+                                   int32_t max_prefix_len, const int32_t *cu_group, int32_t num_groups, int32_t Hq,
+                                   int32_t Hkv, int32_t head_dim, void *workspace, size_t workspace_bytes,
+                                   int32_t *dev_status, cudaStream_t stream)
+{
+    BG_SHARED_PROBLEM(0);
+    return shared_plan_impl(pb, workspace, workspace_bytes, dev_status, stream);
+}
+
+bg_status_t bg_shared_last_token_plan(const int32_t *cu_seqlens, int32_t num_seqs, int32_t total_tokens,
+                                      int32_t max_seqlen, const int32_t *cu_prefix, int32_t total_prefix,
+                                      int32_t max_prefix_len, const int32_t *cu_group, int32_t num_groups, int32_t Hq,
+                                      int32_t Hkv, int32_t head_dim, void *workspace, size_t workspace_bytes,
+                                      int32_t *dev_status, cudaStream_t stream)
+{
+    BG_SHARED_PROBLEM(1);
+    return shared_plan_impl(pb, workspace, workspace_bytes, dev_status, stream);
+}
+
+#define BG_SHARED_RUN(NAME, LAST, PLAN)                                                                               \
+    bg_status_t NAME(const void *q, const void *k, const void *v, const int32_t *cu_seqlens, int32_t num_seqs,        \
+                     int32_t total_tokens, int32_t max_seqlen, const void *prefix_k, const void *prefix_v,            \
+                     const int32_t *cu_prefix, int32_t total_prefix, int32_t max_prefix_len, const int32_t *cu_group, \
+                     int32_t num_groups, int32_t Hq, int32_t Hkv, int32_t head_dim, float scale, float softcap,       \
+                     void *out, float *lse, void *workspace, size_t workspace_bytes, int32_t *dev_status,             \
+                     cudaStream_t stream)                                                                             \
+    {                                                                                                                 \
+        BG_SHARED_PROBLEM(LAST);                                                                                      \
+        return shared_impl(pb, q, k, v, prefix_k, prefix_v, scale, softcap, out, lse, workspace, workspace_bytes,     \
+                           dev_status, stream, PLAN);                                                                 \
+    }
+BG_SHARED_RUN(bg_shared_prefill_attn, 0, true)
+BG_SHARED_RUN(bg_shared_prefill_attn_planned, 0, false)
+BG_SHARED_RUN(bg_shared_last_token_attn, 1, true)
+BG_SHARED_RUN(bg_shared_last_token_attn_planned, 1, false)
+#undef BG_SHARED_RUN
+#undef BG_SHARED_PROBLEM
 
 }  // extern "C"

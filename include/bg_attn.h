@@ -60,6 +60,8 @@ typedef enum {
 #define BG_DEVSTAT_EMPTY_ROW    0x10  /* prompt length 0 with suffix_len 0          */
 #define BG_DEVSTAT_PLAN         0x20  /* planned run: the workspace's work list is
                                          for another packing (nothing written)     */
+#define BG_DEVSTAT_GROUP        0x40  /* cu_group[0]!=0, decreasing, or cu_group[R]!=num_seqs */
+#define BG_DEVSTAT_TOKEN        0x80  /* a given token is outside [0, V)            */
 #define BG_DEVSTAT_TIMEOUT      0x100 /* an internal pipeline wait ran out          */
 
 /* Supported shapes: head_dim in {64, 128}; Hq % Hkv == 0; for decode
@@ -393,6 +395,111 @@ bg_status_t bg_beam_select(const float *logits, const float *cum,
                            int32_t R, int32_t W, int32_t V,
                            int32_t *token_out, int32_t *parent_out, float *score_out,
                            void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Attention of the samples of a request over the request's one prefix.
+ * Source: abstract (shared-prefix K/V layout inside a request; Prefill-Only
+ * requests with several samples) and section 1.2 (state that a request's
+ * sequences share is kept once) of the page above.  Request r has prefix rows
+ * cu_prefix[r] .. cu_prefix[r+1]-1 of prefix_k/prefix_v and the samples
+ * cu_group[r] .. cu_group[r+1]-1; sample s has rows cu_seqlens[s] ..
+ * cu_seqlens[s+1]-1 of k/v.  With kvh = h / (Hq/Hkv) and the softmax over
+ *     keys = [all prefix rows of r ; the rows of s that the query sees]
+ *     x_j  = scale * q . key_j,kvh                          (softcap == 0)
+ *     x_j  = softcap * tanh(scale * q . key_j,kvh / softcap)    (softcap > 0)
+ * two calls compute sum_j softmax_j(x) value_j,kvh:
+ *   bg_shared_prefill_attn      one query per sample token, which sees its
+ *                               sample's rows up to itself (causal);
+ *   bg_shared_last_token_attn   one query per sample, which sees the whole
+ *                               sample: the last layer of a Prefill-Only
+ *                               request, or a decode step of samples drawn
+ *                               from one prompt (k/v then hold the new rows).
+ * A request without a prefix (length 0), a sample without rows and a request
+ * without samples are allowed; a query without any key is not written and
+ * raises BG_DEVSTAT_EMPTY_ROW.  The K/V of the prefix is what
+ * bg_packed_prefill_attn over the prefixes reads.
+ *
+ *   q            bf16 [total_tokens, Hq, head_dim] (prefill) or
+ *                [num_seqs, Hq, head_dim] (last token)
+ *   k, v         bf16 [total_tokens, Hkv, head_dim]; NULL if total_tokens == 0
+ *   cu_seqlens   int32 [num_seqs+1], device; cu[0]=0, non-decreasing,
+ *                cu[num_seqs]=total_tokens
+ *   max_seqlen   host upper bound of every sample's length (checked on device)
+ *   prefix_k, prefix_v  bf16 [total_prefix, Hkv, head_dim]; NULL if
+ *                total_prefix == 0
+ *   cu_prefix    int32 [num_groups+1], device; as cu_seqlens, for total_prefix
+ *   max_prefix_len  host upper bound of every prefix (checked on device)
+ *   cu_group     int32 [num_groups+1], device; as cu_seqlens, for num_seqs
+ *   scale        finite, > 0;  softcap finite, >= 0 (0: scores are not capped)
+ *   out          bf16, the shape of q
+ *   lse          fp32 [rows of q, Hq] natural-log sum-exp of x, or NULL
+ *   workspace    device buffer of at least bg_shared_attn_workspace_size(...)
+ *                bytes (enough for both calls), 256-byte aligned; contents on
+ *                entry do not matter; not for calls that overlap in time
+ * Two or three launches on `stream`: a pre-pass that checks the offsets and
+ * writes the work list, the attention, and where the sizes allow it the join
+ * of key ranges that were split over several SMs.  Bad offsets raise
+ * BG_DEVSTAT_CU_SEQLENS, _SEQ_TOO_LONG, _CU_PROMPT (cu_prefix) or _GROUP, and
+ * nothing is written.  Results do not depend on the order in which the SMs
+ * run.  Non-finite K or V rows reach only queries of the same request.
+ *
+ * For layers that share one packing the pre-pass can be made once:
+ * bg_shared_prefill_plan or bg_shared_last_token_plan, then the _planned call
+ * of the same kind per layer, with the same offsets and sizes and no other use
+ * of the workspace between the plan and the last layer than these calls.  A
+ * planned call whose sizes are not the plan's writes nothing and raises
+ * BG_DEVSTAT_PLAN.
+ *
+ * Errors: BG_ERR_INVALID_ARG for NULL or misaligned pointers, negative sizes,
+ * num_groups == 0 with samples or prefix rows, Hq % Hkv != 0, a bad scale or
+ * softcap (or one whose quotient or product with log2(e) is not a normal
+ * number), a too-small workspace, or an output or the workspace overlapping
+ * another argument; BG_ERR_UNSUPPORTED for head_dim not in {64, 128},
+ * Hq/Hkv > 128, or max_seqlen or max_prefix_len > BG_MAX_SEQLEN.  No queries
+ * (total_tokens == 0, or num_seqs == 0 for the last-token call) is a valid
+ * no-op.  bg_shared_attn_workspace_size gives 0 for sizes the calls refuse.
+ */
+size_t bg_shared_attn_workspace_size(int32_t num_groups, int32_t num_seqs, int32_t total_tokens,
+                                     int32_t max_seqlen, int32_t max_prefix_len, int32_t Hq,
+                                     int32_t Hkv, int32_t head_dim);
+bg_status_t bg_shared_prefill_attn(const void *q, const void *k, const void *v, const int32_t *cu_seqlens,
+                       int32_t num_seqs, int32_t total_tokens, int32_t max_seqlen,
+                       const void *prefix_k, const void *prefix_v, const int32_t *cu_prefix,
+                       int32_t total_prefix, int32_t max_prefix_len, const int32_t *cu_group,
+                       int32_t num_groups, int32_t Hq, int32_t Hkv, int32_t head_dim, float scale,
+                       float softcap, void *out, float *lse, void *workspace,
+                       size_t workspace_bytes, int32_t *dev_status, cudaStream_t stream);
+bg_status_t bg_shared_last_token_attn(const void *q, const void *k, const void *v, const int32_t *cu_seqlens,
+                       int32_t num_seqs, int32_t total_tokens, int32_t max_seqlen,
+                       const void *prefix_k, const void *prefix_v, const int32_t *cu_prefix,
+                       int32_t total_prefix, int32_t max_prefix_len, const int32_t *cu_group,
+                       int32_t num_groups, int32_t Hq, int32_t Hkv, int32_t head_dim, float scale,
+                       float softcap, void *out, float *lse, void *workspace,
+                       size_t workspace_bytes, int32_t *dev_status, cudaStream_t stream);
+bg_status_t bg_shared_prefill_plan(const int32_t *cu_seqlens, int32_t num_seqs, int32_t total_tokens,
+                       int32_t max_seqlen, const int32_t *cu_prefix, int32_t total_prefix,
+                       int32_t max_prefix_len, const int32_t *cu_group, int32_t num_groups,
+                       int32_t Hq, int32_t Hkv, int32_t head_dim, void *workspace,
+                       size_t workspace_bytes, int32_t *dev_status, cudaStream_t stream);
+bg_status_t bg_shared_last_token_plan(const int32_t *cu_seqlens, int32_t num_seqs, int32_t total_tokens,
+                       int32_t max_seqlen, const int32_t *cu_prefix, int32_t total_prefix,
+                       int32_t max_prefix_len, const int32_t *cu_group, int32_t num_groups,
+                       int32_t Hq, int32_t Hkv, int32_t head_dim, void *workspace,
+                       size_t workspace_bytes, int32_t *dev_status, cudaStream_t stream);
+bg_status_t bg_shared_prefill_attn_planned(const void *q, const void *k, const void *v, const int32_t *cu_seqlens,
+                       int32_t num_seqs, int32_t total_tokens, int32_t max_seqlen,
+                       const void *prefix_k, const void *prefix_v, const int32_t *cu_prefix,
+                       int32_t total_prefix, int32_t max_prefix_len, const int32_t *cu_group,
+                       int32_t num_groups, int32_t Hq, int32_t Hkv, int32_t head_dim, float scale,
+                       float softcap, void *out, float *lse, void *workspace,
+                       size_t workspace_bytes, int32_t *dev_status, cudaStream_t stream);
+bg_status_t bg_shared_last_token_attn_planned(const void *q, const void *k, const void *v, const int32_t *cu_seqlens,
+                       int32_t num_seqs, int32_t total_tokens, int32_t max_seqlen,
+                       const void *prefix_k, const void *prefix_v, const int32_t *cu_prefix,
+                       int32_t total_prefix, int32_t max_prefix_len, const int32_t *cu_group,
+                       int32_t num_groups, int32_t Hq, int32_t Hkv, int32_t head_dim, float scale,
+                       float softcap, void *out, float *lse, void *workspace,
+                       size_t workspace_bytes, int32_t *dev_status, cudaStream_t stream);
 
 /*
  * Allocation-free variant of bg_packed_prefill_attn.  The paper has no
