@@ -34,6 +34,8 @@ BG_MAX_SEQLEN = 65536
 BG_NOALLOC_SCRATCH_BYTES = 1 << 20
 BG_MAX_BEAM = 512
 BG_MAX_VOCAB = 1 << 22
+BG_MAX_TOP = 32
+BG_DTYPE_F32, BG_DTYPE_BF16 = 0, 1
 
 # Every symbol include/bg_attn.h declares, with its ctypes signature.
 _P, _I32, _F32, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
@@ -68,6 +70,7 @@ SIGNATURES = {
     "bg_shared_prefill_attn_planned": (_SHARED_RUN, ctypes.c_int),
     "bg_shared_last_token_attn": (_SHARED_RUN, ctypes.c_int),
     "bg_shared_last_token_attn_planned": (_SHARED_RUN, ctypes.c_int),
+    "bg_token_logprobs": ([_P, _I32, ctypes.c_int64, _I32, _I32, _P, _I32, _P, _P, _P, _P, _P, _P], ctypes.c_int),
     "bg_selftest_wait_timeout": ([_P, _P, _P], ctypes.c_int),
     "bg_beam_select": ([_P, _P, _I32, _I32, _I32, _P, _P, _P, _P, _SZ, _P], ctypes.c_int),
 }
@@ -446,3 +449,28 @@ def bg_shared_last_token_plan(cu_seqlens, total_tokens: int, max_seqlen: int, cu
     """The work list of a packing into workspace, for bg_shared_last_token_attn_planned calls with it."""
     _shared_plan("bg_shared_last_token_plan", cu_seqlens, total_tokens, max_seqlen, cu_prefix, total_prefix,
                  max_prefix_len, cu_group, Hq, Hkv, head_dim, workspace, dev_status, stream)
+
+
+def bg_token_logprobs(logits, tokens=None, *, logprob=None, entropy=None, top_token=None, top_logprob=None,
+                      dev_status=None, stream=None):
+    """logits fp32 or bf16 [N,V] (rows may be strided, columns not); tokens int32 [N] or None;
+    written: logprob fp32 [N] (with tokens), entropy fp32 [N] or None, top_token int32 [N,K] and
+    top_logprob fp32 [N,K] or both None."""
+    fn = "bg_token_logprobs"
+    N, V = logits.shape
+    dtype = {"torch.float32": BG_DTYPE_F32, "torch.bfloat16": BG_DTYPE_BF16}.get(str(logits.dtype))
+    if dtype is None or (V > 1 and N > 0 and logits.stride(1) != 1):
+        raise ValueError(f"{fn}: logits must be float32 or bfloat16 with contiguous rows, got {logits.dtype} with "
+                         f"strides {logits.stride()}")
+    dev = logits.device
+    K = 0 if top_token is None else top_token.shape[-1]
+    _expect(fn, dev, tokens=(tokens, "int32", (N,)), logprob=(logprob, "float32", (N,)),
+            entropy=(entropy, "float32", (N,)), top_token=(top_token, "int32", (N, K)),
+            top_logprob=(top_logprob, "float32", (N, K)),
+            dev_status=(dev_status, "int32", () if dev_status is None else dev_status.shape))
+    ctx, st = _on(dev, stream)
+    with ctx:
+        _check(fn, load().bg_token_logprobs(_ptr(logits), dtype, logits.stride(0) if N > 1 else max(V, 1), N, V,
+                                            _ptr(tokens), K, _ptr(logprob), _ptr(entropy), _ptr(top_token),
+                                            _ptr(top_logprob), _ptr(dev_status), st))
+    return logprob, entropy, top_token, top_logprob

@@ -20,7 +20,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(PKG, "libbgattn.so")
 SOURCES = ["abi.cu", "prefill.cu", "decode.cu", "reorder.cu", "noalloc.cu", "lasttok.cu", "select.cu", "selftest.cu",
-           "shared_attn.cu"]
+           "shared_attn.cu", "logprobs.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

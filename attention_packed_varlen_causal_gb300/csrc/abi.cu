@@ -779,4 +779,39 @@ BG_SHARED_RUN(bg_shared_last_token_attn_planned, 1, false)
 #undef BG_SHARED_RUN
 #undef BG_SHARED_PROBLEM
 
+bg_status_t bg_token_logprobs(const void *logits, int32_t dtype, int64_t row_stride, int32_t N, int32_t V,
+                              const int32_t *tokens, int32_t K, float *logprob_out, float *entropy_out,
+                              int32_t *top_token_out, float *top_logprob_out, int32_t *dev_status,
+                              cudaStream_t stream)
+{
+    if (N < 0 || (dtype != BG_DTYPE_F32 && dtype != BG_DTYPE_BF16)) return BG_ERR_INVALID_ARG;
+    if (V < 1 || V > BG_MAX_VOCAB || K < 0 || K > BG_MAX_TOP || K > V) return BG_ERR_UNSUPPORTED;
+    if (row_stride < V) return BG_ERR_INVALID_ARG;
+    if (N == 0) return BG_OK;
+    const uintptr_t es = dtype == BG_DTYPE_F32 ? 4 : 2;
+    if (!logits || !aligned(logits, es) || !aligned(tokens, 4) || !aligned(logprob_out, 4) ||
+        !aligned(entropy_out, 4) || !aligned(top_token_out, 4) || !aligned(top_logprob_out, 4) ||
+        !aligned(dev_status, 4))
+        return BG_ERR_INVALID_ARG;
+    if ((tokens != nullptr) != (logprob_out != nullptr) || (K > 0) != (top_token_out != nullptr) ||
+        (K > 0) != (top_logprob_out != nullptr) || (!tokens && !entropy_out && K == 0))
+        return BG_ERR_INVALID_ARG;
+    const size_t n = static_cast<size_t>(N);
+    const size_t lbytes = ((n - 1) * static_cast<size_t>(row_stride) + V) * es;
+    const void *outs[4] = {logprob_out, entropy_out, top_token_out, top_logprob_out};
+    const size_t outb[4] = {n * 4, n * 4, n * K * 4, n * K * 4};
+    for (int o = 0; o < 4; ++o) {
+        if (overlap(outs[o], outb[o], logits, lbytes) || overlap(outs[o], outb[o], tokens, n * 4))
+            return BG_ERR_INVALID_ARG;
+        for (int o2 = o + 1; o2 < 4; ++o2)
+            if (overlap(outs[o], outb[o], outs[o2], outb[o2])) return BG_ERR_INVALID_ARG;
+    }
+    const int nsm = sm_count();
+    if (nsm <= 0) return BG_ERR_CUDA;
+    return launch_token_logprobs(logits, dtype, row_stride, N, V, tokens, K, logprob_out, entropy_out, top_token_out,
+                                 top_logprob_out, dev_status, nsm, stream) == cudaSuccess
+               ? BG_OK
+               : BG_ERR_CUDA;
+}
+
 }  // extern "C"

@@ -72,6 +72,10 @@ typedef enum {
  * keep at most 400 beams); vocabulary: W <= V <= BG_MAX_VOCAB. */
 #define BG_MAX_BEAM 512
 #define BG_MAX_VOCAB (1 << 22)
+/* Alternatives per row of bg_token_logprobs, and its logits' types. */
+#define BG_MAX_TOP 32
+#define BG_DTYPE_F32 0
+#define BG_DTYPE_BF16 1
 
 /* Human-readable name of a status code (static storage, never NULL). */
 const char *bg_status_string(bg_status_t status);
@@ -500,6 +504,42 @@ bg_status_t bg_shared_last_token_attn_planned(const void *q, const void *k, cons
                        int32_t num_groups, int32_t Hq, int32_t Hkv, int32_t head_dim, float scale,
                        float softcap, void *out, float *lse, void *workspace,
                        size_t workspace_bytes, int32_t *dev_status, cudaStream_t stream);
+
+/*
+ * Log-probability of a given token, entropy and the best alternatives of rows
+ * of logits.  Source: section 1.1 of the page above (a Prefill-Only request is
+ * answered from the next-token logits: softmax, Top-K).  For row i, with the
+ * softmax p over its V logits x (all in fp32):
+ *     logprob_out[i]      = log p(tokens[i])
+ *     entropy_out[i]      = - sum_v p(v) log p(v)     (0 log 0 = 0; in nats)
+ *     top_token_out[i, :] = the K tokens with the largest logits, best first,
+ *                           equal logits by the smaller token
+ *     top_logprob_out[i, :] = their log-probabilities
+ *
+ *   logits       fp32 (dtype BG_DTYPE_F32) or bf16 (BG_DTYPE_BF16), row i at
+ *                logits + i * row_stride elements, row_stride >= V; aligned
+ *                to its element; -inf marks a banned token
+ *   tokens       int32 [N], or NULL (then logprob_out is NULL too).  A token
+ *                outside [0, V) leaves its logprob_out as it was and raises
+ *                BG_DEVSTAT_TOKEN; the row's other outputs are written.
+ *   K            0 .. min(V, BG_MAX_TOP); with 0 the top outputs are NULL
+ *   logprob_out, entropy_out  fp32 [N], each may be NULL
+ *   top_token_out int32 [N, K], top_logprob_out fp32 [N, K]
+ *   dev_status   device int32 or NULL
+ * A row with a NaN or +inf logit gets NaN and tokens -1; a row of -inf only
+ * gets log-probabilities -inf, entropy 0 and the tokens 0 .. K-1.
+ * One launch, no workspace; the logits come from memory once (a row with
+ * thousands of logits equal to its K-th best is read K times more).
+ * Errors: BG_ERR_INVALID_ARG for N < 0, an unknown dtype, row_stride < V, NULL
+ * or misaligned pointers, one of the top outputs or of tokens / logprob_out
+ * without the other, no output at all, or an output overlapping another
+ * argument; BG_ERR_UNSUPPORTED unless 1 <= V <= BG_MAX_VOCAB and
+ * 0 <= K <= min(V, BG_MAX_TOP).  N == 0 is a valid no-op.
+ */
+bg_status_t bg_token_logprobs(const void *logits, int32_t dtype, int64_t row_stride, int32_t N,
+                              int32_t V, const int32_t *tokens, int32_t K, float *logprob_out,
+                              float *entropy_out, int32_t *top_token_out,
+                              float *top_logprob_out, int32_t *dev_status, cudaStream_t stream);
 
 /*
  * Allocation-free variant of bg_packed_prefill_attn.  The paper has no
