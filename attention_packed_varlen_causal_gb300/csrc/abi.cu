@@ -597,9 +597,18 @@ bg_status_t shared_check_sizes(const ShProblem &pb)
     if (!supported_head_dim(pb.head_dim) || pb.Hq / pb.Hkv > kShRows || pb.max_seqlen > BG_MAX_SEQLEN ||
         pb.max_prefix_len > BG_MAX_SEQLEN)
         return BG_ERR_UNSUPPORTED;
-    const ShLayout lay = shared_layout(pb);
-    if ((lay.max_entries + kShSlots) * pb.Hkv >= (int64_t(1) << 31)) return BG_ERR_UNSUPPORTED;
+    if (shared_layout(pb).max_entries * pb.Hkv >= (int64_t(1) << 31)) return BG_ERR_UNSUPPORTED;
     return BG_OK;
+}
+
+// CTAs of the attention kernel: one per SM, no more than there can be items (or parts of them).
+int shared_grid(const ShProblem &pb, const ShLayout &lay)
+{
+    int64_t n = sm_count();
+    const int64_t items = lay.max_entries * pb.Hkv;
+    if (lay.slots == 0 && items < n) n = items;
+    if (lay.slots > 0 && lay.slots / 2 < n) n = lay.slots / 2;
+    return static_cast<int>(n < kShMaxCtas ? n : kShMaxCtas);
 }
 
 bool shared_is_noop(const ShProblem &pb) { return pb.last ? pb.num_seqs == 0 : pb.total_tokens == 0; }
@@ -625,8 +634,10 @@ bg_status_t shared_plan_impl(const ShProblem &pb, void *workspace, size_t worksp
     if (st != BG_OK || shared_is_noop(pb)) return st;
     st = shared_check_plan(pb, workspace, workspace_bytes, dev_status);
     if (st != BG_OK) return st;
-    return launch_shared_plan(pb, shared_layout(pb), workspace, dev_status, stream) == cudaSuccess ? BG_OK
-                                                                                                   : BG_ERR_CUDA;
+    const ShLayout lay = shared_layout(pb);
+    const int grid = shared_grid(pb, lay);
+    if (grid <= 0) return BG_ERR_CUDA;
+    return launch_shared_plan(pb, lay, workspace, grid, dev_status, stream) == cudaSuccess ? BG_OK : BG_ERR_CUDA;
 }
 
 bg_status_t shared_impl(const ShProblem &pb, const void *q, const void *k, const void *v, const void *prefix_k,
@@ -663,8 +674,9 @@ bg_status_t shared_impl(const ShProblem &pb, const void *q, const void *k, const
         overlap(lse, lsebytes, workspace, workspace_bytes))
         return BG_ERR_INVALID_ARG;
 
-    const int nsm = sm_count();
-    if (nsm <= 0) return BG_ERR_CUDA;
+    const ShLayout lay = shared_layout(pb);
+    const int grid = shared_grid(pb, lay);
+    if (grid <= 0) return BG_ERR_CUDA;
     const int32_t g = pb.Hq / pb.Hkv;
     const int32_t bt = kShRows / g;
     CUtensorMap tm_q, tm_k, tm_v, tm_pk, tm_pv;
@@ -684,8 +696,8 @@ bg_status_t shared_impl(const ShProblem &pb, const void *q, const void *k, const
         !kv_map(&tm_pv, prefix_v, pb.total_prefix))
         return BG_ERR_CUDA;
 
-    const ShLayout lay = shared_layout(pb);
-    if (with_plan && launch_shared_plan(pb, lay, workspace, dev_status, stream) != cudaSuccess) return BG_ERR_CUDA;
+    if (with_plan && launch_shared_plan(pb, lay, workspace, grid, dev_status, stream) != cudaSuccess)
+        return BG_ERR_CUDA;
 
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     ShParams p;
@@ -702,16 +714,15 @@ bg_status_t shared_impl(const ShProblem &pb, const void *q, const void *k, const
     p.out = static_cast<__nv_bfloat16 *>(out);
     p.lse = lse;
     p.dev_status = dev_status;
-    p.key = shared_key(pb);
+    p.key = shared_key(pb, grid);
     p.cu_seqlens = pb.cu_seqlens;
     p.hdr = reinterpret_cast<const int32_t *>(ws);
     p.entries = reinterpret_cast<const ShEntry *>(ws + lay.entries);
+    p.starts = reinterpret_cast<const ShStart *>(ws + lay.starts);
     p.splits = reinterpret_cast<const ShSplit *>(ws + lay.splits);
     p.part_o = reinterpret_cast<float *>(ws + lay.part_o);
     p.part_l = reinterpret_cast<float *>(ws + lay.part_l);
     p.part_fix = lay.slots * kShTiles * kShRows;
-    const int64_t items = (lay.max_entries + (lay.slots > 0 ? kShSlots : 0)) * pb.Hkv;
-    const int grid = static_cast<int>(items < nsm ? items : nsm);
     return launch_shared_attn(pb.head_dim, capped, tm_q, tm_k, tm_v, tm_pk, tm_pv, p, grid, lay.slots > 0, stream) ==
                    cudaSuccess
                ? BG_OK

@@ -17,18 +17,19 @@
 // kShTiles query tiles share every K/V tile that is loaded.
 //
 // Three launches on the caller's stream:
-//   1. shared_plan_kernel (one CTA) checks the offsets on the device and writes the work list,
-//      costliest entries first; entries with long key ranges are split into pieces when there are
-//      too few of them to fill the GPU.
-//   2. shared_attn_kernel: one persistent CTA per SM, 12 warps:
-//        warp 0      TMA producer of K and V tiles of 128 keys (one ring for both)
+//   1. shared_plan_kernel (one CTA) checks the offsets on the device, writes the list of entries
+//      and cuts the whole work, as one line of (kv head, entry, key tile), into equal shares, one
+//      per CTA of the next kernel.  A cut through a long key range leaves two partial results.
+//   2. shared_attn_kernel: one CTA per SM, 12 warps:
+//        warp 0      walks the CTA's share, tells the other roles each item (through a ring in
+//                    shared memory), and loads K and V tiles of 128 keys by TMA (one ring for both)
 //        warp 2      TMA producer of Q
 //        warps 1, 3  tcgen05.mma issuers, one thread per query tile
 //        warps 4-11  softmax and output, one warpgroup per query tile, one thread per row
 //      The scores of a query tile (128 fp32 TMEM columns) are overwritten by its weights P (64
 //      columns), so a tile alternates between its softmax and its two products; the two tiles of
 //      a CTA take turns on the tensor core.
-//   3. shared_join_kernel joins the pieces of split entries (only where sizes allow a split).
+//   3. shared_join_kernel joins the partial results (only where the sizes allow a cut).
 // Every wait is bounded (bg::mbar_wait); on a time-out every role leaves, copies and MMAs in
 // flight are drained, TMEM is freed and BG_DEVSTAT_TIMEOUT is reported.
 #include <cuda_bf16.h>
@@ -47,7 +48,6 @@ namespace {
 
 // ------------------------------------------------------------------------------------ plan
 constexpr int kPlanThreads = 1024;
-constexpr int kPlanBuckets = kPlanThreads;      // cost classes of the work list (the last: and above)
 
 __host__ __device__ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -64,18 +64,10 @@ __device__ int block_exclusive(int v, int *s_warp, int *total)
     __syncthreads();                 // s_warp may still be read from the last call
     if (lane == 31) s_warp[warp] = incl;
     __syncthreads();
-    if (warp == 0) {
-        int w = s_warp[lane];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, w, o);
-            if (lane >= o) w += u;
-        }
-        s_warp[lane] = w;
-    }
-    __syncthreads();
-    *total = s_warp[kPlanThreads / 32 - 1];
-    return incl - v + (warp > 0 ? s_warp[warp - 1] : 0);
+    // every warp sums the warps before it
+    const int w = s_warp[lane];
+    *total = __reduce_add_sync(0xffffffffu, w);
+    return incl - v + __reduce_add_sync(0xffffffffu, lane < warp ? w : 0);
 }
 
 // The sample among [s, end) that holds packed row `row` (cu[s] <= row < cu[end]).
@@ -88,27 +80,26 @@ __device__ int sample_of(const int32_t *cu, int s, int end, int row)
     return s;
 }
 
+// Cost of an entry in units of one key tile: its tiles, and one for loading Q and storing the rows.
+__device__ __forceinline__ int entry_units(const ShEntry &E) { return E.tiles > 0 ? E.tiles + 1 : 0; }
+
 __global__ void __launch_bounds__(kPlanThreads)
     shared_plan_kernel(const ShProblem pb, const ShKey key, int bt, int32_t *hdr, ShEntry *__restrict__ entries,
-                       ShEntry *__restrict__ raw, ShSplit *__restrict__ splits, int64_t slots, int32_t *dev_status)
+                       ShStart *__restrict__ starts, ShSplit *__restrict__ splits, int grid, int can_split,
+                       int32_t *dev_status)
 {
-    __shared__ int s_err, s_nsplit, s_nslot;
+    __shared__ int s_err, s_nsplit;
     __shared__ int s_warp[32];
     __shared__ int s_base[kPlanThreads];
-    __shared__ int s_hist[kPlanBuckets];
-    __shared__ unsigned long long s_work;
+    __shared__ ShStart s_start[kShMaxCtas + 1];
     const int tid = threadIdx.x;
     grid_dep_launch();
     if (tid == 0) {
         s_err = 0;
         s_nsplit = 0;
-        s_nslot = 0;
-        s_work = 0;
     }
-    s_hist[tid] = 0;
     grid_dep_wait();
     __syncthreads();
-
     if (tid < 12) hdr[kShHdrKey + tid] = key.w[tid];
 
     // ---- the offsets, before anything is read through them
@@ -135,18 +126,18 @@ __global__ void __launch_bounds__(kPlanThreads)
     if (s_err) {
         if (tid == 0) {
             hdr[kShHdrStatus] = s_err;
-            hdr[kShHdrEntries] = 0;
+            hdr[kShHdrCtas] = 0;
             hdr[kShHdrSplits] = 0;
             if (dev_status) atomicOr(dev_status, s_err);
         }
         return;
     }
 
-    // ---- entries in request order, and their total cost in key tiles
+    // ---- the entries, in request order
     const int per = kShTiles * bt;         // rows of an entry
     const int32_t *cu = pb.cu_seqlens;
-    int n_raw = 0;
-    unsigned long long work = 0;
+    int n_entries = 0;
+    int64_t units = 0;
     for (int r0 = 0; r0 < pb.num_groups; r0 += kPlanThreads) {
         const int r = r0 + tid;
         int items = 0;
@@ -155,97 +146,104 @@ __global__ void __launch_bounds__(kPlanThreads)
             items = static_cast<int>(ceil_div(pb.last ? b - a : cu[b] - cu[a], per));
         }
         int total;
-        const int excl = block_exclusive(items, s_warp, &total);
-        s_base[tid] = excl;
+        s_base[tid] = block_exclusive(items, s_warp, &total);
         __syncthreads();
-        for (int e = tid; e < total; e += kPlanThreads) {
-            int t = 0, end = kPlanThreads;     // the request whose entries include e
-            while (end - t > 1) {
-                const int mid = (t + end) >> 1;
-                if (s_base[mid] <= e) t = mid; else end = mid;
+        for (int e0 = 0; e0 < total; e0 += kPlanThreads) {
+            const int e = e0 + tid;
+            ShEntry E = {};
+            if (e < total) {
+                int t = 0, end = kPlanThreads;     // the request whose entries include e
+                while (end - t > 1) {
+                    const int mid = (t + end) >> 1;
+                    if (s_base[mid] <= e) t = mid; else end = mid;
+                }
+                const int grp = r0 + t, first = (e - s_base[t]) * per;
+                const int sa = pb.cu_group[grp], sb = pb.cu_group[grp + 1];
+                E.prow0 = pb.cu_prefix[grp];
+                E.plen = pb.cu_prefix[grp + 1] - E.prow0;
+                const int base = pb.last ? sa : cu[sa];
+                const int end_row = pb.last ? sb : cu[sb];
+                E.row0 = base + first;
+                E.nrows = min(per, end_row - E.row0);
+                const int n0 = min(bt, E.nrows);
+                if (pb.last) {
+                    E.s0 = E.row0;
+                    E.ka0 = cu[E.row0];
+                    E.kb0 = cu[E.row0 + n0];
+                    E.ka1 = E.kb0;
+                    E.kb1 = cu[E.row0 + E.nrows];
+                } else {
+                    E.s0 = sample_of(cu, sa, sb, E.row0);
+                    E.ka0 = cu[E.s0];
+                    E.kb0 = E.row0 + n0;
+                    E.ka1 = E.nrows > bt ? cu[sample_of(cu, E.s0, sb, E.row0 + bt)] : E.kb0;
+                    E.kb1 = E.row0 + E.nrows;
+                }
+                E.tiles = static_cast<int>(ceil_div(E.plen, kShKeys) + ceil_div(E.kb1 - E.ka0, kShKeys));
+                if (E.tiles == 0 && dev_status) atomicOr(dev_status, BG_DEVSTAT_EMPTY_ROW);
             }
-            const int grp = r0 + t, first = (e - s_base[t]) * per;
-            const int sa = pb.cu_group[grp], sb = pb.cu_group[grp + 1];
-            ShEntry E;
-            E.prow0 = pb.cu_prefix[grp];
-            E.plen = pb.cu_prefix[grp + 1] - E.prow0;
-            const int base = pb.last ? sa : cu[sa];
-            const int end_row = pb.last ? sb : cu[sb];
-            E.row0 = base + first;
-            E.nrows = min(per, end_row - E.row0);
-            const int n0 = min(bt, E.nrows);
-            if (pb.last) {
-                E.s0 = E.row0;
-                E.ka0 = cu[E.row0];
-                E.kb0 = cu[E.row0 + n0];
-                E.ka1 = E.kb0;
-                E.kb1 = cu[E.row0 + E.nrows];
-            } else {
-                E.s0 = sample_of(cu, sa, sb, E.row0);
-                E.ka0 = cu[E.s0];
-                E.kb0 = E.row0 + n0;
-                E.ka1 = E.nrows > bt ? cu[sample_of(cu, E.s0, sb, E.row0 + bt)] : E.kb0;
-                E.kb1 = E.row0 + E.nrows;
+            int sum;
+            const int excl = block_exclusive(entry_units(E), s_warp, &sum);
+            if (e < total) {
+                E.pos = units + excl;
+                entries[n_entries + e] = E;
             }
-            E.tb = 0;
-            E.te = static_cast<int>(ceil_div(E.plen, kShKeys) + ceil_div(E.kb1 - E.ka0, kShKeys));
-            E.slot = -1;
-            raw[n_raw + e] = E;
-            work += E.te;
-            if (E.te == 0 && dev_status) atomicOr(dev_status, BG_DEVSTAT_EMPTY_ROW);
+            units += sum;
         }
-        n_raw += total;
+        n_entries += total;
         __syncthreads();
     }
-    if (work) atomicAdd(&s_work, work);
-    __syncthreads();
 
-    // ---- pieces: at most `chunk` key tiles each, such that all pieces of split entries fit the
-    // slots (an entry of n > chunk tiles gives ceil(n / chunk) < 2 n / chunk pieces, so together
-    // fewer than 2 * work * Hkv / chunk <= 2 * kShSplitTarget)
-    long long chunk = 0x7fffffff;
-    if (slots > 0) {
-        chunk = ceil_div(static_cast<long long>(s_work) * pb.Hkv, kShSplitTarget);
-        if (chunk < kShSplitMin) chunk = kShSplitMin;
-    }
-    auto pieces_of = [&](int n) { return n > chunk ? static_cast<int>(ceil_div(n, chunk)) : 1; };
-    auto bucket_of = [&](int n, int pieces) { return min(static_cast<int>(ceil_div(n, pieces)), kPlanBuckets - 1); };
-    for (int e = tid; e < n_raw; e += kPlanThreads) {
-        const int n = raw[e].te;
-        if (n == 0) continue;
-        const int pieces = pieces_of(n);
-        atomicAdd(&s_hist[bucket_of(n, pieces)], pieces);
-    }
-    __syncthreads();
-    int total;
-    const int mine = kPlanBuckets - 1 - tid;       // buckets from the costliest down
-    const int off = block_exclusive(s_hist[mine], s_warp, &total);
-    __syncthreads();
-    s_hist[mine] = off;
-    __syncthreads();
-    for (int e = tid; e < n_raw; e += kPlanThreads) {
-        ShEntry E = raw[e];
-        const int n = E.te;
-        if (n == 0) continue;
-        const int pieces = pieces_of(n);
-        const int pos = atomicAdd(&s_hist[bucket_of(n, pieces)], pieces);
-        int slot0 = -1;
-        if (pieces > 1) {
-            slot0 = atomicAdd(&s_nslot, pieces);
-            splits[atomicAdd(&s_nsplit, 1)] = ShSplit{E.row0, E.nrows, slot0, pieces};
+    // ---- equal shares of units * Hkv; fewer CTAs where a share would be below kShSplitMin
+    const int64_t work = units * pb.Hkv;
+    const int ctas = static_cast<int>(min(static_cast<int64_t>(grid), ceil_div(work, kShSplitMin)));
+    for (int c = tid; c <= ctas; c += kPlanThreads) {
+        ShStart S = {pb.Hkv, 0, 0, 0};             // the end of the line
+        if (c < ctas) {
+            const int64_t at = work * c / ctas;
+            S.kh = static_cast<int>(at / units);
+            const int64_t u = at - S.kh * units;
+            int lo = 0, end = n_entries;           // the last entry that begins at or before u
+            while (end - lo > 1) {
+                const int mid = (lo + end) >> 1;
+                if (entries[mid].pos <= u) lo = mid; else end = mid;
+            }
+            S.entry = lo;
+            const int n = entries[lo].tiles;
+            const int into = static_cast<int>(u - entries[lo].pos);
+            // a cut near an end of the item, or through a short one, moves to the end that is nearer
+            const int least = max(kShSplitMin / 2, static_cast<int>(min(work / ctas / 32, static_cast<int64_t>(n))));
+            S.tile = into;
+            if (!can_split || into < least || n - into < least) {
+                S.tile = 0;
+                if (2 * into > n) ++S.entry;
+            }
         }
-        for (int i = 0; i < pieces; ++i) {
-            E.tb = static_cast<int>(static_cast<long long>(n) * i / pieces);
-            E.te = static_cast<int>(static_cast<long long>(n) * (i + 1) / pieces);
-            E.slot = pieces > 1 ? slot0 + i : -1;
-            entries[pos + i] = E;
+        if (S.kh < pb.Hkv && S.entry == n_entries) {
+            ++S.kh;
+            S.entry = 0;
         }
+        s_start[c] = S;
+        starts[c] = S;
+    }
+    __syncthreads();
+    // ---- the items that a cut goes through: the first CTA of each one writes it down
+    for (int c = tid; c < ctas; c += kPlanThreads) {
+        const ShStart A = s_start[c], B = s_start[c + 1];
+        if (B.tile == 0 || (A.kh == B.kh && A.entry == B.entry && A.tile > 0)) continue;
+        int pieces = 2;
+        while (c + pieces < ctas && s_start[c + pieces].tile > 0 && s_start[c + pieces].kh == B.kh &&
+               s_start[c + pieces].entry == B.entry)
+            ++pieces;
+        const ShEntry &E = entries[B.entry];
+        splits[atomicAdd(&s_nsplit, 1)] = ShSplit{E.row0, E.nrows, B.kh, c, pieces, {}};
     }
     __syncthreads();
     if (tid == 0) {
         hdr[kShHdrStatus] = 0;
-        hdr[kShHdrEntries] = total;
+        hdr[kShHdrCtas] = ctas;
         hdr[kShHdrSplits] = s_nsplit;
+        hdr[kShHdrEntries] = n_entries;
     }
 }
 
@@ -265,6 +263,47 @@ __device__ bool plan_ready(const ShParams &p, bool *other)
 }
 
 // ------------------------------------------------------------------------------------ attention
+constexpr int kShRing = 4;                     // items in the ring that warp 0 fills
+constexpr int kShReaders = 1 + 2 + 8;          // Q producer, MMA issuers, softmax warps
+
+// The part of an item (an entry for one kv head) that this CTA computes, as the roles read it.
+struct __align__(16) ShItem {
+    int32_t prow0, plen, row0, nrows;
+    int32_t ka0, kb0, ka1, kb1;
+    int32_t s0, tb, te;       // key tiles [tb, te)
+    int32_t npt;              // prefix tiles
+    int32_t kh;
+    int32_t slot;             // partial result this part goes to, or -1
+    int32_t act[kShTiles];    // key tiles with keys for each query tile
+    int32_t more, pad[3];     // 0: no further item
+
+    __device__ int rows(int h, int bt) const { return h == 0 ? min(nrows, bt) : max(nrows - bt, 0); }
+    __device__ int ka(int h) const { return h == 0 ? ka0 : ka1; }
+    __device__ int kb(int h) const { return h == 0 ? kb0 : kb1; }
+    // first packed key row of own tile j (j >= npt)
+    __device__ int own_base(int j) const { return ka0 + (j - npt) * kShKeys; }
+    // keys of tile j that any row of the item sees (1..128)
+    __device__ int keys(int j) const { return min(kShKeys, j < npt ? plen - j * kShKeys : kb1 - own_base(j)); }
+    // keys of tile j up to the last one that a row of query tile h sees (<= 0: none); act[h] > 0
+    __device__ int keys_of(int h, int j) const
+    {
+        if (j < npt) return min(kShKeys, plen - j * kShKeys);
+        const int base = own_base(j);
+        return kb(h) <= ka(h) || base + kShKeys <= ka(h) ? 0 : min(kShKeys, kb(h) - base);
+    }
+    // number of key tiles of this part with keys for query tile h
+    __device__ int active(int h, int bt) const
+    {
+        if (rows(h, bt) == 0) return 0;
+        const int pre = max(min(te, npt) - tb, 0);
+        if (kb(h) <= ka(h)) return pre;
+        const int lo = npt + (ka(h) - ka0) / kShKeys;
+        const int hi = npt + (kb(h) - ka0 + kShKeys - 1) / kShKeys;
+        return pre + max(min(te, hi) - max(tb, lo), 0);
+    }
+};
+static_assert(sizeof(ShItem) == 80, "five 16-byte stores");
+
 template <int D>
 struct ShCfg {
     static constexpr int kBox = 128 * 128;                   // 128 rows x one 128-byte column block
@@ -274,9 +313,11 @@ struct ShCfg {
     static constexpr int kOffQ = 0;
     static constexpr int kOffKV = kShTiles * kTileBytes;
     static constexpr int kOffBar = kOffKV + kStages * kTileBytes;
-    // q_full[2] q_empty[2] s_full[2] p_full[2] o_full[2] mma_final kv_full[kStages] kv_empty[kStages]
-    static constexpr int kNumBars = 11 + 2 * kStages;
-    static constexpr int kOffMisc = kOffBar + kNumBars * 8;
+    // q_full[2] q_empty[2] s_full[2] p_full[2][2] o_full[2] mma_final kv_full[kStages] kv_empty[kStages]
+    // item_full[kShRing] item_empty[kShRing]
+    static constexpr int kNumBars = 13 + 2 * kStages + 2 * kShRing;
+    static constexpr int kOffItems = (kOffBar + kNumBars * 8 + 15) / 16 * 16;
+    static constexpr int kOffMisc = kOffItems + kShRing * static_cast<int>(sizeof(ShItem));
     static constexpr int kSmemBytes = kOffMisc + 16 + 1024;  // + slack for 1024-byte alignment
     static constexpr int kThreads = 384;
     // Register split, as in the attention kernel of the other modes: compiled for kRegsLaunch,
@@ -290,93 +331,81 @@ struct ShCfg {
     static_assert(kSmemBytes <= 232448, "shared memory overflow");
 };
 
-// One work item: an entry for one kv head.
-struct ShItem {
-    ShEntry e;
-    int kh, npt;              // kv head; prefix key tiles
-
-    __device__ int rows(int h, int bt) const { return h == 0 ? min(e.nrows, bt) : max(e.nrows - bt, 0); }
-    __device__ int ka(int h) const { return h == 0 ? e.ka0 : e.ka1; }
-    __device__ int kb(int h) const { return h == 0 ? e.kb0 : e.kb1; }
-    // first packed key row of own tile j (j >= npt)
-    __device__ int own_base(int j) const { return e.ka0 + (j - npt) * kShKeys; }
-    // keys of tile j that any row of the entry sees (1..128)
-    __device__ int keys(int j) const
-    {
-        return min(kShKeys, j < npt ? e.plen - j * kShKeys : e.kb1 - own_base(j));
-    }
-    // keys of tile j up to the last one that a row of query tile h sees (<= 0: none)
-    __device__ int keys_of(int h, int j, int bt) const
-    {
-        if (rows(h, bt) == 0) return 0;
-        if (j < npt) return min(kShKeys, e.plen - j * kShKeys);
-        const int base = own_base(j);
-        return kb(h) <= ka(h) || base + kShKeys <= ka(h) ? 0 : min(kShKeys, kb(h) - base);
-    }
-    // number of key tiles of this piece with keys for query tile h
-    __device__ int active(int h, int bt) const
-    {
-        if (rows(h, bt) == 0) return 0;
-        const int pre = max(min(e.te, npt) - e.tb, 0);
-        if (kb(h) <= ka(h)) return pre;
-        const int lo = npt + (ka(h) - e.ka0) / kShKeys;
-        const int hi = npt + (kb(h) - e.ka0 + kShKeys - 1) / kShKeys;
-        return pre + max(min(e.te, hi) - max(e.tb, lo), 0);
-    }
-};
-
-// The items of this CTA, round by round in alternating direction (the list is sorted by cost, so
-// the CTA that got the costliest item of one round gets the cheapest of the next).  Every role
-// walks the same items; the next entry is fetched while the current item runs.
-struct ShWalker {
-    int round, n_items, hkv;
-    const int4 *entries;
-    int4 n0, n1, n2;
-    int n_kh;
-
-    __device__ int index(int r) const
-    {
-        const int64_t i = static_cast<int64_t>(r) * gridDim.x + ((r & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-        return i < n_items ? static_cast<int>(i) : -1;
-    }
-    __device__ void fetch()
-    {
-        const int i = index(round);
-        if (i < 0) return;
-        const int4 *p = entries + 3 * static_cast<int64_t>(i / hkv);
-        n0 = p[0];
-        n1 = p[1];
-        n2 = p[2];
-        n_kh = i % hkv;
-    }
-    __device__ void first(const ShParams &p, int n)
-    {
-        round = 0;
-        n_items = n;
-        hkv = p.Hkv;
-        entries = reinterpret_cast<const int4 *>(p.entries);
-        fetch();
-    }
-    __device__ bool next(ShItem &I)
-    {
-        if (index(round) < 0) return false;
-        I.e.prow0 = n0.x; I.e.plen = n0.y; I.e.row0 = n0.z; I.e.nrows = n0.w;
-        I.e.ka0 = n1.x; I.e.kb0 = n1.y; I.e.ka1 = n1.z; I.e.kb1 = n1.w;
-        I.e.s0 = n2.x; I.e.tb = n2.y; I.e.te = n2.z; I.e.slot = n2.w;
-        I.kh = n_kh;
-        I.npt = (I.e.plen + kShKeys - 1) / kShKeys;
-        ++round;
-        fetch();
-        return true;
-    }
-};
-
-// Lane 0 waits, the result is broadcast: the whole warp leaves together.
+// The whole warp waits, without diverging (bounded, as mbar_wait).
 __device__ __forceinline__ bool sh_warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort)
 {
-    int ok = 0;
-    if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, abort) ? 1 : 0;
-    return __shfl_sync(0xffffffffu, ok, 0) != 0;
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t it = 1;; ++it) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        if ((it & 63u) == 0) {
+            const bool late = globaltimer_ns() - t0 > kWaitTimeoutNs;
+            if (__any_sync(0xffffffffu, late || *abort)) {
+                *abort = 1;
+                return false;
+            }
+        }
+    }
+}
+
+// S = Q K^T over D = 64 * NB, then commits to `full` and `empty`: one asm statement per tile, so that
+// the descriptors' offsets are immediates and the MMAs go out back to back.  Q and K column blocks
+// are 16 KB (1024 descriptor units) apart, 16-element steps 32 bytes (2 units).
+template <int NB>
+__device__ __forceinline__ void sh_mma_qk(uint32_t d, uint64_t dq, uint64_t dk, uint32_t idesc, uint64_t *full,
+                                          uint64_t *empty)
+{
+    if constexpr (NB == 2) {
+        asm volatile(
+            "{\n\t.reg .pred pf, pt;\n\t.reg .b64 a1, a2, a3, a4, a5, a6, a7, b1, b2, b3, b4, b5, b6, b7;\n\t"
+            "setp.ne.b32 pf, 0, 0;\n\tsetp.eq.b32 pt, 0, 0;\n\t"
+            "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\t"
+            "add.s64 a4, %1, 1024;\n\tadd.s64 a5, %1, 1026;\n\tadd.s64 a6, %1, 1028;\n\tadd.s64 a7, %1, 1030;\n\t"
+            "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\t"
+            "add.s64 b4, %2, 1024;\n\tadd.s64 b5, %2, 1026;\n\tadd.s64 b6, %2, 1028;\n\tadd.s64 b7, %2, 1030;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, pf;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, pt;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, pt;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, pt;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a4, b4, %3, pt;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a5, b5, %3, pt;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a6, b6, %3, pt;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a7, b7, %3, pt;\n\t"
+            "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%4];\n\t"
+            "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t}" ::"r"(d),
+            "l"(dq), "l"(dk), "r"(idesc), "r"(smem_u32(full)), "r"(smem_u32(empty))
+            : "memory");
+    } else {
+        asm volatile(
+            "{\n\t.reg .pred pf, pt;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+            "setp.ne.b32 pf, 0, 0;\n\tsetp.eq.b32 pt, 0, 0;\n\t"
+            "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\t"
+            "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, pf;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, pt;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, pt;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, pt;\n\t"
+            "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%4];\n\t"
+            "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t}" ::"r"(d),
+            "l"(dq), "l"(dk), "r"(idesc), "r"(smem_u32(full)), "r"(smem_u32(empty))
+            : "memory");
+    }
+}
+
+// O (+)= P V over 64 keys: P in TMEM (8 columns per 16 keys), V's 16-key steps 2 KB (128 units) apart.
+__device__ __forceinline__ void sh_mma_pv4(uint32_t d, uint32_t a, uint64_t dv, uint32_t idesc, uint32_t acc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p0, pt;\n\t.reg .b64 b1, b2, b3;\n\t.reg .b32 t1, t2, t3;\n\t"
+        "setp.ne.b32 p0, %4, 0;\n\tsetp.eq.b32 pt, 0, 0;\n\t"
+        "add.s64 b1, %2, 128;\n\tadd.s64 b2, %2, 256;\n\tadd.s64 b3, %2, 384;\n\t"
+        "add.u32 t1, %1, 8;\n\tadd.u32 t2, %1, 16;\n\tadd.u32 t3, %1, 24;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [t1], b1, %3, pt;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [t2], b2, %3, pt;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [t3], b3, %3, pt;\n\t}" ::"r"(d),
+        "r"(a), "l"(dv), "r"(idesc), "r"(acc)
+        : "memory");
 }
 
 // 32 bytes to global memory (one whole sector per lane).
@@ -416,9 +445,11 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kOffBar);
-    uint64_t *q_full = bars, *q_empty = bars + 2, *s_full = bars + 4, *p_full = bars + 6, *o_full = bars + 8;
-    uint64_t *mma_final = bars + 10;
-    uint64_t *kv_full = bars + 11, *kv_empty = kv_full + C::kStages;
+    uint64_t *q_full = bars, *q_empty = bars + 2, *s_full = bars + 4, *p_full = bars + 6, *o_full = bars + 10;
+    uint64_t *mma_final = bars + 12;
+    uint64_t *kv_full = bars + 13, *kv_empty = kv_full + C::kStages;
+    uint64_t *item_full = kv_empty + C::kStages, *item_empty = item_full + kShRing;
+    ShItem *ring = reinterpret_cast<ShItem *>(smem + C::kOffItems);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kOffMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::kOffMisc + 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -429,19 +460,24 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
             mbar_init(&q_full[h], 1);
             mbar_init(&q_empty[h], 1);
             mbar_init(&s_full[h], 1);
-            mbar_init(&p_full[h], 4);      // one arrive per softmax warp
+            mbar_init(&p_full[2 * h], 4);      // one arrive per softmax warp: keys 0-63 of the tile
+            mbar_init(&p_full[2 * h + 1], 4);  // ... and keys 64-127
             mbar_init(&o_full[h], 1);
         }
         mbar_init(mma_final, kShTiles);
-        for (int s = 0; s < C::kStages; ++s) {
-            mbar_init(&kv_full[s], 1);
-            mbar_init(&kv_empty[s], kShTiles);   // one per MMA issuer
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(&kv_full[i], 1);
+            mbar_init(&kv_empty[i], kShTiles);   // one per MMA issuer
+        }
+        for (int i = 0; i < kShRing; ++i) {
+            mbar_init(&item_full[i], 1);
+            mbar_init(&item_empty[i], kShReaders);
         }
         *abort_flag = 0;
         fence_barrier_init();
     }
     // Query tiles fill bt * g <= 128 rows; the rows past them stay zero.
-    {
+    if (p.bt * p.g < kShRows) {
         uint4 *z4 = reinterpret_cast<uint4 *>(smem + C::kOffQ);
         for (int i = threadIdx.x; i < kShTiles * C::kTileBytes / 16; i += blockDim.x) z4[i] = make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
@@ -462,30 +498,85 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    bool other;
-    const int n_items = plan_ready(p, &other) ? p.hdr[kShHdrEntries] * p.Hkv : 0;
-    if (other && blockIdx.x == 0 && threadIdx.x == 0 && p.dev_status) atomicOr(p.dev_status, BG_DEVSTAT_PLAN);
+    const int cta = static_cast<int>(blockIdx.x);
 
     if (warp < 4) {
         reg_dealloc<C::kRegsLight>();
         if (warp == 0) {
-            // ============================================================ K / V producer
+            // ============================================================ items, K and V
             if (lane == 0) {
+                bool other;
+                const bool mine = plan_ready(p, &other) && cta < p.hdr[kShHdrCtas];
+                if (other && cta == 0 && p.dev_status) atomicOr(p.dev_status, BG_DEVSTAT_PLAN);
+                ShStart A = {}, B = {};
+                int n_entries = 0;
+                if (mine) {
+                    A = p.starts[cta];
+                    B = p.starts[cta + 1];
+                    n_entries = p.hdr[kShHdrEntries];
+                }
                 const uint64_t pol = l2_policy_evict_last();
-                ShWalker w;
-                ShItem I;
-                w.first(p, n_items);
-                uint32_t n = 0;              // K and V tiles issued
+                const int4 *list = reinterpret_cast<const int4 *>(p.entries);
+                int kh = A.kh, entry = A.entry, tb = A.tile;
+                auto before_end = [&]() {
+                    return kh < B.kh || (kh == B.kh && (entry < B.entry || (entry == B.entry && tb < B.tile)));
+                };
+                int4 e0 = {}, e1 = {}, e2 = {};
+                auto fetch = [&]() {
+                    const int4 *q = list + 3 * static_cast<int64_t>(entry);
+                    e0 = q[0];
+                    e1 = q[1];
+                    e2 = q[2];
+                };
+                if (before_end()) fetch();
+                uint32_t st = 0, ph = 1;         // stage, and the parity of its release (1: free at first)
+                uint32_t n_items = 0;
+                uint32_t used = 0;               // stages that hold or await a copy, counted up to kStages
                 bool ok = true;
-                while (ok && w.next(I)) {
-                    for (int j = I.e.tb; j < I.e.te && ok; ++j) {
+                for (;;) {
+                    const bool more = before_end();
+                    const uint32_t slot = n_items % kShRing;
+                    if (!mbar_wait(&item_empty[slot], ((n_items / kShRing) & 1) ^ 1, abort_flag)) break;
+                    ShItem I;
+                    I.prow0 = e0.x; I.plen = e0.y; I.row0 = e0.z; I.nrows = e0.w;
+                    I.ka0 = e1.x; I.kb0 = e1.y; I.ka1 = e1.z; I.kb1 = e1.w;
+                    I.s0 = e2.x;
+                    const int tiles = e2.y;
+                    I.kh = kh;
+                    I.npt = (I.plen + kShKeys - 1) / kShKeys;
+                    I.tb = tb;
+                    I.te = kh == B.kh && entry == B.entry ? B.tile : tiles;
+                    I.slot = tb > 0 ? 2 * cta : I.te < tiles ? 2 * cta + 1 : -1;
+                    if (more && tiles > 0) {
+                        I.act[0] = I.active(0, p.bt);
+                        I.act[1] = I.active(1, p.bt);
+                    }
+                    I.more = more ? 1 : 0;
+                    if (!more || tiles > 0) {
+                        int4 *dst = reinterpret_cast<int4 *>(&ring[slot]);
+                        dst[0] = make_int4(I.prow0, I.plen, I.row0, I.nrows);
+                        dst[1] = make_int4(I.ka0, I.kb0, I.ka1, I.kb1);
+                        dst[2] = make_int4(I.s0, I.tb, I.te, I.npt);
+                        dst[3] = make_int4(I.kh, I.slot, I.act[0], I.act[1]);
+                        dst[4] = make_int4(I.more, 0, 0, 0);
+                        mbar_arrive(&item_full[slot]);
+                        ++n_items;
+                    }
+                    if (!more) break;
+                    // the next item, fetched while this one's tiles are loaded
+                    tb = 0;
+                    if (++entry == n_entries) {
+                        entry = 0;
+                        ++kh;
+                    }
+                    if (before_end()) fetch();
+                    if (tiles == 0) continue;
+                    for (int j = I.tb; j < I.te && ok; ++j) {
                         const bool pre = j < I.npt;
-                        const int row = pre ? I.e.prow0 + j * kShKeys : I.own_base(j);
-#pragma unroll
-                        for (int kv = 0; kv < 2; ++kv, ++n) {
-                            const int st = n % C::kStages;
-                            const uint32_t use = n / C::kStages;
-                            if (use > 0 && !mbar_wait(&kv_empty[st], (use - 1) & 1, abort_flag)) {
+                        const int row = pre ? I.prow0 + j * kShKeys : I.own_base(j);
+#pragma unroll 1
+                        for (int kv = 0; kv < 2; ++kv) {
+                            if (!mbar_wait(&kv_empty[st], ph, abort_flag)) {
                                 ok = false;
                                 break;
                             }
@@ -495,29 +586,36 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
 #pragma unroll
                             for (int b = 0; b < C::kNB; ++b)
                                 tma_load_3d(dst + b * C::kBox, tm, &kv_full[st], b * 64, I.kh, row, pol);
+                            if (used < C::kStages) ++used;
+                            if (++st == C::kStages) {
+                                st = 0;
+                                ph ^= 1u;
+                            }
                         }
                     }
+                    if (!ok) break;
                 }
-                for (int st = 0; st < C::kStages; ++st) {   // every copy has landed before the CTA exits
-                    const uint32_t uses = n / C::kStages + (st < static_cast<int>(n % C::kStages) ? 1u : 0u);
-                    if (uses > 0) mbar_wait_drain(&kv_full[st], (uses - 1) & 1);
-                }
+                // every copy has landed before the CTA exits: the last use of each stage was in the
+                // current round (parity ph ^ 1) below `st`, in the one before from `st` on
+                for (uint32_t i = 0; i < used; ++i) mbar_wait_drain(&kv_full[i], i < st ? ph ^ 1u : ph);
             }
             __syncwarp();
         } else if (warp == 2) {
             // ============================================================ Q producer
             if (lane == 0) {
                 const uint64_t pol = l2_policy_evict_first();
-                ShWalker w;
-                ShItem I;
-                w.first(p, n_items);
                 uint32_t n[kShTiles] = {0, 0};
                 const uint32_t bytes = static_cast<uint32_t>(C::kNB * p.bt * p.g * 128);
-                bool ok = true;
-                while (ok && w.next(I)) {
+                for (uint32_t it = 0;; ++it) {
+                    const uint32_t slot = it % kShRing;
+                    if (!mbar_wait(&item_full[slot], (it / kShRing) & 1, abort_flag) || !ring[slot].more) break;
+                    const int row0 = ring[slot].row0, kh = ring[slot].kh;
+                    const int act[kShTiles] = {ring[slot].act[0], ring[slot].act[1]};
+                    mbar_arrive(&item_empty[slot]);
+                    bool ok = true;
 #pragma unroll
                     for (int h = 0; h < kShTiles; ++h) {
-                        if (!ok || I.active(h, p.bt) == 0) continue;
+                        if (!ok || act[h] == 0) continue;
                         if (n[h] > 0 && !mbar_wait(&q_empty[h], (n[h] - 1) & 1, abort_flag)) {
                             ok = false;
                             continue;
@@ -526,9 +624,10 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
 #pragma unroll
                         for (int b = 0; b < C::kNB; ++b)
                             tma_load_4d(smem + C::kOffQ + h * C::kTileBytes + b * C::kBox, &tm_q, &q_full[h], b * 64, 0,
-                                        I.kh, I.e.row0 + h * p.bt, pol);
+                                        kh, row0 + h * p.bt, pol);
                         ++n[h];
                     }
+                    if (!ok) break;
                 }
                 for (int h = 0; h < kShTiles; ++h)
                     if (n[h] > 0) mbar_wait_drain(&q_full[h], (n[h] - 1) & 1);
@@ -544,55 +643,80 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
                 const uint64_t dk0 = sdesc_sw128(smem_u32(smem + C::kOffKV), 16, 1024);
                 const uint64_t dv0 = sdesc_sw128(smem_u32(smem + C::kOffKV), C::kBox, 1024);
                 const uint32_t tS = tmem + C::kColS + kShKeys * h, tO = tmem + C::kColO + D * h;
-                ShWalker w;
-                ShItem I;
-                w.first(p, n_items);
-                uint32_t n = 0;              // K and V tiles passed
-                uint32_t items = 0, tiles = 0;
+                uint32_t st = 0, ph = 0;         // stage of the next K or V tile, and its parity
+                uint32_t q_uses = 0, tiles = 0;
+                auto bump = [&]() {
+                    if (++st == C::kStages) {
+                        st = 0;
+                        ph ^= 1u;
+                    }
+                };
                 bool ok = true;
-                while (ok && w.next(I)) {
-                    const int act = I.active(h, p.bt);
+                for (uint32_t it = 0; ok; ++it) {
+                    const uint32_t slot = it % kShRing;
+                    if (!mbar_wait(&item_full[slot], (it / kShRing) & 1, abort_flag) || !ring[slot].more) break;
+                    const ShItem &I = ring[slot];
+                    const int act = I.act[h], tb = I.tb, te = I.te;
                     int done = 0;
-                    for (int j = I.e.tb; j < I.e.te; ++j, n += 2) {
-                        const int ks = n % C::kStages, vs = (n + 1) % C::kStages;
-                        const uint32_t kp = (n / C::kStages) & 1, vp = ((n + 1) / C::kStages) & 1;
-                        const int nk = I.keys_of(h, j, p.bt);
-                        if (nk <= 0) {       // nothing for this query tile: only pass the stages on
-                            if (!mbar_wait(&kv_full[ks], kp, abort_flag)) { ok = false; break; }
-                            mbar_arrive(&kv_empty[ks]);
-                            if (!mbar_wait(&kv_full[vs], vp, abort_flag)) { ok = false; break; }
-                            mbar_arrive(&kv_empty[vs]);
+                    bool ready = false;          // the next tile's K has been waited for
+                    if (act > 0) {
+                        if (!mbar_wait(&q_full[h], q_uses & 1, abort_flag)) break;
+                        ++q_uses;
+                    }
+                    for (int j = tb; j < te; ++j) {
+                        const int nk = act > 0 ? I.keys_of(h, j) : 0;
+                        if (nk <= 0) {           // nothing for this query tile: only pass the stages on
+#pragma unroll 1
+                            for (int kv = 0; kv < 2 && ok; ++kv) {
+                                ok = mbar_wait(&kv_full[st], ph, abort_flag);
+                                if (ok) mbar_arrive(&kv_empty[st]);
+                                bump();
+                            }
+                            if (!ok) break;
                             continue;
                         }
                         const int steps = (nk + 15) >> 4;       // 16-key steps of P.V; S has 16 * steps columns
-                        if (done == 0 && !mbar_wait(&q_full[h], items & 1, abort_flag)) { ok = false; break; }
-                        if (!mbar_wait(&kv_full[ks], kp, abort_flag)) { ok = false; break; }
+                        if (!ready && !mbar_wait(&kv_full[st], ph, abort_flag)) { ok = false; break; }
                         // S overwrites the P of the previous tile, which the P.V issued before it reads:
                         // tcgen05.mma operations of one thread execute in issue order.
                         tc_fence_after();
-                        const uint64_t dk = dk0 + static_cast<uint64_t>((ks * C::kTileBytes) >> 4);
-                        const uint32_t idesc_qk = kIdescQK0 | (static_cast<uint32_t>(2 * steps) << 17);
-#pragma unroll
-                        for (int k = 0; k < D / 16; ++k) {
-                            const uint64_t off = static_cast<uint64_t>((k >> 2) * (C::kBox >> 4) + (k & 3) * 2);
-                            mma_ss(tS, dq + off, dk + off, idesc_qk, k > 0 ? 1u : 0u);
-                        }
-                        mma_commit(&s_full[h]);
-                        mma_commit(&kv_empty[ks]);
-                        if (done == act - 1) mma_commit(&q_empty[h]);
-                        if (!mbar_wait(&kv_full[vs], vp, abort_flag)) { ok = false; break; }
-                        if (!mbar_wait(&p_full[h], tiles & 1, abort_flag)) { ok = false; break; }
-                        tc_fence_after();
+                        sh_mma_qk<C::kNB>(tS, dq, dk0 + static_cast<uint64_t>((st * C::kTileBytes) >> 4),
+                                          kIdescQK0 | (static_cast<uint32_t>(2 * steps) << 17), &s_full[h], &kv_empty[st]);
+                        const bool first = done == 0, last = ++done == act;
+                        if (last) mma_commit(&q_empty[h]);
+                        bump();
+                        const uint32_t vs = st, vph = ph;
+                        bump();
+                        // While the softmax works: this tile's V, and the K right behind it if it is used.  (One
+                        // further ahead could wait for a stage that this V still holds.)
+                        if (!mbar_wait(&kv_full[vs], vph, abort_flag)) { ok = false; break; }
+                        ready = j + 1 < te && I.keys_of(h, j + 1) > 0;
+                        if (ready && !mbar_wait(&kv_full[st], ph, abort_flag)) { ok = false; break; }
                         const uint64_t dv = dv0 + static_cast<uint64_t>((vs * C::kTileBytes) >> 4);
-                        for (int k = 0; k < steps; ++k)
-                            mma_ts(tO, tS + 8 * k, dv + static_cast<uint64_t>(128 * k), kIdescPV,
-                                   (done > 0 || k > 0) ? 1u : 0u);
+                        if (!mbar_wait(&p_full[2 * h], tiles & 1, abort_flag)) { ok = false; break; }
+                        tc_fence_after();
+                        if (steps >= 4) {
+                            sh_mma_pv4(tO, tS, dv, kIdescPV, first ? 0u : 1u);
+                        } else {
+#pragma unroll 1
+                            for (int k = 0; k < steps; ++k)
+                                mma_ts(tO, tS + 8 * k, dv + static_cast<uint64_t>(128 * k), kIdescPV,
+                                       (!first || k > 0) ? 1u : 0u);
+                        }
+                        if (!mbar_wait(&p_full[2 * h + 1], tiles & 1, abort_flag)) { ok = false; break; }
+                        tc_fence_after();
+                        if (steps == 8) {
+                            sh_mma_pv4(tO, tS + 32, dv + 512, kIdescPV, 1u);
+                        } else {
+#pragma unroll 1
+                            for (int k = 4; k < steps; ++k)
+                                mma_ts(tO, tS + 8 * k, dv + static_cast<uint64_t>(128 * k), kIdescPV, 1u);
+                        }
                         mma_commit(&kv_empty[vs]);
-                        if (done == act - 1) mma_commit(&o_full[h]);
-                        ++done;
+                        if (last) mma_commit(&o_full[h]);
                         ++tiles;
                     }
-                    if (act > 0) ++items;
+                    mbar_arrive(&item_empty[slot]);
                 }
                 mma_commit(mma_final);           // every MMA issued completes before TMEM is released
                 mbar_wait_drain(mma_final, 0);
@@ -612,20 +736,35 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
         const uint32_t tO = tmem + lane_addr + C::kColO + D * h;
         const float sl2 = CAP ? 1.f : p.scale_log2;
         const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
-        ShWalker w;
-        ShItem I;
-        w.first(p, n_items);
-        uint32_t n = 0, tiles = 0, items = 0;
+        uint32_t n = 0, tiles = 0, outs = 0;               // K and V tiles passed; tiles and outputs of h
         bool ok = true;
-        while (ok && w.next(I)) {
+        for (uint32_t it = 0; ok; ++it) {
+            const uint32_t rslot = it % kShRing;
+            if (!sh_warp_wait(&item_full[rslot], (it / kShRing) & 1, abort_flag)) break;
+            const ShItem &I = ring[rslot];
+            if (!I.more) break;
+            const int act = I.act[h];
             const int rows_h = I.rows(h, p.bt);
             const bool live = lr < p.bt && lr < rows_h;
             const bool warp_live = __any_sync(0xffffffffu, live);
-            const int act = I.active(h, p.bt);
-            const int row = I.e.row0 + h * p.bt + lr;      // packed token, or sample
+            const int row = I.row0 + h * p.bt + lr;        // packed token, or sample
+            float m = -INFINITY;       // running maximum, base-2 units
+            float l = 0.f;             // running sum of 2^(x - m)
+            float fix = 0.f;           // what rounding the tiles' largest weights to bf16 adds to l
+            bool seen = false;         // this row has a key in one of the tiles
+            int done = 0;              // tiles of this item so far
+
+            // P of the first (half 0) or second 64 keys of the tile is stored
+            auto hand_over = [&](int half) {
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[2 * h + half]);
+            };
+
             // own keys this row sees: [lo, hi)
             int lo = 0, hi = 0;
-            if (act > 0) {
+            if (act > 0 && I.te > I.npt) {
                 if (p.last) {
                     if (live) {
                         lo = p.cu_seqlens[row];
@@ -633,196 +772,211 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
                     }
                 } else {
                     // the last sample start that is not behind the row; 32 sample starts at a time
-                    const int last_row = I.e.row0 + I.e.nrows - 1;
-                    lo = I.e.ka0;
-                    for (int s = I.e.s0 + 1;; s += 32) {
-                        const int start = p.cu_seqlens[min(s + lane, p.num_seqs)];
-                        const unsigned in = __ballot_sync(0xffffffffu, start <= last_row && s + lane < p.num_seqs);
+                    const int last_row = I.row0 + I.nrows - 1;
+                    lo = I.ka0;
+#pragma unroll 1
+                    for (int s0 = I.s0 + 1;; s0 += 32) {
+                        const int start = p.cu_seqlens[min(s0 + lane, p.num_seqs)];
+                        const unsigned in = __ballot_sync(0xffffffffu, start <= last_row && s0 + lane < p.num_seqs);
+#pragma unroll 1
                         for (int i = 0; i < 32 && ((in >> i) & 1u); ++i) {
                             const int b = __shfl_sync(0xffffffffu, start, i);
                             if (b <= row) lo = b;
                         }
                         if (in != 0xffffffffu) break;
                     }
-                    hi = row + 1;
-                    if (!live) hi = lo;
+                    hi = live ? row + 1 : lo;
                 }
             }
-            float m = -INFINITY;       // running maximum, base-2 units
-            float l = 0.f;             // running sum of 2^(x - m)
-            bool seen = false;         // this row has a key in one of the tiles
-            float fix = 0.f;           // what rounding the tiles' largest weights to bf16 adds to l
-            int done = 0;
-            for (int j = I.e.tb; j < I.e.te; ++j, n += 2) {
-                const int nk = I.keys_of(h, j, p.bt);
-                if (nk <= 0) continue;
-                const bool pre = j < I.npt;
-                const int base = pre ? 0 : I.own_base(j);
-                // this row's columns of the tile: [c0, c1)
-                const int c0 = pre ? 0 : min(max(lo - base, 0), kShKeys);
-                const int c1 = pre ? nk : min(max(hi - base, 0), nk);
+            const int npt = I.npt, tb = I.tb, te = act > 0 ? I.te : I.tb;
+            const int whole_end = I.plen / kShKeys;        // tiles below it: every row sees all 128 keys
+#pragma unroll 1
+            for (int j = tb; j < te; ++j) {
+                int nk = kShKeys, c0 = 0, c1 = kShKeys;    // keys of the tile; this row's columns [c0, c1)
+                bool some = warp_live, masked = false, zero_v = false;
+                if (j >= whole_end) {
+                    nk = I.keys_of(h, j);
+                    if (nk <= 0) continue;
+                    if (j >= npt) {
+                        const int base = I.own_base(j);
+                        c0 = min(max(lo - base, 0), kShKeys);
+                        c1 = min(max(hi - base, 0), nk);
+                    } else {
+                        c1 = nk;
+                    }
+                    some = __any_sync(0xffffffffu, live && c1 > c0);
+                    masked = __any_sync(0xffffffffu, live && (c0 > 0 || c1 < (nk > 64 ? 128 : 64)));
+                    zero_v = ((nk + 15) & ~15) > I.keys(j);
+                }
+                seen = seen || c1 > c0;
                 if (!sh_warp_wait(&s_full[h], tiles & 1, abort_flag)) { ok = false; break; }
                 tc_fence_after();
-                // Keys behind the last one that any row of the entry sees (a later token, another
+                // Keys behind the last one that any row of the item sees (a later token, another
                 // request's rows) have weight 0, but 0 * Inf is NaN: their V rows become zeros.
-                const int nkeys = I.keys(j);
-                if (((nk + 15) & ~15) > nkeys) {
-                    const int vs = (n + 1) % C::kStages;
-                    if (!sh_warp_wait(&kv_full[vs], ((n + 1) / C::kStages) & 1, abort_flag)) { ok = false; break; }
-                    uint8_t *vt = smem + C::kOffKV + vs * C::kTileBytes;
-                    const int chunks = (((nkeys + 15) & ~15) - nkeys) * 8;      // 16-byte chunks per column block
-                    for (int i = trow; i < chunks * C::kNB; i += 128) {
-                        const int b = i / chunks, c = i - b * chunks;
-                        *reinterpret_cast<uint4 *>(vt + b * C::kBox + nkeys * 128 + c * 16) = make_uint4(0, 0, 0, 0);
-                    }
+                if (zero_v) {
+                    const uint32_t nv = n + 2 * (j - tb) + 1;
+                    const uint32_t vs = nv % C::kStages;
+                    if (!sh_warp_wait(&kv_full[vs], (nv / C::kStages) & 1, abort_flag)) { ok = false; break; }
+                    const int nkeys = I.keys(j);
+                    uint8_t *vt = smem + C::kOffKV + vs * C::kTileBytes + nkeys * 128;
+                    const int bytes = (((nkeys + 15) & ~15) - nkeys) * 128;      // per column block, at most 15 rows
+                    for (int i = trow * 16; i < bytes; i += 128 * 16)
+#pragma unroll
+                        for (int b = 0; b < C::kNB; ++b)
+                            *reinterpret_cast<uint4 *>(vt + b * C::kBox + i) = make_uint4(0, 0, 0, 0);
                     fence_proxy_async_smem();
                 }
-                if (warp_live) {
-                    const bool any = __any_sync(0xffffffffu, live && c1 > c0);
-                    if (!any) {
-                        // no row of this warp has a key in the tile: P = 0
+                if (!some) {
+                    // no row of this warp has a key in the tile: P = 0 (without rows: whatever it is)
+                    if (warp_live) {
                         uint32_t zr[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) zr[i] = 0u;
 #pragma unroll
                         for (int c = 0; c < 4; ++c) tmem_st16(tS + 16 * c, zr);
-                    } else {
-                        const bool masked = __any_sync(0xffffffffu, live && (c0 > 0 || c1 < (nk > 64 ? 128 : 64)));
-                        seen = seen || c1 > c0;
-                        auto tile = [&](auto ncols) {
-                            constexpr int NC = decltype(ncols)::value;
-                            float s[NC];
-#pragma unroll
-                            for (int c = 0; c < NC / 64; ++c) tmem_ld64(tS + 64 * c, s + 64 * c);
-                            if constexpr (CAP) {
-#pragma unroll
-                                for (int c = 0; c < NC; ++c) s[c] = capped(s[c], p.cap_in, p.cap_log2);
-                            }
-                            if (masked) {
-                                const unsigned width = static_cast<unsigned>(max(c1 - c0, 0));
-#pragma unroll
-                                for (int c = 0; c < NC; ++c)
-                                    if (static_cast<unsigned>(c - c0) >= width) s[c] = -INFINITY;
-                            }
-                            float mq[4];
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) mq[q] = fmaxf(s[(NC / 4) * q], s[(NC / 4) * q + 1]);
-#pragma unroll
-                            for (int c = 2; c < NC / 4; c += 2)
-#pragma unroll
-                                for (int q = 0; q < 4; ++q)
-                                    mq[q] = fmax3f(mq[q], s[(NC / 4) * q + c], s[(NC / 4) * q + c + 1]);
-                            const float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
-                            const float m_new = fmaxf(m, mx * sl2);
-                            if (done == 0) {
-                                m = m_new;
-                            } else if (__any_sync(0xffffffffu, m_new > m + 8.f)) {
-                                // O holds the earlier tiles, all complete (the commit behind this S covers
-                                // every MMA issued before it); rescaled only when the maximum grows by > 2^8
-                                const float alpha = m == -INFINITY ? 0.f : ex2(m - m_new);
-                                m = m_new;
-                                l *= alpha;
-                                fix *= alpha;
-#pragma unroll
-                                for (int c = 0; c < D / 32; ++c) {
-                                    float o[32];
-                                    tmem_ld32(tO + 32 * c, o);
-#pragma unroll
-                                    for (int i = 0; i < 32; ++i) o[i] *= alpha;
-                                    tmem_st32f(tO + 32 * c, o);
-                                }
-                            }
-                            const float mu = m == -INFINITY ? 0.f : m;      // no key yet: p = 0, not NaN
-                            const float2 negm = make_float2(-mu, -mu), sl2x2 = make_float2(sl2, sl2);
-                            float2 rs[4];
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) rs[q] = make_float2(0.f, 0.f);
-                            // P.V multiplies weights rounded to bf16.  The rounding of the tile's largest
-                            // weight enters the sum that O is divided by, which makes the dominant term
-                            // exact; the log-sum-exp keeps the unrounded sum.
-                            const float pmax = ex2(ffma2(make_float2(mx, mx), sl2x2, negm).x);
-                            fix += __uint_as_float(pack_bf16x2(pmax, 0.f) << 16) - pmax;
-#pragma unroll
-                            for (int c = 0; c < NC / 32; ++c) {
-                                uint32_t pk[16];
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) {
-                                    const float2 x =
-                                        ffma2(make_float2(s[32 * c + 2 * i], s[32 * c + 2 * i + 1]), sl2x2, negm);
-                                    const float2 e = make_float2(ex2(x.x), ex2(x.y));
-                                    rs[i & 3] = fadd2(rs[i & 3], e);
-                                    pk[i] = pack_bf16x2(e.x, e.y);
-                                }
-                                tmem_st16(tS + 16 * c, pk);
-                            }
-                            const float2 r01 = fadd2(rs[0], rs[1]), r23 = fadd2(rs[2], rs[3]);
-                            l += (r01.x + r23.x) + (r01.y + r23.y);
-                        };
-                        if (nk > 64)
-                            tile(std::integral_constant<int, 128>{});
-                        else
-                            tile(std::integral_constant<int, 64>{});
                     }
-                    tmem_st_wait();
-                    tc_fence_before();
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[h]);
-                ++done;
-                ++tiles;
-            }
-            if (!ok) break;
-            // ------------------------------------------------------------ output of the item
-            if (act > 0) {
-                if (!sh_warp_wait(&o_full[h], items & 1, abort_flag)) { ok = false; break; }
-                tc_fence_after();
-                ++items;
-            }
-            const int head = I.kh * p.g + hh;
-            const bool empty = !seen;              // this row has no key (in this piece)
-            if (I.e.slot >= 0) {
-                if (warp_live) {
-                    const int64_t prow = (static_cast<int64_t>(I.e.slot) * p.Hkv + I.kh) * (kShTiles * kShRows) +
-                                         h * kShRows + trow;
-                    // -inf marks a row that was not written; a sum of 0 over keys (scores of -inf) is NaN
-                    if (live) p.part_l[prow] = empty ? -INFINITY : l == 0.f ? NAN : m + __log2f(l);
-                    if (live) p.part_l[p.part_fix + prow] = empty ? 0.f : fix / l;
-                    if (act > 0) {
-                        const float inv = 1.f / l;
+                    hand_over(0);
+                    hand_over(1);
+                } else {
+                    const bool two = nk > 64;              // columns 64-127 are used
+                    float s[kShKeys];
+                    tmem_ld64(tS, s);
+                    if (two) {
+                        tmem_ld64(tS + 64, s + 64);
+                    } else {
 #pragma unroll
+                        for (int i = 64; i < 128; ++i) s[i] = -INFINITY;
+                    }
+                    if constexpr (CAP) {
+#pragma unroll
+                        for (int i = 0; i < 64; ++i) s[i] = capped(s[i], p.cap_in, p.cap_log2);
+                        if (two) {
+#pragma unroll
+                            for (int i = 64; i < 128; ++i) s[i] = capped(s[i], p.cap_in, p.cap_log2);
+                        }
+                    }
+                    if (masked) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            // bit i: column 32 c + i is in [c0, c1)
+                            const int a = min(max(c0 - 32 * c, 0), 32), b = min(max(c1 - 32 * c, 0), 32);
+                            const uint32_t below_b = b == 32 ? ~0u : (1u << b) - 1u;
+                            const uint32_t keep = a == 32 ? 0u : below_b & ~((1u << a) - 1u);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (!((keep >> i) & 1u)) s[32 * c + i] = -INFINITY;
+                        }
+                    }
+                    float mq[8];
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) mq[q] = fmaxf(s[16 * q], s[16 * q + 1]);
+#pragma unroll
+                    for (int c = 2; c < 16; c += 2)
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) mq[q] = fmax3f(mq[q], s[16 * q + c], s[16 * q + c + 1]);
+                    const float mx =
+                        fmax3f(fmax3f(mq[0], mq[1], mq[2]), fmax3f(mq[3], mq[4], mq[5]), fmaxf(mq[6], mq[7]));
+                    const float m_new = fmaxf(m, mx * sl2);
+                    if (done == 0) {
+                        m = m_new;
+                    } else if (__any_sync(0xffffffffu, m_new > m + 8.f)) {
+                        // O holds the earlier tiles, all complete (the commit behind this S covers every
+                        // MMA issued before it); rescaled only when the maximum grows by > 2^8
+                        const float alpha = m == -INFINITY ? 0.f : ex2(m - m_new);
+                        m = m_new;
+                        l *= alpha;
+                        fix *= alpha;
+#pragma unroll 1
                         for (int c = 0; c < D / 32; ++c) {
                             float o[32];
                             tmem_ld32(tO + 32 * c, o);
-                            if (live && !empty) {
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    uint32_t wv[8];
-#pragma unroll
-                                    for (int e = 0; e < 8; ++e) wv[e] = __float_as_uint(o[8 * i + e] * inv);
-                                    st_global_32b(p.part_o + prow * D + 32 * c + 8 * i, wv);
-                                }
-                            }
+                            for (int i = 0; i < 32; ++i) o[i] *= alpha;
+                            tmem_st32f(tO + 32 * c, o);
                         }
                     }
-                }
-            } else if (warp_live) {
-                if (live && empty && p.dev_status) atomicOr(p.dev_status, BG_DEVSTAT_EMPTY_ROW);
-                if (act > 0) {
-                    const float inv = 1.f / (l + fix);
-                    const int64_t orow = static_cast<int64_t>(row) * p.Hq + head;
+                    const float mu = m == -INFINITY ? 0.f : m;      // no key yet: p = 0, not NaN
+                    const float2 negm = make_float2(-mu, -mu), sl2x2 = make_float2(sl2, sl2);
+                    float2 rs[4];
 #pragma unroll
-                    for (int c = 0; c < D / 32; ++c) {
-                        float o[32];
-                        tmem_ld32(tO + 32 * c, o);
-                        if (live && !empty) {
+                    for (int q = 0; q < 4; ++q) rs[q] = make_float2(0.f, 0.f);
+                    auto weights = [&](int c) {            // P of columns 32 c .. 32 c + 31
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float2 x = ffma2(make_float2(s[32 * c + 2 * i], s[32 * c + 2 * i + 1]), sl2x2, negm);
+                            const float2 e = make_float2(ex2(x.x), ex2(x.y));
+                            rs[i & 3] = fadd2(rs[i & 3], e);
+                            pk[i] = pack_bf16x2(e.x, e.y);
+                        }
+                        tmem_st16(tS + 16 * c, pk);
+                    };
+                    weights(0);
+                    weights(1);
+                    hand_over(0);
+                    if (two) {
+                        weights(2);
+                        weights(3);
+                    }
+                    hand_over(1);
+                    // P.V multiplies weights rounded to bf16.  The rounding of the tile's largest weight
+                    // enters the sum that O is divided by, which makes the dominant term exact; the
+                    // log-sum-exp keeps the unrounded sum.
+                    const float pmax = ex2(ffma2(make_float2(mx, mx), sl2x2, negm).x);
+                    fix += __uint_as_float(pack_bf16x2(pmax, 0.f) << 16) - pmax;
+                    const float2 r01 = fadd2(rs[0], rs[1]), r23 = fadd2(rs[2], rs[3]);
+                    l += (r01.x + r23.x) + (r01.y + r23.y);
+                }
+                ++done;
+                ++tiles;
+            }
+            n += 2 * (I.te - tb);
+            if (!ok) break;
+            // ------------------------------------------------------------ output of the item
+            const int slot = I.slot, kh = I.kh;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&item_empty[rslot]);    // the item has been read
+            if (act > 0) {
+                if (!sh_warp_wait(&o_full[h], outs & 1, abort_flag)) { ok = false; break; }
+                tc_fence_after();
+                ++outs;
+            }
+            if (!warp_live) continue;
+            const int64_t orow = static_cast<int64_t>(row) * p.Hq + kh * p.g + hh;
+            const int64_t prow = static_cast<int64_t>(slot) * (kShTiles * kShRows) + h * kShRows + trow;
+            const bool whole = slot < 0;                       // the item's only part
+            if (live) {
+                if (whole) {
+                    if (!seen && p.dev_status) atomicOr(p.dev_status, BG_DEVSTAT_EMPTY_ROW);
+                    if (seen && p.lse) p.lse[orow] = (m + __log2f(l)) * 0.69314718055994530942f;
+                } else {
+                    // -inf marks a row that was not written; a sum of 0 over keys (scores of -inf) is NaN
+                    p.part_l[prow] = !seen ? -INFINITY : l == 0.f ? NAN : m + __log2f(l);
+                    p.part_l[p.part_fix + prow] = seen ? fix / l : 0.f;
+                }
+            }
+            if (act > 0) {
+                const float inv = 1.f / (whole ? l + fix : l);
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    float o[32];
+                    tmem_ld32(tO + 32 * c, o);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] *= inv;
+                    if (live && seen) {
+                        if (whole) {
                             uint32_t wv[16];
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) wv[i] = pack_bf16x2(o[2 * i] * inv, o[2 * i + 1] * inv);
+                            for (int i = 0; i < 16; ++i) wv[i] = pack_bf16x2(o[2 * i], o[2 * i + 1]);
                             st_out_32b(p.out + orow * D + 32 * c, wv, wide);
                             st_out_32b(p.out + orow * D + 32 * c + 16, wv + 8, wide);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                st_global_32b(p.part_o + prow * D + 32 * c + 8 * i,
+                                              reinterpret_cast<const uint32_t *>(o) + 8 * i);
                         }
                     }
-                    if (p.lse && live && !empty) p.lse[orow] = (m + __log2f(l)) * 0.69314718055994530942f;
                 }
             }
             tc_fence_before();         // O is read before the next item's first P.V overwrites it
@@ -853,19 +1007,18 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const ShParam
     if (!plan_ready(p, &other)) return;
     const int n_split = p.hdr[kShHdrSplits];
     const int lane = threadIdx.x & 31;
-    const int64_t total = static_cast<int64_t>(n_split) * p.Hkv * kShTiles * kShRows;
+    const int64_t total = static_cast<int64_t>(n_split) * (kShTiles * kShRows);
     const int64_t stride = static_cast<int64_t>(gridDim.x) * (kJoinThreads / 32);
     constexpr int E = D / 32;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * (kJoinThreads / 32) + (threadIdx.x >> 5); i < total; i += stride) {
         const int r = static_cast<int>(i % (kShTiles * kShRows));
-        const int64_t q = i / (kShTiles * kShRows);
-        const int kh = static_cast<int>(q % p.Hkv);
-        const ShSplit S = p.splits[q / p.Hkv];
+        const ShSplit S = p.splits[i / (kShTiles * kShRows)];
         const int h = r / kShRows, trow = r - h * kShRows;
         const int lr = trow / p.g, hh = trow - lr * p.g;
         if (lr >= p.bt || h * p.bt + lr >= S.nrows) continue;
+        // the first CTA's second slot, then the others' first
         auto prow = [&](int piece) {
-            return (static_cast<int64_t>(S.slot0 + piece) * p.Hkv + kh) * (kShTiles * kShRows) + r;
+            return static_cast<int64_t>(2 * (S.cta + piece) + (piece == 0 ? 1 : 0)) * (kShTiles * kShRows) + r;
         };
         float mx = -INFINITY;
         bool nan = false;
@@ -899,7 +1052,7 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const ShParam
             for (int e = 0; e < E; ++e) acc[e] = fmaf(wt, o[e], acc[e]);
         }
         const float inv = 1.f / (sum + fix);
-        const int64_t orow = (static_cast<int64_t>(S.row0) + h * p.bt + lr) * p.Hq + kh * p.g + hh;
+        const int64_t orow = (static_cast<int64_t>(S.row0) + h * p.bt + lr) * p.Hq + S.kh * p.g + hh;
         uint32_t *dst = reinterpret_cast<uint32_t *>(p.out + orow * D + lane * E);
 #pragma unroll
         for (int e = 0; e < E / 2; ++e) dst[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
@@ -937,39 +1090,36 @@ ShLayout shared_layout(const ShProblem &pb)
     int64_t own = pb.last ? static_cast<int64_t>(kShTiles) * bt * pb.max_seqlen : pb.max_seqlen + kShTiles * bt;
     if (own > pb.total_tokens) own = pb.total_tokens;
     const int64_t tiles = ceil_div(pb.max_prefix_len, kShKeys) + ceil_div(own, kShKeys);
+    // a cut leaves at least kShSplitMin / 2 tiles on either side
     L.slots = 0;
-    if (tiles > kShSplitMin) {
-        // fewer than 2 * work / kShSplitMin pieces, and never more than the plan makes
-        L.slots = kShSlots;
-        if (L.max_entries * pb.Hkv < kShSlots) {
-            const int64_t most = 2 * ceil_div(L.max_entries * pb.Hkv * tiles, kShSplitMin);
-            if (most < L.slots) L.slots = most;
-        }
+    if (tiles >= kShSplitMin) {
+        const int64_t ctas = ceil_div(L.max_entries * pb.Hkv * (tiles + 1), kShSplitMin);
+        L.slots = 2 * (ctas < kShMaxCtas ? ctas : kShMaxCtas);
     }
     auto al = [](size_t b) { return (b + 255) & ~size_t(255); };
     L.entries = 256;
-    L.raw = L.entries + al((L.max_entries + kShSlots) * sizeof(ShEntry));
-    L.splits = L.raw + al(L.max_entries * sizeof(ShEntry));
-    L.part_l = L.splits + al(kShSlots * sizeof(ShSplit));
+    L.starts = L.entries + al(L.max_entries * sizeof(ShEntry));
+    L.splits = L.starts + al((kShMaxCtas + 1) * sizeof(ShStart));
+    L.part_l = L.splits + al(kShMaxCtas * sizeof(ShSplit));
     L.part_o = L.part_l + al(static_cast<size_t>(L.slots) * kShTiles * kShRows * 2 * sizeof(float));
     L.total = L.part_o + al(static_cast<size_t>(L.slots) * kShTiles * kShRows * pb.head_dim * sizeof(float));
     return L;
 }
 
-ShKey shared_key(const ShProblem &pb)
+ShKey shared_key(const ShProblem &pb, int grid)
 {
     return ShKey{{pb.last, pb.num_seqs, pb.total_tokens, pb.max_seqlen, pb.num_groups, pb.total_prefix,
-                  pb.max_prefix_len, pb.Hq, pb.Hkv, pb.head_dim, 0x5348, 1}};
+                  pb.max_prefix_len, pb.Hq, pb.Hkv, pb.head_dim, grid, 0x5348}};
 }
 
-cudaError_t launch_shared_plan(const ShProblem &pb, const ShLayout &lay, void *workspace, int32_t *dev_status,
-                               cudaStream_t stream)
+cudaError_t launch_shared_plan(const ShProblem &pb, const ShLayout &lay, void *workspace, int grid,
+                               int32_t *dev_status, cudaStream_t stream)
 {
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    return launch_dependent(shared_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, pb, shared_key(pb),
+    return launch_dependent(shared_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, pb, shared_key(pb, grid),
                             kShRows / (pb.Hq / pb.Hkv), reinterpret_cast<int32_t *>(ws),
-                            reinterpret_cast<ShEntry *>(ws + lay.entries), reinterpret_cast<ShEntry *>(ws + lay.raw),
-                            reinterpret_cast<ShSplit *>(ws + lay.splits), lay.slots, dev_status);
+                            reinterpret_cast<ShEntry *>(ws + lay.entries), reinterpret_cast<ShStart *>(ws + lay.starts),
+                            reinterpret_cast<ShSplit *>(ws + lay.splits), grid, lay.slots > 0 ? 1 : 0, dev_status);
 }
 
 cudaError_t launch_shared_attn(int head_dim, bool is_capped, const CUtensorMap &tm_q, const CUtensorMap &tm_k,

@@ -14,12 +14,11 @@ namespace bg {
 constexpr int kShKeys = 128;          // keys per K/V tile
 constexpr int kShRows = 128;          // query rows (token, head) per tile = TMEM lanes
 constexpr int kShTiles = 2;           // query tiles per work item
-constexpr int kShSplitTarget = 152;   // pieces of work aimed at when long key ranges are split
-constexpr int kShSlots = 2 * kShSplitTarget;   // partial results the workspace holds at most
-constexpr int kShSplitMin = 8;        // key tiles below which an item is never split
+constexpr int kShMaxCtas = 256;       // CTAs of the attention kernel at most (one per SM)
+constexpr int kShSplitMin = 4;        // cost units per CTA below which fewer CTAs share the work
 
-// One work entry: kShTiles tiles of query rows of one request against its keys; the kernel runs
-// it once per kv head.  Rows are (row, head of the kv head) pairs, row-major; "row" is a token
+// One work entry: kShTiles tiles of query rows of one request against its keys; an entry for one
+// kv head is an item.  Rows are (row, head of the kv head) pairs, row-major; "row" is a token
 // (prefill) or a sample (last token).
 struct __align__(16) ShEntry {
     int32_t prow0, plen;      // prefix rows of the request
@@ -27,27 +26,33 @@ struct __align__(16) ShEntry {
     int32_t ka0, kb0;         // own (packed) keys that tile 0's rows can see: [ka0, kb0)
     int32_t ka1, kb1;         // the same for tile 1 (empty when the entry has one tile)
     int32_t s0;               // prefill: sample of the first row
-    int32_t tb, te;           // key tiles [tb, te) of the prefix tiles followed by the own tiles
-    int32_t slot;             // partial-result slot of a split entry's piece (times Hkv, plus kv head), or -1
+    int32_t tiles;            // key tiles: the prefix's, then those of the own keys
+    int64_t pos;              // cost units of all entries before this one
 };
 static_assert(sizeof(ShEntry) == 48, "three 16-byte loads");
 
-struct ShSplit {              // a split entry, for the join
-    int32_t row0, nrows, slot0, pieces;
+// The first tile of a CTA's share of the work, in the order (kv head, entry, key tile).
+struct __align__(16) ShStart {
+    int32_t kh, entry, tile, pad;
+};
+
+// An item whose key tiles are shared by `pieces` CTAs from `cta` on, for the join.
+struct __align__(16) ShSplit {
+    int32_t row0, nrows, kh, cta, pieces, pad[3];
 };
 
 // Header words at the start of the workspace; from kShHdrKey on the problem the plan is for, which
 // every run that reads the plan compares with its own.
-enum { kShHdrStatus = 0, kShHdrEntries = 1, kShHdrSplits = 2, kShHdrKey = 4 };
+enum { kShHdrStatus = 0, kShHdrCtas = 1, kShHdrSplits = 2, kShHdrEntries = 3, kShHdrKey = 4 };
 struct __align__(16) ShKey {
     int32_t w[12];
 };
 
 // Workspace layout (byte offsets); every part is 256-byte aligned.
 struct ShLayout {
-    size_t entries, raw, splits, part_o, part_l, total;
-    int64_t max_entries;      // unsplit entries
-    int64_t slots;            // 0: no entry can be split
+    size_t entries, starts, splits, part_l, part_o, total;
+    int64_t max_entries;
+    int64_t slots;            // partial results (two per CTA), or 0: no item can be split
 };
 
 struct ShProblem {
@@ -59,7 +64,7 @@ struct ShProblem {
 };
 
 ShLayout shared_layout(const ShProblem &pb);
-ShKey shared_key(const ShProblem &pb);
+ShKey shared_key(const ShProblem &pb, int grid);
 
 struct ShParams {
     int32_t Hq, Hkv, g, bt;   // bt = rows of g heads per query tile
@@ -73,13 +78,14 @@ struct ShParams {
     const int32_t *cu_seqlens;
     const int32_t *hdr;
     const ShEntry *entries;
+    const ShStart *starts;    // [CTAs + 1]
     const ShSplit *splits;
-    float *part_o, *part_l;   // [slot][kv head][256 rows]: [D] outputs; log2 sums, and behind them
+    float *part_o, *part_l;   // [slot][256 rows]: [D] outputs; log2 sums, and behind them
     int64_t part_fix;         // at this offset what the weights' rounding adds to a sum of 1
 };
 
-cudaError_t launch_shared_plan(const ShProblem &pb, const ShLayout &lay, void *workspace, int32_t *dev_status,
-                               cudaStream_t stream);
+cudaError_t launch_shared_plan(const ShProblem &pb, const ShLayout &lay, void *workspace, int grid,
+                               int32_t *dev_status, cudaStream_t stream);
 cudaError_t launch_shared_attn(int head_dim, bool capped, const CUtensorMap &tm_q, const CUtensorMap &tm_k,
                                const CUtensorMap &tm_v, const CUtensorMap &tm_pk, const CUtensorMap &tm_pv,
                                const ShParams &p, int grid, bool join, cudaStream_t stream);
