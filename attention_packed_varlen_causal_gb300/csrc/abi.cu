@@ -721,8 +721,7 @@ bg_status_t shared_impl(const ShProblem &pb, const void *q, const void *k, const
     p.starts = reinterpret_cast<const ShStart *>(ws + lay.starts);
     p.splits = reinterpret_cast<const ShSplit *>(ws + lay.splits);
     p.part_o = reinterpret_cast<float *>(ws + lay.part_o);
-    p.part_l = reinterpret_cast<float *>(ws + lay.part_l);
-    p.part_fix = lay.slots * kShTiles * kShRows;
+    p.part_l = reinterpret_cast<float2 *>(ws + lay.part_l);
     return launch_shared_attn(pb.head_dim, capped, tm_q, tm_k, tm_v, tm_pk, tm_pv, p, grid, lay.slots > 0, stream) ==
                    cudaSuccess
                ? BG_OK

@@ -24,7 +24,7 @@
 //        warp 0      walks the CTA's share, tells the other roles each item (through a ring in
 //                    shared memory), and loads K and V tiles of 128 keys by TMA (one ring for both)
 //        warp 2      TMA producer of Q
-//        warps 1, 3  tcgen05.mma issuers, one thread per query tile
+//        warp 1      tcgen05.mma issuer (one thread); warp 3 has no part
 //        warps 4-11  softmax and output, one warpgroup per query tile, one thread per row
 //      The scores of a query tile (128 fp32 TMEM columns) are overwritten by its weights P (64
 //      columns), so a tile alternates between its softmax and its two products; the two tiles of
@@ -48,6 +48,7 @@ namespace {
 
 // ------------------------------------------------------------------------------------ plan
 constexpr int kPlanThreads = 1024;
+constexpr int kPlanSeqs = 4096, kPlanGroups = 512;   // offsets up to these counts are held in shared memory
 
 __host__ __device__ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -92,6 +93,8 @@ __global__ void __launch_bounds__(kPlanThreads)
     __shared__ int s_warp[32];
     __shared__ int s_base[kPlanThreads];
     __shared__ ShStart s_start[kShMaxCtas + 1];
+    __shared__ int32_t s_cu[kPlanSeqs + 1], s_cup[kPlanGroups + 1], s_cug[kPlanGroups + 1];
+    __shared__ int64_t s_pos[kPlanThreads];
     const int tid = threadIdx.x;
     grid_dep_launch();
     if (tid == 0) {
@@ -101,20 +104,32 @@ __global__ void __launch_bounds__(kPlanThreads)
     grid_dep_wait();
     __syncthreads();
     if (tid < 12) hdr[kShHdrKey + tid] = key.w[tid];
+    const int32_t *cu = pb.cu_seqlens, *cup = pb.cu_prefix, *cug = pb.cu_group;
+    if (pb.num_seqs <= kPlanSeqs && pb.num_groups <= kPlanGroups) {
+        for (int i = tid; i <= pb.num_seqs; i += kPlanThreads) s_cu[i] = cu[i];
+        if (tid <= pb.num_groups) {
+            s_cup[tid] = cup[tid];
+            s_cug[tid] = cug[tid];
+        }
+        cu = s_cu;
+        cup = s_cup;
+        cug = s_cug;
+        __syncthreads();
+    }
 
     // ---- the offsets, before anything is read through them
     int err = 0;
     for (int i = tid; i < pb.num_groups; i += kPlanThreads) {
-        const int a = pb.cu_group[i], b = pb.cu_group[i + 1];
+        const int a = cug[i], b = cug[i + 1];
         if (a < 0 || b < a || b > pb.num_seqs || (i == 0 && a != 0) || (i == pb.num_groups - 1 && b != pb.num_seqs))
             err |= BG_DEVSTAT_GROUP;
-        const int c = pb.cu_prefix[i], d = pb.cu_prefix[i + 1];
+        const int c = cup[i], d = cup[i + 1];
         if (c < 0 || d < c || d > pb.total_prefix || d - c > pb.max_prefix_len || (i == 0 && c != 0) ||
             (i == pb.num_groups - 1 && d != pb.total_prefix))
             err |= BG_DEVSTAT_CU_PROMPT;
     }
     for (int i = tid; i < pb.num_seqs; i += kPlanThreads) {
-        const int a = pb.cu_seqlens[i], b = pb.cu_seqlens[i + 1];
+        const int a = cu[i], b = cu[i + 1];
         if (a < 0 || b < a || b > pb.total_tokens || (i == 0 && a != 0) ||
             (i == pb.num_seqs - 1 && b != pb.total_tokens))
             err |= BG_DEVSTAT_CU_SEQLENS;
@@ -135,14 +150,13 @@ __global__ void __launch_bounds__(kPlanThreads)
 
     // ---- the entries, in request order
     const int per = kShTiles * bt;         // rows of an entry
-    const int32_t *cu = pb.cu_seqlens;
     int n_entries = 0;
     int64_t units = 0;
     for (int r0 = 0; r0 < pb.num_groups; r0 += kPlanThreads) {
         const int r = r0 + tid;
         int items = 0;
         if (r < pb.num_groups) {
-            const int a = pb.cu_group[r], b = pb.cu_group[r + 1];
+            const int a = cug[r], b = cug[r + 1];
             items = static_cast<int>(ceil_div(pb.last ? b - a : cu[b] - cu[a], per));
         }
         int total;
@@ -158,9 +172,9 @@ __global__ void __launch_bounds__(kPlanThreads)
                     if (s_base[mid] <= e) t = mid; else end = mid;
                 }
                 const int grp = r0 + t, first = (e - s_base[t]) * per;
-                const int sa = pb.cu_group[grp], sb = pb.cu_group[grp + 1];
-                E.prow0 = pb.cu_prefix[grp];
-                E.plen = pb.cu_prefix[grp + 1] - E.prow0;
+                const int sa = cug[grp], sb = cug[grp + 1];
+                E.prow0 = cup[grp];
+                E.plen = cup[grp + 1] - E.prow0;
                 const int base = pb.last ? sa : cu[sa];
                 const int end_row = pb.last ? sb : cu[sb];
                 E.row0 = base + first;
@@ -187,6 +201,7 @@ __global__ void __launch_bounds__(kPlanThreads)
             if (e < total) {
                 E.pos = units + excl;
                 entries[n_entries + e] = E;
+                if (n_entries + e < kPlanThreads) s_pos[n_entries + e] = E.pos;
             }
             units += sum;
         }
@@ -195,6 +210,7 @@ __global__ void __launch_bounds__(kPlanThreads)
     }
 
     // ---- equal shares of units * Hkv; fewer CTAs where a share would be below kShSplitMin
+    auto pos_of = [&](int e) { return n_entries <= kPlanThreads ? s_pos[e] : entries[e].pos; };
     const int64_t work = units * pb.Hkv;
     const int ctas = static_cast<int>(min(static_cast<int64_t>(grid), ceil_div(work, kShSplitMin)));
     for (int c = tid; c <= ctas; c += kPlanThreads) {
@@ -206,11 +222,11 @@ __global__ void __launch_bounds__(kPlanThreads)
             int lo = 0, end = n_entries;           // the last entry that begins at or before u
             while (end - lo > 1) {
                 const int mid = (lo + end) >> 1;
-                if (entries[mid].pos <= u) lo = mid; else end = mid;
+                if (pos_of(mid) <= u) lo = mid; else end = mid;
             }
             S.entry = lo;
             const int n = entries[lo].tiles;
-            const int into = static_cast<int>(u - entries[lo].pos);
+            const int into = static_cast<int>(u - pos_of(lo));
             // a cut near an end of the item, or through a short one, moves to the end that is nearer
             const int least = max(kShSplitMin / 2, static_cast<int>(min(work / ctas / 32, static_cast<int64_t>(n))));
             S.tile = into;
@@ -264,7 +280,7 @@ __device__ bool plan_ready(const ShParams &p, bool *other)
 
 // ------------------------------------------------------------------------------------ attention
 constexpr int kShRing = 4;                     // items in the ring that warp 0 fills
-constexpr int kShReaders = 1 + 2 + 8;          // Q producer, MMA issuers, softmax warps
+constexpr int kShReaders = 1 + 1 + 8;          // Q producer, MMA issuer, softmax warps
 
 // The part of an item (an entry for one kv head) that this CTA computes, as the roles read it.
 struct __align__(16) ShItem {
@@ -348,12 +364,11 @@ __device__ __forceinline__ bool sh_warp_wait(uint64_t *bar, uint32_t parity, vol
     }
 }
 
-// S = Q K^T over D = 64 * NB, then commits to `full` and `empty`: one asm statement per tile, so that
+// S = Q K^T over D = 64 * NB, then a commit to `full`: one asm statement per tile, so that
 // the descriptors' offsets are immediates and the MMAs go out back to back.  Q and K column blocks
 // are 16 KB (1024 descriptor units) apart, 16-element steps 32 bytes (2 units).
 template <int NB>
-__device__ __forceinline__ void sh_mma_qk(uint32_t d, uint64_t dq, uint64_t dk, uint32_t idesc, uint64_t *full,
-                                          uint64_t *empty)
+__device__ __forceinline__ void sh_mma_qk(uint32_t d, uint64_t dq, uint64_t dk, uint32_t idesc, uint64_t *full)
 {
     if constexpr (NB == 2) {
         asm volatile(
@@ -371,9 +386,8 @@ __device__ __forceinline__ void sh_mma_qk(uint32_t d, uint64_t dq, uint64_t dk, 
             "tcgen05.mma.cta_group::1.kind::f16 [%0], a5, b5, %3, pt;\n\t"
             "tcgen05.mma.cta_group::1.kind::f16 [%0], a6, b6, %3, pt;\n\t"
             "tcgen05.mma.cta_group::1.kind::f16 [%0], a7, b7, %3, pt;\n\t"
-            "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%4];\n\t"
-            "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t}" ::"r"(d),
-            "l"(dq), "l"(dk), "r"(idesc), "r"(smem_u32(full)), "r"(smem_u32(empty))
+            "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%4];\n\t}" ::"r"(d),
+            "l"(dq), "l"(dk), "r"(idesc), "r"(smem_u32(full))
             : "memory");
     } else {
         asm volatile(
@@ -385,9 +399,8 @@ __device__ __forceinline__ void sh_mma_qk(uint32_t d, uint64_t dq, uint64_t dk, 
             "tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, pt;\n\t"
             "tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, pt;\n\t"
             "tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, pt;\n\t"
-            "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%4];\n\t"
-            "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t}" ::"r"(d),
-            "l"(dq), "l"(dk), "r"(idesc), "r"(smem_u32(full)), "r"(smem_u32(empty))
+            "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%4];\n\t}" ::"r"(d),
+            "l"(dq), "l"(dk), "r"(idesc), "r"(smem_u32(full))
             : "memory");
     }
 }
@@ -464,10 +477,10 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
             mbar_init(&p_full[2 * h + 1], 4);  // ... and keys 64-127
             mbar_init(&o_full[h], 1);
         }
-        mbar_init(mma_final, kShTiles);
+        mbar_init(mma_final, 1);
         for (int i = 0; i < C::kStages; ++i) {
             mbar_init(&kv_full[i], 1);
-            mbar_init(&kv_empty[i], kShTiles);   // one per MMA issuer
+            mbar_init(&kv_empty[i], 1);
         }
         for (int i = 0; i < kShRing; ++i) {
             mbar_init(&item_full[i], 1);
@@ -613,6 +626,13 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
                     const int act[kShTiles] = {ring[slot].act[0], ring[slot].act[1]};
                     mbar_arrive(&item_empty[slot]);
                     bool ok = true;
+                    // into L2 while the item before still uses the buffers
+#pragma unroll
+                    for (int h = 0; h < kShTiles; ++h)
+                        if (act[h] > 0) {
+#pragma unroll
+                            for (int b = 0; b < C::kNB; ++b) tma_prefetch_4d(&tm_q, b * 64, 0, kh, row0 + h * p.bt);
+                        }
 #pragma unroll
                     for (int h = 0; h < kShTiles; ++h) {
                         if (!ok || act[h] == 0) continue;
@@ -633,90 +653,126 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
                     if (n[h] > 0) mbar_wait_drain(&q_full[h], (n[h] - 1) & 1);
             }
             __syncwarp();
-        } else {
-            // ============================================================ MMA issuers (warps 1, 3)
+        } else if (warp == 1) {
+            // ============================================================ MMA issuer
+            // One thread for both query tiles, so that [P.V of a tile, QK of its next] of one query tile
+            // runs whole before the other's: that staggers the two softmax warpgroups, and each has the
+            // special-function units to itself while the tensor core works for the other.
             if (lane == 0) {
-                const int h = warp == 1 ? 0 : 1;
                 constexpr uint32_t kIdescQK0 = idesc_bf16_f32(128, 0, 0);      // N is set per tile
                 constexpr uint32_t kIdescPV = idesc_bf16_f32(128, D, 1);
-                const uint64_t dq = sdesc_sw128(smem_u32(smem + C::kOffQ + h * C::kTileBytes), 16, 1024);
+                const uint64_t dq = sdesc_sw128(smem_u32(smem + C::kOffQ), 16, 1024);
                 const uint64_t dk0 = sdesc_sw128(smem_u32(smem + C::kOffKV), 16, 1024);
                 const uint64_t dv0 = sdesc_sw128(smem_u32(smem + C::kOffKV), C::kBox, 1024);
-                const uint32_t tS = tmem + C::kColS + kShKeys * h, tO = tmem + C::kColO + D * h;
+                const uint32_t tS = tmem + C::kColS, tO = tmem + C::kColO;
                 uint32_t st = 0, ph = 0;         // stage of the next K or V tile, and its parity
-                uint32_t q_uses = 0, tiles = 0;
                 auto bump = [&]() {
                     if (++st == C::kStages) {
                         st = 0;
                         ph ^= 1u;
                     }
                 };
+                uint32_t q_uses[kShTiles] = {0, 0}, tiles[kShTiles] = {0, 0};
+                // the tile whose P.V comes next: its V stage, and per query tile its 16-key steps (0: none)
+                // and whether it is the first or last of the item
+                bool have = false;
+                uint32_t vs = 0, vph = 0;
+                int steps[kShTiles] = {0, 0};
+                bool first[kShTiles] = {}, last[kShTiles] = {};
                 bool ok = true;
+                auto pv = [&](int h) {
+                    if (!ok || steps[h] == 0) return;
+                    const uint64_t dv = dv0 + static_cast<uint64_t>((vs * C::kTileBytes) >> 4);
+                    const uint32_t a = tS + kShKeys * h, d = tO + D * h;
+                    ok = mbar_wait(&p_full[2 * h], tiles[h] & 1, abort_flag);
+                    if (!ok) return;
+                    tc_fence_after();
+                    if (steps[h] >= 4) {
+                        sh_mma_pv4(d, a, dv, kIdescPV, first[h] ? 0u : 1u);
+                    } else {
+#pragma unroll 1
+                        for (int k = 0; k < steps[h]; ++k)
+                            mma_ts(d, a + 8 * k, dv + static_cast<uint64_t>(128 * k), kIdescPV, (!first[h] || k > 0) ? 1u : 0u);
+                    }
+                    ok = mbar_wait(&p_full[2 * h + 1], tiles[h] & 1, abort_flag);
+                    if (!ok) return;
+                    tc_fence_after();
+                    if (steps[h] == 8) {
+                        sh_mma_pv4(d, a + 32, dv + 512, kIdescPV, 1u);
+                    } else {
+#pragma unroll 1
+                        for (int k = 4; k < steps[h]; ++k)
+                            mma_ts(d, a + 8 * k, dv + static_cast<uint64_t>(128 * k), kIdescPV, 1u);
+                    }
+                    if (last[h]) mma_commit(&o_full[h]);
+                    ++tiles[h];
+                };
                 for (uint32_t it = 0; ok; ++it) {
                     const uint32_t slot = it % kShRing;
                     if (!mbar_wait(&item_full[slot], (it / kShRing) & 1, abort_flag) || !ring[slot].more) break;
                     const ShItem &I = ring[slot];
-                    const int act = I.act[h], tb = I.tb, te = I.te;
-                    int done = 0;
-                    bool ready = false;          // the next tile's K has been waited for
-                    if (act > 0) {
-                        if (!mbar_wait(&q_full[h], q_uses & 1, abort_flag)) break;
-                        ++q_uses;
-                    }
-                    for (int j = tb; j < te; ++j) {
-                        const int nk = act > 0 ? I.keys_of(h, j) : 0;
-                        if (nk <= 0) {           // nothing for this query tile: only pass the stages on
-#pragma unroll 1
-                            for (int kv = 0; kv < 2 && ok; ++kv) {
-                                ok = mbar_wait(&kv_full[st], ph, abort_flag);
-                                if (ok) mbar_arrive(&kv_empty[st]);
-                                bump();
-                            }
-                            if (!ok) break;
-                            continue;
+                    const int tb = I.tb, te = I.te;
+                    const int act[kShTiles] = {I.act[0], I.act[1]};
+                    int done[kShTiles] = {0, 0};
+                    for (int j = tb; j < te && ok; ++j) {
+                        const uint32_t ks = st, kph = ph;
+                        bump();
+                        int nsteps[kShTiles];
+                        bool nfirst[kShTiles], nlast[kShTiles];
+#pragma unroll
+                        for (int h = 0; h < kShTiles; ++h) {
+                            const int nk = act[h] > 0 ? I.keys_of(h, j) : 0;
+                            nsteps[h] = nk > 0 ? (nk + 15) >> 4 : 0;      // S then has 16 * steps columns
+                            nfirst[h] = done[h] == 0;
+                            if (nk > 0) ++done[h];
+                            nlast[h] = done[h] == act[h];
                         }
-                        const int steps = (nk + 15) >> 4;       // 16-key steps of P.V; S has 16 * steps columns
-                        if (!ready && !mbar_wait(&kv_full[st], ph, abort_flag)) { ok = false; break; }
+                        if (have && !mbar_wait(&kv_full[vs], vph, abort_flag)) { ok = false; break; }
+                        if (!mbar_wait(&kv_full[ks], kph, abort_flag)) { ok = false; break; }
                         // S overwrites the P of the previous tile, which the P.V issued before it reads:
                         // tcgen05.mma operations of one thread execute in issue order.
-                        tc_fence_after();
-                        sh_mma_qk<C::kNB>(tS, dq, dk0 + static_cast<uint64_t>((st * C::kTileBytes) >> 4),
-                                          kIdescQK0 | (static_cast<uint32_t>(2 * steps) << 17), &s_full[h], &kv_empty[st]);
-                        const bool first = done == 0, last = ++done == act;
-                        if (last) mma_commit(&q_empty[h]);
-                        bump();
-                        const uint32_t vs = st, vph = ph;
-                        bump();
-                        // While the softmax works: this tile's V, and the K right behind it if it is used.  (One
-                        // further ahead could wait for a stage that this V still holds.)
-                        if (!mbar_wait(&kv_full[vs], vph, abort_flag)) { ok = false; break; }
-                        ready = j + 1 < te && I.keys_of(h, j + 1) > 0;
-                        if (ready && !mbar_wait(&kv_full[st], ph, abort_flag)) { ok = false; break; }
-                        const uint64_t dv = dv0 + static_cast<uint64_t>((vs * C::kTileBytes) >> 4);
-                        if (!mbar_wait(&p_full[2 * h], tiles & 1, abort_flag)) { ok = false; break; }
-                        tc_fence_after();
-                        if (steps >= 4) {
-                            sh_mma_pv4(tO, tS, dv, kIdescPV, first ? 0u : 1u);
+                        const uint64_t dk = dk0 + static_cast<uint64_t>((ks * C::kTileBytes) >> 4);
+                        auto qk = [&](int h) {
+                            if (!ok || nsteps[h] == 0) return;
+                            if (nfirst[h]) {
+                                ok = mbar_wait(&q_full[h], q_uses[h] & 1, abort_flag);
+                                if (!ok) return;
+                                ++q_uses[h];
+                            }
+                            tc_fence_after();
+                            sh_mma_qk<C::kNB>(tS + kShKeys * h, dq + static_cast<uint64_t>((h * C::kTileBytes) >> 4), dk,
+                                              kIdescQK0 | (static_cast<uint32_t>(2 * nsteps[h]) << 17), &s_full[h]);
+                            if (nlast[h]) mma_commit(&q_empty[h]);
+                        };
+                        // Behind an item's last tile its P.V do not wait for the next item's Q.
+                        pv(0);
+                        if (j > tb) qk(0);
+                        pv(1);
+                        if (j > tb) {
+                            qk(1);
                         } else {
-#pragma unroll 1
-                            for (int k = 0; k < steps; ++k)
-                                mma_ts(tO, tS + 8 * k, dv + static_cast<uint64_t>(128 * k), kIdescPV,
-                                       (!first || k > 0) ? 1u : 0u);
+                            qk(0);
+                            qk(1);
                         }
-                        if (!mbar_wait(&p_full[2 * h + 1], tiles & 1, abort_flag)) { ok = false; break; }
-                        tc_fence_after();
-                        if (steps == 8) {
-                            sh_mma_pv4(tO, tS + 32, dv + 512, kIdescPV, 1u);
-                        } else {
-#pragma unroll 1
-                            for (int k = 4; k < steps; ++k)
-                                mma_ts(tO, tS + 8 * k, dv + static_cast<uint64_t>(128 * k), kIdescPV, 1u);
+                        if (!ok) break;
+                        if (have) mma_commit(&kv_empty[vs]);
+                        mma_commit(&kv_empty[ks]);
+                        have = true;
+                        vs = st;
+                        vph = ph;
+                        bump();
+#pragma unroll
+                        for (int h = 0; h < kShTiles; ++h) {
+                            steps[h] = nsteps[h];
+                            first[h] = nfirst[h];
+                            last[h] = nlast[h];
                         }
-                        mma_commit(&kv_empty[vs]);
-                        if (last) mma_commit(&o_full[h]);
-                        ++tiles;
                     }
                     mbar_arrive(&item_empty[slot]);
+                }
+                if (ok && have && mbar_wait(&kv_full[vs], vph, abort_flag)) {
+                    pv(0);
+                    pv(1);
                 }
                 mma_commit(mma_final);           // every MMA issued completes before TMEM is released
                 mbar_wait_drain(mma_final, 0);
@@ -877,11 +933,32 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
                     const float mx =
                         fmax3f(fmax3f(mq[0], mq[1], mq[2]), fmax3f(mq[3], mq[4], mq[5]), fmaxf(mq[6], mq[7]));
                     const float m_new = fmaxf(m, mx * sl2);
-                    if (done == 0) {
-                        m = m_new;
-                    } else if (__any_sync(0xffffffffu, m_new > m + 8.f)) {
+                    if (done == 0) m = m_new;
+                    const float2 sl2x2 = make_float2(sl2, sl2);
+                    float2 negm, rs[4];
+                    uint32_t pk[32];
+                    auto weights = [&](int c, uint32_t *w) {       // of columns 32 c .. 32 c + 31, as bf16 pairs
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float2 x = ffma2(make_float2(s[32 * c + 2 * i], s[32 * c + 2 * i + 1]), sl2x2, negm);
+                            const float2 e = make_float2(ex2(x.x), ex2(x.y));
+                            rs[i & 3] = fadd2(rs[i & 3], e);
+                            w[i] = pack_bf16x2(e.x, e.y);
+                        }
+                    };
+                    // The first half's weights use the maximum so far, so that they need not wait for
+                    // this tile's; only when that grows by more than 2^8 is O rescaled and the half redone.
+#pragma unroll 1
+                    for (;;) {
+                        const float mu = m == -INFINITY ? 0.f : m;  // no key yet: p = 0, not NaN
+                        negm = make_float2(-mu, -mu);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) rs[q] = make_float2(0.f, 0.f);
+                        weights(0, pk);
+                        weights(1, pk + 16);
+                        if (!__any_sync(0xffffffffu, m_new > m + 8.f)) break;
                         // O holds the earlier tiles, all complete (the commit behind this S covers every
-                        // MMA issued before it); rescaled only when the maximum grows by > 2^8
+                        // MMA issued before it)
                         const float alpha = m == -INFINITY ? 0.f : ex2(m - m_new);
                         m = m_new;
                         l *= alpha;
@@ -895,28 +972,14 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
                             tmem_st32f(tO + 32 * c, o);
                         }
                     }
-                    const float mu = m == -INFINITY ? 0.f : m;      // no key yet: p = 0, not NaN
-                    const float2 negm = make_float2(-mu, -mu), sl2x2 = make_float2(sl2, sl2);
-                    float2 rs[4];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) rs[q] = make_float2(0.f, 0.f);
-                    auto weights = [&](int c) {            // P of columns 32 c .. 32 c + 31
-                        uint32_t pk[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float2 x = ffma2(make_float2(s[32 * c + 2 * i], s[32 * c + 2 * i + 1]), sl2x2, negm);
-                            const float2 e = make_float2(ex2(x.x), ex2(x.y));
-                            rs[i & 3] = fadd2(rs[i & 3], e);
-                            pk[i] = pack_bf16x2(e.x, e.y);
-                        }
-                        tmem_st16(tS + 16 * c, pk);
-                    };
-                    weights(0);
-                    weights(1);
+                    tmem_st16(tS, pk);
+                    tmem_st16(tS + 16, pk + 16);
                     hand_over(0);
                     if (two) {
-                        weights(2);
-                        weights(3);
+                        weights(2, pk);
+                        tmem_st16(tS + 32, pk);
+                        weights(3, pk + 16);
+                        tmem_st16(tS + 48, pk + 16);
                     }
                     hand_over(1);
                     // P.V multiplies weights rounded to bf16.  The rounding of the tile's largest weight
@@ -951,8 +1014,7 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
                     if (seen && p.lse) p.lse[orow] = (m + __log2f(l)) * 0.69314718055994530942f;
                 } else {
                     // -inf marks a row that was not written; a sum of 0 over keys (scores of -inf) is NaN
-                    p.part_l[prow] = !seen ? -INFINITY : l == 0.f ? NAN : m + __log2f(l);
-                    p.part_l[p.part_fix + prow] = seen ? fix / l : 0.f;
+                    p.part_l[prow] = make_float2(!seen ? -INFINITY : l == 0.f ? NAN : m + __log2f(l), seen ? fix / l : 0.f);
                 }
             }
             if (act > 0) {
@@ -995,69 +1057,69 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
 
 // ------------------------------------------------------------------------------------ join
 // out = sum_i 2^(L_i - L) O_i / (1 + sum_i 2^(L_i - L) fix_i) with L = log2 sum_i 2^(L_i): the
-// pieces' own normalised outputs, in piece order.  One warp per row.
-constexpr int kJoinThreads = 256;
+// pieces' own normalised outputs, in piece order.
+constexpr int kJoinThreads = 512;              // one warp per row
+constexpr int kJoinRows = kJoinThreads / 32;
 
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const ShParams p)
 {
     grid_dep_launch();
     grid_dep_wait();
-    bool other;
-    if (!plan_ready(p, &other)) return;
-    const int n_split = p.hdr[kShHdrSplits];
+    constexpr int kParts = kShTiles * kShRows / kJoinRows;
+    const int split = static_cast<int>(blockIdx.x) / kParts;
     const int lane = threadIdx.x & 31;
-    const int64_t total = static_cast<int64_t>(n_split) * (kShTiles * kShRows);
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * (kJoinThreads / 32);
+    const int r = (static_cast<int>(blockIdx.x) - split * kParts) * kJoinRows + (threadIdx.x >> 5);
+    const ShSplit S = p.splits[split];         // (not looked at unless it is one)
+    bool other;
+    if (!plan_ready(p, &other) || split >= p.hdr[kShHdrSplits]) return;
+    const int h = r / kShRows, trow = r - h * kShRows;
+    const int lr = trow / p.g, hh = trow - lr * p.g;
+    if (lr >= p.bt || h * p.bt + lr >= S.nrows) return;
     constexpr int E = D / 32;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * (kJoinThreads / 32) + (threadIdx.x >> 5); i < total; i += stride) {
-        const int r = static_cast<int>(i % (kShTiles * kShRows));
-        const ShSplit S = p.splits[i / (kShTiles * kShRows)];
-        const int h = r / kShRows, trow = r - h * kShRows;
-        const int lr = trow / p.g, hh = trow - lr * p.g;
-        if (lr >= p.bt || h * p.bt + lr >= S.nrows) continue;
-        // the first CTA's second slot, then the others' first
-        auto prow = [&](int piece) {
-            return static_cast<int64_t>(2 * (S.cta + piece) + (piece == 0 ? 1 : 0)) * (kShTiles * kShRows) + r;
-        };
-        float mx = -INFINITY;
-        bool nan = false;
-        for (int t = lane; t < S.pieces; t += 32) {
-            const float lt = p.part_l[prow(t)];
-            mx = fmaxf(mx, lt);
-            nan = nan || lt != lt;
-        }
-        nan = __any_sync(0xffffffffu, nan);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        if (mx == -INFINITY && !nan) {          // no piece has a key for this row
-            if (lane == 0 && p.dev_status) atomicOr(p.dev_status, BG_DEVSTAT_EMPTY_ROW);
-            continue;
-        }
-        float sum = 0.f, fix = 0.f, acc[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = 0.f;
-        for (int t = 0; t < S.pieces; ++t) {
-            const float lt = p.part_l[prow(t)];
-            if (lt == -INFINITY) continue;          // its row of part_o was not written
-            const float wt = ex2(lt - mx);
-            sum += wt;
-            fix = fmaf(wt, p.part_l[p.part_fix + prow(t)], fix);
-            float o[E];
-            if constexpr (E == 4)
-                *reinterpret_cast<float4 *>(o) = *reinterpret_cast<const float4 *>(p.part_o + prow(t) * D + lane * E);
-            else
-                *reinterpret_cast<float2 *>(o) = *reinterpret_cast<const float2 *>(p.part_o + prow(t) * D + lane * E);
-#pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] = fmaf(wt, o[e], acc[e]);
-        }
-        const float inv = 1.f / (sum + fix);
-        const int64_t orow = (static_cast<int64_t>(S.row0) + h * p.bt + lr) * p.Hq + S.kh * p.g + hh;
-        uint32_t *dst = reinterpret_cast<uint32_t *>(p.out + orow * D + lane * E);
-#pragma unroll
-        for (int e = 0; e < E / 2; ++e) dst[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-        if (p.lse && lane == 0) p.lse[orow] = (mx + __log2f(sum)) * 0.69314718055994530942f;
+    // piece 0 is in the first CTA's second slot, the others in their CTA's first: slot0 + 2 t - (t > 0)
+    const int64_t row0 = static_cast<int64_t>(2 * S.cta + 1) * (kShTiles * kShRows) + r;
+    auto row_of = [&](int t) { return row0 + (t > 0 ? 2 * t - 1 : 0) * (kShTiles * kShRows); };
+    float mx = -INFINITY;
+    bool nan = false;
+#pragma unroll 1
+    for (int t = lane; t < S.pieces; t += 32) {
+        const float lt = p.part_l[row_of(t)].x;
+        mx = fmaxf(mx, lt);
+        nan = nan || lt != lt;
     }
+    nan = __any_sync(0xffffffffu, nan);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    if (mx == -INFINITY && !nan) {             // no piece has a key for this row
+        if (lane == 0 && p.dev_status) atomicOr(p.dev_status, BG_DEVSTAT_EMPTY_ROW);
+        return;
+    }
+    float sum = 0.f, fix = 0.f, acc[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll 4
+    for (int t = 0; t < S.pieces; ++t) {
+        const int64_t at = row_of(t);
+        const float2 lf = p.part_l[at];
+        float o[E];
+        if constexpr (E == 4)
+            *reinterpret_cast<float4 *>(o) = *reinterpret_cast<const float4 *>(p.part_o + at * D + lane * E);
+        else
+            *reinterpret_cast<float2 *>(o) = *reinterpret_cast<const float2 *>(p.part_o + at * D + lane * E);
+        const bool written = lf.x != -INFINITY;      // else part_o holds anything
+        const float wt = written ? ex2(lf.x - mx) : 0.f;
+        sum += wt;
+        fix = fmaf(wt, lf.y, fix);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(wt, written ? o[e] : 0.f, acc[e]);
+    }
+    const float inv = 1.f / (sum + fix);
+    const int64_t orow = (static_cast<int64_t>(S.row0) + h * p.bt + lr) * p.Hq + S.kh * p.g + hh;
+    uint32_t *dst = reinterpret_cast<uint32_t *>(p.out + orow * D + lane * E);
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) dst[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    if (p.lse && lane == 0) p.lse[orow] = (mx + __log2f(sum)) * 0.69314718055994530942f;
 }
 
 template <int D, bool CAP>
@@ -1074,7 +1136,9 @@ cudaError_t launch_one(const CUtensorMap &tm_q, const CUtensorMap &tm_k, const C
     if (e != cudaSuccess) return e;
     e = launch_dependent(kern, dim3(grid), dim3(C::kThreads), C::kSmemBytes, stream, tm_q, tm_k, tm_v, tm_pk, tm_pv, p);
     if (e != cudaSuccess || !join) return e;
-    return launch_dependent(shared_join_kernel<D>, dim3(2 * grid), dim3(kJoinThreads), 0, stream, p);
+    // at most one cut item per CTA
+    return launch_dependent(shared_join_kernel<D>, dim3(grid * (kShTiles * kShRows / kJoinRows)), dim3(kJoinThreads), 0,
+                            stream, p);
 }
 
 }  // namespace

@@ -80,8 +80,8 @@ struct ShParams {
     const ShEntry *entries;
     const ShStart *starts;    // [CTAs + 1]
     const ShSplit *splits;
-    float *part_o, *part_l;   // [slot][256 rows]: [D] outputs; log2 sums, and behind them
-    int64_t part_fix;         // at this offset what the weights' rounding adds to a sum of 1
+    float *part_o;            // [slot][256 rows][D] partial outputs
+    float2 *part_l;           // [slot][256 rows] log2 sums, and what the weights' rounding adds to a sum of 1
 };
 
 cudaError_t launch_shared_plan(const ShProblem &pb, const ShLayout &lay, void *workspace, int grid,
