@@ -7,17 +7,21 @@
 //     logprob(t) = d_t - ln Z
 //     entropy    = ln Z - sum_v e^(d_v) d_v / Z          (every term of the sum has one sign)
 //     top        = the K largest logits, equal ones by the smaller index, as (v, d_v - ln Z)
-// Only the row's bytes bound it, so everything comes out of one pass over them, by a team of W warps
-// (a power of two up to the 16 of a CTA; with fewer rows than CTAs, a cluster of up to 8 CTAs):
+// Only the row's bytes bound it, so everything comes out of one pass over them, by a team of 4 warps
+// or of the 16 of a CTA (with fewer rows than CTAs, a cluster of up to 8 CTAs):
 //   pass    every lane keeps a running maximum with Z and the entropy's sum relative to it, and in
-//           shared memory the maximum of each batch of 64 bytes it read, rounded up to bf16;
+//           shared memory the maximum of each batch of 64 bytes it read, rounded up to bf16; bulk
+//           copies bring the batches into shared memory, over the rows' ends;
 //   bound   the 32 / W largest lane maxima of each warp are 32 >= K distinct logits, so the K-th
 //           largest of them bounds the row's K-th best from below;
-//   gather  only the batches whose maximum reaches the bound are read again (from L2), one logit
-//           per lane; the few logits at or above it go to a list in shared memory, where each one's
+//   gather  only the batches whose maximum reaches the bound are read again (from L2), eight at a
+//           time; the few logits at or above it go to a list in shared memory, where each one's
 //           rank is the number of larger (logit, index) pairs.
 // A row with more such logits than the list holds (thousands of equal ones) is searched K times
-// instead.
+// instead.  Two CTAs of 16 warps per SM keep 64 KB of copies in flight; what is left to the bound is
+// issue slots (about 9 instructions per logit and lane, the K best among them): 8192 rows of 65,536
+// bf16 logits take 205 us for the 20 best, 5.25 TB/s, and 190 us without the best; 480 rows of 50,001
+// fp32 logits with an eighth of them banned 25.9 us, 3.7 TB/s.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <stdint.h>
@@ -35,11 +39,14 @@ namespace {
 constexpr int kLpThreads = 512;
 constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kLpLoads = 4;              // 16-byte loads per lane and batch
-constexpr int kLpSlots = 64;             // stored batch maxima per lane (of one or more batches each)
-constexpr int kLpCap = 288;              // gathered logits per warp of the team (a row too short to give
+constexpr int kLpStages = 2;             // batches in flight per team (32 KB each over a CTA's teams)
+constexpr int kLpSlots = 16;             // stored batch maxima per lane (of one or more batches each)
+constexpr int kLpCap = 144;              // gathered logits per warp of the team (a row too short to give
                                          // 32 lane maxima fits)
 constexpr int kLpMaxCluster = 8;
+constexpr uint32_t kLpPolls = 1u << 22;  // polls after which a wait gives up (a second or more)
 static_assert(BG_MAX_TOP <= 32, "at least K lane maxima");
+static_assert(kLpSlots == 16, "a lane's stored maxima are two vectors, one mask");
 
 // A slice's results: what the warps of a team, and the CTAs of a cluster, tell each other.
 struct LpPart {
@@ -48,7 +55,11 @@ struct LpPart {
 };
 
 struct LpShared {
-    __nv_bfloat16 slot[kLpWarps][kLpSlots][32];
+    uint4 data[kLpStages * kLpThreads * kLpLoads];      // per team: its stages
+    uint64_t full[kLpWarps][kLpStages], empty[kLpWarps][kLpStages];
+    int abort;
+    uint4 slot[kLpWarps][32][kLpSlots / 8];      // bf16 [kLpSlots] per lane
+    int pick[kLpWarps][8];                       // batches that a warp reads again
     unsigned long long key[kLpWarps * kLpCap];   // order-preserving logit << 32 | ~index; per team
     LpPart part[kLpMaxCluster];                  // first CTA: one per CTA
     LpPart all[kLpWarps];                        // per team
@@ -112,13 +123,6 @@ struct Running {
     }
 };
 
-__device__ __forceinline__ float fmin3f(float a, float b, float c)
-{
-    float d;
-    asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
-
 template <typename T>
 struct LpVec;
 template <>
@@ -130,18 +134,16 @@ struct LpVec<float> {
         x[2] = __uint_as_float(w.z); x[3] = __uint_as_float(w.w);
     }
     static __device__ float load(const float *p) { return *p; }
-    static __device__ void bounds(const uint4 *w, float *hi, float *lo)      // of kLpLoads vectors
+    static __device__ float largest(const uint4 *w)      // of kLpLoads vectors
     {
-        float h[kLpLoads], l[kLpLoads];
+        float h[kLpLoads];
 #pragma unroll
         for (int i = 0; i < kLpLoads; ++i) {
             float x[4];
             unpack(w[i], x);
             h[i] = fmaxf(fmax3f(x[0], x[1], x[2]), x[3]);
-            l[i] = fminf(fmin3f(x[0], x[1], x[2]), x[3]);
         }
-        *hi = fmaxf(fmax3f(h[0], h[1], h[2]), h[3]);
-        *lo = fminf(fmin3f(l[0], l[1], l[2]), l[3]);
+        return fmaxf(fmax3f(h[0], h[1], h[2]), h[3]);
     }
     static __device__ uint4 nothing() { return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u); }
 };
@@ -158,19 +160,15 @@ struct LpVec<__nv_bfloat16> {
         }
     }
     static __device__ float load(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
-    static __device__ void bounds(const uint4 *w, float *hi, float *lo)
+    static __device__ float largest(const uint4 *w)
     {
         auto pair = [](uint32_t u) { return *reinterpret_cast<__nv_bfloat162 *>(&u); };
-        __nv_bfloat162 h[kLpLoads], l[kLpLoads];
+        __nv_bfloat162 h[kLpLoads];
 #pragma unroll
-        for (int i = 0; i < kLpLoads; ++i) {
+        for (int i = 0; i < kLpLoads; ++i)
             h[i] = __hmax2(__hmax2(pair(w[i].x), pair(w[i].y)), __hmax2(pair(w[i].z), pair(w[i].w)));
-            l[i] = __hmin2(__hmin2(pair(w[i].x), pair(w[i].y)), __hmin2(pair(w[i].z), pair(w[i].w)));
-        }
         const float2 a = __bfloat1622float2(__hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3])));
-        const float2 b = __bfloat1622float2(__hmin2(__hmin2(l[0], l[1]), __hmin2(l[2], l[3])));
-        *hi = fmaxf(a.x, a.y);
-        *lo = fminf(b.x, b.y);
+        return fmaxf(a.x, a.y);
     }
     static __device__ uint4 nothing() { return make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u); }
 };
@@ -185,6 +183,48 @@ struct LpParams {
     float *top_logprob;
     int32_t *dev_status;
 };
+
+// `bytes` (a multiple of 16, from a 16-byte boundary) into shared memory, completing on `bar`.
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+// Bounded wait (as bg::mbar_wait) that lets the barrier unit suspend the warp for up to 20 us at a
+// time: the polls of waiting warps would take issue slots from the summing ones.
+__device__ __forceinline__ bool lp_wait(uint64_t *bar, uint32_t parity, volatile int *abort)
+{
+    for (uint32_t it = 0;; ++it) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
+            : "memory");
+        if (ok) return true;
+        if (it >= kLpPolls) *abort = 1;
+        if (*abort) return false;
+    }
+}
+
+// The warp's 32 keys, largest first.
+__device__ __forceinline__ uint32_t sort_desc(uint32_t k, int lane)
+{
+#pragma unroll
+    for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+        for (int o = size >> 1; o > 0; o >>= 1) {
+            const uint32_t u = __shfl_xor_sync(0xffffffffu, k, o);
+            const bool up = ((lane & size) != 0) == ((lane & o) != 0);      // this lane keeps the larger
+            k = up ? max(k, u) : min(k, u);
+        }
+    return k;
+}
 
 // A batch maximum as it is stored: not below x (exact for bf16 logits; -inf stays).
 __device__ __forceinline__ __nv_bfloat16 slot_value(float x)
@@ -211,26 +251,83 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LpParams 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int team = warp / W, tw = warp - team * W;     // team of the CTA, warp of the team
     const int tid = tw * 32 + lane;                      // lane of the team
-    LpShared *lead = C == 1 ? &sh : cluster.map_shared_rank(&sh, 0);
-    unsigned long long *list = lead->key + team * kCap;
+    unsigned long long *list = sh.key + team * kCap;
     auto team_sync = [&]() {
-        if constexpr (W == 1) __syncwarp();
-        else if constexpr (W == kLpWarps) __syncthreads();
+        if constexpr (W == kLpWarps) __syncthreads();
         else named_bar_sync(1 + team, kLanes);
     };
     grid_dep_launch();
+    uint64_t *full = sh.full[team], *empty = sh.empty[team];
+    volatile int *abort = &sh.abort;
+    if (tid == 0) {
+        for (int i = 0; i < kLpStages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], W);
+        }
+        fence_barrier_init();
+    }
+    if (threadIdx.x == 0) sh.abort = 0;
+    // every CTA of the cluster has started before one writes into another's shared memory
+    if (C > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     grid_dep_wait();
+    __syncthreads();
+    uint4 *data = sh.data + team * kLpStages * kBatch;
 
+    // consecutive rows in different CTAs, so that a few rows spread over the SMs; a cluster has one row
     const int64_t rows_at_once = static_cast<int64_t>(gridDim.x / C) * kTeams;
-    for (int64_t row = static_cast<int64_t>(blockIdx.x / C) * kTeams + team; row < p.N; row += rows_at_once) {
-        const T *x = static_cast<const T *>(p.logits) + row * p.stride;
-        // [0, head) before the first 16-byte boundary, nv whole vectors, [tail, V) behind them
-        const int head = min(static_cast<int>(((16u - (reinterpret_cast<uintptr_t>(x) & 15u)) & 15u) / sizeof(T)), p.V);
-        const int nv = (p.V - head) / VN;
-        const int tail = head + nv * VN;
-        const uint4 *xv = reinterpret_cast<const uint4 *>(x + head);
-        const int v0 = C == 1 ? 0 : static_cast<int>(static_cast<int64_t>(nv) * c / C);
-        const int v1 = C == 1 ? nv : static_cast<int>(static_cast<int64_t>(nv) * (c + 1) / C);
+    const int64_t row0 = static_cast<int64_t>(team) * (gridDim.x / C) + blockIdx.x / C;
+    // A row in memory: [0, head) before the first 16-byte boundary, whole vectors, [tail, V) behind
+    // them; of the vectors, this CTA's [v0, v1).
+    struct Slice {
+        const T *x;
+        int head, tail, v0, v1;
+    };
+    auto slice_of = [&](int64_t row) {
+        Slice S;
+        S.x = static_cast<const T *>(p.logits) + row * p.stride;
+        S.head = min(static_cast<int>(((16u - (reinterpret_cast<uintptr_t>(S.x) & 15u)) & 15u) / sizeof(T)), p.V);
+        const int nv = (p.V - S.head) / VN;
+        S.tail = S.head + nv * VN;
+        S.v0 = C == 1 ? 0 : static_cast<int>(static_cast<int64_t>(nv) * c / C);
+        S.v1 = C == 1 ? nv : static_cast<int>(static_cast<int64_t>(nv) * (c + 1) / C);
+        return S;
+    };
+    // The first lane of the team issues the copies, kLpStages - 1 batches ahead of the one that is
+    // summed, over the rows' ends.
+    int64_t load_row = row0 - rows_at_once;
+    const T *load_x = nullptr;
+    int load_v = 0, load_end = 0;
+    uint32_t loads = 0;                                  // batches issued
+    auto issue = [&]() {
+        while (load_v >= load_end) {                     // the next row that has vectors
+            load_row += rows_at_once;
+            if (load_row >= p.N) return;
+            const Slice L = slice_of(load_row);
+            load_x = L.x + L.head;
+            load_v = L.v0;
+            load_end = L.v1;
+        }
+        const uint32_t st = loads % kLpStages, use = loads / kLpStages;
+        if (use > 0 && !lp_wait(&empty[st], (use - 1) & 1, abort)) {
+            load_row = p.N;                              // give up: nothing more is issued
+            load_v = load_end = 0;
+            return;
+        }
+        const int n = min(kBatch, load_end - load_v);
+        mbar_arrive_expect_tx(&full[st], n * 16);
+        bulk_load(data + st * kBatch, reinterpret_cast<const uint4 *>(load_x) + load_v, n * 16, &full[st]);
+        load_v += n;
+        ++loads;
+    };
+    if (tid == 0)
+        for (int i = 0; i < kLpStages - 1; ++i) issue();
+    uint32_t sums = 0;                                   // batches summed
+
+    if (C > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    for (int64_t row = row0; row < p.N; row += rows_at_once) {
+        const Slice S = slice_of(row);
+        const T *x = S.x;
+        const int head = S.head, tail = S.tail, v0 = S.v0, v1 = S.v1;
         const int nb = (v1 - v0 + kBatch - 1) / kBatch;
         const int per_slot = (nb + kLpSlots - 1) / kLpSlots;
         // the loose logits: the head belongs to the first CTA of the row, the tail to the last
@@ -238,57 +335,83 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LpParams 
         const int loose = lane < n_head ? lane : lane >= 16 && lane - 16 < n_tail ? tail + lane - 16 : -1;
         const float loose_x = tw == 0 && loose >= 0 ? Vec::load(x + loose) : -INFINITY;
         if (tid == 0) sh.n[team] = 0;
+        if (C > 1 && tid == 1) sh.n[1] = 0;
+        // the given token's logit, loaded ahead of its use
+        int token = -1;
+        float token_x = 0.f;
+        if (c == 0 && tid == 0 && p.tokens) {
+            token = p.tokens[row];
+            if (token >= 0 && token < p.V) token_x = Vec::load(x + token);
+        }
 
         Running a;
         float best = -INFINITY;           // this lane's largest logit
         int in_slot = 0, slot = 0;
+        __nv_bfloat16 *slots = reinterpret_cast<__nv_bfloat16 *>(sh.slot[warp][lane]);
         float slot_max = -INFINITY;
-        uint4 w[kLpLoads];
-        auto fetch = [&](int at) {        // past the slice's end -inf, which adds nothing
-#pragma unroll
-            for (int i = 0; i < kLpLoads; ++i) {
-                w[i] = Vec::nothing();
-                if (at + i * kLanes < v1) w[i] = __ldg(xv + at + i * kLanes);
-            }
-        };
-        int at = v0 + tid;
-        if (nb > 0) fetch(at);
+        bool far = false;                                 // (of the warp) see below
 #pragma unroll 1
-        for (int b = 0; b < nb; ++b) {
+        for (int b = 0; b < nb; ++b, ++sums) {
+            if (tid == 0) issue();
+            __syncwarp();
+            const uint32_t st = sums % kLpStages;
+            lp_wait(&full[st], (sums / kLpStages) & 1, abort);     // (given up: the sums are not used)
+            const int left = v1 - v0 - b * kBatch;
             uint4 g[kLpLoads];
 #pragma unroll
-            for (int i = 0; i < kLpLoads; ++i) g[i] = w[i];
-            at += kBatch;
-            if (b + 1 < nb) fetch(at);    // the next batch while this one is summed
-            float bm, bl;
-            Vec::bounds(g, &bm, &bl);
+            for (int i = 0; i < kLpLoads; ++i) g[i] = data[st * kBatch + i * kLanes + tid];
+            if (left < kBatch) {                          // past the slice's end -inf, which adds nothing
+#pragma unroll
+                for (int i = 0; i < kLpLoads; ++i)
+                    if (i * kLanes + tid >= left) g[i] = Vec::nothing();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[st]);
+            const float bm = Vec::largest(g);
             if (bm > a.m) a.rebase(bm);
             slot_max = fmaxf(slot_max, bm);
             const float2 c2 = make_float2(kLog2e, kLog2e);
-            float2 z2 = make_float2(0.f, 0.f), s2 = make_float2(0.f, 0.f);
-            // Far below the maximum (banned logits, or past the slice's end) differences are held; with
-            // -inf only there is no reference.  (NaN takes either way and stays.)
-            const bool far = !(bl - a.m > kLpFar);
-            const float nm = a.m == -INFINITY ? 0.f : -a.m;
+            const float nm = a.m == -INFINITY ? 0.f : -a.m;      // -inf only so far: no reference
             const float2 nm2 = make_float2(nm, nm);
+            float2 z2 = make_float2(0.f, 0.f), s2 = make_float2(0.f, 0.f);
+            if (!far) {
 #pragma unroll
-            for (int i = 0; i < kLpLoads; ++i) {
-                float f[VN];
-                Vec::unpack(g[i], f);
+                for (int i = 0; i < kLpLoads; ++i) {
+                    float f[VN];
+                    Vec::unpack(g[i], f);
 #pragma unroll
-                for (int e = 0; e < VN; e += 2) {
-                    float2 d = fadd2(make_float2(f[e], f[e + 1]), nm2);
-                    if (far) d = make_float2(max_nan(d.x, kLpFar), max_nan(d.y, kLpFar));
-                    const float2 t = fmul2(d, c2);
-                    const float2 q = make_float2(ex2(t.x), ex2(t.y));
-                    z2 = fadd2(z2, q);
-                    s2 = ffma2(q, t, s2);
+                    for (int e = 0; e < VN; e += 2) {
+                        const float2 t = fmul2(fadd2(make_float2(f[e], f[e + 1]), nm2), c2);
+                        const float2 q = make_float2(ex2(t.x), ex2(t.y));
+                        z2 = fadd2(z2, q);
+                        s2 = ffma2(q, t, s2);
+                    }
+                }
+                // NaN: 0 * inf of a logit far below the maximum (banned, or past the end), or a NaN logit.
+                // Then this batch, and the row's others at once, with the differences held.
+                far = __any_sync(0xffffffffu, s2.x + s2.y != s2.x + s2.y);
+            }
+            if (far) {
+                z2 = s2 = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int i = 0; i < kLpLoads; ++i) {
+                    float f[VN];
+                    Vec::unpack(g[i], f);
+#pragma unroll
+                    for (int e = 0; e < VN; e += 2) {
+                        float2 d = fadd2(make_float2(f[e], f[e + 1]), nm2);
+                        d = make_float2(max_nan(d.x, kLpFar), max_nan(d.y, kLpFar));
+                        const float2 t = fmul2(d, c2);
+                        const float2 q = make_float2(ex2(t.x), ex2(t.y));
+                        z2 = fadd2(z2, q);
+                        s2 = ffma2(q, t, s2);
+                    }
                 }
             }
             a.z += z2.x + z2.y;
             a.s += s2.x + s2.y;
             if (++in_slot == per_slot || b == nb - 1) {
-                sh.slot[warp][slot++][lane] = slot_value(slot_max);
+                slots[slot++] = slot_value(slot_max);
                 best = fmaxf(best, slot_max);
                 slot_max = -INFINITY;
                 in_slot = 0;
@@ -303,17 +426,10 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LpParams 
         }
 
         // ---- the warp's sums and lane maxima, the team's, the row's
-        uint32_t mine = order_key(best);
-        if (p.K > 0 && W > 1) {
-#pragma unroll 1
-            for (int i = 0; i < 32 / W; ++i) {
-                const uint32_t top = __reduce_max_sync(0xffffffffu, mine);
-                const unsigned who = __ballot_sync(0xffffffffu, mine == top);
-                if (lane == __ffs(who) - 1) {
-                    sh.top[team * W][tw * (32 / W) + i] = top;
-                    mine = 0;
-                }
-            }
+        uint32_t mine = 0;
+        if (p.K > 0) {
+            mine = sort_desc(order_key(best), lane);
+            if (lane < 32 / W) sh.top[team * W][tw * (32 / W) + lane] = mine;
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
@@ -322,56 +438,42 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LpParams 
             a.join(om, oz, os);
         }
         LpPart A{a.m, a.z, a.s, -INFINITY};
-        auto kth = [&](uint32_t k) {      // the K-th largest of the warp's 32 keys
-            int rank = 0;
-#pragma unroll 8
-            for (int i = 0; i < 32; ++i) {
-                const uint32_t u = __shfl_sync(0xffffffffu, k, i);
-                rank += u > k || (u == k && i < lane) ? 1 : 0;
-            }
-            const unsigned who = __ballot_sync(0xffffffffu, rank == p.K - 1);
-            return order_value(__shfl_sync(0xffffffffu, k, __ffs(who) - 1));
-        };
-        if constexpr (W == 1) {
-            if (p.K > 0) A.bound = kth(mine);
-        } else {
-            if (lane == 0) sh.warp[warp] = A;
-            team_sync();
-            if (tw == 0) {
-                const LpPart q = sh.warp[team * W + (lane & (W - 1))];
-                Running u;
-                u.m = q.m; u.z = q.z; u.s = q.s;
+        if (lane == 0) sh.warp[warp] = A;
+        team_sync();
+        if (tw == 0) {
+            const LpPart q = sh.warp[team * W + (lane & (W - 1))];
+            Running u;
+            u.m = q.m; u.z = q.z; u.s = q.s;
 #pragma unroll
-                for (int o = W / 2; o > 0; o >>= 1) {
-                    const float om = __shfl_xor_sync(0xffffffffu, u.m, o), oz = __shfl_xor_sync(0xffffffffu, u.z, o),
-                                os = __shfl_xor_sync(0xffffffffu, u.s, o);
-                    u.join(om, oz, os);
-                }
-                const float bd = p.K > 0 ? kth(sh.top[team * W][lane]) : -INFINITY;
-                if (lane == 0) {
-                    const LpPart part{u.m, u.z, u.s, bd};
-                    if (C > 1) lead->part[c] = part;
-                    else sh.all[team] = part;
-                }
+            for (int o = W / 2; o > 0; o >>= 1) {
+                const float om = __shfl_xor_sync(0xffffffffu, u.m, o), oz = __shfl_xor_sync(0xffffffffu, u.z, o),
+                            os = __shfl_xor_sync(0xffffffffu, u.s, o);
+                u.join(om, oz, os);
             }
-            if (C > 1) {
-                cluster.sync();
-                if (warp == 0) {
-                    // every CTA joins all slices' sums in the same order
-                    const LpPart q = lane < C ? lead->part[lane] : LpPart{-INFINITY, 0.f, 0.f, -INFINITY};
-                    Running u;
-                    float bd = -INFINITY;
-                    for (int i = 0; i < C; ++i) {
-                        u.join(__shfl_sync(0xffffffffu, q.m, i), __shfl_sync(0xffffffffu, q.z, i),
-                               __shfl_sync(0xffffffffu, q.s, i));
-                        bd = fmaxf(bd, __shfl_sync(0xffffffffu, q.bound, i));
-                    }
-                    if (lane == 0) sh.all[0] = LpPart{u.m, u.z, u.s, bd};
-                }
-            }
-            team_sync();
-            A = sh.all[team];
+            float bd = -INFINITY;
+            if (p.K > 0)
+                bd = order_value(__shfl_sync(0xffffffffu, sort_desc(sh.top[team * W][lane], lane), p.K - 1));
+            const LpPart part{u.m, u.z, u.s, bd};
+            if (C == 1 && lane == 0) sh.all[team] = part;
+            if (C > 1 && lane < C) cluster.map_shared_rank(&sh, lane)->part[c] = part;
         }
+        if (C > 1) {
+            cluster.sync();
+            if (warp == 0) {
+                // every CTA joins all slices' sums in the same order
+                const LpPart q = lane < C ? sh.part[lane] : LpPart{-INFINITY, 0.f, 0.f, -INFINITY};
+                Running u;
+                float bd = -INFINITY;
+                for (int i = 0; i < C; ++i) {
+                    u.join(__shfl_sync(0xffffffffu, q.m, i), __shfl_sync(0xffffffffu, q.z, i),
+                           __shfl_sync(0xffffffffu, q.s, i));
+                    bd = fmaxf(bd, __shfl_sync(0xffffffffu, q.bound, i));
+                }
+                if (lane == 0) sh.all[0] = LpPart{u.m, u.z, u.s, bd};
+            }
+        }
+        team_sync();
+        A = sh.all[team];
         const bool bad = A.z != A.z;                       // a NaN or +inf in the row
         const float log2z = log2f(A.z);                    // -inf for a row of -inf
         auto logprob = [&](float f) {
@@ -379,8 +481,7 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LpParams 
         };
         if (c == 0 && tid == 0) {
             if (p.tokens && p.logprob) {
-                const int t = p.tokens[row];
-                if (t >= 0 && t < p.V) p.logprob[row] = bad ? NAN : logprob(Vec::load(x + t));
+                if (token >= 0 && token < p.V) p.logprob[row] = bad ? NAN : logprob(token_x);
                 else if (p.dev_status) atomicOr(p.dev_status, BG_DEVSTAT_TOKEN);
             }
             if (p.entropy) p.entropy[row] = A.z == 0.f ? 0.f : (log2z - A.s / A.z) * 0.69314718055994530942f;
@@ -391,34 +492,65 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LpParams 
                 const unsigned who = __ballot_sync(0xffffffffu, in);
                 if (who == 0) return;
                 int pos = 0;
-                if (lane == 0) pos = atomicAdd(&lead->n[team], __popc(who));
+                if (lane == 0) pos = atomicAdd(&sh.n[team], __popc(who));
                 pos = __shfl_sync(0xffffffffu, pos, 0) + __popc(who & ((1u << lane) - 1u));
                 if (in && pos < kCap) list[pos] = pair_key(f, v);
             };
             if (!bad) {
+// bit t: stored maximum t of this lane reaches the bound
+                unsigned mask = 0;
+#pragma unroll
+                for (int i = 0; i < kLpSlots / 8; ++i) {
+                    float f[8];
+                    LpVec<__nv_bfloat16>::unpack(sh.slot[warp][lane][i], f);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) mask |= f[e] >= A.bound ? 1u << (8 * i + e) : 0u;
+                }
+                mask &= (1u << slot) - 1u;
+                // eight such batches at a time, a lane for each of their vectors
+                for (;;) {
+                    const unsigned who = __ballot_sync(0xffffffffu, mask != 0);
+                    if (who == 0) break;
+                    const int nth = __popc(who & ((1u << lane) - 1u));
+                    if (mask != 0 && nth < 8) {
+                        sh.pick[warp][nth] = (__ffs(mask) - 1) << 5 | lane;
+                        mask &= mask - 1;
+                    }
+                    __syncwarp();
+                    const int n = min(__popc(who), 8);
+                    const int pick = lane / kLpLoads < n ? sh.pick[warp][lane / kLpLoads] : -1;
+                    __syncwarp();
 #pragma unroll 1
-                for (int t = 0; t < slot; ++t) {
-                    unsigned who = __ballot_sync(0xffffffffu, __bfloat162float(sh.slot[warp][t][lane]) >= A.bound);
-                    while (who != 0) {
-                        const int owner = __ffs(who) - 1;
-                        who &= who - 1;
-#pragma unroll 1
-                        for (int b = t * per_slot; b < min((t + 1) * per_slot, nb); ++b) {
-                            // element e of the owner's batch: its vector e / VN, place e % VN there
-                            const int vec = v0 + b * kBatch + tw * 32 + owner + (lane / VN) * kLanes;
-                            const int v = head + vec * VN + lane % VN;
-                            const bool there = lane < kLpLoads * VN && vec < v1;
-                            const float f = there ? Vec::load(x + v) : -INFINITY;
-                            put(there && f >= A.bound, f, v);
-                        }
+                    for (int b = 0; b < per_slot; ++b) {
+                        const int vec = v0 + ((pick >> 5) * per_slot + b) * kBatch + tw * 32 + (pick & 31) +
+                                        (lane % kLpLoads) * kLanes;
+                        const bool there = pick >= 0 && vec < v1;
+                        const uint4 w = there ? reinterpret_cast<const uint4 *>(x + head)[vec] : Vec::nothing();
+                        float f[VN];
+                        Vec::unpack(w, f);
+#pragma unroll
+                        for (int e = 0; e < VN; ++e) put(there && f[e] >= A.bound, f[e], head + vec * VN + e);
                     }
                 }
                 if (tw == 0) put(loose >= 0 && loose_x >= A.bound, loose_x, loose);
             }
-            if (C > 1) cluster.sync();
-            else team_sync();
-            if (c == 0 && (tw == 0 || sh.n[team] > kCap)) {
-                const int n = sh.n[team];
+            team_sync();
+            if (C > 1) {
+                // the lists of all CTAs into the first one's stages, which are empty by now
+                LpShared *lead = cluster.map_shared_rank(&sh, 0);
+                const int n = sh.n[0];
+                if (warp == 0) {
+                    int pos = 0;
+                    if (lane == 0) pos = atomicAdd(&lead->n[1], n);
+                    pos = __shfl_sync(0xffffffffu, pos, 0);
+                    unsigned long long *joined = reinterpret_cast<unsigned long long *>(lead->data);
+                    for (int i = lane; i < min(n, kCap) && pos + i < kCap; i += 32) joined[pos + i] = list[i];
+                }
+                cluster.sync();
+                list = reinterpret_cast<unsigned long long *>(sh.data);
+            }
+            const int n = sh.n[C > 1 ? 1 : team];
+            if (c == 0 && (tw == 0 || n > kCap)) {
                 int32_t *tt = p.top_token + row * p.K;
                 float *tl = p.top_logprob + row * p.K;
                 auto store = [&](int i, unsigned long long k) {
@@ -455,17 +587,15 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LpParams 
                             const unsigned long long u = __shfl_xor_sync(0xffffffffu, k, o);
                             k = u > k ? u : k;
                         }
-                        if constexpr (W > 1) {
-                            if (lane == 0) sh.best[warp] = k;
-                            team_sync();
-                            k = sh.best[team * W + (lane & (W - 1))];
+                        if (lane == 0) sh.best[warp] = k;
+                        team_sync();
+                        k = sh.best[team * W + (lane & (W - 1))];
 #pragma unroll
-                            for (int o = W / 2; o > 0; o >>= 1) {
-                                const unsigned long long u = __shfl_xor_sync(0xffffffffu, k, o);
-                                k = u > k ? u : k;
-                            }
-                            team_sync();
+                        for (int o = W / 2; o > 0; o >>= 1) {
+                            const unsigned long long u = __shfl_xor_sync(0xffffffffu, k, o);
+                            k = u > k ? u : k;
                         }
+                        team_sync();
                         found = k;
                         if (tid == 0) store(i, found);
                     }
@@ -473,7 +603,12 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LpParams 
             }
         }
         team_sync();                  // the team's shared memory is written again by its next row
-        if (C > 1) cluster.sync();    // ... also by the other CTAs, and no CTA leaves while it is read
+    }
+    // every copy has landed before the CTA exits
+    if (tid == 0) {
+        for (uint32_t k = loads > kLpStages ? loads - kLpStages : 0; k < loads; ++k)
+            mbar_wait_drain(&full[k % kLpStages], (k / kLpStages) & 1);
+        if (*abort && p.dev_status) atomicOr(p.dev_status, BG_DEVSTAT_TIMEOUT);
     }
 }
 
@@ -484,13 +619,13 @@ cudaError_t launch_lp(const LpParams &p, int nsm, cudaStream_t stream)
     static std::atomic<uint64_t> smem_done{0};
     cudaError_t e = ensure_smem_attribute(kern, static_cast<int>(sizeof(LpShared)), smem_done);
     if (e != cudaSuccess) return e;
-    // with fewer rows than CTAs (2 per SM), clusters of CTAs per row, but at least 16 KB for each
+    // with fewer rows than SMs, clusters of CTAs per row, but at least 16 KB for each
     int C = 1;
     if (W == kLpWarps)
         while (C < kLpMaxCluster && static_cast<int64_t>(p.N) * C * 2 <= 2 * nsm &&
                static_cast<int64_t>(p.V) * sizeof(T) >= (static_cast<int64_t>(C) << 15))
             C *= 2;
-    const int64_t most = 2 * nsm / C, need = (p.N + kLpWarps / W - 1) / (kLpWarps / W);
+    const int64_t most = 2 * nsm / C, need = p.N;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>((need < most ? need : most) * C));
     cfg.blockDim = dim3(kLpThreads);
@@ -508,16 +643,14 @@ cudaError_t launch_lp(const LpParams &p, int nsm, cudaStream_t stream)
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-// Warps per row: as few as keep 32 warps per SM busy, and none without a vector for each lane.
+// Up to two rows per SM the whole CTA takes one row (304 rows of 50,001 fp32 logits: 16.1 us, and 23.0
+// with 4 warps per row), from then on 4 warps do, eight rows at a time per SM (480 rows: 27.4 and
+// 25.8 us; 1200 rows: 52.8 and 41.4).  Rows under 16 KB are too short for 16 warps.
 template <typename T>
 cudaError_t launch_team(const LpParams &p, int nsm, cudaStream_t stream)
 {
-    const int64_t nv = static_cast<int64_t>(p.V) * sizeof(T) / 16;
-    int W = 1;
-    while (W < kLpWarps && static_cast<int64_t>(p.N) * W < 32 * nsm && nv >= 64 * W) W *= 2;
-    if (W == 16) return launch_lp<T, 16>(p, nsm, stream);
-    if (W >= 4) return launch_lp<T, 4>(p, nsm, stream);
-    return launch_lp<T, 1>(p, nsm, stream);
+    return p.N <= 2 * nsm && static_cast<int64_t>(p.V) * sizeof(T) >= 16384 ? launch_lp<T, 16>(p, nsm, stream)
+                                                                          : launch_lp<T, 4>(p, nsm, stream);
 }
 
 }  // namespace
