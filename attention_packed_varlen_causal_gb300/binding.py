@@ -11,6 +11,7 @@ ctypes functions themselves for callers that manage pointers directly.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -321,23 +322,23 @@ def bg_beam_select(logits, cum, token_out, parent_out, score_out, *, workspace=N
     return token_out, parent_out, score_out
 
 
-def _expect(fn: str, device, **tensors):
-    """Each of ``tensors`` is (tensor or None, dtype name, shape): a contiguous CUDA tensor on ``device``."""
-    for name, (t, dtype, shape) in tensors.items():
-        if t is None:
-            continue
-        if t.device != device or str(t.dtype) != f"torch.{dtype}" or tuple(t.shape) != tuple(shape) or \
-                not t.is_contiguous():
+def _expect(fn: str, device, checks):
+    """Each of ``checks`` is (name, tensor or None, dtype, shape): contiguous, on ``device``."""
+    for name, t, dtype, shape in checks:
+        if t is not None and not (t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous()):
             raise ValueError(f"{fn}: {name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, "
-                             f"got {str(t.dtype)[6:]} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
+                             f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
 
 
-def _on(device, stream):
+def _on(fn: str, device, stream):
     """The context of ``device`` and the stream to use there: the given one, or its current one."""
     import torch
     if device.type != "cuda":
-        raise ValueError(f"CUDA tensors expected, got {device}")
-    return torch.cuda.device(device), _stream(torch.cuda.current_stream(device) if stream is None else stream)
+        raise ValueError(f"{fn}: CUDA tensors expected, got {device}")
+    st = _stream(torch.cuda.current_stream(device) if stream is None else stream)
+    if device.index == torch.cuda.current_device():
+        return contextlib.nullcontext(), st
+    return torch.cuda.device(device), st
 
 
 def bg_shared_attn_workspace_size(num_groups: int, num_seqs: int, total_tokens: int, max_seqlen: int,
@@ -346,16 +347,19 @@ def bg_shared_attn_workspace_size(num_groups: int, num_seqs: int, total_tokens: 
                                                     Hkv, head_dim))
 
 
-def _workspace(fn: str, workspace, need: int, device):
+def _workspace(fn: str, workspace, size, device):
+    """Pointer and bytes of the workspace; ``size`` gives the bytes it needs, for the message."""
     if workspace is None:
-        raise ValueError(f"{fn}: workspace of {need} bytes required (the library never allocates)")
+        raise ValueError(f"{fn}: workspace of {size()} bytes required (the library never allocates)")
     if workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"{fn}: workspace must be contiguous on {device}")
-    return _ptr(workspace), workspace.numel() * workspace.element_size()
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def _shared_run(fn: str, last: bool, q, k, v, cu_seqlens, max_seqlen, prefix_k, prefix_v, cu_prefix, max_prefix_len,
                 cu_group, out, lse, scale, softcap, workspace, dev_status, stream):
+    import torch
+    bf16, i32 = torch.bfloat16, torch.int32
     rows, Hq, d = q.shape
     T, Hkv = k.shape[0], k.shape[1]
     P = 0 if prefix_k is None else prefix_k.shape[0]
@@ -363,17 +367,17 @@ def _shared_run(fn: str, last: bool, q, k, v, cu_seqlens, max_seqlen, prefix_k, 
     dev = q.device
     if (prefix_k is None) != (prefix_v is None):
         raise ValueError(f"{fn}: prefix_k and prefix_v come together")
-    _expect(fn, dev, q=(q, "bfloat16", (S if last else T, Hq, d)), k=(k, "bfloat16", (T, Hkv, d)),
-            v=(v, "bfloat16", (T, Hkv, d)), cu_seqlens=(cu_seqlens, "int32", (S + 1,)),
-            prefix_k=(prefix_k, "bfloat16", (P, Hkv, d)), prefix_v=(prefix_v, "bfloat16", (P, Hkv, d)),
-            cu_prefix=(cu_prefix, "int32", (R + 1,)), cu_group=(cu_group, "int32", (R + 1,)),
-            out=(out, "bfloat16", (rows, Hq, d)), lse=(lse, "float32", (rows, Hq)),
-            dev_status=(dev_status, "int32", () if dev_status is None else dev_status.shape))
-    ws, ws_bytes = _workspace(fn, workspace, bg_shared_attn_workspace_size(R, S, T, int(max_seqlen),
-                                                                           int(max_prefix_len), Hq, Hkv, d), dev)
+    _expect(fn, dev, (("q", q, bf16, (S if last else T, Hq, d)), ("k", k, bf16, (T, Hkv, d)), ("v", v, bf16, (T, Hkv, d)),
+                      ("cu_seqlens", cu_seqlens, i32, (S + 1,)), ("prefix_k", prefix_k, bf16, (P, Hkv, d)),
+                      ("prefix_v", prefix_v, bf16, (P, Hkv, d)), ("cu_prefix", cu_prefix, i32, (R + 1,)),
+                      ("cu_group", cu_group, i32, (R + 1,)), ("out", out, bf16, (rows, Hq, d)),
+                      ("lse", lse, torch.float32, (rows, Hq)),
+                      ("dev_status", dev_status, i32, dev_status.shape if dev_status is not None else ())))
+    ws, ws_bytes = _workspace(fn, workspace, lambda: bg_shared_attn_workspace_size(
+        R, S, T, int(max_seqlen), int(max_prefix_len), Hq, Hkv, d), dev)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    ctx, st = _on(dev, stream)
+    ctx, st = _on(fn, dev, stream)
     with ctx:
         _check(fn, getattr(load(), fn)(
             _ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens), S, T, int(max_seqlen), _ptr(prefix_k), _ptr(prefix_v),
@@ -421,14 +425,16 @@ def bg_shared_last_token_attn_planned(q, k, v, cu_seqlens, max_seqlen: int, pref
 
 def _shared_plan(fn: str, cu_seqlens, total_tokens, max_seqlen, cu_prefix, total_prefix, max_prefix_len, cu_group, Hq,
                  Hkv, head_dim, workspace, dev_status, stream):
+    import torch
+    i32 = torch.int32
     S, R = cu_seqlens.numel() - 1, cu_group.numel() - 1
     dev = cu_seqlens.device
-    _expect(fn, dev, cu_seqlens=(cu_seqlens, "int32", (S + 1,)), cu_prefix=(cu_prefix, "int32", (R + 1,)),
-            cu_group=(cu_group, "int32", (R + 1,)),
-            dev_status=(dev_status, "int32", () if dev_status is None else dev_status.shape))
-    ws, ws_bytes = _workspace(fn, workspace, bg_shared_attn_workspace_size(
+    _expect(fn, dev, (("cu_seqlens", cu_seqlens, i32, (S + 1,)), ("cu_prefix", cu_prefix, i32, (R + 1,)),
+                      ("cu_group", cu_group, i32, (R + 1,)),
+                      ("dev_status", dev_status, i32, dev_status.shape if dev_status is not None else ())))
+    ws, ws_bytes = _workspace(fn, workspace, lambda: bg_shared_attn_workspace_size(
         R, S, int(total_tokens), int(max_seqlen), int(max_prefix_len), Hq, Hkv, head_dim), dev)
-    ctx, st = _on(dev, stream)
+    ctx, st = _on(fn, dev, stream)
     with ctx:
         _check(fn, getattr(load(), fn)(_ptr(cu_seqlens), S, int(total_tokens), int(max_seqlen), _ptr(cu_prefix),
                                        int(total_prefix), int(max_prefix_len), _ptr(cu_group), R, Hq, Hkv, head_dim,
@@ -456,19 +462,20 @@ def bg_token_logprobs(logits, tokens=None, *, logprob=None, entropy=None, top_to
     """logits fp32 or bf16 [N,V] (rows may be strided, columns not); tokens int32 [N] or None;
     written: logprob fp32 [N] (with tokens), entropy fp32 [N] or None, top_token int32 [N,K] and
     top_logprob fp32 [N,K] or both None."""
+    import torch
     fn = "bg_token_logprobs"
     N, V = logits.shape
-    dtype = {"torch.float32": BG_DTYPE_F32, "torch.bfloat16": BG_DTYPE_BF16}.get(str(logits.dtype))
+    dtype = {torch.float32: BG_DTYPE_F32, torch.bfloat16: BG_DTYPE_BF16}.get(logits.dtype)
     if dtype is None or (V > 1 and N > 0 and logits.stride(1) != 1):
         raise ValueError(f"{fn}: logits must be float32 or bfloat16 with contiguous rows, got {logits.dtype} with "
                          f"strides {logits.stride()}")
     dev = logits.device
     K = 0 if top_token is None else top_token.shape[-1]
-    _expect(fn, dev, tokens=(tokens, "int32", (N,)), logprob=(logprob, "float32", (N,)),
-            entropy=(entropy, "float32", (N,)), top_token=(top_token, "int32", (N, K)),
-            top_logprob=(top_logprob, "float32", (N, K)),
-            dev_status=(dev_status, "int32", () if dev_status is None else dev_status.shape))
-    ctx, st = _on(dev, stream)
+    f32, i32 = torch.float32, torch.int32
+    _expect(fn, dev, (("tokens", tokens, i32, (N,)), ("logprob", logprob, f32, (N,)), ("entropy", entropy, f32, (N,)),
+                      ("top_token", top_token, i32, (N, K)), ("top_logprob", top_logprob, f32, (N, K)),
+                      ("dev_status", dev_status, i32, dev_status.shape if dev_status is not None else ())))
+    ctx, st = _on(fn, dev, stream)
     with ctx:
         _check(fn, load().bg_token_logprobs(_ptr(logits), dtype, logits.stride(0) if N > 1 else max(V, 1), N, V,
                                             _ptr(tokens), K, _ptr(logprob), _ptr(entropy), _ptr(top_token),

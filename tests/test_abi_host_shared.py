@@ -81,8 +81,8 @@ def test_no_queries_is_a_noop(lib):
 def test_workspace_size():
     size = bg.bg_shared_attn_workspace_size
     assert size(32, 480, 27000, 96, 500, 16, 8, 128) % 256 == 0
-    # short key ranges are never split, long ones bring room for partial results
-    assert size(1, 15, 300, 20, 400, 16, 8, 128) < 200_000 < size(1, 15, 300, 20, 4096, 16, 8, 128)
+    # key ranges of a few tiles are never split, longer ones bring room for partial results
+    assert size(1, 4, 40, 20, 100, 16, 8, 128) < 50_000 < 1_000_000 < size(1, 4, 40, 20, 4096, 16, 8, 128)
     assert size(4, 128, 26000, 400, 32768, 32, 8, 128) < 64 << 20
     for bad in ((-1, 5, 5, 5, 5, 4, 2, 64), (1, 5, 5, 5, 5, 5, 2, 64), (1, 5, 5, 5, 5, 4, 2, 80),
                 (1, 5, 5, 70000, 5, 4, 2, 64), (0, 5, 5, 5, 5, 4, 2, 64)):
