@@ -14,7 +14,7 @@ namespace bg {
 constexpr int kShKeys = 128;          // keys per K/V tile
 constexpr int kShRows = 128;          // query rows (token, head) per tile = TMEM lanes
 constexpr int kShTiles = 2;           // query tiles per work item
-constexpr int kShMaxCtas = 256;       // CTAs of the attention kernel at most (one per SM)
+constexpr int kShMaxCtas = 160;       // CTAs of the attention kernel at most (one per SM: GB300 has 152)
 constexpr int kShSplitMin = 4;        // cost units per CTA below which fewer CTAs share the work
 
 // One work entry: kShTiles tiles of query rows of one request against its keys; an entry for one
