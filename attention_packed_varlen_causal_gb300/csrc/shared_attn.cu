@@ -672,108 +672,123 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
                         ph ^= 1u;
                     }
                 };
-                uint32_t q_uses[kShTiles] = {0, 0}, tiles[kShTiles] = {0, 0};
-                // the tile whose P.V comes next: its V stage, and per query tile its 16-key steps (0: none)
-                // and whether it is the first or last of the item
-                bool have = false;
+                // Per query tile h, in byte h: the 16-key steps of a tile (0: no keys; S then has 16 * steps
+                // columns).  Bit h of the others.
+                uint32_t prev = 0;               // steps of the tile whose P.V come next, with V from stage vs
                 uint32_t vs = 0, vph = 0;
-                int steps[kShTiles] = {0, 0};
-                bool first[kShTiles] = {}, last[kShTiles] = {};
+                uint32_t fresh = 0;              // the item's first P.V is still to come
+                uint32_t outs = 0;               // query tiles whose output the previous item completes
+                uint32_t p_par = 0, q_par = 0;   // parities of p_full and q_full
                 bool ok = true;
-                auto pv = [&](int h) {
-                    if (!ok || steps[h] == 0) return;
-                    const uint64_t dv = dv0 + static_cast<uint64_t>((vs * C::kTileBytes) >> 4);
+                // P.V of the previous tile, then QK of this one with K from stage ks.
+                auto turn = [&](int h, uint32_t cur, uint32_t ks) {
+                    const int sp = (prev >> (8 * h)) & 0xff, sc = (cur >> (8 * h)) & 0xff;
                     const uint32_t a = tS + kShKeys * h, d = tO + D * h;
-                    ok = mbar_wait(&p_full[2 * h], tiles[h] & 1, abort_flag);
-                    if (!ok) return;
-                    tc_fence_after();
-                    if (steps[h] >= 4) {
-                        sh_mma_pv4(d, a, dv, kIdescPV, first[h] ? 0u : 1u);
-                    } else {
-#pragma unroll 1
-                        for (int k = 0; k < steps[h]; ++k)
-                            mma_ts(d, a + 8 * k, dv + static_cast<uint64_t>(128 * k), kIdescPV, (!first[h] || k > 0) ? 1u : 0u);
-                    }
-                    ok = mbar_wait(&p_full[2 * h + 1], tiles[h] & 1, abort_flag);
-                    if (!ok) return;
-                    tc_fence_after();
-                    if (steps[h] == 8) {
-                        sh_mma_pv4(d, a + 32, dv + 512, kIdescPV, 1u);
-                    } else {
-#pragma unroll 1
-                        for (int k = 4; k < steps[h]; ++k)
-                            mma_ts(d, a + 8 * k, dv + static_cast<uint64_t>(128 * k), kIdescPV, 1u);
-                    }
-                    if (last[h]) mma_commit(&o_full[h]);
-                    ++tiles[h];
-                };
-                for (uint32_t it = 0; ok; ++it) {
-                    const uint32_t slot = it % kShRing;
-                    if (!mbar_wait(&item_full[slot], (it / kShRing) & 1, abort_flag) || !ring[slot].more) break;
-                    const ShItem &I = ring[slot];
-                    const int tb = I.tb, te = I.te;
-                    const int act[kShTiles] = {I.act[0], I.act[1]};
-                    int done[kShTiles] = {0, 0};
-                    for (int j = tb; j < te && ok; ++j) {
-                        const uint32_t ks = st, kph = ph;
-                        bump();
-                        int nsteps[kShTiles];
-                        bool nfirst[kShTiles], nlast[kShTiles];
-#pragma unroll
-                        for (int h = 0; h < kShTiles; ++h) {
-                            const int nk = act[h] > 0 ? I.keys_of(h, j) : 0;
-                            nsteps[h] = nk > 0 ? (nk + 15) >> 4 : 0;      // S then has 16 * steps columns
-                            nfirst[h] = done[h] == 0;
-                            if (nk > 0) ++done[h];
-                            nlast[h] = done[h] == act[h];
-                        }
-                        if (have && !mbar_wait(&kv_full[vs], vph, abort_flag)) { ok = false; break; }
-                        if (!mbar_wait(&kv_full[ks], kph, abort_flag)) { ok = false; break; }
-                        // S overwrites the P of the previous tile, which the P.V issued before it reads:
-                        // tcgen05.mma operations of one thread execute in issue order.
-                        const uint64_t dk = dk0 + static_cast<uint64_t>((ks * C::kTileBytes) >> 4);
-                        auto qk = [&](int h) {
-                            if (!ok || nsteps[h] == 0) return;
-                            if (nfirst[h]) {
-                                ok = mbar_wait(&q_full[h], q_uses[h] & 1, abort_flag);
-                                if (!ok) return;
-                                ++q_uses[h];
-                            }
-                            tc_fence_after();
-                            sh_mma_qk<C::kNB>(tS + kShKeys * h, dq + static_cast<uint64_t>((h * C::kTileBytes) >> 4), dk,
-                                              kIdescQK0 | (static_cast<uint32_t>(2 * nsteps[h]) << 17), &s_full[h]);
-                            if (nlast[h]) mma_commit(&q_empty[h]);
-                        };
-                        // Behind an item's last tile its P.V do not wait for the next item's Q.
-                        pv(0);
-                        if (j > tb) qk(0);
-                        pv(1);
-                        if (j > tb) {
-                            qk(1);
+                    if (sp > 0) {
+                        const uint64_t dv = dv0 + static_cast<uint64_t>((vs * C::kTileBytes) >> 4);
+                        const uint32_t par = (p_par >> h) & 1u;
+                        uint32_t acc = ((fresh >> h) & 1u) ^ 1u;
+                        p_par ^= 1u << h;
+                        fresh &= ~(1u << h);
+                        if (!mbar_wait(&p_full[2 * h], par, abort_flag)) return false;
+                        tc_fence_after();
+                        if (sp >= 4) {
+                            sh_mma_pv4(d, a, dv, kIdescPV, acc);
                         } else {
-                            qk(0);
-                            qk(1);
+#pragma unroll 1
+                            for (int k = 0; k < sp; ++k, acc = 1u)
+                                mma_ts(d, a + 8 * k, dv + static_cast<uint64_t>(128 * k), kIdescPV, acc);
                         }
+                        if (!mbar_wait(&p_full[2 * h + 1], par, abort_flag)) return false;
+                        tc_fence_after();
+                        if (sp == 8) {
+                            sh_mma_pv4(d, a + 32, dv + 512, kIdescPV, 1u);
+                        } else {
+#pragma unroll 1
+                            for (int k = 4; k < sp; ++k)
+                                mma_ts(d, a + 8 * k, dv + static_cast<uint64_t>(128 * k), kIdescPV, 1u);
+                        }
+                    }
+                    // S overwrites the P that the P.V just issued reads: tcgen05.mma operations of one
+                    // thread execute in issue order.
+                    if (sc > 0)
+                        sh_mma_qk<C::kNB>(a, dq + static_cast<uint64_t>((h * C::kTileBytes) >> 4),
+                                          dk0 + static_cast<uint64_t>((ks * C::kTileBytes) >> 4),
+                                          kIdescQK0 | (static_cast<uint32_t>(2 * sc) << 17), &s_full[h]);
+                    return true;
+                };
+                // the P.V of an item's last tile
+                auto finish = [&]() {
+                    if (outs == 0) return true;
+                    if (!mbar_wait(&kv_full[vs], vph, abort_flag)) return false;
+#pragma unroll 1
+                    for (int h = 0; h < kShTiles; ++h) {
+                        if (!turn(h, 0, 0)) return false;
+                        if ((outs >> h) & 1u) mma_commit(&o_full[h]);
+                    }
+                    mma_commit(&kv_empty[vs]);
+                    return true;
+                };
+                for (uint32_t it = 0;; ++it) {
+                    const uint32_t slot = it % kShRing;
+                    if (!mbar_wait(&item_full[slot], (it / kShRing) & 1, abort_flag)) { ok = false; break; }
+                    const ShItem &I = ring[slot];
+                    if (!I.more) break;
+                    const int tb = I.tb, te = I.te, whole_end = I.plen / kShKeys;
+                    const uint32_t have = (I.act[0] > 0 ? 1u : 0u) | (I.act[1] > 0 ? 2u : 0u);
+                    auto steps_of = [&](int j) {
+                        if (j < whole_end) return ((have & 1u) ? 8u : 0u) | ((have & 2u) ? 8u << 8 : 0u);
+                        uint32_t r = 0;
+#pragma unroll 1
+                        for (int h = 0; h < kShTiles; ++h)
+                            if ((have >> h) & 1u) r |= static_cast<uint32_t>((max(I.keys_of(h, j), 0) + 15) >> 4) << (8 * h);
+                        return r;
+                    };
+                    uint32_t cur = steps_of(tb);
+                    uint32_t ks = st;
+                    // ---- the first tile: behind the previous item's last P.V, which do not wait for this Q
+                    ok = finish() && mbar_wait(&kv_full[ks], ph, abort_flag);
+                    prev = 0;
+                    fresh = 3u;
+                    outs = have;
+#pragma unroll 1
+                    for (int h = 0; h < kShTiles && ok; ++h) {
+                        if (!((have >> h) & 1u)) continue;
+                        ok = mbar_wait(&q_full[h], (q_par >> h) & 1u, abort_flag);
+                        q_par ^= 1u << h;
+                        if (ok) {
+                            tc_fence_after();
+                            turn(h, cur, ks);
+                        }
+                    }
+                    if (!ok) break;
+                    mma_commit(&kv_empty[ks]);
+                    bump();
+                    vs = st;
+                    vph = ph;
+                    bump();
+                    prev = cur;
+                    // ---- the others
+                    for (int j = tb + 1; j < te; ++j) {
+                        cur = steps_of(j);
+                        ks = st;
+                        ok = mbar_wait(&kv_full[vs], vph, abort_flag) && mbar_wait(&kv_full[ks], ph, abort_flag) &&
+                             turn(0, cur, ks) && turn(1, cur, ks);
                         if (!ok) break;
-                        if (have) mma_commit(&kv_empty[vs]);
+                        mma_commit(&kv_empty[vs]);
                         mma_commit(&kv_empty[ks]);
-                        have = true;
+                        bump();
                         vs = st;
                         vph = ph;
                         bump();
-#pragma unroll
-                        for (int h = 0; h < kShTiles; ++h) {
-                            steps[h] = nsteps[h];
-                            first[h] = nfirst[h];
-                            last[h] = nlast[h];
-                        }
+                        prev = cur;
                     }
+                    if (!ok) break;
+                    if (have & 1u) mma_commit(&q_empty[0]);
+                    if (have & 2u) mma_commit(&q_empty[1]);
                     mbar_arrive(&item_empty[slot]);
                 }
-                if (ok && have && mbar_wait(&kv_full[vs], vph, abort_flag)) {
-                    pv(0);
-                    pv(1);
-                }
+                if (ok) finish();
                 mma_commit(mma_final);           // every MMA issued completes before TMEM is released
                 mbar_wait_drain(mma_final, 0);
             }
