@@ -647,7 +647,7 @@ bg_status_t shared_impl(const ShProblem &pb, const void *q, const void *k, const
     if (!std::isfinite(scale) || !(scale > 0.f) || !std::isfinite(softcap) || softcap < 0.f) return BG_ERR_INVALID_ARG;
     // scale / cap and cap * log2(e) have to be ordinary numbers
     const bool capped = softcap > 0.f;
-    if (capped && (!std::isnormal(scale / softcap) || !std::isnormal(softcap * 1.4426950408889634f)))
+    if (capped && (!std::isnormal(3.f * (scale / softcap)) || !std::isnormal(softcap * 1.4426950408889634f)))
         return BG_ERR_INVALID_ARG;
     bg_status_t st = shared_check_sizes(pb);
     if (st != BG_OK || shared_is_noop(pb)) return st;
@@ -709,7 +709,7 @@ bg_status_t shared_impl(const ShProblem &pb, const void *q, const void *k, const
     p.last = pb.last;
     p.num_seqs = pb.num_seqs;
     p.scale_log2 = scale * 1.4426950408889634f;
-    p.cap_in = capped ? scale / softcap : 0.f;
+    p.cap_in = capped ? 2.f * 1.4426950408889634f * (scale / softcap) : 0.f;
     p.cap_log2 = softcap * 1.4426950408889634f;
     p.out = static_cast<__nv_bfloat16 *>(out);
     p.lse = lse;

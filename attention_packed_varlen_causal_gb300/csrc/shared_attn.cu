@@ -440,12 +440,25 @@ __device__ __forceinline__ void st_out_32b(void *dst, const uint32_t *w, bool wi
     }
 }
 
-// cap * log2(e) * tanh(y) for y = score * scale / cap, from e^(-2|y|).
-__device__ __forceinline__ float capped(float s, float cap_in, float cap_log2)
+__device__ __forceinline__ float min_nan(float a, float b)
 {
-    const float y = s * cap_in;
-    const float t = ex2(-2.f * 1.44269504088896f * fabsf(y));
-    return copysignf(cap_log2 * __fdividef(1.f - t, 1.f + t), y);
+    float d;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+// cap * log2(e) * tanh(y) = cap_log2 - 2 cap_log2 / (1 + e^(2y)) for two scores s, y = s * scale / cap
+// (cap_in = 2 log2(e) scale / cap).  One reciprocal serves both, since the special-function unit is
+// what bounds capped scores: 1 / a = b * (1 / ab).  The exponent is held below 2^60, where tanh is 1
+// to the last bit, so that ab stays finite; NaN stays, and reaches both.  Next to 0 the difference
+// leaves an error of about 2^-23 of the cap.
+__device__ __forceinline__ void capped_pair(float &s0, float &s1, float cap_in, float cap_log2)
+{
+    const float a = ex2(min_nan(s0 * cap_in, 60.f)) + 1.f, b = ex2(min_nan(s1 * cap_in, 60.f)) + 1.f;
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a * b));
+    r *= -2.f * cap_log2;
+    s0 = fmaf(r, b, cap_log2);
+    s1 = fmaf(r, a, cap_log2);
 }
 
 template <int D, bool CAP>
@@ -918,25 +931,33 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
 #pragma unroll
                         for (int i = 64; i < 128; ++i) s[i] = -INFINITY;
                     }
-                    if constexpr (CAP) {
+                    uint32_t keep[4];                      // bit i of keep[c]: column 32 c + i is in [c0, c1)
+                    if (masked) {
 #pragma unroll
-                        for (int i = 0; i < 64; ++i) s[i] = capped(s[i], p.cap_in, p.cap_log2);
+                        for (int c = 0; c < 4; ++c) {
+                            const int a = min(max(c0 - 32 * c, 0), 32), b = min(max(c1 - 32 * c, 0), 32);
+                            const uint32_t below_b = b == 32 ? ~0u : (1u << b) - 1u;
+                            keep[c] = a == 32 ? 0u : below_b & ~((1u << a) - 1u);
+                        }
+                    }
+                    if constexpr (CAP) {
+                        // a masked score may be NaN, and is not to reach its neighbour
+                        if (masked) {
+#pragma unroll
+                            for (int i = 0; i < kShKeys; ++i)
+                                if (!((keep[i >> 5] >> (i & 31)) & 1u)) s[i] = 0.f;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 64; i += 2) capped_pair(s[i], s[i + 1], p.cap_in, p.cap_log2);
                         if (two) {
 #pragma unroll
-                            for (int i = 64; i < 128; ++i) s[i] = capped(s[i], p.cap_in, p.cap_log2);
+                            for (int i = 64; i < 128; i += 2) capped_pair(s[i], s[i + 1], p.cap_in, p.cap_log2);
                         }
                     }
                     if (masked) {
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            // bit i: column 32 c + i is in [c0, c1)
-                            const int a = min(max(c0 - 32 * c, 0), 32), b = min(max(c1 - 32 * c, 0), 32);
-                            const uint32_t below_b = b == 32 ? ~0u : (1u << b) - 1u;
-                            const uint32_t keep = a == 32 ? 0u : below_b & ~((1u << a) - 1u);
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (!((keep >> i) & 1u)) s[32 * c + i] = -INFINITY;
-                        }
+                        for (int i = 0; i < kShKeys; ++i)
+                            if (!((keep[i >> 5] >> (i & 31)) & 1u)) s[i] = -INFINITY;
                     }
                     float mq[8];
 #pragma unroll

@@ -70,7 +70,7 @@ struct ShParams {
     int32_t Hq, Hkv, g, bt;   // bt = rows of g heads per query tile
     int32_t last, num_seqs;
     float scale_log2;         // plain scores: softmax scale * log2(e)
-    float cap_in, cap_log2;   // capped scores: scale / cap, and cap * log2(e)
+    float cap_in, cap_log2;   // capped scores: 2 log2(e) scale / cap, and cap * log2(e)
     __nv_bfloat16 *out;
     float *lse;
     int32_t *dev_status;
