@@ -446,22 +446,54 @@ __device__ __forceinline__ float min_nan(float a, float b)
     asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
     return d;
 }
-// cap * log2(e) * tanh(y) = cap_log2 - 2 cap_log2 / (1 + e^(2y)) for two scores s, y = s * scale / cap
-// (cap_in = 2 log2(e) scale / cap).  One reciprocal serves both, since the special-function unit is
-// what bounds capped scores: 1 / a = b * (1 / ab).  The exponent is held below 2^60, where tanh is 1
-// to the last bit, so that ab stays finite; NaN stays, and reaches both.  Next to 0 the difference
-// leaves an error of about 2^-23 of the cap.
-__device__ __forceinline__ void capped_pair(float &s0, float &s1, float cap_in, float cap_log2)
+// Four scores s to cap_log2 * tanh(y) = cap_log2 - 2 cap_log2 / (1 + e^(2y)), y = s * scale / cap
+// (cap_in = 2 log2(e) scale / cap).  One reciprocal serves all four, since the special-function unit
+// is what bounds capped scores (16 reciprocals and 32 exponentials per cycle and SM): 1 / a =
+// b * cd * (1 / abcd).  e^(2y) is held at 2^30, where tanh is 1 to the last bit, so that abcd stays
+// finite; NaN stays, and reaches all four.  Next to 0 the difference leaves an error of about 2^-23
+// of the cap.
+__device__ __forceinline__ void capped4(float *s, float cap_in, float cap_log2)
 {
-    const float a = ex2(min_nan(s0 * cap_in, 60.f)) + 1.f, b = ex2(min_nan(s1 * cap_in, 60.f)) + 1.f;
+    float a[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[i] = ex2(min_nan(s[i] * cap_in, 30.f)) + 1.f;
+    const float ab = a[0] * a[1], cd = a[2] * a[3];
     float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a * b));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ab * cd));
     r *= -2.f * cap_log2;
-    s0 = fmaf(r, b, cap_log2);
-    s1 = fmaf(r, a, cap_log2);
+    const float rcd = r * cd, rab = r * ab;
+    s[0] = fmaf(rcd, a[1], cap_log2);
+    s[1] = fmaf(rcd, a[0], cap_log2);
+    s[2] = fmaf(rab, a[3], cap_log2);
+    s[3] = fmaf(rab, a[2], cap_log2);
 }
 
-template <int D, bool CAP>
+// The same for caps of any size, where that error could be large next to the scores: below |y| = 0.3
+// the series y - y^3 / 3 + 2 y^5 / 15 - 17 y^7 / 315 + 62 y^9 / 2835 (the next term is below 2^-24 of y).
+__device__ __forceinline__ void capped4_any(float *s, float cap_in, float cap_log2)
+{
+    float y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = s[i] * cap_in * 0.34657359027997264f;      // ln(2) / 2
+    capped4(s, cap_in, cap_log2);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float u = y[i] * y[i];
+        float t = fmaf(u, 62.f / 2835.f, -17.f / 315.f);
+        t = fmaf(u, t, 2.f / 15.f);
+        t = fmaf(u, t, -1.f / 3.f);
+        const float small = cap_log2 * fmaf(y[i] * u, t, y[i]);
+        s[i] = fabsf(y[i]) < 0.3f ? small : s[i];
+    }
+}
+
+// How scores become weights: plain; capped, by the same running maximum; or capped by at most
+// kShCapFixed (in base 2), where 2^x of any score and any sum of them is an ordinary fp32 number, so
+// that no maximum is needed and the tile goes from S to P 32 columns at a time.
+enum : int { kShPlain = 0, kShCapped = 1, kShCappedFixed = 2 };
+constexpr float kShCapFixed = 80.f;
+
+template <int D, int MODE>
 __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
     shared_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_pk,
@@ -818,7 +850,7 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
         const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
         const uint32_t tS = tmem + lane_addr + C::kColS + kShKeys * h;
         const uint32_t tO = tmem + lane_addr + C::kColO + D * h;
-        const float sl2 = CAP ? 1.f : p.scale_log2;
+        const float sl2 = MODE == kShPlain ? p.scale_log2 : 1.f;
         const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
         uint32_t n = 0, tiles = 0, outs = 0;               // K and V tiles passed; tiles and outputs of h
         bool ok = true;
@@ -832,7 +864,7 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
             const bool live = lr < p.bt && lr < rows_h;
             const bool warp_live = __any_sync(0xffffffffu, live);
             const int row = I.row0 + h * p.bt + lr;        // packed token, or sample
-            float m = -INFINITY;       // running maximum, base-2 units
+            float m = MODE == kShCappedFixed ? 0.f : -INFINITY;      // running maximum, base-2 units
             float l = 0.f;             // running sum of 2^(x - m)
             float fix = 0.f;           // what rounding the tiles' largest weights to bf16 adds to l
             bool seen = false;         // this row has a key in one of the tiles
@@ -923,6 +955,48 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
                     hand_over(1);
                 } else {
                     const bool two = nk > 64;              // columns 64-127 are used
+                    // bit i: column 32 c + i is in [c0, c1)
+                    auto columns = [&](int c) {
+                        const int a = min(max(c0 - 32 * c, 0), 32), b = min(max(c1 - 32 * c, 0), 32);
+                        const uint32_t below_b = b == 32 ? ~0u : (1u << b) - 1u;
+                        return a == 32 ? 0u : below_b & ~((1u << a) - 1u);
+                    };
+                    if constexpr (MODE == kShCappedFixed) {
+                        float2 rs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c) {
+                            if (c < 2 || two) {
+                                float x[32];
+                                uint32_t pk[16];
+                                const uint32_t keep = masked ? columns(c) : ~0u;
+                                tmem_ld32(tS + 32 * c, x);
+                                if (masked) {              // may be NaN, which is not to reach its neighbours
+#pragma unroll
+                                    for (int i = 0; i < 32; ++i)
+                                        if (!((keep >> i) & 1u)) x[i] = 0.f;
+                                }
+#pragma unroll
+                                for (int i = 0; i < 32; i += 4) {
+                                    capped4(x + i, p.cap_in, p.cap_log2);
+#pragma unroll
+                                    for (int k = i; k < i + 4; ++k) x[k] = ex2(x[k]);
+                                }
+                                if (masked) {
+#pragma unroll
+                                    for (int i = 0; i < 32; ++i)
+                                        if (!((keep >> i) & 1u)) x[i] = 0.f;
+                                }
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) {
+                                    rs[i & 1] = fadd2(rs[i & 1], make_float2(x[2 * i], x[2 * i + 1]));
+                                    pk[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+                                }
+                                tmem_st16(tS + 16 * c, pk);      // over scores that have been read
+                            }
+                            if (c & 1) hand_over(c >> 1);
+                        }
+                        l += (rs[0].x + rs[1].x) + (rs[0].y + rs[1].y);
+                    } else {
                     float s[kShKeys];
                     tmem_ld64(tS, s);
                     if (two) {
@@ -931,33 +1005,26 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
 #pragma unroll
                         for (int i = 64; i < 128; ++i) s[i] = -INFINITY;
                     }
-                    uint32_t keep[4];                      // bit i of keep[c]: column 32 c + i is in [c0, c1)
-                    if (masked) {
+                    if constexpr (MODE == kShCapped) {
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
-                            const int a = min(max(c0 - 32 * c, 0), 32), b = min(max(c1 - 32 * c, 0), 32);
-                            const uint32_t below_b = b == 32 ? ~0u : (1u << b) - 1u;
-                            keep[c] = a == 32 ? 0u : below_b & ~((1u << a) - 1u);
+                            // a masked score may be NaN, and is not to reach its neighbours
+                            const uint32_t keep = masked ? columns(c) : ~0u;
+#pragma unroll
+                            for (int i = 32 * c; i < 32 * c + 32; ++i)
+                                if (!((keep >> (i & 31)) & 1u)) s[i] = 0.f;
+#pragma unroll
+                            for (int i = 32 * c; i < 32 * c + 32; i += 4) capped4_any(s + i, p.cap_in, p.cap_log2);
                         }
                     }
-                    if constexpr (CAP) {
-                        // a masked score may be NaN, and is not to reach its neighbour
-                        if (masked) {
+                    if (masked || (MODE == kShCapped && !two)) {
 #pragma unroll
-                            for (int i = 0; i < kShKeys; ++i)
-                                if (!((keep[i >> 5] >> (i & 31)) & 1u)) s[i] = 0.f;
+                        for (int c = 0; c < 4; ++c) {
+                            const uint32_t keep = columns(c);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (!((keep >> i) & 1u)) s[32 * c + i] = -INFINITY;
                         }
-#pragma unroll
-                        for (int i = 0; i < 64; i += 2) capped_pair(s[i], s[i + 1], p.cap_in, p.cap_log2);
-                        if (two) {
-#pragma unroll
-                            for (int i = 64; i < 128; i += 2) capped_pair(s[i], s[i + 1], p.cap_in, p.cap_log2);
-                        }
-                    }
-                    if (masked) {
-#pragma unroll
-                        for (int i = 0; i < kShKeys; ++i)
-                            if (!((keep[i >> 5] >> (i & 31)) & 1u)) s[i] = -INFINITY;
                     }
                     float mq[8];
 #pragma unroll
@@ -1025,6 +1092,7 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
                     fix += __uint_as_float(pack_bf16x2(pmax, 0.f) << 16) - pmax;
                     const float2 r01 = fadd2(rs[0], rs[1]), r23 = fadd2(rs[2], rs[3]);
                     l += (r01.x + r23.x) + (r01.y + r23.y);
+                    }
                 }
                 ++done;
                 ++tiles;
@@ -1158,13 +1226,13 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const ShParam
     if (p.lse && lane == 0) p.lse[orow] = (mx + __log2f(sum)) * 0.69314718055994530942f;
 }
 
-template <int D, bool CAP>
+template <int D, int MODE>
 cudaError_t launch_one(const CUtensorMap &tm_q, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
                        const CUtensorMap &tm_pk, const CUtensorMap &tm_pv, const ShParams &p, int grid, bool join,
                        cudaStream_t stream)
 {
     using C = ShCfg<D>;
-    auto kern = shared_attn_kernel<D, CAP>;
+    auto kern = shared_attn_kernel<D, MODE>;
     static std::atomic<uint64_t> smem_done{0}, split_done{0};
     cudaError_t e = ensure_smem_attribute(kern, C::kSmemBytes, smem_done);
     if (e != cudaSuccess) return e;
@@ -1226,12 +1294,16 @@ cudaError_t launch_shared_attn(int head_dim, bool is_capped, const CUtensorMap &
                                const CUtensorMap &tm_v, const CUtensorMap &tm_pk, const CUtensorMap &tm_pv,
                                const ShParams &p, int grid, bool join, cudaStream_t stream)
 {
-    if (head_dim == 128)
-        return is_capped ? launch_one<128, true>(tm_q, tm_k, tm_v, tm_pk, tm_pv, p, grid, join, stream)
-                         : launch_one<128, false>(tm_q, tm_k, tm_v, tm_pk, tm_pv, p, grid, join, stream);
-    if (head_dim == 64)
-        return is_capped ? launch_one<64, true>(tm_q, tm_k, tm_v, tm_pk, tm_pv, p, grid, join, stream)
-                         : launch_one<64, false>(tm_q, tm_k, tm_v, tm_pk, tm_pv, p, grid, join, stream);
+    const int mode = !is_capped ? kShPlain : p.cap_log2 <= kShCapFixed ? kShCappedFixed : kShCapped;
+#define BG_SHARED(DD, MM) \
+    if (head_dim == DD && mode == MM) return launch_one<DD, MM>(tm_q, tm_k, tm_v, tm_pk, tm_pv, p, grid, join, stream)
+    BG_SHARED(128, kShPlain);
+    BG_SHARED(128, kShCapped);
+    BG_SHARED(128, kShCappedFixed);
+    BG_SHARED(64, kShPlain);
+    BG_SHARED(64, kShCapped);
+    BG_SHARED(64, kShCappedFixed);
+#undef BG_SHARED
     return cudaErrorInvalidValue;
 }
 
