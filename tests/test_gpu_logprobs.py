@@ -190,3 +190,16 @@ def test_repeats_graph_and_side_stream():
             graph.replay()
             torch.cuda.synchronize()
             assert all(torch.equal(out[n], ref[n]) for n in a)
+
+
+def test_row_offsets_past_32_bits():
+    """Rows of a buffer of more than 2^32 elements, whose stride is far above the vocabulary."""
+    import torch
+    N, V, stride = 4200, 5000, 1 << 20
+    assert N * stride > 1 << 32
+    buf = torch.empty((N, stride), dtype=torch.bfloat16, device="cuda")
+    x = logits(15, N, V, "bfloat16").cuda()
+    buf[:, :V] = x
+    tok = np.random.default_rng(15).integers(0, V, N)
+    a, b = run(x, tok, 8), run(buf[:, :V], tok, 8)
+    assert all(torch.equal(a[n], b[n]) for n in a)

@@ -307,3 +307,100 @@ def test_side_stream_and_graph_replay():
         graph.replay()
         torch.cuda.synchronize()
         assert_close(from_dev(out), None, reference(z, False), "replay")
+
+
+@pytest.mark.parametrize("last", [False, True], ids=["prefill", "last"])
+@pytest.mark.parametrize("num_groups,samples,heads", [(600, 2, (2, 2, 64)), (1300, 4, (4, 2, 64)), (3, 1500, (128, 1, 64))],
+                         ids=["groups600", "groups1300_seqs5200", "entries_above_1024"])
+def test_large_work_lists(num_groups, samples, heads, last):
+    """More requests, samples and entries than the pre-pass holds in shared memory or handles at once."""
+    rng = np.random.default_rng(24)
+    groups = [rng.integers(0, 3, samples).tolist() for _ in range(num_groups)]
+    prefix = rng.integers(0, 4, num_groups).tolist()
+    check(make(24, prefix, groups, *heads), last, what=f"{num_groups} requests of {samples}")
+
+
+def test_key_offsets_past_32_bits():
+    """A prefix cache of more than 2^32 elements, of which the last request's rows count."""
+    import torch
+    x = make(25, [65000, 300], [[3, 40], [20]], 8, 8, 128)
+    t, ws = device(x), workspace(x)
+    small = [torch.zeros((n, 8, 128), dtype=torch.bfloat16, device="cuda") for n in (63, 3)]
+    for last in (False, True):
+        call(x, t, last, small[last], ws=ws)
+    before = 65 * 65536                                     # rows of 65 requests without samples: 2^32 elements
+    y = dict(x, cup=np.concatenate((np.arange(66) * 65536, before + x["cup"][1:])).astype(np.int32),
+             cug=np.concatenate((np.zeros(65), x["cug"])).astype(np.int32), max_prefix=65536)
+    P = int(y["cup"][-1])
+    assert (P - 65300) * 8 * 128 > 1 << 32
+    for n in ("pk", "pv"):
+        big = torch.zeros((P, 8, 128), dtype=torch.bfloat16, device="cuda")
+        big[before:] = t[n]
+        t[n] = big
+    t.update({n: i32_dev(y[n]) for n in ("cup", "cug")})
+    for last in (False, True):
+        out = torch.zeros_like(small[last])
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        call(y, t, last, out, dev_status=st)
+        assert int(st.item()) == 0 and torch.equal(out, small[last])
+
+
+@pytest.mark.parametrize("last", [False, True], ids=["prefill", "last"])
+def test_query_offsets_past_31_bits(last):
+    """Queries and outputs of more than 2^31 elements: samples of one token; the rows at both ends are compared."""
+    import torch
+    S, Hq, d, n = (1 << 18) + 77, 128, 64, 40
+    x = make(26, [n], [[1] * 50], Hq, 1, d)
+    t = device(x)
+    gen = torch.Generator(device="cuda").manual_seed(26)
+    q = torch.randn((S, Hq, d), generator=gen, device="cuda", dtype=torch.bfloat16)
+    assert q.numel() > 1 << 31
+    k, v = (torch.randn((S, 1, d), generator=gen, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    cu = torch.arange(S + 1, dtype=torch.int32, device="cuda")
+    cug = i32_dev(np.array([0, S], np.int32))
+    out = torch.zeros_like(q)
+    ws = torch.empty(bg.bg_shared_attn_workspace_size(1, S, S, 1, n, Hq, 1, d), dtype=torch.uint8, device="cuda")
+    fn = bg.bg_shared_last_token_attn if last else bg.bg_shared_prefill_attn
+    fn(q, k, v, cu, 1, t["pk"], t["pv"], t["cup"], n, cug, out, workspace=ws)
+    for rows in (slice(0, 50), slice(S - 50, S)):
+        y = {m: np.ascontiguousarray(a[rows].view(torch.int16).cpu().numpy().view(np.uint16))
+             for m, a in (("q", q), ("k", k), ("v", v))}
+        ref = sh.attn(f64(y["q"]), f64(y["k"]), f64(y["v"]), np.arange(51), f64(x["pk"]), f64(x["pv"]), x["cup"],
+                      [0, 50], 1 / math.sqrt(d), last=last)
+        assert_close(from_dev(out[rows].contiguous()), None, ref, f"rows {rows}")
+
+
+def test_two_streams_and_shared_workspace_of_two_graphs():
+    """Two problems at once on two streams, each with its workspace; then two captured graphs that
+    share one workspace, replayed in turn on one stream."""
+    import torch
+    xs = [make(27, [3000, 100], [[30, 5], [61, 200, 1]], 16, 8, 128), make(28, [700], [[90, 1, 300]], 14, 2, 64)]
+    ts = [device(x) for x in xs]
+    outs = [[torch.zeros_like(t["ql"] if last else t["q"]) for last in (False, True)] for t in ts]
+    sizes = [workspace(x) for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for x, t, o, ws, st in zip(xs, ts, outs, sizes, streams):
+            for last in (False, True):
+                call(x, t, last, o[last], ws=ws, stream=st)
+    torch.cuda.synchronize()
+    for x, o in zip(xs, outs):
+        for last in (False, True):
+            assert_close(from_dev(o[last]), None, reference(x, last), "two streams")
+    ref = [[o.clone() for o in pair] for pair in outs]
+    ws = max(sizes, key=lambda w: w.numel())
+    graphs = []
+    for x, t, o in zip(xs, ts, outs):
+        for last in (False, True):
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                call(x, t, last, o[last], ws=ws)
+            graphs.append((g, o[last], ref[len(graphs) // 2][last]))
+    for _ in range(2):
+        for g, o, _ in graphs:
+            o.zero_()
+        for g, _, _ in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, r) for _, o, r in graphs)
