@@ -5,6 +5,9 @@
     python profile_case.py beam_long --iters 2 --two-call
     python profile_case.py select_long --iters 2
     python profile_case.py prefill_only --iters 3 --fp8
+    python profile_case.py shared_prefill --iters 3
+    python profile_case.py shared_last --iters 3
+    python profile_case.py logprobs --iters 3
 
 Prefill workloads (tiny, prefill_only, skewed) call bg_packed_prefill_attn
 ``iters`` times on one layer of inputs; decode workloads (beam_short,
@@ -13,8 +16,12 @@ suffix reorder + append, then the decode attention: one bg_beam_decode_step
 call, or with ``--two-call`` bg_beam_suffix_reorder, then
 bg_beam_decode_attn); selection workloads
 (select_short, select_long) call bg_beam_select ``iters`` times on the beam
-configurations' shapes with fp32 logits N(0, 3) over 65,536 tokens.  Inputs are drawn on the
-device with a seeded generator, shaped as in ``workloads``.  Nothing is
+configurations' shapes with fp32 logits N(0, 3) over 65,536 tokens;
+shared_prefill and shared_last call bg_shared_prefill_attn and
+bg_shared_last_token_attn on 32 requests of 15 samples of 56 tokens after a
+prefix of 350 (16/8 heads, d 128); logprobs calls bg_token_logprobs on 8192 rows of
+65,536 bf16 logits.  Inputs are drawn on the device with a seeded generator,
+shaped as in ``workloads``.  Nothing is
 timed here: use ncu (or bench.py for timings).
 """
 from __future__ import annotations
@@ -39,7 +46,8 @@ def main(argv=None):
 
     ap = argparse.ArgumentParser()
     select = {"select_short": "beam_short", "select_long": "beam_long"}
-    ap.add_argument("workload", choices=sorted(list(wl.PREFILL_CONFIGS) + list(wl.DECODE_CONFIGS) + list(select)))
+    scoring = ["shared_prefill", "shared_last", "logprobs"]
+    ap.add_argument("workload", choices=sorted(list(wl.PREFILL_CONFIGS) + list(wl.DECODE_CONFIGS) + list(select) + scoring))
     ap.add_argument("--iters", type=int, default=3)
     ap.add_argument("--two-call", action="store_true", help="decode: separate reorder and attention calls")
     ap.add_argument("--fp8", action="store_true", help="prefill: E4M3 Q and K (bg_packed_prefill_attn_fp8)")
@@ -61,6 +69,30 @@ def main(argv=None):
         ws = torch.empty(bg.bg_beam_select_workspace_size(R, W, V), dtype=torch.uint8, device=dev)
         for _ in range(args.iters):
             bg.bg_beam_select(logits, cum, tok, par, sc, workspace=ws)
+    elif args.workload == "logprobs":
+        N, V, K = 8192, 65536, 20
+        logits = (torch.randn((N, V), generator=g, device=dev) * 3.0).to(bf)
+        tok = torch.randint(V, (N,), generator=g, device=dev, dtype=torch.int32)
+        lp, ent = (torch.empty(N, dtype=torch.float32, device=dev) for _ in range(2))
+        tt = torch.empty((N, K), dtype=torch.int32, device=dev)
+        tl = torch.empty((N, K), dtype=torch.float32, device=dev)
+        for _ in range(args.iters):
+            bg.bg_token_logprobs(logits, tok, logprob=lp, entropy=ent, top_token=tt, top_logprob=tl)
+    elif args.workload in scoring:
+        R, S, n, plen, Hq, Hkv, d = 32, 15, 56, 350, 16, 8, 128
+        last = args.workload == "shared_last"
+        T = R * S * n
+        q = torch.randn((R * S if last else T, Hq, d), generator=g, device=dev).to(bf)
+        k, v = (torch.randn((T, Hkv, d), generator=g, device=dev).to(bf) for _ in range(2))
+        pk, pv = (torch.randn((R * plen, Hkv, d), generator=g, device=dev).to(bf) for _ in range(2))
+        cu = torch.arange(R * S + 1, dtype=torch.int32, device=dev) * n
+        cup = torch.arange(R + 1, dtype=torch.int32, device=dev) * plen
+        cug = torch.arange(R + 1, dtype=torch.int32, device=dev) * S
+        out = torch.empty_like(q)
+        ws = torch.empty(bg.bg_shared_attn_workspace_size(R, R * S, T, n, plen, Hq, Hkv, d), dtype=torch.uint8, device=dev)
+        call = bg.bg_shared_last_token_attn if last else bg.bg_shared_prefill_attn
+        for _ in range(args.iters):
+            call(q, k, v, cu, n, pk, pv, cup, plen, cug, out, workspace=ws)
     elif args.workload in wl.PREFILL_CONFIGS:
         cfg = wl.PREFILL_CONFIGS[args.workload]
         lengths = wl.prefill_lengths(cfg)
