@@ -30,7 +30,7 @@
 //      columns), so a tile alternates between its softmax and its two products; the two tiles of
 //      a CTA take turns on the tensor core.
 //   3. shared_join_kernel joins the partial results (only where the sizes allow a cut).
-// Every wait is bounded (bg::mbar_wait); on a time-out every role leaves, copies and MMAs in
+// Every wait is bounded (sh_wait); on a time-out every role leaves, copies and MMAs in
 // flight are drained, TMEM is freed and BG_DEVSTAT_TIMEOUT is reported.
 #include <cuda_bf16.h>
 
@@ -279,6 +279,8 @@ __device__ bool plan_ready(const ShParams &p, bool *other)
 }
 
 // ------------------------------------------------------------------------------------ attention
+constexpr int kShKeysLog = 7;                  // kShKeys as a shift (counts are not negative)
+static_assert(1 << kShKeysLog == kShKeys, "a power of two");
 constexpr int kShRing = 4;                     // items in the ring that warp 0 fills
 constexpr int kShReaders = 1 + 1 + 8;          // Q producer, MMA issuer, softmax warps
 
@@ -313,8 +315,8 @@ struct __align__(16) ShItem {
         if (rows(h, bt) == 0) return 0;
         const int pre = max(min(te, npt) - tb, 0);
         if (kb(h) <= ka(h)) return pre;
-        const int lo = npt + (ka(h) - ka0) / kShKeys;
-        const int hi = npt + (kb(h) - ka0 + kShKeys - 1) / kShKeys;
+        const int lo = npt + ((ka(h) - ka0) >> kShKeysLog);
+        const int hi = npt + ((kb(h) - ka0 + kShKeys - 1) >> kShKeysLog);
         return pre + max(min(te, hi) - max(tb, lo), 0);
     }
 };
@@ -347,21 +349,44 @@ struct ShCfg {
     static_assert(kSmemBytes <= 232448, "shared memory overflow");
 };
 
-// The whole warp waits, without diverging (bounded, as mbar_wait).
-__device__ __forceinline__ bool sh_warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort)
+// mbar_wait, and its form for a whole warp, in less code: the instruction cache serves the loops of all
+// roles, whose waits' slow paths lie between.  The clock is first read when 64 polls have failed (read
+// at each poll it held the wake-ups up: 16 MMA-bound samples over 8000 keys took 484 us instead of 408).
+__device__ __forceinline__ uint32_t sh_time()
 {
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-    const uint64_t t0 = globaltimer_ns();
-    for (uint32_t it = 1;; ++it) {
-        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-        if ((it & 63u) == 0) {
-            const bool late = globaltimer_ns() - t0 > kWaitTimeoutNs;
-            if (__any_sync(0xffffffffu, late || *abort)) {
-                *abort = 1;
-                return false;
-            }
+    uint32_t t;
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+    return t;
+}
+__device__ __forceinline__ bool sh_wait(uint64_t *bar, uint32_t parity, volatile int *abort)
+{
+    uint32_t t0 = 0;
+#pragma unroll 1
+    for (uint32_t it = 1; !mbar_try_wait(bar, parity); ++it) {
+        if ((it & 63u) != 0) continue;
+        const uint32_t now = sh_time();
+        if (it == 64) t0 = now;
+        if (*abort || now - t0 > static_cast<uint32_t>(kWaitTimeoutNs)) {
+            *abort = 1;
+            return false;
         }
     }
+    return true;
+}
+__device__ __forceinline__ bool sh_warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort)
+{
+    uint32_t t0 = 0;
+#pragma unroll 1
+    for (uint32_t it = 1; !__all_sync(0xffffffffu, mbar_try_wait(bar, parity)); ++it) {
+        if ((it & 63u) != 0) continue;
+        const uint32_t now = sh_time();
+        if (it == 64) t0 = now;
+        if (__any_sync(0xffffffffu, *abort || now - t0 > static_cast<uint32_t>(kWaitTimeoutNs))) {
+            *abort = 1;
+            return false;
+        }
+    }
+    return true;
 }
 
 // S = Q K^T over D = 64 * NB, then a commit to `full`: one asm statement per tile, so that
@@ -594,14 +619,14 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
                 for (;;) {
                     const bool more = before_end();
                     const uint32_t slot = n_items % kShRing;
-                    if (!mbar_wait(&item_empty[slot], ((n_items / kShRing) & 1) ^ 1, abort_flag)) break;
+                    if (!sh_wait(&item_empty[slot], ((n_items / kShRing) & 1) ^ 1, abort_flag)) break;
                     ShItem I;
                     I.prow0 = e0.x; I.plen = e0.y; I.row0 = e0.z; I.nrows = e0.w;
                     I.ka0 = e1.x; I.kb0 = e1.y; I.ka1 = e1.z; I.kb1 = e1.w;
                     I.s0 = e2.x;
                     const int tiles = e2.y;
                     I.kh = kh;
-                    I.npt = (I.plen + kShKeys - 1) / kShKeys;
+                    I.npt = (I.plen + kShKeys - 1) >> kShKeysLog;
                     I.tb = tb;
                     I.te = kh == B.kh && entry == B.entry ? B.tile : tiles;
                     I.slot = tb > 0 ? 2 * cta : I.te < tiles ? 2 * cta + 1 : -1;
@@ -634,7 +659,7 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
                         const int row = pre ? I.prow0 + j * kShKeys : I.own_base(j);
 #pragma unroll 1
                         for (int kv = 0; kv < 2; ++kv) {
-                            if (!mbar_wait(&kv_empty[st], ph, abort_flag)) {
+                            if (!sh_wait(&kv_empty[st], ph, abort_flag)) {
                                 ok = false;
                                 break;
                             }
@@ -662,40 +687,41 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
             // ============================================================ Q producer
             if (lane == 0) {
                 const uint64_t pol = l2_policy_evict_first();
-                uint32_t n[kShTiles] = {0, 0};
+                uint32_t used = 0, par = 0;        // bit h: the buffer was used; parity of its last use
                 const uint32_t bytes = static_cast<uint32_t>(C::kNB * p.bt * p.g * 128);
                 for (uint32_t it = 0;; ++it) {
                     const uint32_t slot = it % kShRing;
-                    if (!mbar_wait(&item_full[slot], (it / kShRing) & 1, abort_flag) || !ring[slot].more) break;
+                    if (!sh_wait(&item_full[slot], (it / kShRing) & 1, abort_flag) || !ring[slot].more) break;
                     const int row0 = ring[slot].row0, kh = ring[slot].kh;
-                    const int act[kShTiles] = {ring[slot].act[0], ring[slot].act[1]};
+                    const uint32_t have = (ring[slot].act[0] > 0 ? 1u : 0u) | (ring[slot].act[1] > 0 ? 2u : 0u);
                     mbar_arrive(&item_empty[slot]);
                     bool ok = true;
                     // into L2 while the item before still uses the buffers
-#pragma unroll
+#pragma unroll 1
                     for (int h = 0; h < kShTiles; ++h)
-                        if (act[h] > 0) {
-#pragma unroll
+                        if ((have >> h) & 1u) {
+#pragma unroll 1
                             for (int b = 0; b < C::kNB; ++b) tma_prefetch_4d(&tm_q, b * 64, 0, kh, row0 + h * p.bt);
                         }
-#pragma unroll
+#pragma unroll 1
                     for (int h = 0; h < kShTiles; ++h) {
-                        if (!ok || act[h] == 0) continue;
-                        if (n[h] > 0 && !mbar_wait(&q_empty[h], (n[h] - 1) & 1, abort_flag)) {
+                        if (!ok || !((have >> h) & 1u)) continue;
+                        if (((used >> h) & 1u) && !sh_wait(&q_empty[h], (par >> h) & 1u, abort_flag)) {
                             ok = false;
                             continue;
                         }
                         mbar_arrive_expect_tx(&q_full[h], bytes);
-#pragma unroll
+#pragma unroll 1
                         for (int b = 0; b < C::kNB; ++b)
                             tma_load_4d(smem + C::kOffQ + h * C::kTileBytes + b * C::kBox, &tm_q, &q_full[h], b * 64, 0,
                                         kh, row0 + h * p.bt, pol);
-                        ++n[h];
+                        if ((used >> h) & 1u) par ^= 1u << h;
+                        used |= 1u << h;
                     }
                     if (!ok) break;
                 }
                 for (int h = 0; h < kShTiles; ++h)
-                    if (n[h] > 0) mbar_wait_drain(&q_full[h], (n[h] - 1) & 1);
+                    if ((used >> h) & 1u) mbar_wait_drain(&q_full[h], (par >> h) & 1u);
             }
             __syncwarp();
         } else if (warp == 1) {
@@ -735,7 +761,7 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
                         uint32_t acc = ((fresh >> h) & 1u) ^ 1u;
                         p_par ^= 1u << h;
                         fresh &= ~(1u << h);
-                        if (!mbar_wait(&p_full[2 * h], par, abort_flag)) return false;
+                        if (!sh_wait(&p_full[2 * h], par, abort_flag)) return false;
                         tc_fence_after();
                         if (sp >= 4) {
                             sh_mma_pv4(d, a, dv, kIdescPV, acc);
@@ -744,7 +770,7 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
                             for (int k = 0; k < sp; ++k, acc = 1u)
                                 mma_ts(d, a + 8 * k, dv + static_cast<uint64_t>(128 * k), kIdescPV, acc);
                         }
-                        if (!mbar_wait(&p_full[2 * h + 1], par, abort_flag)) return false;
+                        if (!sh_wait(&p_full[2 * h + 1], par, abort_flag)) return false;
                         tc_fence_after();
                         if (sp == 8) {
                             sh_mma_pv4(d, a + 32, dv + 512, kIdescPV, 1u);
@@ -765,7 +791,7 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
                 // the P.V of an item's last tile
                 auto finish = [&]() {
                     if (outs == 0) return true;
-                    if (!mbar_wait(&kv_full[vs], vph, abort_flag)) return false;
+                    if (!sh_wait(&kv_full[vs], vph, abort_flag)) return false;
 #pragma unroll 1
                     for (int h = 0; h < kShTiles; ++h) {
                         if (!turn(h, 0, 0)) return false;
@@ -776,10 +802,12 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
                 };
                 for (uint32_t it = 0;; ++it) {
                     const uint32_t slot = it % kShRing;
-                    if (!mbar_wait(&item_full[slot], (it / kShRing) & 1, abort_flag)) { ok = false; break; }
+                    if (!sh_wait(&item_full[slot], (it / kShRing) & 1, abort_flag)) { ok = false; break; }
                     const ShItem &I = ring[slot];
-                    if (!I.more) break;
-                    const int tb = I.tb, te = I.te, whole_end = I.plen / kShKeys;
+                    // the previous item's last P.V, which do not wait for this one's Q
+                    ok = finish();
+                    if (!ok || !I.more) break;
+                    const int tb = I.tb, te = I.te, whole_end = I.plen >> kShKeysLog;
                     const uint32_t have = (I.act[0] > 0 ? 1u : 0u) | (I.act[1] > 0 ? 2u : 0u);
                     auto steps_of = [&](int j) {
                         if (j < whole_end) return ((have & 1u) ? 8u : 0u) | ((have & 2u) ? 8u << 8 : 0u);
@@ -791,15 +819,15 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
                     };
                     uint32_t cur = steps_of(tb);
                     uint32_t ks = st;
-                    // ---- the first tile: behind the previous item's last P.V, which do not wait for this Q
-                    ok = finish() && mbar_wait(&kv_full[ks], ph, abort_flag);
+                    // ---- the first tile
+                    ok = sh_wait(&kv_full[ks], ph, abort_flag);
                     prev = 0;
                     fresh = 3u;
                     outs = have;
 #pragma unroll 1
                     for (int h = 0; h < kShTiles && ok; ++h) {
                         if (!((have >> h) & 1u)) continue;
-                        ok = mbar_wait(&q_full[h], (q_par >> h) & 1u, abort_flag);
+                        ok = sh_wait(&q_full[h], (q_par >> h) & 1u, abort_flag);
                         q_par ^= 1u << h;
                         if (ok) {
                             tc_fence_after();
@@ -817,7 +845,7 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
                     for (int j = tb + 1; j < te; ++j) {
                         cur = steps_of(j);
                         ks = st;
-                        ok = mbar_wait(&kv_full[vs], vph, abort_flag) && mbar_wait(&kv_full[ks], ph, abort_flag) &&
+                        ok = sh_wait(&kv_full[vs], vph, abort_flag) && sh_wait(&kv_full[ks], ph, abort_flag) &&
                              turn(0, cur, ks) && turn(1, cur, ks);
                         if (!ok) break;
                         mma_commit(&kv_empty[vs]);
@@ -833,7 +861,6 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
                     if (have & 2u) mma_commit(&q_empty[1]);
                     mbar_arrive(&item_empty[slot]);
                 }
-                if (ok) finish();
                 mma_commit(mma_final);           // every MMA issued completes before TMEM is released
                 mbar_wait_drain(mma_final, 0);
             }
@@ -878,6 +905,31 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
                 if (lane == 0) mbar_arrive(&p_full[2 * h + half]);
             };
 
+            // The running maximum becomes m_new.  O holds the earlier tiles, all complete (the commit
+            // behind this tile's S covers every MMA issued before it).
+            auto rescale = [&](float m_new) {
+                const float alpha = m == -INFINITY ? 0.f : ex2(m - m_new);
+                m = m_new;
+                l *= alpha;
+                fix *= alpha;
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    float o[32];
+                    tmem_ld32(tO + 32 * c, o);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] *= alpha;
+                    tmem_st32f(tO + 32 * c, o);
+                }
+            };
+            // A tile's sum of weights.  P.V multiplies weights rounded to bf16.  The rounding of the tile's
+            // largest weight enters the sum that O is divided by, which makes the dominant term exact; the
+            // log-sum-exp keeps the unrounded sum.
+            auto add_sums = [&](float mx, float2 negm, float sum) {
+                const float pmax = ex2(ffma2(make_float2(mx, mx), make_float2(sl2, sl2), negm).x);
+                fix += __uint_as_float(pack_bf16x2(pmax, 0.f) << 16) - pmax;
+                l += sum;
+            };
+
             // own keys this row sees: [lo, hi)
             int lo = 0, hi = 0;
             if (act > 0 && I.te > I.npt) {
@@ -905,7 +957,7 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
                 }
             }
             const int npt = I.npt, tb = I.tb, te = act > 0 ? I.te : I.tb;
-            const int whole_end = I.plen / kShKeys;        // tiles below it: every row sees all 128 keys
+            const int whole_end = I.plen >> kShKeysLog;        // tiles below it: every row sees all 128 keys
 #pragma unroll 1
             for (int j = tb; j < te; ++j) {
                 int nk = kShKeys, c0 = 0, c1 = kShKeys;    // keys of the tile; this row's columns [c0, c1)
@@ -921,7 +973,7 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
                         c1 = nk;
                     }
                     some = __any_sync(0xffffffffu, live && c1 > c0);
-                    masked = __any_sync(0xffffffffu, live && (c0 > 0 || c1 < (nk > 64 ? 128 : 64)));
+                    masked = __any_sync(0xffffffffu, live && (c0 > 0 || c1 < kShKeys));
                     zero_v = ((nk + 15) & ~15) > I.keys(j);
                 }
                 seen = seen || c1 > c0;
@@ -954,7 +1006,13 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
                     hand_over(0);
                     hand_over(1);
                 } else {
-                    const bool two = nk > 64;              // columns 64-127 are used
+                    // 32-column chunks in which any row of the warp sees a key: [cf, ce)
+                    int cf = 0, ce = kShKeys / 32;
+                    if (masked) {
+                        const bool sees = live && c1 > c0;
+                        cf = __reduce_min_sync(0xffffffffu, sees ? c0 : kShKeys) >> 5;
+                        ce = (__reduce_max_sync(0xffffffffu, sees ? c1 : 0) + 31) >> 5;
+                    }
                     // bit i: column 32 c + i is in [c0, c1)
                     auto columns = [&](int c) {
                         const int a = min(max(c0 - 32 * c, 0), 32), b = min(max(c1 - 32 * c, 0), 32);
@@ -965,9 +1023,12 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
                         float2 rs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll 1
                         for (int c = 0; c < 4; ++c) {
-                            if (c < 2 || two) {
+                            uint32_t pk[16];
+                            if (c < cf || c >= ce) {
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) pk[i] = 0u;
+                            } else {
                                 float x[32];
-                                uint32_t pk[16];
                                 const uint32_t keep = masked ? columns(c) : ~0u;
                                 tmem_ld32(tS + 32 * c, x);
                                 if (masked) {              // may be NaN, which is not to reach its neighbours
@@ -991,20 +1052,61 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
                                     rs[i & 1] = fadd2(rs[i & 1], make_float2(x[2 * i], x[2 * i + 1]));
                                     pk[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
                                 }
-                                tmem_st16(tS + 16 * c, pk);      // over scores that have been read
                             }
+                            tmem_st16(tS + 16 * c, pk);          // over scores that have been read
                             if (c & 1) hand_over(c >> 1);
                         }
                         l += (rs[0].x + rs[1].x) + (rs[0].y + rs[1].y);
+                    } else if (MODE == kShPlain && ce - cf <= 3) {
+                        // Few columns count, as in most own tiles of prefill: the maximum over those chunks first,
+                        // then their weights, 32 columns at a time in short code.  With four chunks the path
+                        // below is the faster one (32 samples of 200 keys, last token: 121 us, 131 by this one);
+                        // a limit of two leaves too many prefill tiles to it (32 requests of 15 samples of 16-96
+                        // tokens: 184 us, 160 with three).
+                        float x[32], mx = -INFINITY;
+                        auto load = [&](int c) {
+                            const uint32_t keep = columns(c);
+                            tmem_ld32(tS + 32 * c, x);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (!((keep >> i) & 1u)) x[i] = -INFINITY;
+                        };
+#pragma unroll 1
+                        for (int c = cf; c < ce; ++c) {
+                            load(c);
+#pragma unroll
+                            for (int i = 0; i < 32; i += 2) mx = fmax3f(mx, x[i], x[i + 1]);
+                        }
+                        const float m_new = fmaxf(m, mx * sl2);
+                        if (done == 0) m = m_new;
+                        if (__any_sync(0xffffffffu, m_new > m + 8.f)) rescale(m_new);
+                        const float mu = m == -INFINITY ? 0.f : m;
+                        const float2 sl2x2 = make_float2(sl2, sl2), negm = make_float2(-mu, -mu);
+                        float2 rs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t pk[16];
+                            if (c < cf || c >= ce) {
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) pk[i] = 0u;
+                            } else {
+                                load(c);
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) {
+                                    const float2 t = ffma2(make_float2(x[2 * i], x[2 * i + 1]), sl2x2, negm);
+                                    const float2 w = make_float2(ex2(t.x), ex2(t.y));
+                                    rs[i & 1] = fadd2(rs[i & 1], w);
+                                    pk[i] = pack_bf16x2(w.x, w.y);
+                                }
+                            }
+                            tmem_st16(tS + 16 * c, pk);          // over scores that have been read
+                            if (c & 1) hand_over(c >> 1);
+                        }
+                        add_sums(mx, negm, (rs[0].x + rs[1].x) + (rs[0].y + rs[1].y));
                     } else {
                     float s[kShKeys];
                     tmem_ld64(tS, s);
-                    if (two) {
-                        tmem_ld64(tS + 64, s + 64);
-                    } else {
-#pragma unroll
-                        for (int i = 64; i < 128; ++i) s[i] = -INFINITY;
-                    }
+                    tmem_ld64(tS + 64, s + 64);
                     if constexpr (MODE == kShCapped) {
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
@@ -1017,7 +1119,7 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
                             for (int i = 32 * c; i < 32 * c + 32; i += 4) capped4_any(s + i, p.cap_in, p.cap_log2);
                         }
                     }
-                    if (masked || (MODE == kShCapped && !two)) {
+                    if (masked) {
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
                             const uint32_t keep = columns(c);
@@ -1060,38 +1162,18 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
                         weights(0, pk);
                         weights(1, pk + 16);
                         if (!__any_sync(0xffffffffu, m_new > m + 8.f)) break;
-                        // O holds the earlier tiles, all complete (the commit behind this S covers every
-                        // MMA issued before it)
-                        const float alpha = m == -INFINITY ? 0.f : ex2(m - m_new);
-                        m = m_new;
-                        l *= alpha;
-                        fix *= alpha;
-#pragma unroll 1
-                        for (int c = 0; c < D / 32; ++c) {
-                            float o[32];
-                            tmem_ld32(tO + 32 * c, o);
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] *= alpha;
-                            tmem_st32f(tO + 32 * c, o);
-                        }
+                        rescale(m_new);
                     }
                     tmem_st16(tS, pk);
                     tmem_st16(tS + 16, pk + 16);
                     hand_over(0);
-                    if (two) {
-                        weights(2, pk);
-                        tmem_st16(tS + 32, pk);
-                        weights(3, pk + 16);
-                        tmem_st16(tS + 48, pk + 16);
-                    }
+                    weights(2, pk);
+                    tmem_st16(tS + 32, pk);
+                    weights(3, pk + 16);
+                    tmem_st16(tS + 48, pk + 16);
                     hand_over(1);
-                    // P.V multiplies weights rounded to bf16.  The rounding of the tile's largest weight
-                    // enters the sum that O is divided by, which makes the dominant term exact; the
-                    // log-sum-exp keeps the unrounded sum.
-                    const float pmax = ex2(ffma2(make_float2(mx, mx), sl2x2, negm).x);
-                    fix += __uint_as_float(pack_bf16x2(pmax, 0.f) << 16) - pmax;
                     const float2 r01 = fadd2(rs[0], rs[1]), r23 = fadd2(rs[2], rs[3]);
-                    l += (r01.x + r23.x) + (r01.y + r23.y);
+                    add_sums(mx, negm, (r01.x + r23.x) + (r01.y + r23.y));
                     }
                 }
                 ++done;
