@@ -605,8 +605,9 @@ bg_status_t shared_check_sizes(const ShProblem &pb)
 int shared_grid(const ShProblem &pb, const ShLayout &lay)
 {
     int64_t n = sm_count();
-    const int64_t items = lay.max_entries * pb.Hkv;
-    if (lay.slots == 0 && items < n) n = items;
+    const int heads = shared_heads(pb);
+    const int64_t most = lay.slots == 0 ? lay.max_entries * pb.Hkv : (lay.units * heads + kShSplitMin - 1) / kShSplitMin;
+    if (most < n) n = most;
     if (lay.slots > 0 && lay.slots / 2 < n) n = lay.slots / 2;
     return static_cast<int>(n < kShMaxCtas ? n : kShMaxCtas);
 }
@@ -706,6 +707,7 @@ bg_status_t shared_impl(const ShProblem &pb, const void *q, const void *k, const
     p.Hkv = pb.Hkv;
     p.g = g;
     p.bt = bt;
+    p.heads = shared_heads(pb);
     p.last = pb.last;
     p.num_seqs = pb.num_seqs;
     p.scale_log2 = scale * 1.4426950408889634f;

@@ -14,12 +14,13 @@
 // Against the prefix nothing but the prefix's end is masked, so short samples and few heads still
 // fill the tensor core's 128 rows; against the own keys every row keeps the interval [lo, hi) of
 // its sample (block-diagonal), and key tiles that no row of a query tile sees are skipped.
-// kShTiles query tiles share every K/V tile that is loaded.
+// kShTiles query tiles share every K/V tile that is loaded; in the last-token form, where few rows often
+// fill only one, the two may hold the same rows for two kv heads, each with K/V tiles of its own.
 //
 // Three launches on the caller's stream:
 //   1. shared_plan_kernel (one CTA) checks the offsets on the device, writes the list of entries
-//      and cuts the whole work, as one line of (kv head, entry, key tile), into equal shares, one
-//      per CTA of the next kernel.  A cut through a long key range leaves two partial results.
+//      and cuts the whole work, as one line of (kv head or pair, entry, key tile), into equal shares,
+//      one per CTA of the next kernel.  A cut through a long key range leaves two partial results.
 //   2. shared_attn_kernel: one CTA per SM, 12 warps:
 //        warp 0      walks the CTA's share, tells the other roles each item (through a ring in
 //                    shared memory), and loads K and V tiles of 128 keys by TMA (one ring for both)
@@ -86,7 +87,7 @@ __device__ __forceinline__ int entry_units(const ShEntry &E) { return E.tiles > 
 
 __global__ void __launch_bounds__(kPlanThreads)
     shared_plan_kernel(const ShProblem pb, const ShKey key, int bt, int32_t *hdr, ShEntry *__restrict__ entries,
-                       ShStart *__restrict__ starts, ShSplit *__restrict__ splits, int grid, int can_split,
+                       ShStart *__restrict__ starts, ShSplit *__restrict__ splits, int grid, int can_split, int heads,
                        int32_t *dev_status)
 {
     __shared__ int s_err, s_nsplit;
@@ -157,7 +158,10 @@ __global__ void __launch_bounds__(kPlanThreads)
         int items = 0;
         if (r < pb.num_groups) {
             const int a = cug[r], b = cug[r + 1];
-            items = static_cast<int>(ceil_div(pb.last ? b - a : cu[b] - cu[a], per));
+            const int rows = pb.last ? b - a : cu[b] - cu[a];
+            items = static_cast<int>(ceil_div(rows, per));
+            // paired heads: an entry of one query tile serves both heads, the others come once for each
+            if (heads == 2 && items > 0) items = 2 * items - (rows - (items - 1) * per <= bt ? 1 : 0);
         }
         int total;
         s_base[tid] = block_exclusive(items, s_warp, &total);
@@ -171,7 +175,7 @@ __global__ void __launch_bounds__(kPlanThreads)
                     const int mid = (t + end) >> 1;
                     if (s_base[mid] <= e) t = mid; else end = mid;
                 }
-                const int grp = r0 + t, first = (e - s_base[t]) * per;
+                const int grp = r0 + t, first = ((e - s_base[t]) >> (heads - 1)) * per;
                 const int sa = cug[grp], sb = cug[grp + 1];
                 E.prow0 = cup[grp];
                 E.plen = cup[grp + 1] - E.prow0;
@@ -181,7 +185,7 @@ __global__ void __launch_bounds__(kPlanThreads)
                 E.nrows = min(per, end_row - E.row0);
                 const int n0 = min(bt, E.nrows);
                 if (pb.last) {
-                    E.s0 = E.row0;
+                    E.s0 = 0;
                     E.ka0 = cu[E.row0];
                     E.kb0 = cu[E.row0 + n0];
                     E.ka1 = E.kb0;
@@ -194,6 +198,14 @@ __global__ void __launch_bounds__(kPlanThreads)
                     E.kb1 = E.row0 + E.nrows;
                 }
                 E.tiles = static_cast<int>(ceil_div(E.plen, kShKeys) + ceil_div(E.kb1 - E.ka0, kShKeys));
+                if (heads == 2) {
+                    if (E.nrows <= bt) {
+                        E.s0 = kShPair;
+                        E.ka1 = E.ka0;
+                    } else {
+                        E.s0 = (e - s_base[t]) & 1;
+                    }
+                }
                 if (E.tiles == 0 && dev_status) atomicOr(dev_status, BG_DEVSTAT_EMPTY_ROW);
             }
             int sum;
@@ -209,12 +221,15 @@ __global__ void __launch_bounds__(kPlanThreads)
         __syncthreads();
     }
 
-    // ---- equal shares of units * Hkv; fewer CTAs where a share would be below kShSplitMin
+    // ---- equal shares of the line; fewer CTAs where a share would be below kShSplitMin (half of it for pairs,
+    // whose tiles count twice)
     auto pos_of = [&](int e) { return n_entries <= kPlanThreads ? s_pos[e] : entries[e].pos; };
-    const int64_t work = units * pb.Hkv;
-    const int ctas = static_cast<int>(min(static_cast<int64_t>(grid), ceil_div(work, kShSplitMin)));
+    const int lines = pb.Hkv >> (heads - 1);
+    const int64_t work = units * lines;
+    const int split_min = kShSplitMin >> (heads - 1);
+    const int ctas = static_cast<int>(min(static_cast<int64_t>(grid), ceil_div(work, split_min)));
     for (int c = tid; c <= ctas; c += kPlanThreads) {
-        ShStart S = {pb.Hkv, 0, 0, 0};             // the end of the line
+        ShStart S = {lines, 0, 0, 0};              // the end of the line
         if (c < ctas) {
             const int64_t at = work * c / ctas;
             S.kh = static_cast<int>(at / units);
@@ -228,14 +243,14 @@ __global__ void __launch_bounds__(kPlanThreads)
             const int n = entries[lo].tiles;
             const int into = static_cast<int>(u - pos_of(lo));
             // a cut near an end of the item, or through a short one, moves to the end that is nearer
-            const int least = max(kShSplitMin / 2, static_cast<int>(min(work / ctas / 32, static_cast<int64_t>(n))));
+            const int least = max(split_min / 2, static_cast<int>(min(work / ctas / 32, static_cast<int64_t>(n))));
             S.tile = into;
             if (!can_split || into < least || n - into < least) {
                 S.tile = 0;
                 if (2 * into > n) ++S.entry;
             }
         }
-        if (S.kh < pb.Hkv && S.entry == n_entries) {
+        if (S.kh < lines && S.entry == n_entries) {
             ++S.kh;
             S.entry = 0;
         }
@@ -252,7 +267,9 @@ __global__ void __launch_bounds__(kPlanThreads)
                s_start[c + pieces].entry == B.entry)
             ++pieces;
         const ShEntry &E = entries[B.entry];
-        splits[atomicAdd(&s_nsplit, 1)] = ShSplit{E.row0, E.nrows, B.kh, c, pieces, {}};
+        splits[atomicAdd(&s_nsplit, 1)] =
+            ShSplit{E.row0, E.nrows, B.kh * heads + (heads == 2 ? E.s0 & 1 : 0), c, pieces,
+                    heads == 2 ? E.s0 & kShPair : 0, {}};
     }
     __syncthreads();
     if (tid == 0) {
@@ -285,6 +302,7 @@ constexpr int kShRing = 4;                     // items in the ring that warp 0 
 constexpr int kShReaders = 1 + 1 + 8;          // Q producer, MMA issuer, softmax warps
 
 // The part of an item (an entry for one kv head) that this CTA computes, as the roles read it.
+template <bool LAST>
 struct __align__(16) ShItem {
     int32_t prow0, plen, row0, nrows;
     int32_t ka0, kb0, ka1, kb1;
@@ -293,9 +311,16 @@ struct __align__(16) ShItem {
     int32_t kh;
     int32_t slot;             // partial result this part goes to, or -1
     int32_t act[kShTiles];    // key tiles with keys for each query tile
-    int32_t more, pad[3];     // 0: no further item
+    int32_t more;             // 0: no further item
+    int32_t pair, pad[2];     // 1: query tile 1 holds tile 0's rows for the next kv head
 
-    __device__ int rows(int h, int bt) const { return h == 0 ? min(nrows, bt) : max(nrows - bt, 0); }
+    __device__ bool paired() const { return LAST && pair != 0; }
+    __device__ int rows(int h, int bt) const
+    {
+        return h == 0 || paired() ? min(nrows, bt) : max(nrows - bt, 0);
+    }
+    __device__ int first_row(int h, int bt) const { return paired() ? row0 : row0 + h * bt; }
+    __device__ int head(int h) const { return paired() ? kh + h : kh; }
     __device__ int ka(int h) const { return h == 0 ? ka0 : ka1; }
     __device__ int kb(int h) const { return h == 0 ? kb0 : kb1; }
     // first packed key row of own tile j (j >= npt)
@@ -320,7 +345,7 @@ struct __align__(16) ShItem {
         return pre + max(min(te, hi) - max(tb, lo), 0);
     }
 };
-static_assert(sizeof(ShItem) == 80, "five 16-byte stores");
+static_assert(sizeof(ShItem<false>) == 80, "five 16-byte stores");
 
 template <int D>
 struct ShCfg {
@@ -335,7 +360,7 @@ struct ShCfg {
     // item_full[kShRing] item_empty[kShRing]
     static constexpr int kNumBars = 13 + 2 * kStages + 2 * kShRing;
     static constexpr int kOffItems = (kOffBar + kNumBars * 8 + 15) / 16 * 16;
-    static constexpr int kOffMisc = kOffItems + kShRing * static_cast<int>(sizeof(ShItem));
+    static constexpr int kOffMisc = kOffItems + kShRing * static_cast<int>(sizeof(ShItem<false>));
     static constexpr int kSmemBytes = kOffMisc + 16 + 1024;  // + slack for 1024-byte alignment
     static constexpr int kThreads = 384;
     // Register split, as in the attention kernel of the other modes: compiled for kRegsLaunch,
@@ -518,7 +543,7 @@ __device__ __forceinline__ void capped4_any(float *s, float cap_in, float cap_lo
 enum : int { kShPlain = 0, kShCapped = 1, kShCappedFixed = 2 };
 constexpr float kShCapFixed = 80.f;
 
-template <int D, int MODE>
+template <int D, int MODE, bool LAST>
 __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
     shared_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_pk,
@@ -532,7 +557,8 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
     uint64_t *mma_final = bars + 12;
     uint64_t *kv_full = bars + 13, *kv_empty = kv_full + C::kStages;
     uint64_t *item_full = kv_empty + C::kStages, *item_empty = item_full + kShRing;
-    ShItem *ring = reinterpret_cast<ShItem *>(smem + C::kOffItems);
+    using Item = ShItem<LAST>;
+    Item *ring = reinterpret_cast<Item *>(smem + C::kOffItems);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kOffMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::kOffMisc + 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -620,12 +646,14 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
                     const bool more = before_end();
                     const uint32_t slot = n_items % kShRing;
                     if (!sh_wait(&item_empty[slot], ((n_items / kShRing) & 1) ^ 1, abort_flag)) break;
-                    ShItem I;
+                    Item I;
                     I.prow0 = e0.x; I.plen = e0.y; I.row0 = e0.z; I.nrows = e0.w;
                     I.ka0 = e1.x; I.kb0 = e1.y; I.ka1 = e1.z; I.kb1 = e1.w;
                     I.s0 = e2.x;
                     const int tiles = e2.y;
-                    I.kh = kh;
+                    const int code = LAST ? e2.x : 0;
+                    I.kh = LAST ? kh * p.heads + (code & 1) : kh;
+                    I.pair = code & kShPair;
                     I.npt = (I.plen + kShKeys - 1) >> kShKeysLog;
                     I.tb = tb;
                     I.te = kh == B.kh && entry == B.entry ? B.tile : tiles;
@@ -641,7 +669,7 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
                         dst[1] = make_int4(I.ka0, I.kb0, I.ka1, I.kb1);
                         dst[2] = make_int4(I.s0, I.tb, I.te, I.npt);
                         dst[3] = make_int4(I.kh, I.slot, I.act[0], I.act[1]);
-                        dst[4] = make_int4(I.more, 0, 0, 0);
+                        dst[4] = make_int4(I.more, I.pair, 0, 0);
                         mbar_arrive(&item_full[slot]);
                         ++n_items;
                     }
@@ -654,26 +682,37 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
                     }
                     if (before_end()) fetch();
                     if (tiles == 0) continue;
-                    for (int j = I.tb; j < I.te && ok; ++j) {
+                    // In the order in which the products take them: K of a tile, then V; paired, K of the first
+                    // tile for both heads, then V of a tile and K of the next for one head and for the other.
+                    auto load = [&](int j, int kv, int kh_kv) {
                         const bool pre = j < I.npt;
                         const int row = pre ? I.prow0 + j * kShKeys : I.own_base(j);
-#pragma unroll 1
-                        for (int kv = 0; kv < 2; ++kv) {
-                            if (!sh_wait(&kv_empty[st], ph, abort_flag)) {
-                                ok = false;
-                                break;
-                            }
-                            uint8_t *dst = smem + C::kOffKV + st * C::kTileBytes;
-                            const CUtensorMap *tm = kv == 0 ? (pre ? &tm_pk : &tm_k) : (pre ? &tm_pv : &tm_v);
-                            mbar_arrive_expect_tx(&kv_full[st], C::kTileBytes);
+                        ok = sh_wait(&kv_empty[st], ph, abort_flag);
+                        if (!ok) return;
+                        uint8_t *dst = smem + C::kOffKV + st * C::kTileBytes;
+                        const CUtensorMap *tm = kv == 0 ? (pre ? &tm_pk : &tm_k) : (pre ? &tm_pv : &tm_v);
+                        mbar_arrive_expect_tx(&kv_full[st], C::kTileBytes);
 #pragma unroll
-                            for (int b = 0; b < C::kNB; ++b)
-                                tma_load_3d(dst + b * C::kBox, tm, &kv_full[st], b * 64, I.kh, row, pol);
-                            if (used < C::kStages) ++used;
-                            if (++st == C::kStages) {
-                                st = 0;
-                                ph ^= 1u;
-                            }
+                        for (int b = 0; b < C::kNB; ++b)
+                            tma_load_3d(dst + b * C::kBox, tm, &kv_full[st], b * 64, kh_kv, row, pol);
+                        if (used < C::kStages) ++used;
+                        if (++st == C::kStages) {
+                            st = 0;
+                            ph ^= 1u;
+                        }
+                    };
+                    if (I.paired()) {
+                        const int loads = 4 * (I.te - I.tb);
+#pragma unroll 1
+                        for (int i = 0; i < loads && ok; ++i) {
+                            const bool ends = i < 2 || i >= loads - 2;
+                            const int kv = i >= 2 && (i >= loads - 2 || !(i & 1)) ? 1 : 0;
+                            load(I.tb + (i < 2 ? 0 : ((i - 2) >> 2) + 1 - kv), kv, I.kh + ((ends ? i : (i - 2) >> 1) & 1));
+                        }
+                    } else {
+                        for (int j = I.tb; j < I.te && ok; ++j) {
+#pragma unroll 1
+                            for (int kv = 0; kv < 2 && ok; ++kv) load(j, kv, I.kh);
                         }
                     }
                     if (!ok) break;
@@ -693,6 +732,7 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
                     const uint32_t slot = it % kShRing;
                     if (!sh_wait(&item_full[slot], (it / kShRing) & 1, abort_flag) || !ring[slot].more) break;
                     const int row0 = ring[slot].row0, kh = ring[slot].kh;
+                    const int next_row = ring[slot].paired() ? 0 : p.bt, next_head = ring[slot].paired() ? 1 : 0;
                     const uint32_t have = (ring[slot].act[0] > 0 ? 1u : 0u) | (ring[slot].act[1] > 0 ? 2u : 0u);
                     mbar_arrive(&item_empty[slot]);
                     bool ok = true;
@@ -701,7 +741,7 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
                     for (int h = 0; h < kShTiles; ++h)
                         if ((have >> h) & 1u) {
 #pragma unroll 1
-                            for (int b = 0; b < C::kNB; ++b) tma_prefetch_4d(&tm_q, b * 64, 0, kh, row0 + h * p.bt);
+                            for (int b = 0; b < C::kNB; ++b) tma_prefetch_4d(&tm_q, b * 64, 0, kh + h * next_head, row0 + h * next_row);
                         }
 #pragma unroll 1
                     for (int h = 0; h < kShTiles; ++h) {
@@ -714,7 +754,7 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
 #pragma unroll 1
                         for (int b = 0; b < C::kNB; ++b)
                             tma_load_4d(smem + C::kOffQ + h * C::kTileBytes + b * C::kBox, &tm_q, &q_full[h], b * 64, 0,
-                                        kh, row0 + h * p.bt, pol);
+                                        kh + h * next_head, row0 + h * next_row, pol);
                         if ((used >> h) & 1u) par ^= 1u << h;
                         used |= 1u << h;
                     }
@@ -788,78 +828,150 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
                                           kIdescQK0 | (static_cast<uint32_t>(2 * sc) << 17), &s_full[h]);
                     return true;
                 };
-                // the P.V of an item's last tile
-                auto finish = [&]() {
-                    if (outs == 0) return true;
-                    if (!sh_wait(&kv_full[vs], vph, abort_flag)) return false;
-#pragma unroll 1
-                    for (int h = 0; h < kShTiles; ++h) {
-                        if (!turn(h, 0, 0)) return false;
-                        if ((outs >> h) & 1u) mma_commit(&o_full[h]);
-                    }
-                    mma_commit(&kv_empty[vs]);
-                    return true;
-                };
-                for (uint32_t it = 0;; ++it) {
-                    const uint32_t slot = it % kShRing;
-                    if (!sh_wait(&item_full[slot], (it / kShRing) & 1, abort_flag)) { ok = false; break; }
-                    const ShItem &I = ring[slot];
-                    // the previous item's last P.V, which do not wait for this one's Q
-                    ok = finish();
-                    if (!ok || !I.more) break;
-                    const int tb = I.tb, te = I.te, whole_end = I.plen >> kShKeysLog;
-                    const uint32_t have = (I.act[0] > 0 ? 1u : 0u) | (I.act[1] > 0 ? 2u : 0u);
-                    auto steps_of = [&](int j) {
-                        if (j < whole_end) return ((have & 1u) ? 8u : 0u) | ((have & 2u) ? 8u << 8 : 0u);
-                        uint32_t r = 0;
-#pragma unroll 1
-                        for (int h = 0; h < kShTiles; ++h)
-                            if ((have >> h) & 1u) r |= static_cast<uint32_t>((max(I.keys_of(h, j), 0) + 15) >> 4) << (8 * h);
-                        return r;
-                    };
-                    uint32_t cur = steps_of(tb);
-                    uint32_t ks = st;
-                    // ---- the first tile
-                    ok = sh_wait(&kv_full[ks], ph, abort_flag);
-                    prev = 0;
-                    fresh = 3u;
-                    outs = have;
-#pragma unroll 1
-                    for (int h = 0; h < kShTiles && ok; ++h) {
-                        if (!((have >> h) & 1u)) continue;
-                        ok = sh_wait(&q_full[h], (q_par >> h) & 1u, abort_flag);
-                        q_par ^= 1u << h;
-                        if (ok) {
-                            tc_fence_after();
-                            turn(h, cur, ks);
-                        }
-                    }
-                    if (!ok) break;
-                    mma_commit(&kv_empty[ks]);
-                    bump();
-                    vs = st;
-                    vph = ph;
-                    bump();
-                    prev = cur;
-                    // ---- the others
-                    for (int j = tb + 1; j < te; ++j) {
-                        cur = steps_of(j);
-                        ks = st;
-                        ok = sh_wait(&kv_full[vs], vph, abort_flag) && sh_wait(&kv_full[ks], ph, abort_flag) &&
-                             turn(0, cur, ks) && turn(1, cur, ks);
+                if constexpr (LAST) {
+                    // The stages come in the order of the turns.  A turn is in the code twice only: few rows
+                    // leave the tensor core time, and the loops of all roles share the instruction cache.
+                    bool was_pair = false;
+                    for (uint32_t it = 0; ok; ++it) {
+                        const uint32_t slot = it % kShRing;
+                        ok = sh_wait(&item_full[slot], (it / kShRing) & 1, abort_flag);
                         if (!ok) break;
+                        const Item &I = ring[slot];
+                        // ---- the previous item's last P.V, which do not wait for this one's Q
+#pragma unroll 1
+                        for (int h = 0; h < kShTiles && outs != 0; ++h) {
+                            vs = st;
+                            ok = (h > 0 && !was_pair) || sh_wait(&kv_full[st], ph, abort_flag);
+                            ok = ok && turn(h, 0, 0);
+                            if (!ok) break;
+                            if ((outs >> h) & 1u) mma_commit(&o_full[h]);
+                            if (h == 1 || was_pair) {
+                                mma_commit(&kv_empty[st]);
+                                bump();
+                            }
+                        }
+                        if (!ok || !I.more) break;
+                        const int tb = I.tb, te = I.te, whole_end = I.plen >> kShKeysLog;
+                        const uint32_t have = (I.act[0] > 0 ? 1u : 0u) | (I.act[1] > 0 ? 2u : 0u);
+                        const bool pair = I.paired();
+                        was_pair = pair;
+                        prev = 0;
+                        fresh = 3u;
+                        outs = have;
+#pragma unroll 1
+                        for (int j = tb; j < te && ok; ++j) {
+                            uint32_t cur = 0;
+#pragma unroll 1
+                            for (int h = 0; h < kShTiles; ++h)
+                                if ((have >> h) & 1u)
+                                    cur |= (j < whole_end ? 8u : static_cast<uint32_t>((max(I.keys_of(h, j), 0) + 15) >> 4))
+                                           << (8 * h);
+                            uint32_t ks = 0;
+#pragma unroll 1
+                            for (int h = 0; h < kShTiles; ++h) {
+                                if (pair || h == 0) {
+                                    if (j > tb) {
+                                        vs = st;
+                                        ok = sh_wait(&kv_full[vs], ph, abort_flag);
+                                        bump();
+                                    }
+                                    ks = st;
+                                    ok = ok && sh_wait(&kv_full[ks], ph, abort_flag);
+                                    bump();
+                                }
+                                if (j == tb && ok && ((have >> h) & 1u)) {
+                                    ok = sh_wait(&q_full[h], (q_par >> h) & 1u, abort_flag);
+                                    q_par ^= 1u << h;
+                                    tc_fence_after();
+                                }
+                                ok = ok && turn(h, cur, ks);
+                                if (!ok) break;
+                                if (pair || h == 1) {
+                                    if (j > tb) mma_commit(&kv_empty[vs]);
+                                    mma_commit(&kv_empty[ks]);
+                                }
+                            }
+                            prev = cur;
+                        }
+                        if (!ok) break;
+                        if (have & 1u) mma_commit(&q_empty[0]);
+                        if (have & 2u) mma_commit(&q_empty[1]);
+                        mbar_arrive(&item_empty[slot]);
+                    }
+                } else {
+                    // the P.V of an item's last tile
+                    auto finish = [&]() {
+                        if (outs == 0) return true;
+                        if (!sh_wait(&kv_full[vs], vph, abort_flag)) return false;
+#pragma unroll 1
+                        for (int h = 0; h < kShTiles; ++h) {
+                            if (!turn(h, 0, 0)) return false;
+                            if ((outs >> h) & 1u) mma_commit(&o_full[h]);
+                        }
                         mma_commit(&kv_empty[vs]);
+                        return true;
+                    };
+                    for (uint32_t it = 0;; ++it) {
+                        const uint32_t slot = it % kShRing;
+                        if (!sh_wait(&item_full[slot], (it / kShRing) & 1, abort_flag)) { ok = false; break; }
+                        const Item &I = ring[slot];
+                        // the previous item's last P.V, which do not wait for this one's Q
+                        ok = finish();
+                        if (!ok || !I.more) break;
+                        const int tb = I.tb, te = I.te, whole_end = I.plen >> kShKeysLog;
+                        const uint32_t have = (I.act[0] > 0 ? 1u : 0u) | (I.act[1] > 0 ? 2u : 0u);
+                        auto steps_of = [&](int j) {
+                            if (j < whole_end) return ((have & 1u) ? 8u : 0u) | ((have & 2u) ? 8u << 8 : 0u);
+                            uint32_t r = 0;
+#pragma unroll 1
+                            for (int h = 0; h < kShTiles; ++h)
+                                if ((have >> h) & 1u) r |= static_cast<uint32_t>((max(I.keys_of(h, j), 0) + 15) >> 4) << (8 * h);
+                            return r;
+                        };
+                        uint32_t cur = steps_of(tb);
+                        uint32_t ks = st;
+                        // ---- the first tile
+                        ok = sh_wait(&kv_full[ks], ph, abort_flag);
+                        prev = 0;
+                        fresh = 3u;
+                        outs = have;
+#pragma unroll 1
+                        for (int h = 0; h < kShTiles && ok; ++h) {
+                            if (!((have >> h) & 1u)) continue;
+                            ok = sh_wait(&q_full[h], (q_par >> h) & 1u, abort_flag);
+                            q_par ^= 1u << h;
+                            if (ok) {
+                                tc_fence_after();
+                                turn(h, cur, ks);
+                            }
+                        }
+                        if (!ok) break;
                         mma_commit(&kv_empty[ks]);
                         bump();
                         vs = st;
                         vph = ph;
                         bump();
                         prev = cur;
+                        // ---- the others
+                        for (int j = tb + 1; j < te; ++j) {
+                            cur = steps_of(j);
+                            ks = st;
+                            ok = sh_wait(&kv_full[vs], vph, abort_flag) && sh_wait(&kv_full[ks], ph, abort_flag) &&
+                                 turn(0, cur, ks) && turn(1, cur, ks);
+                            if (!ok) break;
+                            mma_commit(&kv_empty[vs]);
+                            mma_commit(&kv_empty[ks]);
+                            bump();
+                            vs = st;
+                            vph = ph;
+                            bump();
+                            prev = cur;
+                        }
+                        if (!ok) break;
+                        if (have & 1u) mma_commit(&q_empty[0]);
+                        if (have & 2u) mma_commit(&q_empty[1]);
+                        mbar_arrive(&item_empty[slot]);
                     }
-                    if (!ok) break;
-                    if (have & 1u) mma_commit(&q_empty[0]);
-                    if (have & 2u) mma_commit(&q_empty[1]);
-                    mbar_arrive(&item_empty[slot]);
                 }
                 mma_commit(mma_final);           // every MMA issued completes before TMEM is released
                 mbar_wait_drain(mma_final, 0);
@@ -884,13 +996,13 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
         for (uint32_t it = 0; ok; ++it) {
             const uint32_t rslot = it % kShRing;
             if (!sh_warp_wait(&item_full[rslot], (it / kShRing) & 1, abort_flag)) break;
-            const ShItem &I = ring[rslot];
+            const Item &I = ring[rslot];
             if (!I.more) break;
             const int act = I.act[h];
             const int rows_h = I.rows(h, p.bt);
             const bool live = lr < p.bt && lr < rows_h;
             const bool warp_live = __any_sync(0xffffffffu, live);
-            const int row = I.row0 + h * p.bt + lr;        // packed token, or sample
+            const int row = I.first_row(h, p.bt) + lr;     // packed token, or sample
             float m = MODE == kShCappedFixed ? 0.f : -INFINITY;      // running maximum, base-2 units
             float l = 0.f;             // running sum of 2^(x - m)
             float fix = 0.f;           // what rounding the tiles' largest weights to bf16 adds to l
@@ -933,7 +1045,7 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
             // own keys this row sees: [lo, hi)
             int lo = 0, hi = 0;
             if (act > 0 && I.te > I.npt) {
-                if (p.last) {
+                if constexpr (LAST) {
                     if (live) {
                         lo = p.cu_seqlens[row];
                         hi = p.cu_seqlens[row + 1];
@@ -982,7 +1094,7 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
                 // Keys behind the last one that any row of the item sees (a later token, another
                 // request's rows) have weight 0, but 0 * Inf is NaN: their V rows become zeros.
                 if (zero_v) {
-                    const uint32_t nv = n + 2 * (j - tb) + 1;
+                    const uint32_t nv = n + (I.paired() ? 4 * (j - tb) + 2 + (j == I.te - 1 ? h : 2 * h) : 2 * (j - tb) + 1);
                     const uint32_t vs = nv % C::kStages;
                     if (!sh_warp_wait(&kv_full[vs], (nv / C::kStages) & 1, abort_flag)) { ok = false; break; }
                     const int nkeys = I.keys(j);
@@ -1179,10 +1291,10 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
                 ++done;
                 ++tiles;
             }
-            n += 2 * (I.te - tb);
+            n += (I.paired() ? 4 : 2) * (I.te - tb);
             if (!ok) break;
             // ------------------------------------------------------------ output of the item
-            const int slot = I.slot, kh = I.kh;
+            const int slot = I.slot, kh = I.head(h);
             __syncwarp();
             if (lane == 0) mbar_arrive(&item_empty[rslot]);    // the item has been read
             if (act > 0) {
@@ -1261,7 +1373,8 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const ShParam
     if (!plan_ready(p, &other) || split >= p.hdr[kShHdrSplits]) return;
     const int h = r / kShRows, trow = r - h * kShRows;
     const int lr = trow / p.g, hh = trow - lr * p.g;
-    if (lr >= p.bt || h * p.bt + lr >= S.nrows) return;
+    const int row = S.pair ? lr : h * p.bt + lr, kh = S.pair ? S.kh + h : S.kh;
+    if (lr >= p.bt || row >= S.nrows) return;
     constexpr int E = D / 32;
     // piece 0 is in the first CTA's second slot, the others in their CTA's first: slot0 + 2 t - (t > 0)
     const int64_t row0 = static_cast<int64_t>(2 * S.cta + 1) * (kShTiles * kShRows) + r;
@@ -1301,20 +1414,20 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const ShParam
         for (int e = 0; e < E; ++e) acc[e] = fmaf(wt, written ? o[e] : 0.f, acc[e]);
     }
     const float inv = 1.f / (sum + fix);
-    const int64_t orow = (static_cast<int64_t>(S.row0) + h * p.bt + lr) * p.Hq + S.kh * p.g + hh;
+    const int64_t orow = (static_cast<int64_t>(S.row0) + row) * p.Hq + kh * p.g + hh;
     uint32_t *dst = reinterpret_cast<uint32_t *>(p.out + orow * D + lane * E);
 #pragma unroll
     for (int e = 0; e < E / 2; ++e) dst[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
     if (p.lse && lane == 0) p.lse[orow] = (mx + __log2f(sum)) * 0.69314718055994530942f;
 }
 
-template <int D, int MODE>
+template <int D, int MODE, bool LAST>
 cudaError_t launch_one(const CUtensorMap &tm_q, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
                        const CUtensorMap &tm_pk, const CUtensorMap &tm_pv, const ShParams &p, int grid, bool join,
                        cudaStream_t stream)
 {
     using C = ShCfg<D>;
-    auto kern = shared_attn_kernel<D, MODE>;
+    auto kern = shared_attn_kernel<D, MODE, LAST>;
     static std::atomic<uint64_t> smem_done{0}, split_done{0};
     cudaError_t e = ensure_smem_attribute(kern, C::kSmemBytes, smem_done);
     if (e != cudaSuccess) return e;
@@ -1329,23 +1442,32 @@ cudaError_t launch_one(const CUtensorMap &tm_q, const CUtensorMap &tm_k, const C
 
 }  // namespace
 
+int shared_heads(const ShProblem &pb)
+{
+    if (!pb.last || pb.Hkv % 2 != 0) return 1;
+    const int64_t tiles = static_cast<int64_t>(pb.total_prefix) / kShKeys + pb.total_tokens / kShKeys;
+    return 10 * tiles * (pb.Hkv / 2) >= kShMaxCtas * ceil_div(pb.max_prefix_len, kShKeys) ? 2 : 1;
+}
+
 ShLayout shared_layout(const ShProblem &pb)
 {
     ShLayout L;
     const int bt = kShRows / (pb.Hq / pb.Hkv);
     const int64_t rows = pb.last ? pb.num_seqs : pb.total_tokens;
+    const int most = pb.last && pb.Hkv % 2 == 0 ? 2 : 1;       // of shared_heads
     L.max_entries = rows / (kShTiles * bt) + pb.num_groups + 1;
     // most key tiles of an entry: its prefix, and the own keys of the rows it holds (prefill: one
     // sample's start to the entry's last row; last token: whole samples)
     int64_t own = pb.last ? static_cast<int64_t>(kShTiles) * bt * pb.max_seqlen : pb.max_seqlen + kShTiles * bt;
     if (own > pb.total_tokens) own = pb.total_tokens;
     const int64_t tiles = ceil_div(pb.max_prefix_len, kShKeys) + ceil_div(own, kShKeys);
-    // a cut leaves at least kShSplitMin / 2 tiles on either side
+    L.units = L.max_entries * pb.Hkv * (tiles + 1);
     L.slots = 0;
-    if (tiles >= kShSplitMin) {
-        const int64_t ctas = ceil_div(L.max_entries * pb.Hkv * (tiles + 1), kShSplitMin);
+    if (tiles >= kShSplitMin) {                // (shorter ranges are not cut)
+        const int64_t ctas = ceil_div(L.units * most, kShSplitMin);
         L.slots = 2 * (ctas < kShMaxCtas ? ctas : kShMaxCtas);
     }
+    L.max_entries *= most;
     auto al = [](size_t b) { return (b + 255) & ~size_t(255); };
     L.entries = 256;
     L.starts = L.entries + al(L.max_entries * sizeof(ShEntry));
@@ -1369,7 +1491,7 @@ cudaError_t launch_shared_plan(const ShProblem &pb, const ShLayout &lay, void *w
     return launch_dependent(shared_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, pb, shared_key(pb, grid),
                             kShRows / (pb.Hq / pb.Hkv), reinterpret_cast<int32_t *>(ws),
                             reinterpret_cast<ShEntry *>(ws + lay.entries), reinterpret_cast<ShStart *>(ws + lay.starts),
-                            reinterpret_cast<ShSplit *>(ws + lay.splits), grid, lay.slots > 0 ? 1 : 0, dev_status);
+                            reinterpret_cast<ShSplit *>(ws + lay.splits), grid, lay.slots > 0 ? 1 : 0, shared_heads(pb), dev_status);
 }
 
 cudaError_t launch_shared_attn(int head_dim, bool is_capped, const CUtensorMap &tm_q, const CUtensorMap &tm_k,
@@ -1377,8 +1499,10 @@ cudaError_t launch_shared_attn(int head_dim, bool is_capped, const CUtensorMap &
                                const ShParams &p, int grid, bool join, cudaStream_t stream)
 {
     const int mode = !is_capped ? kShPlain : p.cap_log2 <= kShCapFixed ? kShCappedFixed : kShCapped;
-#define BG_SHARED(DD, MM) \
-    if (head_dim == DD && mode == MM) return launch_one<DD, MM>(tm_q, tm_k, tm_v, tm_pk, tm_pv, p, grid, join, stream)
+#define BG_SHARED(DD, MM)                                                                                   \
+    if (head_dim == DD && mode == MM)                                                                       \
+        return p.last ? launch_one<DD, MM, true>(tm_q, tm_k, tm_v, tm_pk, tm_pv, p, grid, join, stream)      \
+                      : launch_one<DD, MM, false>(tm_q, tm_k, tm_v, tm_pk, tm_pv, p, grid, join, stream)
     BG_SHARED(128, kShPlain);
     BG_SHARED(128, kShCapped);
     BG_SHARED(128, kShCappedFixed);

@@ -25,20 +25,21 @@ struct __align__(16) ShEntry {
     int32_t row0, nrows;      // first row and number of rows
     int32_t ka0, kb0;         // own (packed) keys that tile 0's rows can see: [ka0, kb0)
     int32_t ka1, kb1;         // the same for tile 1 (empty when the entry has one tile)
-    int32_t s0;               // prefill: sample of the first row
+    int32_t s0;               // prefill: sample of the first row; last token: 0 or 1 (kv head of a pair) or kShPair
     int32_t tiles;            // key tiles: the prefix's, then those of the own keys
     int64_t pos;              // cost units of all entries before this one
 };
 static_assert(sizeof(ShEntry) == 48, "three 16-byte loads");
 
-// The first tile of a CTA's share of the work, in the order (kv head, entry, key tile).
+// The first tile of a CTA's share of the work, in the order (kv head or pair of them, entry, key tile).
 struct __align__(16) ShStart {
     int32_t kh, entry, tile, pad;
 };
 
-// An item whose key tiles are shared by `pieces` CTAs from `cta` on, for the join.
+// An item whose key tiles are shared by `pieces` CTAs from `cta` on, for the join; pair: of the kv heads
+// kh and kh + 1.
 struct __align__(16) ShSplit {
-    int32_t row0, nrows, kh, cta, pieces, pad[3];
+    int32_t row0, nrows, kh, cta, pieces, pair, pad[2];
 };
 
 // Header words at the start of the workspace; from kShHdrKey on the problem the plan is for, which
@@ -52,8 +53,11 @@ struct __align__(16) ShKey {
 struct ShLayout {
     size_t entries, starts, splits, part_l, part_o, total;
     int64_t max_entries;
+    int64_t units;            // cost units of the work at most, by single heads
     int64_t slots;            // partial results (two per CTA), or 0: no item can be split
 };
+
+constexpr int kShPair = 2;
 
 struct ShProblem {
     const int32_t *cu_seqlens, *cu_prefix, *cu_group;
@@ -63,11 +67,19 @@ struct ShProblem {
     int32_t last;             // 1: one query row per sample, 0: one per token
 };
 
+// kv heads that the work line takes at once: 2 pairs them.  In the last-token call a request has a row per
+// sample, often not enough for two query tiles; then two kv heads fill both, and the softmax of one runs
+// beside the products of the other.  Measured, 16 / 8 heads of 128: 32 requests of 15 samples over
+// 200-500 keys 53.0 us by single heads, 48.1 paired; 4 of 32 samples over 32768 keys 121 and 115.  Not
+// where the key ranges would be cut into more than about ten parts, whose joining takes what is won: one
+// request of 8 samples over 4096 keys 23.4 single, 26.4 paired; four of them 29.0 and 29.8.
+int shared_heads(const ShProblem &pb);
 ShLayout shared_layout(const ShProblem &pb);
 ShKey shared_key(const ShProblem &pb, int grid);
 
 struct ShParams {
     int32_t Hq, Hkv, g, bt;   // bt = rows of g heads per query tile
+    int32_t heads;            // shared_heads
     int32_t last, num_seqs;
     float scale_log2;         // plain scores: softmax scale * log2(e)
     float cap_in, cap_log2;   // capped scores: 2 log2(e) scale / cap, and cap * log2(e)

@@ -324,10 +324,7 @@ def test_key_offsets_past_32_bits():
     """A prefix cache of more than 2^32 elements, of which the last request's rows count."""
     import torch
     x = make(25, [65000, 300], [[3, 40], [20]], 8, 8, 128)
-    t, ws = device(x), workspace(x)
-    small = [torch.zeros((n, 8, 128), dtype=torch.bfloat16, device="cuda") for n in (63, 3)]
-    for last in (False, True):
-        call(x, t, last, small[last], ws=ws)
+    t = device(x)
     before = 65 * 65536                                     # rows of 65 requests without samples: 2^32 elements
     y = dict(x, cup=np.concatenate((np.arange(66) * 65536, before + x["cup"][1:])).astype(np.int32),
              cug=np.concatenate((np.zeros(65), x["cug"])).astype(np.int32), max_prefix=65536)
@@ -339,10 +336,11 @@ def test_key_offsets_past_32_bits():
         t[n] = big
     t.update({n: i32_dev(y[n]) for n in ("cup", "cug")})
     for last in (False, True):
-        out = torch.zeros_like(small[last])
+        out = torch.zeros((3 if last else 63, 8, 128), dtype=torch.bfloat16, device="cuda")
         st = torch.zeros(1, dtype=torch.int32, device="cuda")
         call(y, t, last, out, dev_status=st)
-        assert int(st.item()) == 0 and torch.equal(out, small[last])
+        assert int(st.item()) == 0
+        assert_close(from_dev(out), None, reference(x, last), "offsets past 32 bits")
 
 
 @pytest.mark.parametrize("last", [False, True], ids=["prefill", "last"])
@@ -404,3 +402,37 @@ def test_two_streams_and_shared_workspace_of_two_graphs():
             g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(o, r) for _, o, r in graphs)
+
+
+PAIRED = {
+    # most requests fill one query tile or less: two kv heads share an entry
+    "batch": ([300, 0, 129, 255, 64, 300], [[30, 5, 60], [64, 1], [17] * 9, [90, 80, 1], [128], [0, 3]]),
+    # entries of two tiles, of one (the rest of a request, its last rows), and of few rows
+    "tiles": ([10, 7, 0], [[3, 9, 5] * 23, [4, 2] * 65, [6]]),
+    # key ranges that several CTAs share
+    "cuts": ([2000] * 5 + [0, 1999], [[3, 40, 1]] * 7),
+}
+
+
+@pytest.mark.parametrize("softcap", [0.0, 30.0])
+@pytest.mark.parametrize("heads", [(16, 8, 128), (14, 2, 64), (32, 16, 64), (48, 24, 128)], ids=lambda h: "h%d_%d_d%d" % h)
+@pytest.mark.parametrize("packing", PAIRED)
+def test_last_token_of_paired_heads(packing, heads, softcap):
+    check(make(29, *PAIRED[packing], *heads), True, softcap=softcap, what=f"paired {packing} {heads}")
+
+
+def test_paired_heads_keep_non_finite_rows_in_their_request():
+    import torch
+    x = make(30, [145, 150, 177], [[20, 3] * 8, [9, 30] * 8, [70, 1] * 4], 16, 8, 128)
+    outs = []
+    for bad in (False, True):
+        t = device(x)
+        if bad:
+            for n, c in (("k", x["cu"][x["cug"]]), ("v", x["cu"][x["cug"]]), ("pk", x["cup"]), ("pv", x["cup"])):
+                t[n][c[1]:c[2]] = float("nan") if n != "v" else float("inf")
+        out = torch.zeros((len(x["cu"]) - 1, 16, 128), dtype=torch.bfloat16, device="cuda")
+        call(x, t, True, out)
+        outs.append(out)
+    b = x["cug"]
+    assert torch.equal(outs[0][:b[1]], outs[1][:b[1]]) and torch.equal(outs[0][b[2]:], outs[1][b[2]:])
+    assert torch.isnan(outs[1][b[1]:b[2]].float()).all()
