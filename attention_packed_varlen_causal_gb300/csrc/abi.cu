@@ -724,7 +724,9 @@ bg_status_t shared_impl(const ShProblem &pb, const void *q, const void *k, const
     p.splits = reinterpret_cast<const ShSplit *>(ws + lay.splits);
     p.part_o = reinterpret_cast<float *>(ws + lay.part_o);
     p.part_l = reinterpret_cast<float2 *>(ws + lay.part_l);
-    return launch_shared_attn(pb.head_dim, capped, tm_q, tm_k, tm_v, tm_pk, tm_pv, p, grid, lay.slots > 0, stream) ==
+    // many: with more than four CTAs to an item
+    const int join = lay.slots == 0 ? kShJoinNone : 4 * lay.items <= grid * p.heads ? kShJoinMany : kShJoinFew;
+    return launch_shared_attn(pb.head_dim, capped, tm_q, tm_k, tm_v, tm_pk, tm_pv, p, grid, join, stream) ==
                    cudaSuccess
                ? BG_OK
                : BG_ERR_CUDA;

@@ -1356,18 +1356,22 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
 // ------------------------------------------------------------------------------------ join
 // out = sum_i 2^(L_i - L) O_i / (1 + sum_i 2^(L_i - L) fix_i) with L = log2 sum_i 2^(L_i): the
 // pieces' own normalised outputs, in piece order.
-constexpr int kJoinThreads = 512;              // one warp per row
-constexpr int kJoinRows = kJoinThreads / 32;
+constexpr int kJoinThreads = 256;
 
-template <int D>
+// LANES of a row, AT_ONCE pieces of it under way.  Many rows of two or three pieces are bound by the
+// latencies of the few loads each needs, times the waves of CTAs: few lanes and registers per row.  Few
+// rows of many pieces leave the SMs empty: twice the lanes, more pieces at once (4 requests of 32 samples
+// over 32768 keys, 10 pieces: 114.4 us, 119.6 by the first form; 32 requests of 15 samples, last token:
+// 46.3 by the first, 47.3 by the second).
+template <int D, int LANES, int AT_ONCE>
 __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const ShParams p)
 {
     grid_dep_launch();
     grid_dep_wait();
-    constexpr int kParts = kShTiles * kShRows / kJoinRows;
+    constexpr int kRows = kJoinThreads / LANES, kParts = kShTiles * kShRows / kRows, N4 = D / (4 * LANES);
     const int split = static_cast<int>(blockIdx.x) / kParts;
-    const int lane = threadIdx.x & 31;
-    const int r = (static_cast<int>(blockIdx.x) - split * kParts) * kJoinRows + (threadIdx.x >> 5);
+    const int sub = threadIdx.x % LANES;
+    const int r = (static_cast<int>(blockIdx.x) - split * kParts) * kRows + threadIdx.x / LANES;
     const ShSplit S = p.splits[split];         // (not looked at unless it is one)
     bool other;
     if (!plan_ready(p, &other) || split >= p.hdr[kShHdrSplits]) return;
@@ -1375,55 +1379,75 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const ShParam
     const int lr = trow / p.g, hh = trow - lr * p.g;
     const int row = S.pair ? lr : h * p.bt + lr, kh = S.pair ? S.kh + h : S.kh;
     if (lr >= p.bt || row >= S.nrows) return;
-    constexpr int E = D / 32;
+    const unsigned lanes = ((1u << LANES) - 1u) << (threadIdx.x & (32 - LANES));      // of this row
     // piece 0 is in the first CTA's second slot, the others in their CTA's first: slot0 + 2 t - (t > 0)
     const int64_t row0 = static_cast<int64_t>(2 * S.cta + 1) * (kShTiles * kShRows) + r;
     auto row_of = [&](int t) { return row0 + (t > 0 ? 2 * t - 1 : 0) * (kShTiles * kShRows); };
+    float2 lf[AT_ONCE];
+    float4 o[AT_ONCE][N4];                     // float4 i of a lane is at 4 * (sub + LANES * i)
+    auto load = [&](int t0) {
+#pragma unroll
+        for (int k = 0; k < AT_ONCE; ++k) {
+            const int64_t at = row_of(min(t0 + k, S.pieces - 1));
+            lf[k] = t0 + k < S.pieces ? p.part_l[at] : make_float2(-INFINITY, 0.f);
+            const float4 *src = reinterpret_cast<const float4 *>(p.part_o + at * D) + sub;
+#pragma unroll
+            for (int i = 0; i < N4; ++i) o[k][i] = src[LANES * i];
+        }
+    };
+    load(0);                                   // under way while the maximum is found
     float mx = -INFINITY;
     bool nan = false;
 #pragma unroll 1
-    for (int t = lane; t < S.pieces; t += 32) {
+    for (int t = sub; t < S.pieces; t += LANES) {
         const float lt = p.part_l[row_of(t)].x;
         mx = fmaxf(mx, lt);
         nan = nan || lt != lt;
     }
-    nan = __any_sync(0xffffffffu, nan);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    for (int w = LANES / 2; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(lanes, mx, w));
+    nan = (__ballot_sync(lanes, nan) & lanes) != 0;
     if (mx == -INFINITY && !nan) {             // no piece has a key for this row
-        if (lane == 0 && p.dev_status) atomicOr(p.dev_status, BG_DEVSTAT_EMPTY_ROW);
+        if (sub == 0 && p.dev_status) atomicOr(p.dev_status, BG_DEVSTAT_EMPTY_ROW);
         return;
     }
-    float sum = 0.f, fix = 0.f, acc[E];
+    float sum = 0.f, fix = 0.f;
+    float4 acc[N4];
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll 4
-    for (int t = 0; t < S.pieces; ++t) {
-        const int64_t at = row_of(t);
-        const float2 lf = p.part_l[at];
-        float o[E];
-        if constexpr (E == 4)
-            *reinterpret_cast<float4 *>(o) = *reinterpret_cast<const float4 *>(p.part_o + at * D + lane * E);
-        else
-            *reinterpret_cast<float2 *>(o) = *reinterpret_cast<const float2 *>(p.part_o + at * D + lane * E);
-        const bool written = lf.x != -INFINITY;      // else part_o holds anything
-        const float wt = written ? ex2(lf.x - mx) : 0.f;
-        sum += wt;
-        fix = fmaf(wt, lf.y, fix);
+    for (int i = 0; i < N4; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int t0 = 0;;) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = fmaf(wt, written ? o[e] : 0.f, acc[e]);
+        for (int k = 0; k < AT_ONCE; ++k) {
+            if (lf[k].x == -INFINITY) continue;              // not written: part_o holds anything
+            const float wt = ex2(lf[k].x - mx);
+            sum += wt;
+            fix = fmaf(wt, lf[k].y, fix);
+#pragma unroll
+            for (int i = 0; i < N4; ++i) {
+                acc[i].x = fmaf(wt, o[k][i].x, acc[i].x);
+                acc[i].y = fmaf(wt, o[k][i].y, acc[i].y);
+                acc[i].z = fmaf(wt, o[k][i].z, acc[i].z);
+                acc[i].w = fmaf(wt, o[k][i].w, acc[i].w);
+            }
+        }
+        t0 += AT_ONCE;
+        if (t0 >= S.pieces) break;
+        load(t0);
     }
     const float inv = 1.f / (sum + fix);
     const int64_t orow = (static_cast<int64_t>(S.row0) + row) * p.Hq + kh * p.g + hh;
-    uint32_t *dst = reinterpret_cast<uint32_t *>(p.out + orow * D + lane * E);
+    uint2 *dst = reinterpret_cast<uint2 *>(p.out + orow * D) + sub;
 #pragma unroll
-    for (int e = 0; e < E / 2; ++e) dst[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-    if (p.lse && lane == 0) p.lse[orow] = (mx + __log2f(sum)) * 0.69314718055994530942f;
+    for (int i = 0; i < N4; ++i)
+        dst[LANES * i] = make_uint2(pack_bf16x2(acc[i].x * inv, acc[i].y * inv),
+                                         pack_bf16x2(acc[i].z * inv, acc[i].w * inv));
+    if (p.lse && sub == 0) p.lse[orow] = (mx + __log2f(sum)) * 0.69314718055994530942f;
 }
 
 template <int D, int MODE, bool LAST>
 cudaError_t launch_one(const CUtensorMap &tm_q, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
-                       const CUtensorMap &tm_pk, const CUtensorMap &tm_pv, const ShParams &p, int grid, bool join,
+                       const CUtensorMap &tm_pk, const CUtensorMap &tm_pv, const ShParams &p, int grid, int join,
                        cudaStream_t stream)
 {
     using C = ShCfg<D>;
@@ -1434,10 +1458,13 @@ cudaError_t launch_one(const CUtensorMap &tm_q, const CUtensorMap &tm_k, const C
     e = check_register_split(kern, C::kThreads, C::kSplitRegs, split_done);
     if (e != cudaSuccess) return e;
     e = launch_dependent(kern, dim3(grid), dim3(C::kThreads), C::kSmemBytes, stream, tm_q, tm_k, tm_v, tm_pk, tm_pv, p);
-    if (e != cudaSuccess || !join) return e;
+    if (e != cudaSuccess || join == kShJoinNone) return e;
     // at most one cut item per CTA
-    return launch_dependent(shared_join_kernel<D>, dim3(grid * (kShTiles * kShRows / kJoinRows)), dim3(kJoinThreads), 0,
-                            stream, p);
+    constexpr int kFew = 8, kMany = 16;
+    const bool many = join == kShJoinMany;
+    return launch_dependent(many ? shared_join_kernel<D, kMany, 4> : shared_join_kernel<D, kFew, 2>,
+                            dim3(grid * (kShTiles * kShRows * (many ? kMany : kFew) / kJoinThreads)),
+                            dim3(kJoinThreads), 0, stream, p);
 }
 
 }  // namespace
@@ -1461,7 +1488,8 @@ ShLayout shared_layout(const ShProblem &pb)
     int64_t own = pb.last ? static_cast<int64_t>(kShTiles) * bt * pb.max_seqlen : pb.max_seqlen + kShTiles * bt;
     if (own > pb.total_tokens) own = pb.total_tokens;
     const int64_t tiles = ceil_div(pb.max_prefix_len, kShKeys) + ceil_div(own, kShKeys);
-    L.units = L.max_entries * pb.Hkv * (tiles + 1);
+    L.items = L.max_entries * pb.Hkv;
+    L.units = L.items * (tiles + 1);
     L.slots = 0;
     if (tiles >= kShSplitMin) {                // (shorter ranges are not cut)
         const int64_t ctas = ceil_div(L.units * most, kShSplitMin);
@@ -1496,7 +1524,7 @@ cudaError_t launch_shared_plan(const ShProblem &pb, const ShLayout &lay, void *w
 
 cudaError_t launch_shared_attn(int head_dim, bool is_capped, const CUtensorMap &tm_q, const CUtensorMap &tm_k,
                                const CUtensorMap &tm_v, const CUtensorMap &tm_pk, const CUtensorMap &tm_pv,
-                               const ShParams &p, int grid, bool join, cudaStream_t stream)
+                               const ShParams &p, int grid, int join, cudaStream_t stream)
 {
     const int mode = !is_capped ? kShPlain : p.cap_log2 <= kShCapFixed ? kShCappedFixed : kShCapped;
 #define BG_SHARED(DD, MM)                                                                                   \

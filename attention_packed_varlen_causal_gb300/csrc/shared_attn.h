@@ -53,7 +53,7 @@ struct __align__(16) ShKey {
 struct ShLayout {
     size_t entries, starts, splits, part_l, part_o, total;
     int64_t max_entries;
-    int64_t units;            // cost units of the work at most, by single heads
+    int64_t items, units;     // items and cost units of the work at most, by single heads
     int64_t slots;            // partial results (two per CTA), or 0: no item can be split
 };
 
@@ -96,10 +96,13 @@ struct ShParams {
     float2 *part_l;           // [slot][256 rows] log2 sums, and what the weights' rounding adds to a sum of 1
 };
 
+// How partial results are joined: there are none, an item has a few, or many.
+enum : int { kShJoinNone = 0, kShJoinFew = 1, kShJoinMany = 2 };
+
 cudaError_t launch_shared_plan(const ShProblem &pb, const ShLayout &lay, void *workspace, int grid,
                                int32_t *dev_status, cudaStream_t stream);
 cudaError_t launch_shared_attn(int head_dim, bool capped, const CUtensorMap &tm_q, const CUtensorMap &tm_k,
                                const CUtensorMap &tm_v, const CUtensorMap &tm_pk, const CUtensorMap &tm_pv,
-                               const ShParams &p, int grid, bool join, cudaStream_t stream);
+                               const ShParams &p, int grid, int join, cudaStream_t stream);
 
 }  // namespace bg
