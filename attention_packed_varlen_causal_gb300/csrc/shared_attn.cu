@@ -82,8 +82,11 @@ __device__ int sample_of(const int32_t *cu, int s, int end, int row)
     return s;
 }
 
-// Cost of an entry in units of one key tile: its tiles, and one for loading Q and storing the rows.
-__device__ __forceinline__ int entry_units(const ShEntry &E) { return E.tiles > 0 ? E.tiles + 1 : 0; }
+// Cost of an entry in units of one key tile: its tiles, and two for loading Q and storing the rows (one:
+// 16 samples over 8000 keys 400 us instead of 397, one request of 8 over 4096 keys 23.3 instead of 21.8; 24
+// requests of 31 capped samples, last token, 37.5 instead of 39.4).
+constexpr int kItemUnits = 2;
+__device__ __forceinline__ int entry_units(const ShEntry &E) { return E.tiles > 0 ? E.tiles + kItemUnits : 0; }
 
 __global__ void __launch_bounds__(kPlanThreads)
     shared_plan_kernel(const ShProblem pb, const ShKey key, int bt, int32_t *hdr, ShEntry *__restrict__ entries,
@@ -242,8 +245,12 @@ __global__ void __launch_bounds__(kPlanThreads)
             S.entry = lo;
             const int n = entries[lo].tiles;
             const int into = static_cast<int>(u - pos_of(lo));
-            // a cut near an end of the item, or through a short one, moves to the end that is nearer
-            const int least = max(split_min / 2, static_cast<int>(min(work / ctas / 32, static_cast<int64_t>(n))));
+            // A cut near an end of the item moves to that end, and so does every cut through an item that is
+            // short next to a share: its partial results cost more than the lesser balance (32 requests of
+            // 15 samples over 200-500 keys, 10 items to a share: 159.1 us when cut, 156.4 when not; with a
+            // limit of a sixth of a share 7 samples over 1-500 keys lose 2%).
+            const int64_t share = work / ctas;
+            const int least = n * 10 <= share ? n : max(split_min / 2, static_cast<int>(min(share / 32, static_cast<int64_t>(n))));
             S.tile = into;
             if (!can_split || into < least || n - into < least) {
                 S.tile = 0;
@@ -1489,9 +1496,9 @@ ShLayout shared_layout(const ShProblem &pb)
     if (own > pb.total_tokens) own = pb.total_tokens;
     const int64_t tiles = ceil_div(pb.max_prefix_len, kShKeys) + ceil_div(own, kShKeys);
     L.items = L.max_entries * pb.Hkv;
-    L.units = L.items * (tiles + 1);
+    L.units = L.items * (tiles + kItemUnits);
     L.slots = 0;
-    if (tiles >= kShSplitMin) {                // (shorter ranges are not cut)
+    if (tiles >= kShSplitTiles) {
         const int64_t ctas = ceil_div(L.units * most, kShSplitMin);
         L.slots = 2 * (ctas < kShMaxCtas ? ctas : kShMaxCtas);
     }

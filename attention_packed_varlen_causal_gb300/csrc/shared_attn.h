@@ -15,7 +15,13 @@ constexpr int kShKeys = 128;          // keys per K/V tile
 constexpr int kShRows = 128;          // query rows (token, head) per tile = TMEM lanes
 constexpr int kShTiles = 2;           // query tiles per work item
 constexpr int kShMaxCtas = 160;       // CTAs of the attention kernel at most (one per SM: GB300 has 152)
-constexpr int kShSplitMin = 4;        // cost units per CTA below which fewer CTAs share the work
+// Cost units per CTA below which fewer CTAs share the work (one request of 8 samples over 4096 keys, last
+// token: 21.9 us with 4, 22.3 with 6, 27.3 with 8).
+constexpr int kShSplitMin = 4;
+// Where no entry has this many key tiles none is cut: the join's launch takes longer than a shorter range
+// cut in two saves (one request of 15 samples over 400 keys, 5 tiles: 24.2 us cut, 20.8 not; 2 samples over
+// 1034 keys, 9 tiles: 27.5 cut, 33.1 not).
+constexpr int kShSplitTiles = 8;
 
 // One work entry: kShTiles tiles of query rows of one request against its keys; an entry for one
 // kv head is an item.  Rows are (row, head of the kv head) pairs, row-major; "row" is a token
