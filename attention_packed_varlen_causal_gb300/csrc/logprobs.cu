@@ -7,7 +7,7 @@
 //     logprob(t) = d_t - ln Z
 //     entropy    = ln Z - sum_v e^(d_v) d_v / Z          (every term of the sum has one sign)
 //     top        = the K largest logits, equal ones by the smaller index, as (v, d_v - ln Z)
-// Only the row's bytes bound it, so everything comes out of one pass over them, by a team of 4 warps
+// Only the row's bytes bound it, so everything comes out of one pass over them, by a team of 4 or 8 warps
 // or of the 16 of a CTA (with fewer rows than CTAs, a cluster of up to 8 CTAs):
 //   pass    every lane keeps a running maximum with Z and the entropy's sum relative to it, and in
 //           shared memory the maximum of each batch of 64 bytes it read, rounded up to bf16; bulk
@@ -21,7 +21,7 @@
 // instead.  Two CTAs of 16 warps per SM keep 64 KB of copies in flight; what is left to the bound is
 // issue slots (about 9 instructions per logit and lane, the K best among them): 8192 rows of 65,536
 // bf16 logits take 205 us for the 20 best, 5.25 TB/s, and 190 us without the best; 480 rows of 50,001
-// fp32 logits with an eighth of them banned 25.9 us, 3.7 TB/s.
+// fp32 logits with an eighth of them banned 22.0 us, 4.4 TB/s.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <stdint.h>
@@ -644,13 +644,17 @@ cudaError_t launch_lp(const LpParams &p, int nsm, cudaStream_t stream)
 }
 
 // Up to two rows per SM the whole CTA takes one row (304 rows of 50,001 fp32 logits: 16.1 us, and 23.0
-// with 4 warps per row), from then on 4 warps do, eight rows at a time per SM (480 rows: 27.4 and
-// 25.8 us; 1200 rows: 52.8 and 41.4).  Rows under 16 KB are too short for 16 warps.
+// with 4 warps per row), up to four rows half of it does (480 rows: 27.4 by whole CTAs, 22.0 by 8 warps, 25.9
+// by 4), from then on 4 warps do, eight rows at a time per SM (700 rows: 36.9 by 8 warps, 31.0 by 4; 1200
+// rows: 45.0 and 42.7).  Rows under 16 KB are too short for 16 warps, and under 48 KB for 8 (400 rows of
+// 20,011 bf16 logits: 11.2 us by 8 warps, 10.9 by 4; of 30,011: 13.0 and 14.4).
 template <typename T>
 cudaError_t launch_team(const LpParams &p, int nsm, cudaStream_t stream)
 {
-    return p.N <= 2 * nsm && static_cast<int64_t>(p.V) * sizeof(T) >= 16384 ? launch_lp<T, 16>(p, nsm, stream)
-                                                                          : launch_lp<T, 4>(p, nsm, stream);
+    const int64_t bytes = static_cast<int64_t>(p.V) * sizeof(T);
+    if (p.N <= 2 * nsm && bytes >= 16 << 10) return launch_lp<T, 16>(p, nsm, stream);
+    if (p.N > 2 * nsm && p.N <= 4 * nsm && bytes >= 48 << 10) return launch_lp<T, 8>(p, nsm, stream);
+    return launch_lp<T, 4>(p, nsm, stream);
 }
 
 }  // namespace

@@ -203,3 +203,21 @@ def test_row_offsets_past_32_bits():
     tok = np.random.default_rng(15).integers(0, V, N)
     a, b = run(x, tok, 8), run(buf[:, :V], tok, 8)
     assert all(torch.equal(a[n], b[n]) for n in a)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("N,V", [(330, 30011), (608, 25001), (900, 5003)])
+def test_odd_rows_among_many(N, V, dtype):
+    """Rows for teams of 8 and of 4 warps: ties, flat rows, banned ones and rows without a distribution
+    beside ordinary ones."""
+    import torch
+    x = logits(16, N, V, dtype)
+    x[5] = 0.0
+    x[17] = (x[17] * 0.4).round()
+    x[100] = -float("inf")
+    x[101, V - 1] = float("nan")
+    x[200, ::2] = -float("inf")
+    x[201, 3] = float("inf")
+    x[300] = -torch.finfo(x.dtype).max
+    x[N - 1] = torch.sort(x[N - 1]).values
+    check(x, 32, f"{N} x {V}")
