@@ -11,7 +11,6 @@ ctypes functions themselves for callers that manage pointers directly.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import os
@@ -330,15 +329,26 @@ def _expect(fn: str, device, checks):
                              f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
 
 
-def _on(fn: str, device, stream):
-    """The context of ``device`` and the stream to use there: the given one, or its current one."""
+def _alike(dtype, index: int, tensors) -> bool:
+    """Whether all of ``tensors`` (or None) are contiguous, of ``dtype`` and on device ``index``.  The checks of
+    the shared-prefix and log-probability calls begin with it, as it takes a third of ``_expect``'s time
+    (their smallest problems run for 7 to 20 us); ``_expect`` finds the message if one fails."""
+    for t in tensors:
+        if t is not None and (t.dtype is not dtype or t.get_device() != index or not t.is_contiguous()):
+            return False
+    return True
+
+
+def _launch(fn: str, index: int, stream, *args):
+    """Calls the library's ``fn`` with device ``index`` current, on ``stream`` or that device's current one."""
     import torch
-    if device.type != "cuda":
-        raise ValueError(f"{fn}: CUDA tensors expected, got {device}")
-    st = _stream(torch.cuda.current_stream(device) if stream is None else stream)
-    if device.index == torch.cuda.current_device():
-        return contextlib.nullcontext(), st
-    return torch.cuda.device(device), st
+    if index < 0:
+        raise ValueError(f"{fn}: CUDA tensors expected")
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            return _launch(fn, index, stream, *args)
+    st = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    _check(fn, getattr(load(), fn)(*args, st))
 
 
 def bg_shared_attn_workspace_size(num_groups: int, num_seqs: int, total_tokens: int, max_seqlen: int,
@@ -347,42 +357,46 @@ def bg_shared_attn_workspace_size(num_groups: int, num_seqs: int, total_tokens: 
                                                     Hkv, head_dim))
 
 
-def _workspace(fn: str, workspace, size, device):
-    """Pointer and bytes of the workspace; ``size`` gives the bytes it needs, for the message."""
+def _workspace(fn: str, workspace, sizes, index: int):
+    """Pointer and bytes of the workspace; ``sizes`` are bg_shared_attn_workspace_size's arguments, for the message."""
     if workspace is None:
-        raise ValueError(f"{fn}: workspace of {size()} bytes required (the library never allocates)")
-    if workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"{fn}: workspace must be contiguous on {device}")
+        raise ValueError(f"{fn}: workspace of {bg_shared_attn_workspace_size(*sizes)} bytes required (the library never "
+                         "allocates)")
+    if workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError(f"{fn}: workspace must be contiguous on the other tensors' device, got {workspace.device}")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def _shared_run(fn: str, last: bool, q, k, v, cu_seqlens, max_seqlen, prefix_k, prefix_v, cu_prefix, max_prefix_len,
                 cu_group, out, lse, scale, softcap, workspace, dev_status, stream):
     import torch
-    bf16, i32 = torch.bfloat16, torch.int32
+    bf16, f32, i32 = torch.bfloat16, torch.float32, torch.int32
     rows, Hq, d = q.shape
-    T, Hkv = k.shape[0], k.shape[1]
-    P = 0 if prefix_k is None else prefix_k.shape[0]
+    kv = k.shape
+    T, Hkv = kv[0], kv[1]
     S, R = cu_seqlens.numel() - 1, cu_group.numel() - 1
-    dev = q.device
     if (prefix_k is None) != (prefix_v is None):
         raise ValueError(f"{fn}: prefix_k and prefix_v come together")
-    _expect(fn, dev, (("q", q, bf16, (S if last else T, Hq, d)), ("k", k, bf16, (T, Hkv, d)), ("v", v, bf16, (T, Hkv, d)),
-                      ("cu_seqlens", cu_seqlens, i32, (S + 1,)), ("prefix_k", prefix_k, bf16, (P, Hkv, d)),
-                      ("prefix_v", prefix_v, bf16, (P, Hkv, d)), ("cu_prefix", cu_prefix, i32, (R + 1,)),
-                      ("cu_group", cu_group, i32, (R + 1,)), ("out", out, bf16, (rows, Hq, d)),
-                      ("lse", lse, torch.float32, (rows, Hq)),
-                      ("dev_status", dev_status, i32, dev_status.shape if dev_status is not None else ())))
-    ws, ws_bytes = _workspace(fn, workspace, lambda: bg_shared_attn_workspace_size(
-        R, S, T, int(max_seqlen), int(max_prefix_len), Hq, Hkv, d), dev)
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    ctx, st = _on(fn, dev, stream)
-    with ctx:
-        _check(fn, getattr(load(), fn)(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens), S, T, int(max_seqlen), _ptr(prefix_k), _ptr(prefix_v),
-            _ptr(cu_prefix), P, int(max_prefix_len), _ptr(cu_group), R, Hq, Hkv, d, float(scale), float(softcap),
-            _ptr(out), _ptr(lse), ws, ws_bytes, _ptr(dev_status), st))
+    P = 0 if prefix_k is None else prefix_k.shape[0]
+    index = q.get_device()
+    if not (_alike(bf16, index, (q, k, v, prefix_k, prefix_v, out)) and
+            _alike(i32, index, (cu_seqlens, cu_prefix, cu_group, dev_status)) and
+            (lse is None or (_alike(f32, index, (lse,)) and lse.shape == (rows, Hq))) and
+            rows == (S if last else T) and out.shape == q.shape and kv == (T, Hkv, d) and v.shape == kv and
+            (prefix_k is None or prefix_k.shape == prefix_v.shape == (P, Hkv, d)) and
+            cu_seqlens.dim() == cu_prefix.dim() == cu_group.dim() == 1 and cu_prefix.numel() == R + 1):
+        _expect(fn, q.device, (
+            ("q", q, bf16, (S if last else T, Hq, d)), ("k", k, bf16, (T, Hkv, d)), ("v", v, bf16, (T, Hkv, d)),
+            ("cu_seqlens", cu_seqlens, i32, (S + 1,)), ("prefix_k", prefix_k, bf16, (P, Hkv, d)),
+            ("prefix_v", prefix_v, bf16, (P, Hkv, d)), ("cu_prefix", cu_prefix, i32, (R + 1,)),
+            ("cu_group", cu_group, i32, (R + 1,)), ("out", out, bf16, (rows, Hq, d)), ("lse", lse, f32, (rows, Hq)),
+            ("dev_status", dev_status, i32, dev_status.shape if dev_status is not None else ())))
+    max_seqlen, max_prefix_len = int(max_seqlen), int(max_prefix_len)
+    ws, ws_bytes = _workspace(fn, workspace, (R, S, T, max_seqlen, max_prefix_len, Hq, Hkv, d), index)
+    _launch(fn, index, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), S, T, max_seqlen,
+            _ptr(prefix_k), _ptr(prefix_v), cu_prefix.data_ptr(), P, max_prefix_len, cu_group.data_ptr(), R, Hq, Hkv, d,
+            1.0 / math.sqrt(d) if scale is None else float(scale), float(softcap), out.data_ptr(), _ptr(lse), ws,
+            ws_bytes, _ptr(dev_status))
     return out
 
 
@@ -428,17 +442,15 @@ def _shared_plan(fn: str, cu_seqlens, total_tokens, max_seqlen, cu_prefix, total
     import torch
     i32 = torch.int32
     S, R = cu_seqlens.numel() - 1, cu_group.numel() - 1
-    dev = cu_seqlens.device
-    _expect(fn, dev, (("cu_seqlens", cu_seqlens, i32, (S + 1,)), ("cu_prefix", cu_prefix, i32, (R + 1,)),
-                      ("cu_group", cu_group, i32, (R + 1,)),
-                      ("dev_status", dev_status, i32, dev_status.shape if dev_status is not None else ())))
-    ws, ws_bytes = _workspace(fn, workspace, lambda: bg_shared_attn_workspace_size(
-        R, S, int(total_tokens), int(max_seqlen), int(max_prefix_len), Hq, Hkv, head_dim), dev)
-    ctx, st = _on(fn, dev, stream)
-    with ctx:
-        _check(fn, getattr(load(), fn)(_ptr(cu_seqlens), S, int(total_tokens), int(max_seqlen), _ptr(cu_prefix),
-                                       int(total_prefix), int(max_prefix_len), _ptr(cu_group), R, Hq, Hkv, head_dim,
-                                       ws, ws_bytes, _ptr(dev_status), st))
+    index = cu_seqlens.get_device()
+    _expect(fn, cu_seqlens.device, (
+        ("cu_seqlens", cu_seqlens, i32, (S + 1,)), ("cu_prefix", cu_prefix, i32, (R + 1,)),
+        ("cu_group", cu_group, i32, (R + 1,)),
+        ("dev_status", dev_status, i32, dev_status.shape if dev_status is not None else ())))
+    T, P, max_seqlen, max_prefix_len = int(total_tokens), int(total_prefix), int(max_seqlen), int(max_prefix_len)
+    ws, ws_bytes = _workspace(fn, workspace, (R, S, T, max_seqlen, max_prefix_len, Hq, Hkv, head_dim), index)
+    _launch(fn, index, stream, cu_seqlens.data_ptr(), S, T, max_seqlen, cu_prefix.data_ptr(), P, max_prefix_len,
+            cu_group.data_ptr(), R, Hq, Hkv, head_dim, ws, ws_bytes, _ptr(dev_status))
 
 
 def bg_shared_prefill_plan(cu_seqlens, total_tokens: int, max_seqlen: int, cu_prefix, total_prefix: int,
@@ -469,15 +481,17 @@ def bg_token_logprobs(logits, tokens=None, *, logprob=None, entropy=None, top_to
     if dtype is None or (V > 1 and N > 0 and logits.stride(1) != 1):
         raise ValueError(f"{fn}: logits must be float32 or bfloat16 with contiguous rows, got {logits.dtype} with "
                          f"strides {logits.stride()}")
-    dev = logits.device
+    index = logits.get_device()
     K = 0 if top_token is None else top_token.shape[-1]
     f32, i32 = torch.float32, torch.int32
-    _expect(fn, dev, (("tokens", tokens, i32, (N,)), ("logprob", logprob, f32, (N,)), ("entropy", entropy, f32, (N,)),
-                      ("top_token", top_token, i32, (N, K)), ("top_logprob", top_logprob, f32, (N, K)),
-                      ("dev_status", dev_status, i32, dev_status.shape if dev_status is not None else ())))
-    ctx, st = _on(fn, dev, stream)
-    with ctx:
-        _check(fn, load().bg_token_logprobs(_ptr(logits), dtype, logits.stride(0) if N > 1 else max(V, 1), N, V,
-                                            _ptr(tokens), K, _ptr(logprob), _ptr(entropy), _ptr(top_token),
-                                            _ptr(top_logprob), _ptr(dev_status), st))
+    if not (_alike(i32, index, (tokens, top_token, dev_status)) and _alike(f32, index, (logprob, entropy, top_logprob)) and
+            (tokens is None or tokens.shape == (N,)) and (logprob is None or logprob.shape == (N,)) and
+            (entropy is None or entropy.shape == (N,)) and (top_token is None or top_token.shape == (N, K)) and
+            (top_logprob is None or top_logprob.shape == (N, K))):
+        _expect(fn, logits.device, (
+            ("tokens", tokens, i32, (N,)), ("logprob", logprob, f32, (N,)), ("entropy", entropy, f32, (N,)),
+            ("top_token", top_token, i32, (N, K)), ("top_logprob", top_logprob, f32, (N, K)),
+            ("dev_status", dev_status, i32, dev_status.shape if dev_status is not None else ())))
+    _launch(fn, index, stream, logits.data_ptr(), dtype, logits.stride(0) if N > 1 else max(V, 1), N, V, _ptr(tokens), K,
+            _ptr(logprob), _ptr(entropy), _ptr(top_token), _ptr(top_logprob), _ptr(dev_status))
     return logprob, entropy, top_token, top_logprob
