@@ -48,7 +48,8 @@ namespace bg {
 namespace {
 
 // ------------------------------------------------------------------------------------ plan
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 512;
+constexpr int kPlanPos = 2048;                       // entries whose positions are
 constexpr int kPlanSeqs = 4096, kPlanGroups = 512;   // offsets up to these counts are held in shared memory
 
 __host__ __device__ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -67,7 +68,7 @@ __device__ int block_exclusive(int v, int *s_warp, int *total)
     if (lane == 31) s_warp[warp] = incl;
     __syncthreads();
     // every warp sums the warps before it
-    const int w = s_warp[lane];
+    const int w = lane < kPlanThreads / 32 ? s_warp[lane] : 0;
     *total = __reduce_add_sync(0xffffffffu, w);
     return incl - v + __reduce_add_sync(0xffffffffu, lane < warp ? w : 0);
 }
@@ -90,7 +91,7 @@ __device__ __forceinline__ int entry_units(const ShEntry &E) { return E.tiles > 
 
 __global__ void __launch_bounds__(kPlanThreads)
     shared_plan_kernel(const ShProblem pb, const ShKey key, int bt, int32_t *hdr, ShEntry *__restrict__ entries,
-                       ShStart *__restrict__ starts, ShSplit *__restrict__ splits, int grid, int can_split, int heads,
+                       ShStart *__restrict__ starts, ShSplit *__restrict__ splits, int grid, int can_split, int tiles_per, int heads,
                        int32_t *dev_status)
 {
     __shared__ int s_err, s_nsplit;
@@ -98,7 +99,7 @@ __global__ void __launch_bounds__(kPlanThreads)
     __shared__ int s_base[kPlanThreads];
     __shared__ ShStart s_start[kShMaxCtas + 1];
     __shared__ int32_t s_cu[kPlanSeqs + 1], s_cup[kPlanGroups + 1], s_cug[kPlanGroups + 1];
-    __shared__ int64_t s_pos[kPlanThreads];
+    __shared__ int64_t s_pos[kPlanPos];
     const int tid = threadIdx.x;
     grid_dep_launch();
     if (tid == 0) {
@@ -111,9 +112,9 @@ __global__ void __launch_bounds__(kPlanThreads)
     const int32_t *cu = pb.cu_seqlens, *cup = pb.cu_prefix, *cug = pb.cu_group;
     if (pb.num_seqs <= kPlanSeqs && pb.num_groups <= kPlanGroups) {
         for (int i = tid; i <= pb.num_seqs; i += kPlanThreads) s_cu[i] = cu[i];
-        if (tid <= pb.num_groups) {
-            s_cup[tid] = cup[tid];
-            s_cug[tid] = cug[tid];
+        for (int i = tid; i <= pb.num_groups; i += kPlanThreads) {
+            s_cup[i] = cup[i];
+            s_cug[i] = cug[i];
         }
         cu = s_cu;
         cup = s_cup;
@@ -153,7 +154,7 @@ __global__ void __launch_bounds__(kPlanThreads)
     }
 
     // ---- the entries, in request order
-    const int per = kShTiles * bt;         // rows of an entry
+    const int per = tiles_per * bt;        // rows of an entry
     int n_entries = 0;
     int64_t units = 0;
     for (int r0 = 0; r0 < pb.num_groups; r0 += kPlanThreads) {
@@ -216,7 +217,7 @@ __global__ void __launch_bounds__(kPlanThreads)
             if (e < total) {
                 E.pos = units + excl;
                 entries[n_entries + e] = E;
-                if (n_entries + e < kPlanThreads) s_pos[n_entries + e] = E.pos;
+                if (n_entries + e < kPlanPos) s_pos[n_entries + e] = E.pos;
             }
             units += sum;
         }
@@ -226,7 +227,7 @@ __global__ void __launch_bounds__(kPlanThreads)
 
     // ---- equal shares of the line; fewer CTAs where a share would be below kShSplitMin (half of it for pairs,
     // whose tiles count twice)
-    auto pos_of = [&](int e) { return n_entries <= kPlanThreads ? s_pos[e] : entries[e].pos; };
+    auto pos_of = [&](int e) { return n_entries <= kPlanPos ? s_pos[e] : entries[e].pos; };
     const int lines = pb.Hkv >> (heads - 1);
     const int64_t work = units * lines;
     const int split_min = kShSplitMin >> (heads - 1);
@@ -1476,6 +1477,27 @@ cudaError_t launch_one(const CUtensorMap &tm_q, const CUtensorMap &tm_k, const C
 
 }  // namespace
 
+namespace {
+
+// Most key tiles of an entry: its prefix, and the own keys of the rows it holds (prefill: one sample's
+// start to the entry's last row; last token: whole samples).
+int64_t most_tiles(const ShProblem &pb)
+{
+    const int64_t bt = kShRows / (pb.Hq / pb.Hkv);
+    int64_t own = pb.last ? kShTiles * bt * pb.max_seqlen : pb.max_seqlen + kShTiles * bt;
+    if (own > pb.total_tokens) own = pb.total_tokens;
+    return ceil_div(pb.max_prefix_len, kShKeys) + ceil_div(own, kShKeys);
+}
+
+}  // namespace
+
+int shared_tiles(const ShProblem &pb)
+{
+    const int bt = kShRows / (pb.Hq / pb.Hkv);
+    const int64_t items = (static_cast<int64_t>(pb.total_tokens) / (kShTiles * bt) + pb.num_groups) * pb.Hkv;
+    return !pb.last && 2 * items <= kShMaxCtas && most_tiles(pb) < kShSplitTiles ? 1 : kShTiles;
+}
+
 int shared_heads(const ShProblem &pb)
 {
     if (!pb.last || pb.Hkv % 2 != 0) return 1;
@@ -1489,12 +1511,8 @@ ShLayout shared_layout(const ShProblem &pb)
     const int bt = kShRows / (pb.Hq / pb.Hkv);
     const int64_t rows = pb.last ? pb.num_seqs : pb.total_tokens;
     const int most = pb.last && pb.Hkv % 2 == 0 ? 2 : 1;       // of shared_heads
-    L.max_entries = rows / (kShTiles * bt) + pb.num_groups + 1;
-    // most key tiles of an entry: its prefix, and the own keys of the rows it holds (prefill: one
-    // sample's start to the entry's last row; last token: whole samples)
-    int64_t own = pb.last ? static_cast<int64_t>(kShTiles) * bt * pb.max_seqlen : pb.max_seqlen + kShTiles * bt;
-    if (own > pb.total_tokens) own = pb.total_tokens;
-    const int64_t tiles = ceil_div(pb.max_prefix_len, kShKeys) + ceil_div(own, kShKeys);
+    L.max_entries = rows / (shared_tiles(pb) * bt) + pb.num_groups + 1;
+    const int64_t tiles = most_tiles(pb);
     L.items = L.max_entries * pb.Hkv;
     L.units = L.items * (tiles + kItemUnits);
     L.slots = 0;
@@ -1526,7 +1544,8 @@ cudaError_t launch_shared_plan(const ShProblem &pb, const ShLayout &lay, void *w
     return launch_dependent(shared_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, pb, shared_key(pb, grid),
                             kShRows / (pb.Hq / pb.Hkv), reinterpret_cast<int32_t *>(ws),
                             reinterpret_cast<ShEntry *>(ws + lay.entries), reinterpret_cast<ShStart *>(ws + lay.starts),
-                            reinterpret_cast<ShSplit *>(ws + lay.splits), grid, lay.slots > 0 ? 1 : 0, shared_heads(pb), dev_status);
+                            reinterpret_cast<ShSplit *>(ws + lay.splits), grid, lay.slots > 0 ? 1 : 0, shared_tiles(pb), shared_heads(pb),
+                            dev_status);
 }
 
 cudaError_t launch_shared_attn(int head_dim, bool is_capped, const CUtensorMap &tm_q, const CUtensorMap &tm_k,

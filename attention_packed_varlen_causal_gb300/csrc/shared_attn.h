@@ -80,6 +80,10 @@ struct ShProblem {
 // where the key ranges would be cut into more than about ten parts, whose joining takes what is won: one
 // request of 8 samples over 4096 keys 23.4 single, 26.4 paired; four of them 29.0 and 29.8.
 int shared_heads(const ShProblem &pb);
+// Query tiles of an entry: one in a prefill that would leave half of the SMs without an item of two, unless
+// its key ranges are long enough to be cut.  One request, 16 / 8 heads of 128: 15 samples over 400 keys 20.3 us
+// with two, 16.7 with one; 12 samples over 8000 keys 52.1 and 62.3.
+int shared_tiles(const ShProblem &pb);
 ShLayout shared_layout(const ShProblem &pb);
 ShKey shared_key(const ShProblem &pb, int grid);
 
