@@ -435,6 +435,8 @@ bg_status_t bg_beam_select(const float *logits, const float *cum,
  *   max_prefix_len  host upper bound of every prefix (checked on device)
  *   cu_group     int32 [num_groups+1], device; as cu_seqlens, for num_seqs
  *   scale        finite, > 0;  softcap finite, >= 0 (0: scores are not capped)
+ *                (with 0 < softcap <= 55 weights are not scaled by their
+ *                maximum: finite results for |v| < 2^30)
  *   out          bf16, the shape of q
  *   lse          fp32 [rows of q, Hq] natural-log sum-exp of x, or NULL
  *   workspace    device buffer of at least bg_shared_attn_workspace_size(...)

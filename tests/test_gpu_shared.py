@@ -436,3 +436,9 @@ def test_paired_heads_keep_non_finite_rows_in_their_request():
     b = x["cug"]
     assert torch.equal(outs[0][:b[1]], outs[1][:b[1]]) and torch.equal(outs[0][b[2]:], outs[1][b[2]:])
     assert torch.isnan(outs[1][b[1]:b[2]].float()).all()
+
+
+def test_last_token_of_samples_without_rows():
+    """No sample has a row: every query sees its request's prefix only, and k and v are empty."""
+    x = make(31, [40, 129, 0], [[0, 0, 0], [0], [0, 0]], 16, 8, 128)
+    check(x, True, what="no own rows")
