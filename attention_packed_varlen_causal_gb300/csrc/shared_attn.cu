@@ -515,18 +515,21 @@ __device__ __forceinline__ float min_nan(float a, float b)
 // of the cap.
 __device__ __forceinline__ void capped4(float *s, float cap_in, float cap_log2)
 {
-    float a[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) a[i] = ex2(min_nan(s[i] * cap_in, 30.f)) + 1.f;
-    const float ab = a[0] * a[1], cd = a[2] * a[3];
+    const float2 in2 = make_float2(cap_in, cap_in), one2 = make_float2(1.f, 1.f), cap2 = make_float2(cap_log2, cap_log2);
+    const float2 x01 = fmul2(make_float2(s[0], s[1]), in2), x23 = fmul2(make_float2(s[2], s[3]), in2);
+    const float2 a01 = fadd2(make_float2(ex2(min_nan(x01.x, 30.f)), ex2(min_nan(x01.y, 30.f))), one2);
+    const float2 a23 = fadd2(make_float2(ex2(min_nan(x23.x, 30.f)), ex2(min_nan(x23.y, 30.f))), one2);
+    const float ab = a01.x * a01.y, cd = a23.x * a23.y;
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ab * cd));
     r *= -2.f * cap_log2;
     const float rcd = r * cd, rab = r * ab;
-    s[0] = fmaf(rcd, a[1], cap_log2);
-    s[1] = fmaf(rcd, a[0], cap_log2);
-    s[2] = fmaf(rab, a[3], cap_log2);
-    s[3] = fmaf(rab, a[2], cap_log2);
+    const float2 t01 = ffma2(make_float2(rcd, rcd), make_float2(a01.y, a01.x), cap2);
+    const float2 t23 = ffma2(make_float2(rab, rab), make_float2(a23.y, a23.x), cap2);
+    s[0] = t01.x;
+    s[1] = t01.y;
+    s[2] = t23.x;
+    s[3] = t23.y;
 }
 
 // The same for caps of any size, where that error could be large next to the scores: below |y| = 0.3
@@ -559,7 +562,7 @@ constexpr float kShCapFixed = 80.f;
 // Measured, 16 / 8 heads of 128, device time with plan and join: 16 samples of 257-700 tokens over 8000
 // keys 398 us, 1380 TFLOP/s; 32 requests of 15 samples of 16-96 tokens over 200-500 keys 154.5 us (prefill)
 // and 45 us, 3.5 TB/s (last token); 128 last tokens over 30000-32768 keys 115 us, 5.4 TB/s.  14 / 2 heads
-// of 64, scores capped at 30: 112 samples of 1-300 tokens over 1-500 keys 107 us, 744 last tokens 39 us.
+// of 64, scores capped at 30: 112 samples of 1-300 tokens over 1-500 keys 101 us, 744 last tokens 38 us.
 // What bounds it is the chain of one query tile per key tile: about 2250 cycles of softmax (tensor memory
 // to registers, maximum, 128 exponentials of a row, weights back), then 1400 of hand-overs and products.
 // Two query tiles overlap their chains; tensor memory (S and O of each) has no room for a third at D = 128.
