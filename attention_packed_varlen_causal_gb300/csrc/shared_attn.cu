@@ -37,7 +37,6 @@
 
 #include <atomic>
 #include <cmath>
-#include <type_traits>
 
 #include "bg_internal.h"
 #include "bg_ptx.cuh"
