@@ -20,7 +20,7 @@
 // A row with more such logits than the list holds (thousands of equal ones) is searched K times
 // instead.  Two CTAs of 16 warps per SM keep 64 KB of copies in flight; what is left to the bound is
 // issue slots (about 9 instructions per logit and lane, the K best among them): 8192 rows of 65,536
-// bf16 logits take 205 us for the 20 best, 5.25 TB/s, and 190 us without the best; 480 rows of 50,001
+// bf16 logits take 198 us for the 20 best, 5.4 TB/s; 480 rows of 50,001
 // fp32 logits with an eighth of them banned 22.0 us, 4.4 TB/s.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
@@ -44,7 +44,6 @@ constexpr int kLpSlots = 16;             // stored batch maxima per lane (of one
 constexpr int kLpCap = 144;              // gathered logits per warp of the team (a row too short to give
                                          // 32 lane maxima fits)
 constexpr int kLpMaxCluster = 8;
-constexpr uint32_t kLpPolls = 1u << 22;  // polls after which a wait gives up (a second or more)
 static_assert(BG_MAX_TOP <= 32, "at least K lane maxima");
 static_assert(kLpSlots == 16, "a lane's stored maxima are two vectors, one mask");
 
@@ -197,6 +196,7 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
 // time: the polls of waiting warps would take issue slots from the summing ones.
 __device__ __forceinline__ bool lp_wait(uint64_t *bar, uint32_t parity, volatile int *abort)
 {
+    uint64_t t0 = 0;
     for (uint32_t it = 0;; ++it) {
         uint32_t ok;
         asm volatile(
@@ -207,8 +207,14 @@ __device__ __forceinline__ bool lp_wait(uint64_t *bar, uint32_t parity, volatile
             : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
             : "memory");
         if (ok) return true;
-        if (it >= kLpPolls) *abort = 1;
         if (*abort) return false;
+        if ((it & 63u) != 0) continue;
+        const uint64_t now = globaltimer_ns();
+        if (it == 0) t0 = now;
+        if (now - t0 > kWaitTimeoutNs) {
+            *abort = 1;
+            return false;
+        }
     }
 }
 
