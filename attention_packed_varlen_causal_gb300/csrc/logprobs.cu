@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LpParams 
             if (tid == 0) issue();
             __syncwarp();
             const uint32_t st = sums % kLpStages;
-            lp_wait(&full[st], (sums / kLpStages) & 1, abort);     // (given up: the sums are not used)
+            lp_wait(&full[st], (sums / kLpStages) & 1, abort);     // (given up: BG_DEVSTAT_TIMEOUT)
             const int left = v1 - v0 - b * kBatch;
             uint4 g[kLpLoads];
 #pragma unroll
