@@ -720,6 +720,7 @@ bg_status_t shared_impl(const ShProblem &pb, const void *q, const void *k, const
     p.cu_seqlens = pb.cu_seqlens;
     p.hdr = reinterpret_cast<const int32_t *>(ws);
     p.entries = reinterpret_cast<const ShEntry *>(ws + lay.entries);
+    p.sorted = reinterpret_cast<const ShEntry *>(ws + lay.sorted);
     p.starts = reinterpret_cast<const ShStart *>(ws + lay.starts);
     p.splits = reinterpret_cast<const ShSplit *>(ws + lay.splits);
     p.part_o = reinterpret_cast<float *>(ws + lay.part_o);

@@ -92,7 +92,7 @@ __device__ __forceinline__ int entry_units(const ShEntry &E) { return E.tiles > 
 // with 512 threads (4.9 with 1024; 256 are 0.1 faster for a few requests and 0.7 slower for 500 entries).
 // The offsets are held in shared memory because the searches read them many times.
 __global__ void __launch_bounds__(kPlanThreads)
-    shared_plan_kernel(const ShProblem pb, const ShKey key, int bt, int32_t *hdr, ShEntry *__restrict__ entries,
+    shared_plan_kernel(const ShProblem pb, const ShKey key, int bt, int32_t *hdr, ShEntry *entries, ShEntry *sorted,
                        ShStart *__restrict__ starts, ShSplit *__restrict__ splits, int grid, int can_split, int tiles_per, int heads,
                        int32_t *dev_status)
 {
@@ -102,6 +102,7 @@ __global__ void __launch_bounds__(kPlanThreads)
     __shared__ ShStart s_start[kShMaxCtas + 1];
     __shared__ int32_t s_cu[kPlanSeqs + 1], s_cup[kPlanGroups + 1], s_cug[kPlanGroups + 1];
     __shared__ int64_t s_pos[kPlanPos];
+    __shared__ int s_class[kPlanThreads / 32][kShSplitTiles];
     const int tid = threadIdx.x;
     grid_dep_launch();
     if (tid == 0) {
@@ -150,6 +151,7 @@ __global__ void __launch_bounds__(kPlanThreads)
             hdr[kShHdrStatus] = s_err;
             hdr[kShHdrCtas] = 0;
             hdr[kShHdrSplits] = 0;
+            hdr[kShHdrItems] = 0;
             if (dev_status) atomicOr(dev_status, s_err);
         }
         return;
@@ -231,6 +233,63 @@ __global__ void __launch_bounds__(kPlanThreads)
     // whose tiles count twice)
     auto pos_of = [&](int e) { return n_entries <= kPlanPos ? s_pos[e] : entries[e].pos; };
     const int lines = pb.Hkv >> (heads - 1);
+
+    // ---- nothing is cut: whole items, dealt out to the CTAs in falling order of their tiles, one round from
+    // the first CTA to the last, the next one back.  (Shares of the line that end at items' ends: the
+    // largest 22% above the mean with seven items to a CTA.)
+    if (!can_split) {
+        const int n_items = n_entries * lines;
+        const int ctas = min(grid, n_items);
+        if (n_items > ctas) {
+            // a counting sort, in order within a number of tiles; class c: kShSplitTiles - 1 - c tiles
+            const int lane = tid & 31, warp = tid >> 5;
+            int base = 0;                          // of lane's class (lane < kShSplitTiles)
+            for (int pass = 0; pass < 2; ++pass) {
+                int count = 0;                     // of lane's class, in the chunks so far
+                for (int e0 = 0; e0 < n_entries; e0 += kPlanThreads) {
+                    const int e = e0 + tid;
+                    ShEntry E = {};
+                    if (e < n_entries) E = entries[e];
+                    const int mine = e < n_entries ? kShSplitTiles - 1 - E.tiles : -1;
+                    int before = 0;                // entries of this class in lower lanes
+#pragma unroll
+                    for (int c = 0; c < kShSplitTiles; ++c) {
+                        const unsigned m = __ballot_sync(0xffffffffu, mine == c);
+                        if (mine == c) before = __popc(m & ((1u << lane) - 1u));
+                        if (lane == c) s_class[warp][c] = __popc(m);
+                    }
+                    __syncthreads();
+                    int lower = 0, all = 0;        // of lane's class, in lower warps and in all
+                    if (lane < kShSplitTiles)
+                        for (int w = 0; w < kPlanThreads / 32; ++w) {
+                            const int k = s_class[w][lane];
+                            lower += w < warp ? k : 0;
+                            all += k;
+                        }
+                    const int at = __shfl_sync(0xffffffffu, base + count + lower, max(mine, 0)) + before;
+                    if (pass == 1 && mine >= 0) sorted[at] = E;
+                    count += all;
+                    __syncthreads();
+                }
+                if (pass == 0) {                   // the classes' first places
+                    int incl = count;
+                    for (int o = 1; o < kShSplitTiles; o <<= 1) {
+                        const int u = __shfl_up_sync(0xffffffffu, incl, o);
+                        if (lane >= o) incl += u;
+                    }
+                    base = incl - count;
+                }
+            }
+        }
+        if (tid == 0) {
+            hdr[kShHdrStatus] = 0;
+            hdr[kShHdrCtas] = ctas;
+            hdr[kShHdrSplits] = 0;
+            hdr[kShHdrEntries] = n_entries;
+            hdr[kShHdrItems] = n_items;
+        }
+        return;
+    }
     const int64_t work = units * lines;
     const int split_min = kShSplitMin >> (heads - 1);
     const int ctas = static_cast<int>(min(static_cast<int64_t>(grid), ceil_div(work, split_min)));
@@ -255,7 +314,7 @@ __global__ void __launch_bounds__(kPlanThreads)
             const int64_t share = work / ctas;
             const int least = n * 10 <= share ? n : max(split_min / 2, static_cast<int>(min(share / 32, static_cast<int64_t>(n))));
             S.tile = into;
-            if (!can_split || into < least || n - into < least) {
+            if (into < least || n - into < least) {
                 S.tile = 0;
                 if (2 * into > n) ++S.entry;
             }
@@ -287,6 +346,7 @@ __global__ void __launch_bounds__(kPlanThreads)
         hdr[kShHdrCtas] = ctas;
         hdr[kShHdrSplits] = s_nsplit;
         hdr[kShHdrEntries] = n_entries;
+        hdr[kShHdrItems] = 0;
     }
 }
 
@@ -642,18 +702,33 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
                 const bool mine = plan_ready(p, &other) && cta < p.hdr[kShHdrCtas];
                 if (other && cta == 0 && p.dev_status) atomicOr(p.dev_status, BG_DEVSTAT_PLAN);
                 ShStart A = {}, B = {};
-                int n_entries = 0;
+                int n_entries = 0, ctas = 0, lines = 1;
+                uint32_t n_items = 0, at = 0;              // dealt out: all items, and the place of this one
                 if (mine) {
-                    A = p.starts[cta];
-                    B = p.starts[cta + 1];
                     n_entries = p.hdr[kShHdrEntries];
+                    ctas = p.hdr[kShHdrCtas];
+                    n_items = p.hdr[kShHdrItems];
+                    if (n_items == 0) {
+                        A = p.starts[cta];
+                        B = p.starts[cta + 1];
+                    }
+                }
+                const bool dealt = n_items > 0;
+                if (dealt) {
+                    lines = LAST ? p.Hkv / p.heads : p.Hkv;
+                    at = cta;
+                    A = ShStart{cta % lines, cta / lines, 0, 0};
+                    B.kh = -1;
                 }
                 const uint64_t pol = l2_policy_evict_last();
-                const int4 *list = reinterpret_cast<const int4 *>(p.entries);
+                const int4 *list = reinterpret_cast<const int4 *>(dealt && n_items > ctas ? p.sorted : p.entries);
                 int kh = A.kh, entry = A.entry, tb = A.tile;
                 auto before_end = [&]() {
-                    return kh < B.kh || (kh == B.kh && (entry < B.entry || (entry == B.entry && tb < B.tile)));
+                    return dealt ? at < n_items
+                                 : kh < B.kh || (kh == B.kh && (entry < B.entry || (entry == B.entry && tb < B.tile)));
                 };
+                uint32_t back = static_cast<uint32_t>(2 * (ctas - 1 - cta) + 1);      // to the next place, and then
+                                                                                     // 2 * cta + 1, in turn
                 int4 e0 = {}, e1 = {}, e2 = {};
                 auto fetch = [&]() {
                     const int4 *q = list + 3 * static_cast<int64_t>(entry);
@@ -663,13 +738,13 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
                 };
                 if (before_end()) fetch();
                 uint32_t st = 0, ph = 1;         // stage, and the parity of its release (1: free at first)
-                uint32_t n_items = 0;
+                uint32_t n_told = 0;
                 uint32_t used = 0;               // stages that hold or await a copy, counted up to kStages
                 bool ok = true;
                 for (;;) {
                     const bool more = before_end();
-                    const uint32_t slot = n_items % kShRing;
-                    if (!sh_wait(&item_empty[slot], ((n_items / kShRing) & 1) ^ 1, abort_flag)) break;
+                    const uint32_t slot = n_told % kShRing;
+                    if (!sh_wait(&item_empty[slot], ((n_told / kShRing) & 1) ^ 1, abort_flag)) break;
                     Item I;
                     I.prow0 = e0.x; I.plen = e0.y; I.row0 = e0.z; I.nrows = e0.w;
                     I.ka0 = e1.x; I.kb0 = e1.y; I.ka1 = e1.z; I.kb1 = e1.w;
@@ -695,12 +770,17 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
                         dst[3] = make_int4(I.kh, I.slot, I.act[0], I.act[1]);
                         dst[4] = make_int4(I.more, I.pair, 0, 0);
                         mbar_arrive(&item_full[slot]);
-                        ++n_items;
+                        ++n_told;
                     }
                     if (!more) break;
                     // the next item, fetched while this one's tiles are loaded
                     tb = 0;
-                    if (++entry == n_entries) {
+                    if (dealt) {
+                        at += back;
+                        back = 2 * ctas - back;
+                        entry = at / lines;
+                        kh = at - entry * lines;
+                    } else if (++entry == n_entries) {
                         entry = 0;
                         ++kh;
                     }
@@ -1539,7 +1619,8 @@ ShLayout shared_layout(const ShProblem &pb)
     L.max_entries *= most;
     auto al = [](size_t b) { return (b + 255) & ~size_t(255); };
     L.entries = 256;
-    L.starts = L.entries + al(L.max_entries * sizeof(ShEntry));
+    L.sorted = L.entries + al(L.max_entries * sizeof(ShEntry));
+    L.starts = L.sorted + (L.slots == 0 ? al(L.max_entries * sizeof(ShEntry)) : 0);
     L.splits = L.starts + al((kShMaxCtas + 1) * sizeof(ShStart));
     L.part_l = L.splits + al(kShMaxCtas * sizeof(ShSplit));
     L.part_o = L.part_l + al(static_cast<size_t>(L.slots) * kShTiles * kShRows * 2 * sizeof(float));
@@ -1559,7 +1640,8 @@ cudaError_t launch_shared_plan(const ShProblem &pb, const ShLayout &lay, void *w
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     return launch_dependent(shared_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, pb, shared_key(pb, grid),
                             kShRows / (pb.Hq / pb.Hkv), reinterpret_cast<int32_t *>(ws),
-                            reinterpret_cast<ShEntry *>(ws + lay.entries), reinterpret_cast<ShStart *>(ws + lay.starts),
+                            reinterpret_cast<ShEntry *>(ws + lay.entries), reinterpret_cast<ShEntry *>(ws + lay.sorted),
+                            reinterpret_cast<ShStart *>(ws + lay.starts),
                             reinterpret_cast<ShSplit *>(ws + lay.splits), grid, lay.slots > 0 ? 1 : 0, shared_tiles(pb), shared_heads(pb),
                             dev_status);
 }

@@ -50,14 +50,15 @@ struct __align__(16) ShSplit {
 
 // Header words at the start of the workspace; from kShHdrKey on the problem the plan is for, which
 // every run that reads the plan compares with its own.
-enum { kShHdrStatus = 0, kShHdrCtas = 1, kShHdrSplits = 2, kShHdrEntries = 3, kShHdrKey = 4 };
+// kShHdrItems: items that are dealt out whole, or 0 where the CTAs have shares of the line.
+enum { kShHdrStatus = 0, kShHdrCtas = 1, kShHdrSplits = 2, kShHdrEntries = 3, kShHdrKey = 4, kShHdrItems = 16 };
 struct __align__(16) ShKey {
     int32_t w[12];
 };
 
 // Workspace layout (byte offsets); every part is 256-byte aligned.
 struct ShLayout {
-    size_t entries, starts, splits, part_l, part_o, total;
+    size_t entries, sorted, starts, splits, part_l, part_o, total;
     int64_t max_entries;
     int64_t items, units;     // items and cost units of the work at most, by single heads
     int64_t slots;            // partial results (two per CTA), or 0: no item can be split
@@ -100,6 +101,7 @@ struct ShParams {
     const int32_t *cu_seqlens;
     const int32_t *hdr;
     const ShEntry *entries;
+    const ShEntry *sorted;    // the same in falling order of tiles, where more items than CTAs are dealt out
     const ShStart *starts;    // [CTAs + 1]
     const ShSplit *splits;
     float *part_o;            // [slot][256 rows][D] partial outputs
