@@ -21,6 +21,7 @@
 //   1. shared_plan_kernel (one CTA) checks the offsets on the device, writes the list of entries
 //      and cuts the whole work, as one line of (kv head or pair, entry, key tile), into equal shares,
 //      one per CTA of the next kernel.  A cut through a long key range leaves two partial results.
+//      Where all key ranges are short it deals whole items out instead.
 //   2. shared_attn_kernel: one CTA per SM, 12 warps:
 //        warp 0      walks the CTA's share, tells the other roles each item (through a ring in
 //                    shared memory), and loads K and V tiles of 128 keys by TMA (one ring for both)
@@ -88,8 +89,9 @@ __device__ int sample_of(const int32_t *cu, int s, int end, int row)
 constexpr int kItemUnits = 2;
 __device__ __forceinline__ int entry_units(const ShEntry &E) { return E.tiles > 0 ? E.tiles + kItemUnits : 0; }
 
-// Latency alone bounds it: a few loads of the offsets in a row and about ten barriers of one CTA, 4.5 us
-// with 512 threads (4.9 with 1024; 256 are 0.1 faster for a few requests and 0.7 slower for 500 entries).
+// Latency alone bounds it: a few loads of the offsets in a row and about ten barriers of one CTA, 3.3 us for
+// one request, 4.5 where ranges are cut, with 512 threads (4.9 with 1024; 256 are 0.1 faster for a few
+// requests and 0.7 slower for 500 entries); the sort of 500 entries adds 2.5.
 // The offsets are held in shared memory because the searches read them many times.
 __global__ void __launch_bounds__(kPlanThreads)
     shared_plan_kernel(const ShProblem pb, const ShKey key, int bt, int32_t *hdr, ShEntry *entries, ShEntry *sorted,
@@ -235,8 +237,9 @@ __global__ void __launch_bounds__(kPlanThreads)
     const int lines = pb.Hkv >> (heads - 1);
 
     // ---- nothing is cut: whole items, dealt out to the CTAs in falling order of their tiles, one round from
-    // the first CTA to the last, the next one back.  (Shares of the line that end at items' ends: the
-    // largest 22% above the mean with seven items to a CTA.)
+    // the first CTA to the last, the next one back.  (Shares of the line that end at items' ends leave the
+    // largest 22% above the mean with seven items to a CTA: 112 samples of 1-300 tokens over 1-500 keys,
+    // capped, 102 us instead of 96; 32 requests of 15 samples over 200-500 keys 154.6 instead of 142.5.)
     if (!can_split) {
         const int n_items = n_entries * lines;
         const int ctas = min(grid, n_items);
@@ -309,8 +312,8 @@ __global__ void __launch_bounds__(kPlanThreads)
             const int into = static_cast<int>(u - pos_of(lo));
             // A cut near an end of the item moves to that end, and so does every cut through an item that is
             // short next to a share: its partial results cost more than the lesser balance (32 requests of
-            // 15 samples over 200-500 keys, 10 items to a share: 159.1 us when cut, 156.4 when not; with a
-            // limit of a sixth of a share 7 samples over 1-500 keys lose 2%).
+            // 15 samples over 200-500 keys, 10 items to a share, before they were dealt out: 159.1 us when cut,
+            // 156.4 when not; with a limit of a sixth of a share 7 samples over 1-500 keys lost 2%).
             const int64_t share = work / ctas;
             const int least = n * 10 <= share ? n : max(split_min / 2, static_cast<int>(min(share / 32, static_cast<int64_t>(n))));
             S.tile = into;
@@ -619,9 +622,9 @@ enum : int { kShPlain = 0, kShCapped = 1, kShCappedFixed = 2 };
 constexpr float kShCapFixed = 80.f;
 
 // Measured, 16 / 8 heads of 128, device time with plan and join: 16 samples of 257-700 tokens over 8000
-// keys 398 us, 1380 TFLOP/s; 32 requests of 15 samples of 16-96 tokens over 200-500 keys 154.5 us (prefill)
+// keys 398 us, 1380 TFLOP/s; 32 requests of 15 samples of 16-96 tokens over 200-500 keys 142.5 us (prefill)
 // and 45 us, 3.5 TB/s (last token); 128 last tokens over 30000-32768 keys 115 us, 5.4 TB/s.  14 / 2 heads
-// of 64, scores capped at 30: 112 samples of 1-300 tokens over 1-500 keys 101 us, 744 last tokens 38 us.
+// of 64, scores capped at 30: 112 samples of 1-300 tokens over 1-500 keys 96 us, 744 last tokens 38 us.
 // What bounds it is the chain of one query tile per key tile: about 2250 cycles of softmax (tensor memory
 // to registers, maximum, 128 exponentials of a row, weights back), then 1400 of hand-overs and products.
 // Two query tiles overlap their chains; tensor memory (S and O of each) has no room for a third at D = 128.
