@@ -1418,8 +1418,9 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
                     if (!seen && p.dev_status) atomicOr(p.dev_status, BG_DEVSTAT_EMPTY_ROW);
                     if (seen && p.lse) p.lse[orow] = (m + __log2f(l)) * 0.69314718055994530942f;
                 } else {
-                    // -inf marks a row that was not written; a sum of 0 over keys (scores of -inf) is NaN
-                    p.part_l[prow] = make_float2(!seen ? -INFINITY : l == 0.f ? NAN : m + __log2f(l), seen ? fix / l : 0.f);
+                    // a sum of 0 is -inf: of no key with 0 beside it, of keys whose scores are all -inf with 1
+                    const bool none = !seen || l == 0.f;
+                    p.part_l[prow] = make_float2(none ? -INFINITY : m + __log2f(l), !seen ? 0.f : none ? 1.f : fix / l);
                 }
             }
             if (act > 0) {
@@ -1504,17 +1505,17 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const ShParam
     };
     load(0);                                   // under way while the maximum is found
     float mx = -INFINITY;
-    bool nan = false;
+    bool keys = false;
 #pragma unroll 1
     for (int t = sub; t < S.pieces; t += LANES) {
-        const float lt = p.part_l[row_of(t)].x;
-        mx = fmaxf(mx, lt);
-        nan = nan || lt != lt;
+        const float2 lt = p.part_l[row_of(t)];
+        mx = fmaxf(mx, lt.x);
+        keys = keys || lt.x != -INFINITY || lt.y != 0.f;
     }
 #pragma unroll
     for (int w = LANES / 2; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(lanes, mx, w));
-    nan = (__ballot_sync(lanes, nan) & lanes) != 0;
-    if (mx == -INFINITY && !nan) {             // no piece has a key for this row
+    keys = (__ballot_sync(lanes, keys) & lanes) != 0;
+    if (!keys) {                               // no piece has a key for this row
         if (sub == 0 && p.dev_status) atomicOr(p.dev_status, BG_DEVSTAT_EMPTY_ROW);
         return;
     }
@@ -1526,7 +1527,7 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const ShParam
     for (int t0 = 0;;) {
 #pragma unroll
         for (int k = 0; k < AT_ONCE; ++k) {
-            if (lf[k].x == -INFINITY) continue;              // not written: part_o holds anything
+            if (lf[k].x == -INFINITY) continue;              // weights of 0, or not written: part_o holds anything
             const float wt = ex2(lf[k].x - mx);
             sum += wt;
             fix = fmaf(wt, lf[k].y, fix);

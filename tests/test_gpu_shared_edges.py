@@ -1,0 +1,66 @@
+"""Edges of the shared-prefix attention calls on the GPU: scores of -inf in part of a split key range."""
+import math
+
+import numpy as np
+import pytest
+
+from attention_packed_varlen_causal_gb300 import binding as bg
+from attention_packed_varlen_causal_gb300 import build
+from tests.helpers import from_dev
+from tests.test_gpu_shared import assert_close, call, device, make, reference, workspace
+
+pytestmark = pytest.mark.gpu
+
+HEADS = [(16, 8, 128), (14, 2, 64)]
+ONE, NEG_INF = 0x3F80, 0xFF80            # bf16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    build.build()
+    bg.load()
+
+
+def run(x, last, softcap=0.0, **kw):
+    """(out, lse) as fp64, and the device status."""
+    import torch
+    rows = len(x["cu"]) - 1 if last else int(x["cu"][-1])
+    out = torch.zeros((rows, x["Hq"], x["d"]), dtype=torch.bfloat16, device="cuda")
+    lse = torch.zeros((rows, x["Hq"]), device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    call(x, device(x), last, out, lse=lse, softcap=softcap, dev_status=st, **kw)
+    torch.cuda.synchronize()
+    return from_dev(out), lse.cpu().numpy().astype(np.float64), int(st.item())
+
+
+def hide_prefix(x, n):
+    """The first n prefix rows get scores of -inf: -inf in one place of K, 1 in that place of q."""
+    x["q"][:, :, 0] = x["ql"][:, :, 0] = ONE
+    x["pk"][:n, :, 0] = NEG_INF
+
+
+@pytest.mark.parametrize("last", [False, True], ids=["prefill", "last"])
+@pytest.mark.parametrize("heads", HEADS, ids=lambda h: "h%d_%d_d%d" % h)
+@pytest.mark.parametrize("where", ["front", "back"])
+@pytest.mark.parametrize("n,hidden", [(4000, 2700), (600, 300)], ids=["split", "whole"])
+def test_tiles_whose_scores_are_all_minus_infinity(n, hidden, where, heads, last):
+    """Their weights are 0: the rest of the keys decides, as if these were not there."""
+    x = make(41, [n], [[3, 1, 40]], *heads)
+    assert (workspace(x).numel() > 1 << 20) == (n > 1000)    # room for partial results: the range is cut
+    hide_prefix(x, hidden)
+    y = dict(x, pk=np.ascontiguousarray(x["pk"][hidden:]), pv=np.ascontiguousarray(x["pv"][hidden:]),
+             cup=np.array([0, n - hidden], np.int32))
+    if where == "back":
+        x["pk"], x["pv"] = (np.ascontiguousarray(np.concatenate((x[m][hidden:], x[m][:hidden]))) for m in ("pk", "pv"))
+    out, lse, st = run(x, last)
+    assert st == 0
+    assert_close(out, lse, reference(y, last), f"{where} {heads} last={last}")
+
+
+@pytest.mark.parametrize("n", [100, 4000], ids=["whole", "split"])
+def test_queries_whose_scores_are_all_minus_infinity(n):
+    """A softmax over nothing but -inf: NaN with a log-sum of -inf, whether the range is cut or not."""
+    x = make(42, [n], [[0, 0]], 16, 8, 128)
+    hide_prefix(x, n)
+    out, lse, st = run(x, True)
+    assert np.isnan(out).all() and (lse == -math.inf).all() and st == 0
