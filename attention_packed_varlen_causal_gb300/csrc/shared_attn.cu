@@ -1140,13 +1140,16 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
                     tmem_st32f(tO + 32 * c, o);
                 }
             };
-            // A tile's sum of weights.  P.V multiplies weights rounded to bf16.  The rounding of the tile's
-            // largest weight enters the sum that O is divided by, which makes the dominant term exact; the
-            // log-sum-exp keeps the unrounded sum.
-            auto add_sums = [&](float mx, float2 negm, float sum) {
-                const float pmax = ex2(ffma2(make_float2(mx, mx), make_float2(sl2, sl2), negm).x);
+            // A tile's sum of weights and its largest one.  P.V multiplies weights rounded to bf16, as the matrix
+            // instruction takes P and V of one type.  The rounding of the tile's largest weight enters the sum
+            // that O is divided by, which makes the dominant term exact; the log-sum-exp keeps the unrounded sum.
+            auto add_sums = [&](float pmax, float sum) {
                 fix += __uint_as_float(pack_bf16x2(pmax, 0.f) << 16) - pmax;
                 l += sum;
+            };
+            // the weight of the score mx
+            auto weight_of = [&](float mx, float2 negm) {
+                return ex2(ffma2(make_float2(mx, mx), make_float2(sl2, sl2), negm).x);
             };
 
             // own keys this row sees: [lo, hi)
@@ -1240,6 +1243,7 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
                     };
                     if constexpr (MODE == kShCappedFixed) {
                         float2 rs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                        float pmax = 0.f;
 #pragma unroll 1
                         for (int c = 0; c < 4; ++c) {
                             uint32_t pk[16];
@@ -1269,13 +1273,14 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
 #pragma unroll
                                 for (int i = 0; i < 16; ++i) {
                                     rs[i & 1] = fadd2(rs[i & 1], make_float2(x[2 * i], x[2 * i + 1]));
+                                    pmax = fmax3f(pmax, x[2 * i], x[2 * i + 1]);
                                     pk[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
                                 }
                             }
                             tmem_st16(tS + 16 * c, pk);          // over scores that have been read
                             if (c & 1) hand_over(c >> 1);
                         }
-                        l += (rs[0].x + rs[1].x) + (rs[0].y + rs[1].y);
+                        add_sums(pmax, (rs[0].x + rs[1].x) + (rs[0].y + rs[1].y));
                     } else if (MODE == kShPlain && ce - cf <= 3) {
                         // Few columns count, as in most own tiles of prefill: the maximum over those chunks first,
                         // then their weights, 32 columns at a time in short code.  With four chunks the path
@@ -1321,7 +1326,7 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
                             tmem_st16(tS + 16 * c, pk);          // over scores that have been read
                             if (c & 1) hand_over(c >> 1);
                         }
-                        add_sums(mx, negm, (rs[0].x + rs[1].x) + (rs[0].y + rs[1].y));
+                        add_sums(weight_of(mx, negm), (rs[0].x + rs[1].x) + (rs[0].y + rs[1].y));
                     } else {
                     float s[kShKeys];
                     tmem_ld64(tS, s);
@@ -1392,7 +1397,7 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
                     tmem_st16(tS + 48, pk + 16);
                     hand_over(1);
                     const float2 r01 = fadd2(rs[0], rs[1]), r23 = fadd2(rs[2], rs[3]);
-                    add_sums(mx, negm, (r01.x + r23.x) + (r01.y + r23.y));
+                    add_sums(weight_of(mx, negm), (r01.x + r23.x) + (r01.y + r23.y));
                     }
                 }
                 ++done;

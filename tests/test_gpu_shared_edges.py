@@ -1,4 +1,5 @@
-"""Edges of the shared-prefix attention calls on the GPU: scores of -inf in part of a split key range."""
+"""Edges of the shared-prefix attention calls on the GPU: scores of -inf in part of a key range, and weights
+that one key dominates."""
 import math
 
 import numpy as np
@@ -6,6 +7,7 @@ import pytest
 
 from attention_packed_varlen_causal_gb300 import binding as bg
 from attention_packed_varlen_causal_gb300 import build
+from attention_packed_varlen_causal_gb300 import workloads as wl
 from tests.helpers import from_dev
 from tests.test_gpu_shared import assert_close, call, device, make, reference, workspace
 
@@ -64,3 +66,34 @@ def test_queries_whose_scores_are_all_minus_infinity(n):
     hide_prefix(x, n)
     out, lse, st = run(x, True)
     assert np.isnan(out).all() and (lse == -math.inf).all() and st == 0
+
+
+@pytest.mark.parametrize("last", [False, True], ids=["prefill", "last"])
+@pytest.mark.parametrize("softcap", [0.0, 7.0, 30.0, 55.0, 56.0, 300.0])
+def test_queries_of_one_key_return_its_value(softcap, last):
+    """One key (the first token of a sample without a prefix): its weight cancels out, whatever rounding it
+    had, and out is v bit for bit (what fp32 leaves is 2^-22 of it, far below half a bf16 step)."""
+    x = make(43, [0, 0], [[1] * 30, [1, 5, 1]], 14, 2, 64, q_scale=8.0)
+    out = run(x, last, softcap)[0]
+    v = from_dev(device(x)["v"])
+    rows = np.flatnonzero(np.diff(x["cu"]) == 1)
+    at = x["cu"][rows]
+    assert np.array_equal(out[rows if last else at], np.repeat(v[at], 7, axis=1))
+
+
+@pytest.mark.parametrize("last", [False, True], ids=["prefill", "last"])
+@pytest.mark.parametrize("prefix", [700, 5000], ids=["whole", "split"])
+def test_capped_queries_with_a_dominant_key(prefix, last):
+    """A prefix key along the query has a score of about +50 (a weight of 1.098 2^72, half a bf16 step off), the
+    others -50: the result is that key's v bit for bit (the others' weights add up to less than 2^-130 of it)."""
+    d, Hq = 64, 4
+    x = make(44, [prefix], [[2, 9]], Hq, 2, d)
+    s = np.sign(np.random.default_rng(44).standard_normal(d)).astype(np.float32)
+    big = wl.bf16_bits_from_f32(np.tile(16 * s, (1, 1, 1)))
+    for n in ("q", "ql"):
+        x[n][:] = big
+    x["k"][:] = x["pk"][:] = wl.bf16_bits_from_f32(np.tile(-16 * s, (1, 1, 1)))
+    x["pk"][prefix - 333] = big[0]
+    out = run(x, last, 50.0)[0]
+    v = from_dev(device(x)["pv"])[prefix - 333]
+    assert np.array_equal(out, np.broadcast_to(np.repeat(v, 2, axis=0), out.shape))
