@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(kPlanThreads)
                        ShStart *__restrict__ starts, ShSplit *__restrict__ splits, int grid, int can_split, int tiles_per, int heads,
                        int32_t *dev_status)
 {
-    __shared__ int s_err, s_nsplit;
+    __shared__ int s_err, s_nsplit, s_empty;
     __shared__ int s_warp[32];
     __shared__ int s_base[kPlanThreads];
     __shared__ ShStart s_start[kShMaxCtas + 1];
@@ -110,6 +110,7 @@ __global__ void __launch_bounds__(kPlanThreads)
     if (tid == 0) {
         s_err = 0;
         s_nsplit = 0;
+        s_empty = 0;
     }
     grid_dep_wait();
     __syncthreads();
@@ -216,7 +217,7 @@ __global__ void __launch_bounds__(kPlanThreads)
                         E.s0 = (e - s_base[t]) & 1;
                     }
                 }
-                if (E.tiles == 0 && dev_status) atomicOr(dev_status, BG_DEVSTAT_EMPTY_ROW);
+                if (E.tiles == 0) s_empty = 1;
             }
             int sum;
             const int excl = block_exclusive(entry_units(E), s_warp, &sum);
@@ -229,6 +230,11 @@ __global__ void __launch_bounds__(kPlanThreads)
         }
         n_entries += total;
         __syncthreads();
+    }
+    // the rows of an entry without keys, which no CTA visits: every run of the plan reports them
+    if (tid == 0) {
+        hdr[kShHdrEmpty] = s_empty;
+        if (s_empty && dev_status) atomicOr(dev_status, BG_DEVSTAT_EMPTY_ROW);
     }
 
     // ---- equal shares of the line; fewer CTAs where a share would be below kShSplitMin (half of it for pairs,
@@ -702,8 +708,11 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
             // ============================================================ items, K and V
             if (lane == 0) {
                 bool other;
-                const bool mine = plan_ready(p, &other) && cta < p.hdr[kShHdrCtas];
-                if (other && cta == 0 && p.dev_status) atomicOr(p.dev_status, BG_DEVSTAT_PLAN);
+                const bool ready = plan_ready(p, &other), mine = ready && cta < p.hdr[kShHdrCtas];
+                if (cta == 0 && p.dev_status) {
+                    if (other) atomicOr(p.dev_status, BG_DEVSTAT_PLAN);
+                    if (ready && p.hdr[kShHdrEmpty] != 0) atomicOr(p.dev_status, BG_DEVSTAT_EMPTY_ROW);
+                }
                 ShStart A = {}, B = {};
                 int n_entries = 0, ctas = 0, lines = 1;
                 uint32_t n_items = 0, at = 0;              // dealt out: all items, and the place of this one

@@ -51,7 +51,10 @@ struct __align__(16) ShSplit {
 // Header words at the start of the workspace; from kShHdrKey on the problem the plan is for, which
 // every run that reads the plan compares with its own.
 // kShHdrItems: items that are dealt out whole, or 0 where the CTAs have shares of the line.
-enum { kShHdrStatus = 0, kShHdrCtas = 1, kShHdrSplits = 2, kShHdrEntries = 3, kShHdrKey = 4, kShHdrItems = 16 };
+// kShHdrEmpty: 1 if an entry has no keys at all.
+enum {
+    kShHdrStatus = 0, kShHdrCtas = 1, kShHdrSplits = 2, kShHdrEntries = 3, kShHdrKey = 4, kShHdrItems = 16, kShHdrEmpty = 17
+};
 struct __align__(16) ShKey {
     int32_t w[12];
 };

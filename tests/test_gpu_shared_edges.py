@@ -1,5 +1,5 @@
-"""Edges of the shared-prefix attention calls on the GPU: scores of -inf in part of a key range, and weights
-that one key dominates."""
+"""Edges of the shared-prefix attention calls on the GPU: scores of -inf in part of a key range, weights that
+one key dominates, and queries without keys in planned runs."""
 import math
 
 import numpy as np
@@ -97,3 +97,23 @@ def test_capped_queries_with_a_dominant_key(prefix, last):
     out = run(x, last, 50.0)[0]
     v = from_dev(device(x)["pv"])[prefix - 333]
     assert np.array_equal(out, np.broadcast_to(np.repeat(v, 2, axis=0), out.shape))
+
+
+@pytest.mark.parametrize("prefix,groups,max_prefix", [
+    ([0, 40], [[0, 0], [3]], 40), ([0, 3000], [[0], [3, 1]], 3000), ([0, 0], [[0, 0], [0]], 0), ([0, 0], [[0], [0]], 9000)],
+    ids=["dealt", "cut", "no_key_at_all", "no_key_and_a_large_bound"])
+def test_planned_runs_report_queries_without_keys(prefix, groups, max_prefix):
+    """Every run raises BG_DEVSTAT_EMPTY_ROW, not only the plan, and leaves those rows as they are."""
+    import torch
+    x = dict(make(45, prefix, groups, 16, 8, 128), max_prefix=max_prefix)
+    t, ws = device(x), workspace(x)
+    st = [torch.zeros(1, dtype=torch.int32, device="cuda") for _ in range(3)]
+    bg.bg_shared_last_token_plan(t["cu"], int(x["cu"][-1]), x["max_seqlen"], t["cup"], int(x["cup"][-1]), max_prefix,
+                                 t["cug"], 16, 8, 128, workspace=ws, dev_status=st[0])
+    none = np.diff(x["cu"]) + np.repeat(np.diff(x["cup"]), np.diff(x["cug"])) == 0
+    for i in (1, 2):
+        out = torch.full((len(none), 16, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+        call(x, t, True, out, ws=ws, planned=True, dev_status=st[i])
+        got = from_dev(out)
+        assert (got[none] == 7.0).all() and not (got[~none] == 7.0).all(axis=(1, 2)).any()
+    assert [int(s.item()) for s in st] == [bg.BG_DEVSTAT_EMPTY_ROW] * 3
