@@ -594,6 +594,7 @@ bg_status_t shared_check_sizes(const ShProblem &pb)
         pb.max_prefix_len < 0 || pb.Hq <= 0 || pb.Hkv <= 0 || pb.head_dim <= 0 || pb.Hq % pb.Hkv != 0)
         return BG_ERR_INVALID_ARG;
     if (pb.num_groups == 0 && (pb.num_seqs > 0 || pb.total_prefix > 0)) return BG_ERR_INVALID_ARG;
+    if (!pb.last && pb.num_seqs == 0 && pb.total_tokens > 0) return BG_ERR_INVALID_ARG;
     if (!supported_head_dim(pb.head_dim) || pb.Hq / pb.Hkv > kShRows || pb.max_seqlen > BG_MAX_SEQLEN ||
         pb.max_prefix_len > BG_MAX_SEQLEN)
         return BG_ERR_UNSUPPORTED;

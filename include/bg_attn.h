@@ -457,13 +457,14 @@ bg_status_t bg_beam_select(const float *logits, const float *cum,
  * BG_DEVSTAT_PLAN.
  *
  * Errors: BG_ERR_INVALID_ARG for NULL or misaligned pointers, negative sizes,
- * num_groups == 0 with samples or prefix rows, Hq % Hkv != 0, a bad scale or
- * softcap (or one whose quotient or product with log2(e) is not a normal
- * number), a too-small workspace, or an output or the workspace overlapping
- * another argument; BG_ERR_UNSUPPORTED for head_dim not in {64, 128},
+ * num_groups == 0 with samples or prefix rows, tokens without samples (prefill),
+ * Hq % Hkv != 0, a bad scale or softcap (or one whose quotient or product with
+ * log2(e) is not a normal number), a too-small workspace, or an output or the
+ * workspace overlapping another argument; BG_ERR_UNSUPPORTED for head_dim not in {64, 128},
  * Hq/Hkv > 128, or max_seqlen or max_prefix_len > BG_MAX_SEQLEN.  No queries
  * (total_tokens == 0, or num_seqs == 0 for the last-token call) is a valid
- * no-op.  bg_shared_attn_workspace_size gives 0 for sizes the calls refuse.
+ * no-op.  bg_shared_attn_workspace_size gives 0 for sizes that either call
+ * refuses.
  */
 size_t bg_shared_attn_workspace_size(int32_t num_groups, int32_t num_seqs, int32_t total_tokens,
                                      int32_t max_seqlen, int32_t max_prefix_len, int32_t Hq,
