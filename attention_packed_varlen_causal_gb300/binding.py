@@ -339,6 +339,14 @@ def _alike(dtype, index: int, tensors) -> bool:
     return True
 
 
+def _fits(*sizes) -> bool:
+    """Whether all sizes are int32; ctypes would pass the low 32 bits of larger ones."""
+    for n in sizes:
+        if not -0x80000000 <= n <= 0x7fffffff:
+            return False
+    return True
+
+
 def _launch(fn: str, index: int, stream, *args):
     """Calls the library's ``fn`` with device ``index`` current, on ``stream`` or that device's current one."""
     import torch
@@ -353,6 +361,8 @@ def _launch(fn: str, index: int, stream, *args):
 
 def bg_shared_attn_workspace_size(num_groups: int, num_seqs: int, total_tokens: int, max_seqlen: int,
                                   max_prefix_len: int, Hq: int, Hkv: int, head_dim: int) -> int:
+    if not _fits(num_groups, num_seqs, total_tokens, max_seqlen, max_prefix_len, Hq, Hkv, head_dim):
+        return 0
     return int(load().bg_shared_attn_workspace_size(num_groups, num_seqs, total_tokens, max_seqlen, max_prefix_len, Hq,
                                                     Hkv, head_dim))
 
@@ -392,6 +402,8 @@ def _shared_run(fn: str, last: bool, q, k, v, cu_seqlens, max_seqlen, prefix_k, 
             ("cu_group", cu_group, i32, (R + 1,)), ("out", out, bf16, (rows, Hq, d)), ("lse", lse, f32, (rows, Hq)),
             ("dev_status", dev_status, i32, dev_status.shape if dev_status is not None else ())))
     max_seqlen, max_prefix_len = int(max_seqlen), int(max_prefix_len)
+    if not _fits(S, T, P, max_seqlen, max_prefix_len):
+        raise BgError(fn, BG_ERR_UNSUPPORTED)
     ws, ws_bytes = _workspace(fn, workspace, (R, S, T, max_seqlen, max_prefix_len, Hq, Hkv, d), index)
     _launch(fn, index, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), S, T, max_seqlen,
             _ptr(prefix_k), _ptr(prefix_v), cu_prefix.data_ptr(), P, max_prefix_len, cu_group.data_ptr(), R, Hq, Hkv, d,
@@ -448,6 +460,8 @@ def _shared_plan(fn: str, cu_seqlens, total_tokens, max_seqlen, cu_prefix, total
         ("cu_group", cu_group, i32, (R + 1,)),
         ("dev_status", dev_status, i32, dev_status.shape if dev_status is not None else ())))
     T, P, max_seqlen, max_prefix_len = int(total_tokens), int(total_prefix), int(max_seqlen), int(max_prefix_len)
+    if not _fits(S, T, P, max_seqlen, max_prefix_len, Hq, Hkv, head_dim):
+        raise BgError(fn, BG_ERR_UNSUPPORTED)
     ws, ws_bytes = _workspace(fn, workspace, (R, S, T, max_seqlen, max_prefix_len, Hq, Hkv, head_dim), index)
     _launch(fn, index, stream, cu_seqlens.data_ptr(), S, T, max_seqlen, cu_prefix.data_ptr(), P, max_prefix_len,
             cu_group.data_ptr(), R, Hq, Hkv, head_dim, ws, ws_bytes, _ptr(dev_status))
@@ -481,6 +495,8 @@ def bg_token_logprobs(logits, tokens=None, *, logprob=None, entropy=None, top_to
     if dtype is None or (V > 1 and N > 0 and logits.stride(1) != 1):
         raise ValueError(f"{fn}: logits must be float32 or bfloat16 with contiguous rows, got {logits.dtype} with "
                          f"strides {logits.stride()}")
+    if not _fits(N, V):
+        raise BgError(fn, BG_ERR_UNSUPPORTED)
     index = logits.get_device()
     K = 0 if top_token is None else top_token.shape[-1]
     f32, i32 = torch.float32, torch.int32

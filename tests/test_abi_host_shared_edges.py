@@ -1,6 +1,7 @@
 """Host-side refusals of sizes that contradict each other or do not fit the C ABI's integers, in the
 shared-prefix attention and log-probability calls (no GPU)."""
 import pytest
+import torch
 
 from attention_packed_varlen_causal_gb300 import binding as bg
 from tests.test_abi_host_shared import INV, OK, lib, plan, run  # noqa: F401  (lib: a fixture)
@@ -15,3 +16,25 @@ def test_tokens_without_samples(lib, kw):  # noqa: F811
     # the last-token calls have a query per sample, so none here
     assert run(lib, "bg_shared_last_token_attn", **kw) == OK
     assert bg.bg_shared_attn_workspace_size(kw.get("R", 2), 0, 10, 8, 9, 4, 2, 64) == 0
+
+
+def test_sizes_past_32_bits_are_refused_not_cut(lib):  # noqa: F811
+    """The C ABI takes int32 sizes: 2^32 + 10 must not reach it as 10."""
+    big, bf, i32 = (1 << 32) + 10, torch.bfloat16, torch.int32
+    cu, cug = torch.zeros(4, dtype=i32), torch.zeros(3, dtype=i32)
+    ws = torch.zeros(1 << 16, dtype=torch.uint8)
+    q, k = torch.zeros(10, 4, 64, dtype=bf), torch.zeros(10, 2, 64, dtype=bf)
+    for n, p in ((big, 9), (8, big), (-big, 9)):
+        with pytest.raises(bg.BgError) as e:
+            bg.bg_shared_prefill_attn(q, k, k, cu, n, k, k, cug, p, cug, q.clone(), workspace=ws)
+        assert e.value.status == bg.BG_ERR_UNSUPPORTED
+    for sizes in ((big, 8, 12, 9), (10, big, 12, 9), (10, 8, big, 9), (10, 8, 12, big)):
+        T, n, P, p = sizes
+        with pytest.raises(bg.BgError) as e:
+            bg.bg_shared_last_token_plan(cu, T, n, cug, P, p, cug, 4, 2, 64, workspace=ws)
+        assert e.value.status == bg.BG_ERR_UNSUPPORTED
+        assert bg.bg_shared_attn_workspace_size(2, 3, T, n, p, 4, 2, 64) == 0 or P == big
+    for shape in ((1, big), (big, 1)):
+        with pytest.raises(bg.BgError) as e:
+            bg.bg_token_logprobs(torch.empty(shape, dtype=bf, device="meta"), entropy=torch.zeros(1))
+        assert e.value.status == bg.BG_ERR_UNSUPPORTED
