@@ -19,7 +19,8 @@ sm_103a CUDA kernels:
                                       of the suffix and the decode attention
   * ``bg_beam_select``                beam candidate selection of one step
     (+ ``bg_beam_select_workspace_size``)
-  * ``bg_selftest_wait_timeout``      diagnostic of the bounded-wait failure path
+  * ``bg_selftest_wait_timeout``, ``bg_selftest_logprobs_timeout``  diagnostics of the
+                                      bounded-wait failure path
   * ``bg_status_string``
 
 ``binding`` is a thin ctypes layer over the shared library; importing this

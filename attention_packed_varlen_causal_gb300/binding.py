@@ -72,6 +72,7 @@ SIGNATURES = {
     "bg_shared_last_token_attn_planned": (_SHARED_RUN, ctypes.c_int),
     "bg_token_logprobs": ([_P, _I32, ctypes.c_int64, _I32, _I32, _P, _I32, _P, _P, _P, _P, _P, _P], ctypes.c_int),
     "bg_selftest_wait_timeout": ([_P, _P, _P], ctypes.c_int),
+    "bg_selftest_logprobs_timeout": ([_P, _I32, _I32, _P, _I32, _P, _P, _P, _P, _P, _P], ctypes.c_int),
     "bg_beam_select": ([_P, _P, _I32, _I32, _I32, _P, _P, _P, _P, _SZ, _P], ctypes.c_int),
 }
 
@@ -511,3 +512,21 @@ def bg_token_logprobs(logits, tokens=None, *, logprob=None, entropy=None, top_to
     _launch(fn, index, stream, logits.data_ptr(), dtype, logits.stride(0) if N > 1 else max(V, 1), N, V, _ptr(tokens), K,
             _ptr(logprob), _ptr(entropy), _ptr(top_token), _ptr(top_logprob), _ptr(dev_status))
     return logprob, entropy, top_token, top_logprob
+
+
+def bg_selftest_logprobs_timeout(logits, tokens, stalled_row: int, *, logprob, entropy, top_token, top_logprob, dev_status,
+                                 stream=None):
+    """bg_token_logprobs of fp32 logits [N,V] with K = 1 whose rows from stalled_row on are never loaded: the waits
+    run out after a second, those rows get NaN and -1, and dev_status (int32 [1]) BG_DEVSTAT_TIMEOUT."""
+    import torch
+    fn = "bg_selftest_logprobs_timeout"
+    N, V = logits.shape
+    f32, i32 = torch.float32, torch.int32
+    _expect(fn, logits.device, (
+        ("logits", logits, f32, (N, V)), ("tokens", tokens, i32, (N,)), ("logprob", logprob, f32, (N,)),
+        ("entropy", entropy, f32, (N,)), ("top_token", top_token, i32, (N, 1)), ("top_logprob", top_logprob, f32, (N, 1)),
+        ("dev_status", dev_status, i32, (1,))))
+    if not _fits(N, V, stalled_row):
+        raise BgError(fn, BG_ERR_UNSUPPORTED)
+    _launch(fn, logits.get_device(), stream, logits.data_ptr(), N, V, tokens.data_ptr(), stalled_row, logprob.data_ptr(),
+            entropy.data_ptr(), top_token.data_ptr(), top_logprob.data_ptr(), dev_status.data_ptr())

@@ -830,4 +830,22 @@ bg_status_t bg_token_logprobs(const void *logits, int32_t dtype, int64_t row_str
                : BG_ERR_CUDA;
 }
 
+bg_status_t bg_selftest_logprobs_timeout(const float *logits, int32_t N, int32_t V, const int32_t *tokens,
+                                         int32_t stalled_row, float *logprob_out, float *entropy_out,
+                                         int32_t *top_token_out, float *top_logprob_out, int32_t *dev_status,
+                                         cudaStream_t stream)
+{
+    if (N < 1 || V < 1 || stalled_row < 0 || stalled_row > N) return BG_ERR_INVALID_ARG;
+    if (V > BG_MAX_VOCAB) return BG_ERR_UNSUPPORTED;
+    const void *ptrs[7] = {logits, tokens, logprob_out, entropy_out, top_token_out, top_logprob_out, dev_status};
+    for (const void *q : ptrs)
+        if (!q || !aligned(q, 4)) return BG_ERR_INVALID_ARG;
+    const int nsm = sm_count();
+    if (nsm <= 0) return BG_ERR_CUDA;
+    return launch_logprobs_selftest(logits, N, V, tokens, stalled_row, logprob_out, entropy_out, top_token_out,
+                                    top_logprob_out, dev_status, nsm, stream) == cudaSuccess
+               ? BG_OK
+               : BG_ERR_CUDA;
+}
+
 }  // extern "C"

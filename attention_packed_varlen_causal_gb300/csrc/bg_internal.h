@@ -61,6 +61,11 @@ cudaError_t launch_token_logprobs(const void *logits, int32_t dtype, int64_t row
                                   const int32_t *tokens, int32_t K, float *logprob, float *entropy, int32_t *top_token,
                                   float *top_logprob, int32_t *dev_status, int nsm, cudaStream_t stream);
 
+// The same with K = 1 and rows of fp32 side by side, of which those from `stalled` on are never loaded.
+cudaError_t launch_logprobs_selftest(const float *logits, int32_t N, int32_t V, const int32_t *tokens, int32_t stalled,
+                                     float *logprob, float *entropy, int32_t *top_token, float *top_logprob,
+                                     int32_t *dev_status, int nsm, cudaStream_t stream);
+
 cudaError_t launch_suffix_reorder(const void *src_k, const void *src_v, void *dst_k, void *dst_v,
                                   const int32_t *parent_idx, const void *new_k, const void *new_v, int32_t R,
                                   int32_t W, int32_t suffix_max, int32_t n_tokens, int32_t Hkv, int32_t head_dim,

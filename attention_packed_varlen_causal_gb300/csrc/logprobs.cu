@@ -181,6 +181,7 @@ struct LpParams {
     int32_t *top_token;
     float *top_logprob;
     int32_t *dev_status;
+    int32_t stalled;      // (self-test) rows from this one on are never loaded
 };
 
 // `bytes` (a multiple of 16, from a 16-byte boundary) into shared memory, completing on `bar`.
@@ -240,7 +241,8 @@ __device__ __forceinline__ __nv_bfloat16 slot_value(float x)
     return __float2bfloat16_ru(x);
 }
 
-template <typename T, int W>
+// STALL: the self-test of a wait that runs out.
+template <typename T, int W, bool STALL>
 __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LpParams p)
 {
     extern __shared__ __align__(16) uint8_t lp_smem[];
@@ -307,7 +309,10 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LpParams 
     auto issue = [&]() {
         while (load_v >= load_end) {                     // the next row that has vectors
             load_row += rows_at_once;
-            if (load_row >= p.N) return;
+            if (load_row >= p.N || (STALL && load_row >= p.stalled)) {
+                load_row = p.N;
+                return;
+            }
             const Slice L = slice_of(load_row);
             load_x = L.x + L.head;
             load_v = L.v0;
@@ -328,6 +333,7 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LpParams 
     if (tid == 0)
         for (int i = 0; i < kLpStages - 1; ++i) issue();
     uint32_t sums = 0;                                   // batches summed
+    bool lost = false;                                   // this warp gave a wait up: its rows from then on are NaN
 
     if (C > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     for (int64_t row = row0; row < p.N; row += rows_at_once) {
@@ -357,11 +363,12 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LpParams 
         float slot_max = -INFINITY;
         bool far = false;                                 // (of the warp) see below
 #pragma unroll 1
-        for (int b = 0; b < nb; ++b, ++sums) {
+        for (int b = 0; b < nb && !lost; ++b, ++sums) {
             if (tid == 0) issue();
             __syncwarp();
             const uint32_t st = sums % kLpStages;
-            lp_wait(&full[st], (sums / kLpStages) & 1, abort);     // (given up: BG_DEVSTAT_TIMEOUT)
+            lost = !__all_sync(0xffffffffu, lp_wait(&full[st], (sums / kLpStages) & 1, abort));
+            if (lost) break;
             const int left = v1 - v0 - b * kBatch;
             uint4 g[kLpLoads];
 #pragma unroll
@@ -432,6 +439,7 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LpParams 
         }
 
         // ---- the warp's sums and lane maxima, the team's, the row's
+        if (lost) a.z = NAN;
         uint32_t mine = 0;
         if (p.K > 0) {
             mine = sort_desc(order_key(best), lane);
@@ -480,7 +488,7 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LpParams 
         }
         team_sync();
         A = sh.all[team];
-        const bool bad = A.z != A.z;                       // a NaN or +inf in the row
+        const bool bad = A.z != A.z;                       // a NaN or +inf in the row, or a wait was given up
         const float log2z = log2f(A.z);                    // -inf for a row of -inf
         auto logprob = [&](float f) {
             return A.z == 0.f ? -INFINITY : (f - A.m) - log2z * 0.69314718055994530942f;
@@ -618,10 +626,10 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LpParams 
     }
 }
 
-template <typename T, int W>
+template <typename T, int W, bool STALL>
 cudaError_t launch_lp(const LpParams &p, int nsm, cudaStream_t stream)
 {
-    auto kern = logprobs_kernel<T, W>;
+    auto kern = logprobs_kernel<T, W, STALL>;
     static std::atomic<uint64_t> smem_done{0};
     cudaError_t e = ensure_smem_attribute(kern, static_cast<int>(sizeof(LpShared)), smem_done);
     if (e != cudaSuccess) return e;
@@ -654,13 +662,13 @@ cudaError_t launch_lp(const LpParams &p, int nsm, cudaStream_t stream)
 // by 4), from then on 4 warps do, eight rows at a time per SM (700 rows: 36.9 by 8 warps, 31.0 by 4; 1200
 // rows: 45.0 and 42.7).  Rows under 16 KB are too short for 16 warps, and under 48 KB for 8 (400 rows of
 // 20,011 bf16 logits: 11.2 us by 8 warps, 10.9 by 4; of 30,011: 13.0 and 14.4).
-template <typename T>
+template <typename T, bool STALL>
 cudaError_t launch_team(const LpParams &p, int nsm, cudaStream_t stream)
 {
     const int64_t bytes = static_cast<int64_t>(p.V) * sizeof(T);
-    if (p.N <= 2 * nsm && bytes >= 16 << 10) return launch_lp<T, 16>(p, nsm, stream);
-    if (p.N > 2 * nsm && p.N <= 4 * nsm && bytes >= 48 << 10) return launch_lp<T, 8>(p, nsm, stream);
-    return launch_lp<T, 4>(p, nsm, stream);
+    if (p.N <= 2 * nsm && bytes >= 16 << 10) return launch_lp<T, 16, STALL>(p, nsm, stream);
+    if (p.N > 2 * nsm && p.N <= 4 * nsm && bytes >= 48 << 10) return launch_lp<T, 8, STALL>(p, nsm, stream);
+    return launch_lp<T, 4, STALL>(p, nsm, stream);
 }
 
 }  // namespace
@@ -669,8 +677,17 @@ cudaError_t launch_token_logprobs(const void *logits, int32_t dtype, int64_t row
                                   const int32_t *tokens, int32_t K, float *logprob, float *entropy, int32_t *top_token,
                                   float *top_logprob, int32_t *dev_status, int nsm, cudaStream_t stream)
 {
-    const LpParams p{logits, row_stride, N, V, K, tokens, logprob, entropy, top_token, top_logprob, dev_status};
-    return dtype == BG_DTYPE_F32 ? launch_team<float>(p, nsm, stream) : launch_team<__nv_bfloat16>(p, nsm, stream);
+    const LpParams p{logits, row_stride, N, V, K, tokens, logprob, entropy, top_token, top_logprob, dev_status, N};
+    return dtype == BG_DTYPE_F32 ? launch_team<float, false>(p, nsm, stream)
+                                 : launch_team<__nv_bfloat16, false>(p, nsm, stream);
+}
+
+cudaError_t launch_logprobs_selftest(const float *logits, int32_t N, int32_t V, const int32_t *tokens, int32_t stalled,
+                                     float *logprob, float *entropy, int32_t *top_token, float *top_logprob,
+                                     int32_t *dev_status, int nsm, cudaStream_t stream)
+{
+    const LpParams p{logits, V, N, V, 1, tokens, logprob, entropy, top_token, top_logprob, dev_status, stalled};
+    return launch_team<float, true>(p, nsm, stream);
 }
 
 }  // namespace bg

@@ -530,7 +530,9 @@ bg_status_t bg_shared_last_token_attn_planned(const void *q, const void *k, cons
  *   top_token_out int32 [N, K], top_logprob_out fp32 [N, K]
  *   dev_status   device int32 or NULL
  * A row with a NaN or +inf logit gets NaN and tokens -1; a row of -inf only
- * gets log-probabilities -inf, entropy 0 and the tokens 0 .. K-1.
+ * gets log-probabilities -inf, entropy 0 and the tokens 0 .. K-1.  A wait that
+ * runs out raises BG_DEVSTAT_TIMEOUT, and the rows that it kept from being
+ * computed get NaN and -1.
  * One launch, no workspace; the logits come from memory once (a row with
  * thousands of logits equal to its K-th best is read K times more).
  * Errors: BG_ERR_INVALID_ARG for N < 0, an unknown dtype, row_stride < V, NULL
@@ -543,6 +545,22 @@ bg_status_t bg_token_logprobs(const void *logits, int32_t dtype, int64_t row_str
                               int32_t V, const int32_t *tokens, int32_t K, float *logprob_out,
                               float *entropy_out, int32_t *top_token_out,
                               float *top_logprob_out, int32_t *dev_status, cudaStream_t stream);
+
+/*
+ * Diagnostic of that failure path: bg_token_logprobs of fp32 rows side by side,
+ * with K = 1 and every output, whose rows from stalled_row on are never loaded.
+ * The waits for them run out (about one second, all at once), their outputs are
+ * NaN and -1, BG_DEVSTAT_TIMEOUT is raised, and the rows before are computed as
+ * always.  With stalled_row == N nothing waits in vain.
+ *   dev_status   device int32, not NULL
+ * Errors: BG_ERR_INVALID_ARG for N < 1, V < 1, stalled_row outside [0, N], NULL
+ * or misaligned pointers; BG_ERR_UNSUPPORTED for V > BG_MAX_VOCAB.
+ */
+bg_status_t bg_selftest_logprobs_timeout(const float *logits, int32_t N, int32_t V,
+                                         const int32_t *tokens, int32_t stalled_row,
+                                         float *logprob_out, float *entropy_out,
+                                         int32_t *top_token_out, float *top_logprob_out,
+                                         int32_t *dev_status, cudaStream_t stream);
 
 /*
  * Allocation-free variant of bg_packed_prefill_attn.  The paper has no

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from attention_packed_varlen_causal_gb300 import binding as bg
-from tests.test_abi_host_shared import INV, OK, lib, plan, run  # noqa: F401  (lib: a fixture)
+from tests.test_abi_host_shared import F, INV, OK, UNS, lib, plan, run  # noqa: F401  (lib: a fixture)
 
 
 @pytest.mark.parametrize("kw", [dict(S=0), dict(S=0, P=0), dict(S=0, R=0, P=0)], ids=str)
@@ -38,3 +38,12 @@ def test_sizes_past_32_bits_are_refused_not_cut(lib):  # noqa: F811
         with pytest.raises(bg.BgError) as e:
             bg.bg_token_logprobs(torch.empty(shape, dtype=bf, device="meta"), entropy=torch.zeros(1))
         assert e.value.status == bg.BG_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(N=0), INV), (dict(V=0), INV), (dict(row=-1), INV), (dict(row=5), INV), (dict(V=bg.BG_MAX_VOCAB + 1), UNS)] +
+    [(dict([(n, p)]), INV) for n in ("x", "tok", "lp", "ent", "tt", "tl", "st") for p in (None, F + 2)], ids=str)
+def test_logprobs_selftest_refusals(lib, kw, expect):  # noqa: F811
+    a = {**dict(x=F, N=4, V=100, tok=2 * F, row=2, lp=3 * F, ent=4 * F, tt=5 * F, tl=6 * F, st=7 * F), **kw}
+    assert lib.bg_selftest_logprobs_timeout(a["x"], a["N"], a["V"], a["tok"], a["row"], a["lp"], a["ent"], a["tt"],
+                                            a["tl"], a["st"], None) == expect
