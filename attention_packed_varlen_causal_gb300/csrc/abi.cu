@@ -719,7 +719,7 @@ bg_status_t shared_impl(const ShProblem &pb, const void *q, const void *k, const
     p.dev_status = dev_status;
     p.key = shared_key(pb, grid);
     p.cu_seqlens = pb.cu_seqlens;
-    p.hdr = reinterpret_cast<const int32_t *>(ws);
+    p.hdr = reinterpret_cast<int32_t *>(ws);
     p.entries = reinterpret_cast<const ShEntry *>(ws + lay.entries);
     p.sorted = reinterpret_cast<const ShEntry *>(ws + lay.sorted);
     p.starts = reinterpret_cast<const ShStart *>(ws + lay.starts);

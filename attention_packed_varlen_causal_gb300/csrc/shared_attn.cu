@@ -33,7 +33,8 @@
 //      a CTA take turns on the tensor core.
 //   3. shared_join_kernel joins the partial results (only where the sizes allow a cut).
 // Every wait is bounded (sh_wait); on a time-out every role leaves, copies and MMAs in
-// flight are drained, TMEM is freed and BG_DEVSTAT_TIMEOUT is reported.
+// flight are drained, TMEM is freed, BG_DEVSTAT_TIMEOUT is reported and the plan is void, so that
+// the join writes nothing.
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -1472,7 +1473,10 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
         tc_fence_after();
         tmem_dealloc(tmem, C::kTmemCols);
     }
-    if (threadIdx.x == 0 && *abort_flag && p.dev_status) atomicOr(p.dev_status, BG_DEVSTAT_TIMEOUT);
+    if (threadIdx.x == 0 && *abort_flag) {
+        p.hdr[kShHdrStatus] = BG_DEVSTAT_TIMEOUT;      // the join would read parts that were never written
+        if (p.dev_status) atomicOr(p.dev_status, BG_DEVSTAT_TIMEOUT);
+    }
 }
 
 // ------------------------------------------------------------------------------------ join

@@ -50,6 +50,7 @@ struct __align__(16) ShSplit {
 
 // Header words at the start of the workspace; from kShHdrKey on the problem the plan is for, which
 // every run that reads the plan compares with its own.
+// kShHdrStatus: 0, or why no run may use the plan (bits of BG_DEVSTAT: bad offsets, a wait that ran out).
 // kShHdrItems: items that are dealt out whole, or 0 where the CTAs have shares of the line.
 // kShHdrEmpty: 1 if an entry has no keys at all.
 enum {
@@ -102,7 +103,7 @@ struct ShParams {
     int32_t *dev_status;
     ShKey key;
     const int32_t *cu_seqlens;
-    const int32_t *hdr;
+    int32_t *hdr;
     const ShEntry *entries;
     const ShEntry *sorted;    // the same in falling order of tiles, where more items than CTAs are dealt out
     const ShStart *starts;    // [CTAs + 1]

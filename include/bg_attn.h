@@ -454,7 +454,9 @@ bg_status_t bg_beam_select(const float *logits, const float *cum,
  * of the same kind per layer, with the same offsets and sizes and no other use
  * of the workspace between the plan and the last layer than these calls.  A
  * planned call whose sizes are not the plan's writes nothing and raises
- * BG_DEVSTAT_PLAN.
+ * BG_DEVSTAT_PLAN.  A run whose wait ran out (BG_DEVSTAT_TIMEOUT) leaves the rows
+ * that it did not compute as they were and voids the plan: planned calls write
+ * nothing until the next plan.
  *
  * Errors: BG_ERR_INVALID_ARG for NULL or misaligned pointers, negative sizes,
  * num_groups == 0 with samples or prefix rows, tokens without samples (prefill),

@@ -117,3 +117,22 @@ def test_planned_runs_report_queries_without_keys(prefix, groups, max_prefix):
         got = from_dev(out)
         assert (got[none] == 7.0).all() and not (got[~none] == 7.0).all(axis=(1, 2)).any()
     assert [int(s.item()) for s in st] == [bg.BG_DEVSTAT_EMPTY_ROW] * 3
+
+
+@pytest.mark.parametrize("last", [False, True], ids=["prefill", "last"])
+def test_void_plans_write_nothing(last):
+    """A plan that a run has voided (the status word, the workspace's first) leaves every row of later runs,
+    those of cut key ranges among them, until it is made anew."""
+    import torch
+    x = make(46, [3000, 20], [[3, 50], [30, 7]], 14, 2, 64)
+    t, ws = device(x), workspace(x)
+    plan = bg.bg_shared_last_token_plan if last else bg.bg_shared_prefill_plan
+    args = (t["cu"], int(x["cu"][-1]), x["max_seqlen"], t["cup"], int(x["cup"][-1]), x["max_prefix"], t["cug"], 14, 2, 64)
+    outs = [torch.zeros_like(t["ql"] if last else t["q"]) for _ in range(3)]
+    plan(*args, workspace=ws)
+    call(x, t, last, outs[0], ws=ws, planned=True)
+    ws[:4].view(torch.int32).fill_(bg.BG_DEVSTAT_TIMEOUT)
+    call(x, t, last, outs[1], ws=ws, planned=True)
+    plan(*args, workspace=ws)
+    call(x, t, last, outs[2], ws=ws, planned=True)
+    assert outs[0].any() and not outs[1].any() and torch.equal(outs[2], outs[0])
