@@ -16,12 +16,17 @@
 //           largest of them bounds the row's K-th best from below;
 //   gather  only the batches whose maximum reaches the bound are read again (from L2), eight at a
 //           time; the few logits at or above it go to a list in shared memory, where each one's
-//           rank is the number of larger (logit, index) pairs.
-// A row with more such logits than the list holds (thousands of equal ones) is searched K times
-// instead.  Two CTAs of 16 warps per SM keep 64 KB of copies in flight; what is left to the bound is
-// issue slots (about 9 instructions per logit and lane, the K best among them): 8192 rows of 65,536
-// bf16 logits take 198 us for the 20 best, 5.4 TB/s; 480 rows of 50,001
-// fp32 logits with an eighth of them banned 22.0 us, 4.4 TB/s.
+//           rank is the number of larger (logit, index) pairs (of a long list, the K best are
+//           found bit by bit first).
+// The bound is weak where the largest logits lie in few lanes: a label set of neighbouring tokens with
+// all others banned gives few finite lane maxima.  If more logits reach it than the list holds, the
+// list's own K-th largest becomes the bound and the logits above that are gathered; with the bound at
+// -inf it is the logits above it from the start.  Fewer than K above the bound are followed by the
+// first tokens that equal it.
+// Two CTAs of 16 warps per SM keep 64 KB of copies in flight; what is left to the bound is issue slots
+// (about 9 instructions per logit and lane, the K best among them): 8192 rows of 65,536 bf16 logits take
+// 198 us for the 20 best, 5.4 TB/s; 480 rows of 50,001 fp32 logits with an eighth of them banned 22.0 us,
+// 4.4 TB/s.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <stdint.h>
@@ -41,8 +46,8 @@ constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kLpLoads = 4;              // 16-byte loads per lane and batch
 constexpr int kLpStages = 2;             // batches in flight per team (32 KB each over a CTA's teams)
 constexpr int kLpSlots = 16;             // stored batch maxima per lane (of one or more batches each)
-constexpr int kLpCap = 144;              // gathered logits per warp of the team (a row too short to give
-                                         // 32 lane maxima fits)
+constexpr int kLpCap = 144;              // gathered logits per warp of the team
+constexpr int kLpCount = 128;            // lists up to this long are ranked by counting
 constexpr int kLpMaxCluster = 8;
 static_assert(BG_MAX_TOP <= 32, "at least K lane maxima");
 static_assert(kLpSlots == 16, "a lane's stored maxima are two vectors, one mask");
@@ -64,8 +69,10 @@ struct LpShared {
     LpPart all[kLpWarps];                        // per team
     LpPart warp[kLpWarps];                       // (bound: unused)
     uint32_t top[kLpWarps][32];                  // a team's 32 lane maxima, at its first warp
-    unsigned long long best[kLpWarps];
-    int n[kLpWarps];                             // per team
+    unsigned long long few[kLpWarps / 4][32];    // per team: the K best of a long list
+    int n[2][kLpWarps];                          // per team: logits gathered in this round, in the next
+    int total[2];                                // ... by the CTAs of the cluster
+    int joined[2];                               // first CTA: ... that have a place in its list
 };
 
 __device__ __forceinline__ uint32_t order_key(float f)
@@ -77,6 +84,8 @@ __device__ __forceinline__ float order_value(uint32_t k)
 {
     return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
 }
+// The next number above f (of -inf, the lowest finite one).
+__device__ __forceinline__ float above(float f) { return order_value(order_key(f) + 1u); }
 __device__ __forceinline__ unsigned long long pair_key(float x, int v)
 {
     return static_cast<unsigned long long>(order_key(x)) << 32 | static_cast<uint32_t>(~v);
@@ -346,8 +355,8 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LpParams 
         const int n_head = c == 0 ? head : 0, n_tail = c == C - 1 ? p.V - tail : 0;
         const int loose = lane < n_head ? lane : lane >= 16 && lane - 16 < n_tail ? tail + lane - 16 : -1;
         const float loose_x = tw == 0 && loose >= 0 ? Vec::load(x + loose) : -INFINITY;
-        if (tid == 0) sh.n[team] = 0;
-        if (C > 1 && tid == 1) sh.n[1] = 0;
+        if (tid == 0) sh.n[0][team] = 0;
+        if (C > 1 && tid == 0) sh.total[0] = sh.joined[0] = 0;
         // the given token's logit, loaded ahead of its use
         int token = -1;
         float token_x = 0.f;
@@ -502,116 +511,189 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LpParams 
         }
         // ---- the logits at or above the bound
         if (p.K > 0) {
-            auto put = [&](bool in, float f, int v) {      // whole warps call it
-                const unsigned who = __ballot_sync(0xffffffffu, in);
-                if (who == 0) return;
-                int pos = 0;
-                if (lane == 0) pos = atomicAdd(&sh.n[team], __popc(who));
-                pos = __shfl_sync(0xffffffffu, pos, 0) + __popc(who & ((1u << lane) - 1u));
-                if (in && pos < kCap) list[pos] = pair_key(f, v);
-            };
-            if (!bad) {
-// bit t: stored maximum t of this lane reaches the bound
+            // At least K logits of the row reach `least`; gathered are those from `bound` on, which is least or,
+            // to leave out the logits that equal it, the next number.
+            float least = A.bound, bound = least == -INFINITY ? above(least) : least;
+            int n = 0;
+            unsigned long long *cand = C > 1 ? reinterpret_cast<unsigned long long *>(sh.data) : list;
+            // Every round but the last raises the bound over kCap - K logits at least, usually over nearly all.
+            const int rounds = bad ? 0 : p.V / (kCap - 32) + 2;
+#pragma unroll 1
+            for (int round = 0; round < rounds; ++round) {
+                int *count = &sh.n[round & 1][team];
+                auto put = [&](bool in, float f, int v) {      // whole warps call it
+                    const unsigned who = __ballot_sync(0xffffffffu, in);
+                    if (who == 0) return;
+                    int pos = 0;
+                    if (lane == 0) pos = atomicAdd(count, __popc(who));
+                    pos = __shfl_sync(0xffffffffu, pos, 0) + __popc(who & ((1u << lane) - 1u));
+                    if (in && pos < kCap) list[pos] = pair_key(f, v);
+                };
+                const uint4 *vecs = reinterpret_cast<const uint4 *>(x + head);
+                // bit t: stored maximum t of this lane reaches the bound
                 unsigned mask = 0;
 #pragma unroll
                 for (int i = 0; i < kLpSlots / 8; ++i) {
                     float f[8];
                     LpVec<__nv_bfloat16>::unpack(sh.slot[warp][lane][i], f);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) mask |= f[e] >= A.bound ? 1u << (8 * i + e) : 0u;
+                    for (int e = 0; e < 8; ++e) mask |= f[e] >= bound ? 1u << (8 * i + e) : 0u;
                 }
                 mask &= (1u << slot) - 1u;
+                if (sizeof(T) == 4 && round > 0) {
+                    // a bound that many logits equal: their stored maxima were rounded up to it or above
+                    unsigned left = mask;
+#pragma unroll 1
+                    while (__any_sync(0xffffffffu, left != 0)) {
+                        const int t = __ffs(left) - 1;
+                        bool in = false;
+#pragma unroll 1
+                        for (int b = 0; b < per_slot; ++b) {
+                            const int vec = v0 + (t * per_slot + b) * kBatch + tid;
+                            uint4 w[kLpLoads];
+#pragma unroll
+                            for (int i = 0; i < kLpLoads; ++i)
+                                w[i] = t >= 0 && vec + i * kLanes < v1 ? vecs[vec + i * kLanes] : Vec::nothing();
+                            in = in || Vec::largest(w) >= bound;
+                        }
+                        if (t >= 0 && !in) mask &= ~(1u << t);
+                        left &= left - 1;
+                    }
+                }
                 // eight such batches at a time, a lane for each of their vectors
                 for (;;) {
                     const unsigned who = __ballot_sync(0xffffffffu, mask != 0);
                     if (who == 0) break;
+                    // more than the list holds: this round only serves to raise the bound
+                    if (__any_sync(0xffffffffu, *static_cast<volatile int *>(count) > kCap)) break;
                     const int nth = __popc(who & ((1u << lane) - 1u));
                     if (mask != 0 && nth < 8) {
                         sh.pick[warp][nth] = (__ffs(mask) - 1) << 5 | lane;
                         mask &= mask - 1;
                     }
                     __syncwarp();
-                    const int n = min(__popc(who), 8);
-                    const int pick = lane / kLpLoads < n ? sh.pick[warp][lane / kLpLoads] : -1;
+                    const int picks = min(__popc(who), 8);
+                    const int pick = lane / kLpLoads < picks ? sh.pick[warp][lane / kLpLoads] : -1;
                     __syncwarp();
 #pragma unroll 1
                     for (int b = 0; b < per_slot; ++b) {
                         const int vec = v0 + ((pick >> 5) * per_slot + b) * kBatch + tw * 32 + (pick & 31) +
                                         (lane % kLpLoads) * kLanes;
                         const bool there = pick >= 0 && vec < v1;
-                        const uint4 w = there ? reinterpret_cast<const uint4 *>(x + head)[vec] : Vec::nothing();
+                        const uint4 w = there ? vecs[vec] : Vec::nothing();
                         float f[VN];
                         Vec::unpack(w, f);
 #pragma unroll
-                        for (int e = 0; e < VN; ++e) put(there && f[e] >= A.bound, f[e], head + vec * VN + e);
+                        for (int e = 0; e < VN; ++e) put(there && f[e] >= bound, f[e], head + vec * VN + e);
                     }
                 }
-                if (tw == 0) put(loose >= 0 && loose_x >= A.bound, loose_x, loose);
-            }
-            team_sync();
-            if (C > 1) {
-                // the lists of all CTAs into the first one's stages, which are empty by now
-                LpShared *lead = cluster.map_shared_rank(&sh, 0);
-                const int n = sh.n[0];
-                if (warp == 0) {
-                    int pos = 0;
-                    if (lane == 0) pos = atomicAdd(&lead->n[1], n);
-                    pos = __shfl_sync(0xffffffffu, pos, 0);
-                    unsigned long long *joined = reinterpret_cast<unsigned long long *>(lead->data);
-                    for (int i = lane; i < min(n, kCap) && pos + i < kCap; i += 32) joined[pos + i] = list[i];
+                if (tw == 0) put(loose >= 0 && loose_x >= bound, loose_x, loose);
+                team_sync();
+                n = *count;
+                if (C > 1) {
+                    // the lists of all CTAs into the first one's stages, which are empty by now
+                    if (warp == 0) {
+                        LpShared *lead = cluster.map_shared_rank(&sh, 0);
+                        int pos = 0;
+                        if (lane == 0) pos = atomicAdd(&lead->joined[round & 1], n);
+                        if (lane < C) atomicAdd(&cluster.map_shared_rank(&sh, lane)->total[round & 1], n);
+                        pos = __shfl_sync(0xffffffffu, pos, 0);
+                        unsigned long long *joined = reinterpret_cast<unsigned long long *>(lead->data);
+                        for (int i = lane; i < min(n, kCap) && pos + i < kCap; i += 32) joined[pos + i] = list[i];
+                    }
+                    cluster.sync();
+                    n = sh.total[round & 1];
                 }
-                cluster.sync();
-                list = reinterpret_cast<unsigned long long *>(sh.data);
+                if (n <= kCap) break;
+                // The list is full.  Its K-th largest is a bound too; what exceeds that goes into the next round.
+                if (tid == 0) {
+                    sh.n[(round + 1) & 1][team] = 0;
+                    if (C > 1) sh.total[(round + 1) & 1] = sh.joined[(round + 1) & 1] = 0;
+                }
+                if (c == 0 && tw == 0) {
+                    auto reach = [&](uint32_t key) {
+                        int some = 0;
+#pragma unroll 4
+                        for (int i = lane; i < kCap; i += 32) some += static_cast<uint32_t>(cand[i] >> 32) >= key ? 1 : 0;
+                        return __reduce_add_sync(0xffffffffu, some) >= p.K;
+                    };
+                    uint32_t kth = order_key(bound);       // the largest key that K of the list reach, bit by bit
+                    if (reach(kth + 1)) {                  // (no: a bound that most of the list equal)
+                        kth = 0;
+#pragma unroll 1
+                        for (uint32_t bit = 0x80000000u; bit != 0; bit >>= 1)
+                            if (reach(kth | bit)) kth |= bit;
+                    }
+                    if (lane < C) (C == 1 ? &sh : cluster.map_shared_rank(&sh, lane))->all[team].bound = order_value(kth);
+                }
+                if (C > 1) cluster.sync();
+                else team_sync();
+                least = sh.all[team].bound;
+                bound = above(least);
             }
-            const int n = sh.n[C > 1 ? 1 : team];
-            if (c == 0 && (tw == 0 || n > kCap)) {
+            if (c == 0 && tw == 0) {
                 int32_t *tt = p.top_token + row * p.K;
                 float *tl = p.top_logprob + row * p.K;
-                auto store = [&](int i, unsigned long long k) {
-                    tt[i] = static_cast<int32_t>(~static_cast<uint32_t>(k));
-                    tl[i] = logprob(order_value(static_cast<uint32_t>(k >> 32)));
-                };
                 if (bad) {
                     if (lane < p.K) {
                         tt[lane] = -1;
                         tl[lane] = NAN;
                     }
-                } else if (n <= kCap) {
+                } else {
+                    n = min(n, kCap);
+                    int some = n;
+                    if (n > kLpCount) {
+                        // the largest pair that K of the list reach, bit by bit: those K are all there is to rank
+                        unsigned long long kth = 0;
 #pragma unroll 1
-                    for (int i = lane; i < n; i += 32) {
-                        const unsigned long long k = list[i];
+                        for (unsigned long long bit = 1ull << 63; bit != 0; bit >>= 1) {
+                            int reach = 0;
+#pragma unroll 4
+                            for (int i = lane; i < n; i += 32) reach += cand[i] >= (kth | bit) ? 1 : 0;
+                            if (__reduce_add_sync(0xffffffffu, reach) >= p.K) kth |= bit;
+                        }
+                        some = 0;
+#pragma unroll 1
+                        for (int i0 = 0; i0 < n; i0 += 32) {
+                            const unsigned long long k = i0 + lane < n ? cand[i0 + lane] : 0;
+                            const unsigned who = __ballot_sync(0xffffffffu, k >= kth);
+                            if (k >= kth) sh.few[team][some + __popc(who & ((1u << lane) - 1u))] = k;
+                            some += __popc(who);
+                        }
+                        __syncwarp();
+                        cand = sh.few[team];
+                    }
+#pragma unroll 1
+                    for (int i = lane; i < some; i += 32) {
+                        const unsigned long long k = cand[i];
                         int rank = 0;
 #pragma unroll 4
-                        for (int j = 0; j < n; ++j) rank += list[j] > k ? 1 : 0;
-                        if (rank < p.K) store(rank, k);
+                        for (int j = 0; j < some; ++j) rank += cand[j] > k ? 1 : 0;
+                        if (rank < p.K) {
+                            tt[rank] = static_cast<int32_t>(~static_cast<uint32_t>(k));
+                            tl[rank] = logprob(order_value(static_cast<uint32_t>(k >> 32)));
+                        }
                     }
-                } else {
-                    // the largest pair below the last one found, K times
-                    unsigned long long found = ~0ull;
+                    // fewer than K are above the bound (banned tokens behind the allowed ones, thousands of equal
+                    // logits): the first tokens that equal it
 #pragma unroll 1
-                    for (int i = 0; i < p.K; ++i) {
-                        unsigned long long k = 0;
-#pragma unroll 1
-                        for (int v = tid; v < p.V; v += kLanes) {
-                            const unsigned long long u = pair_key(Vec::load(x + v), v);
-                            if (u < found && u > k) k = u;
+                    for (int first = 0; n < p.K && first < p.V; first += 32 * 8) {
+                        bool eq[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int v = first + 32 * i + lane;
+                            eq[i] = v < p.V && Vec::load(x + min(v, p.V - 1)) == least;
                         }
 #pragma unroll
-                        for (int o = 16; o > 0; o >>= 1) {
-                            const unsigned long long u = __shfl_xor_sync(0xffffffffu, k, o);
-                            k = u > k ? u : k;
+                        for (int i = 0; i < 8; ++i) {
+                            const unsigned who = __ballot_sync(0xffffffffu, eq[i]);
+                            const int rank = n + __popc(who & ((1u << lane) - 1u));
+                            if (eq[i] && rank < p.K) {
+                                tt[rank] = first + 32 * i + lane;
+                                tl[rank] = logprob(least);
+                            }
+                            n += __popc(who);
                         }
-                        if (lane == 0) sh.best[warp] = k;
-                        team_sync();
-                        k = sh.best[team * W + (lane & (W - 1))];
-#pragma unroll
-                        for (int o = W / 2; o > 0; o >>= 1) {
-                            const unsigned long long u = __shfl_xor_sync(0xffffffffu, k, o);
-                            k = u > k ? u : k;
-                        }
-                        team_sync();
-                        found = k;
-                        if (tid == 0) store(i, found);
                     }
                 }
             }

@@ -535,8 +535,9 @@ bg_status_t bg_shared_last_token_attn_planned(const void *q, const void *k, cons
  * gets log-probabilities -inf, entropy 0 and the tokens 0 .. K-1.  A wait that
  * runs out raises BG_DEVSTAT_TIMEOUT, and the rows that it kept from being
  * computed get NaN and -1.
- * One launch, no workspace; the logits come from memory once (a row with
- * thousands of logits equal to its K-th best is read K times more).
+ * One launch, no workspace; the logits come from memory once (parts of a row are
+ * read again to find its K best: a few where those are ordinary ones, up to
+ * all of it a few times where thousands of logits are equal or lie in few places).
  * Errors: BG_ERR_INVALID_ARG for N < 0, an unknown dtype, row_stride < V, NULL
  * or misaligned pointers, one of the top outputs or of tokens / logprob_out
  * without the other, no output at all, or an output overlapping another
