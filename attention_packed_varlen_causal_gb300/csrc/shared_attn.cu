@@ -624,7 +624,8 @@ __device__ __forceinline__ void capped4_any(float *s, float cap_in, float cap_lo
 // kShCapFixed (in base 2), where 2^x of any score and any sum of them is an ordinary fp32 number, so
 // that no maximum is needed and the tile goes from S to P 32 columns at a time (a cap of 30, 112 samples of
 // 1-300 tokens over 1-500 keys: 114 us, with the running maximum 169).  2^80 of a weight and 2^17 keys leave
-// |v| < 2^30 within fp32.
+// |v| < 2^30 within fp32; 2^-80 of one, where all scores of a row are near the negative cap, leaves
+// |v| >= 2^-46 among its normal numbers.
 enum : int { kShPlain = 0, kShCapped = 1, kShCappedFixed = 2 };
 constexpr float kShCapFixed = 80.f;
 

@@ -436,7 +436,10 @@ bg_status_t bg_beam_select(const float *logits, const float *cum,
  *   cu_group     int32 [num_groups+1], device; as cu_seqlens, for num_seqs
  *   scale        finite, > 0;  softcap finite, >= 0 (0: scores are not capped)
  *                (with 0 < softcap <= 55 weights are not scaled by their
- *                maximum: finite results for |v| < 2^30)
+ *                maximum, but lie between 2^-80 and 2^80: results are finite for
+ *                |v| < 2^30, and keep their precision for |v| >= 2^-46, below
+ *                which parts of a row whose scores are all near -softcap can
+ *                fall out of fp32)
  *   out          bf16, the shape of q
  *   lse          fp32 [rows of q, Hq] natural-log sum-exp of x, or NULL
  *   workspace    device buffer of at least bg_shared_attn_workspace_size(...)

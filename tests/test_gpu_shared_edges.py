@@ -1,5 +1,5 @@
 """Edges of the shared-prefix attention calls on the GPU: scores of -inf in part of a key range, weights that
-one key dominates, and queries without keys in planned runs."""
+one key dominates or at the ends of their range, queries without keys in planned runs, and void plans."""
 import math
 
 import numpy as np
@@ -136,3 +136,21 @@ def test_void_plans_write_nothing(last):
     plan(*args, workspace=ws)
     call(x, t, last, outs[2], ws=ws, planned=True)
     assert outs[0].any() and not outs[1].any() and torch.equal(outs[2], outs[0])
+
+
+@pytest.mark.parametrize("last", [False, True], ids=["prefill", "last"])
+@pytest.mark.parametrize("sign,v_lo", [(1, 2.0 ** 29), (-1, 2.0 ** -46)], ids=["at_cap", "at_minus_cap"])
+def test_ends_of_the_range_of_v_under_a_fixed_reference(sign, v_lo, last):
+    """Cap 55, every score at one end: weights of 2^79.3 with |v| next to 2^30, of 2^-79.3 with |v| from 2^-46."""
+    x = make(47, [300], [[5, 40]], 4, 2, 64)
+    rng = np.random.default_rng(47)
+    s = np.sign(rng.standard_normal(64)).astype(np.float32)
+    for n in ("q", "ql"):
+        x[n][:] = wl.bf16_bits_from_f32(np.tile(16 * s, (1, 1, 1)))
+    for n in ("k", "pk"):
+        x[n][:] = wl.bf16_bits_from_f32(np.tile(sign * 16 * s, (1, 1, 1)))
+    for n in ("v", "pv"):
+        v = v_lo * rng.uniform(1, 1.99, x[n].shape) * np.sign(rng.standard_normal(x[n].shape))
+        x[n] = wl.bf16_bits_from_f32(v.astype(np.float32))
+    out, lse, _ = run(x, last, 55.0)
+    assert_close(out, lse, reference(x, last, 55.0), "ends of the range", 55.0)
