@@ -420,7 +420,8 @@ def bg_shared_prefill_attn(q, k, v, cu_seqlens, max_seqlen: int, prefix_k, prefi
     q [T,Hq,d], k/v [T,Hkv,d] bf16, packed by cu_seqlens int32 [S+1]; prefix_k/prefix_v [P,Hkv,d] (or
     None) packed by cu_prefix int32 [R+1]; samples cu_group[r] .. cu_group[r+1]-1 belong to request r
     (int32 [R+1]); out [T,Hq,d] (written); lse fp32 [T,Hq] or None; scores capped by softcap * tanh(x /
-    softcap) if softcap > 0; workspace a uint8 CUDA tensor of bg_shared_attn_workspace_size bytes."""
+    softcap) if softcap > 0 (then the prefixes' own rows too come from this call, each prefix as the one
+    sample of a request without one: bg_packed_prefill_attn does not cap); workspace a uint8 CUDA tensor of bg_shared_attn_workspace_size bytes."""
     return _shared_run("bg_shared_prefill_attn", False, q, k, v, cu_seqlens, max_seqlen, prefix_k, prefix_v, cu_prefix,
                        max_prefix_len, cu_group, out, lse, scale, softcap, workspace, dev_status, stream)
 

@@ -421,7 +421,10 @@ bg_status_t bg_beam_select(const float *logits, const float *cum,
  * A request without a prefix (length 0), a sample without rows and a request
  * without samples are allowed; a query without any key is not written and
  * raises BG_DEVSTAT_EMPTY_ROW.  The K/V of the prefix is what
- * bg_packed_prefill_attn over the prefixes reads.
+ * bg_packed_prefill_attn over the prefixes reads.  That call does not cap scores:
+ * in a model with capped scores the prefixes' own rows go through
+ * bg_shared_prefill_attn with the same softcap, each prefix as the one sample
+ * of a request without a prefix (total_prefix == 0, cu_group 0 .. R).
  *
  *   q            bf16 [total_tokens, Hq, head_dim] (prefill) or
  *                [num_seqs, Hq, head_dim] (last token)

@@ -1,5 +1,6 @@
 """Edges of the shared-prefix attention calls on the GPU: scores of -inf in part of a key range, weights that
-one key dominates or at the ends of their range, queries without keys in planned runs, and void plans."""
+one key dominates or at the ends of their range, queries without keys in planned runs, void plans, and a
+model with capped scores."""
 import math
 
 import numpy as np
@@ -8,8 +9,9 @@ import pytest
 from attention_packed_varlen_causal_gb300 import binding as bg
 from attention_packed_varlen_causal_gb300 import build
 from attention_packed_varlen_causal_gb300 import workloads as wl
-from tests.helpers import from_dev
-from tests.test_gpu_shared import assert_close, call, device, make, reference, workspace
+from oracle import shared as sh
+from tests.helpers import from_dev, i32_dev, to_dev
+from tests.test_gpu_shared import assert_close, call, device, f64, make, reference, workspace
 
 pytestmark = pytest.mark.gpu
 
@@ -154,3 +156,36 @@ def test_ends_of_the_range_of_v_under_a_fixed_reference(sign, v_lo, last):
         x[n] = wl.bf16_bits_from_f32(v.astype(np.float32))
     out, lse, _ = run(x, last, 55.0)
     assert_close(out, lse, reference(x, last, 55.0), "ends of the range", 55.0)
+
+
+@pytest.mark.parametrize("heads", HEADS, ids=lambda h: "h%d_%d_d%d" % h)
+def test_capped_model_from_prefix_to_samples(heads):
+    """A model with capped scores: the prefixes' rows as samples of requests without a prefix, then the samples
+    over the same K and V, against whole sequences [prefix ; sample] of capped scores."""
+    import torch
+    prefix, groups, cap = [150, 1, 33], [[20, 1, 64], [7, 130], [3, 3]], 30.0
+    Hq, Hkv, d = heads
+    x = make(48, prefix, groups, *heads, q_scale=8.0)
+    t = device(x)
+    pq = wl.bf16_bits_from_f32(8 * np.random.default_rng(49).standard_normal((184, Hq, d), dtype=np.float32))
+    pout, out = (torch.zeros((n, Hq, d), dtype=torch.bfloat16, device="cuda") for n in (184, int(x["cu"][-1])))
+    none, each = i32_dev(np.zeros(4, np.int32)), i32_dev(np.arange(4, dtype=np.int32))
+    ws = torch.empty(bg.bg_shared_attn_workspace_size(3, 3, 184, 150, 0, *heads), dtype=torch.uint8, device="cuda")
+    bg.bg_shared_prefill_attn(to_dev(pq), t["pk"], t["pv"], t["cup"], 150, None, None, none, 0, each, pout,
+                              scale=x["scale"], softcap=cap, workspace=ws)
+    call(x, t, False, out, softcap=cap)
+    # whole sequences: every prefix in front of each of its samples
+    seqs, at = [], 0
+    for r, group in enumerate(groups):
+        for n in group:
+            seqs.append((slice(x["cup"][r], x["cup"][r + 1]), slice(at, at + n)))
+            at += n
+    whole = {n: np.concatenate([np.concatenate((f64(a)[p], f64(b)[s])) for p, s in seqs])
+             for n, a, b in (("q", pq, x["q"]), ("k", x["pk"], x["k"]), ("v", x["pv"], x["v"]))}
+    lens = [p.stop - p.start + s.stop - s.start for p, s in seqs]
+    cu = np.concatenate(([0], np.cumsum(lens)))
+    empty = whole["k"][:0]
+    ref = sh.attn(whole["q"], whole["k"], whole["v"], cu, empty, empty, np.zeros(2, int), np.array([0, len(seqs)]),
+                  x["scale"], softcap=cap)
+    both = np.concatenate([np.concatenate((from_dev(pout)[p], from_dev(out)[s])) for p, s in seqs])
+    assert_close(both, None, ref, "capped model", cap)
