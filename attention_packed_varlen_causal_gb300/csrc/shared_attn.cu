@@ -1339,76 +1339,76 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
                         }
                         add_sums(weight_of(mx, negm), (rs[0].x + rs[1].x) + (rs[0].y + rs[1].y));
                     } else {
-                    float s[kShKeys];
-                    tmem_ld64(tS, s);
-                    tmem_ld64(tS + 64, s + 64);
-                    if constexpr (MODE == kShCapped) {
+                        float s[kShKeys];
+                        tmem_ld64(tS, s);
+                        tmem_ld64(tS + 64, s + 64);
+                        if constexpr (MODE == kShCapped) {
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            // a masked score may be NaN, and is not to reach its neighbours
-                            const uint32_t keep = masked ? columns(c) : ~0u;
+                            for (int c = 0; c < 4; ++c) {
+                                // a masked score may be NaN, and is not to reach its neighbours
+                                const uint32_t keep = masked ? columns(c) : ~0u;
 #pragma unroll
-                            for (int i = 32 * c; i < 32 * c + 32; ++i)
-                                if (!((keep >> (i & 31)) & 1u)) s[i] = 0.f;
+                                for (int i = 32 * c; i < 32 * c + 32; ++i)
+                                    if (!((keep >> (i & 31)) & 1u)) s[i] = 0.f;
 #pragma unroll
-                            for (int i = 32 * c; i < 32 * c + 32; i += 4) capped4_any(s + i, p.cap_in, p.cap_log2);
+                                for (int i = 32 * c; i < 32 * c + 32; i += 4) capped4_any(s + i, p.cap_in, p.cap_log2);
+                            }
                         }
-                    }
-                    if (masked) {
+                        if (masked) {
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const uint32_t keep = columns(c);
+                            for (int c = 0; c < 4; ++c) {
+                                const uint32_t keep = columns(c);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (!((keep >> i) & 1u)) s[32 * c + i] = -INFINITY;
+                                for (int i = 0; i < 32; ++i)
+                                    if (!((keep >> i) & 1u)) s[32 * c + i] = -INFINITY;
+                            }
                         }
-                    }
-                    float mq[8];
+                        float mq[8];
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) mq[q] = fmaxf(s[16 * q], s[16 * q + 1]);
+                        for (int q = 0; q < 8; ++q) mq[q] = fmaxf(s[16 * q], s[16 * q + 1]);
 #pragma unroll
-                    for (int c = 2; c < 16; c += 2)
+                        for (int c = 2; c < 16; c += 2)
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) mq[q] = fmax3f(mq[q], s[16 * q + c], s[16 * q + c + 1]);
-                    const float mx =
-                        fmax3f(fmax3f(mq[0], mq[1], mq[2]), fmax3f(mq[3], mq[4], mq[5]), fmaxf(mq[6], mq[7]));
-                    const float m_new = fmaxf(m, mx * sl2);
-                    if (done == 0) m = m_new;
-                    const float2 sl2x2 = make_float2(sl2, sl2);
-                    float2 negm, rs[4];
-                    uint32_t pk[32];
-                    auto weights = [&](int c, uint32_t *w) {       // of columns 32 c .. 32 c + 31, as bf16 pairs
+                            for (int q = 0; q < 8; ++q) mq[q] = fmax3f(mq[q], s[16 * q + c], s[16 * q + c + 1]);
+                        const float mx =
+                            fmax3f(fmax3f(mq[0], mq[1], mq[2]), fmax3f(mq[3], mq[4], mq[5]), fmaxf(mq[6], mq[7]));
+                        const float m_new = fmaxf(m, mx * sl2);
+                        if (done == 0) m = m_new;
+                        const float2 sl2x2 = make_float2(sl2, sl2);
+                        float2 negm, rs[4];
+                        uint32_t pk[32];
+                        auto weights = [&](int c, uint32_t *w) {       // of columns 32 c .. 32 c + 31, as bf16 pairs
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float2 x = ffma2(make_float2(s[32 * c + 2 * i], s[32 * c + 2 * i + 1]), sl2x2, negm);
-                            const float2 e = make_float2(ex2(x.x), ex2(x.y));
-                            rs[i & 3] = fadd2(rs[i & 3], e);
-                            w[i] = pack_bf16x2(e.x, e.y);
-                        }
-                    };
-                    // The first half's weights use the maximum so far, so that they need not wait for
-                    // this tile's; only when that grows by more than 2^8 is O rescaled and the half redone.
+                            for (int i = 0; i < 16; ++i) {
+                                const float2 x = ffma2(make_float2(s[32 * c + 2 * i], s[32 * c + 2 * i + 1]), sl2x2, negm);
+                                const float2 e = make_float2(ex2(x.x), ex2(x.y));
+                                rs[i & 3] = fadd2(rs[i & 3], e);
+                                w[i] = pack_bf16x2(e.x, e.y);
+                            }
+                        };
+                        // The first half's weights use the maximum so far, so that they need not wait for
+                        // this tile's; only when that grows by more than 2^8 is O rescaled and the half redone.
 #pragma unroll 1
-                    for (;;) {
-                        const float mu = m == -INFINITY ? 0.f : m;  // no key yet: p = 0, not NaN
-                        negm = make_float2(-mu, -mu);
+                        for (;;) {
+                            const float mu = m == -INFINITY ? 0.f : m;  // no key yet: p = 0, not NaN
+                            negm = make_float2(-mu, -mu);
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) rs[q] = make_float2(0.f, 0.f);
-                        weights(0, pk);
-                        weights(1, pk + 16);
-                        if (!__any_sync(0xffffffffu, m_new > m + 8.f)) break;
-                        rescale(m_new);
-                    }
-                    tmem_st16(tS, pk);
-                    tmem_st16(tS + 16, pk + 16);
-                    hand_over(0);
-                    weights(2, pk);
-                    tmem_st16(tS + 32, pk);
-                    weights(3, pk + 16);
-                    tmem_st16(tS + 48, pk + 16);
-                    hand_over(1);
-                    const float2 r01 = fadd2(rs[0], rs[1]), r23 = fadd2(rs[2], rs[3]);
-                    add_sums(weight_of(mx, negm), (r01.x + r23.x) + (r01.y + r23.y));
+                            for (int q = 0; q < 4; ++q) rs[q] = make_float2(0.f, 0.f);
+                            weights(0, pk);
+                            weights(1, pk + 16);
+                            if (!__any_sync(0xffffffffu, m_new > m + 8.f)) break;
+                            rescale(m_new);
+                        }
+                        tmem_st16(tS, pk);
+                        tmem_st16(tS + 16, pk + 16);
+                        hand_over(0);
+                        weights(2, pk);
+                        tmem_st16(tS + 32, pk);
+                        weights(3, pk + 16);
+                        tmem_st16(tS + 48, pk + 16);
+                        hand_over(1);
+                        const float2 r01 = fadd2(rs[0], rs[1]), r23 = fadd2(rs[2], rs[3]);
+                        add_sums(weight_of(mx, negm), (r01.x + r23.x) + (r01.y + r23.y));
                     }
                 }
                 ++done;
