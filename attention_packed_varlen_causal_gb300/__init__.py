@@ -19,6 +19,13 @@ sm_103a CUDA kernels:
                                       of the suffix and the decode attention
   * ``bg_beam_select``                beam candidate selection of one step
     (+ ``bg_beam_select_workspace_size``)
+  * ``bg_shared_prefill_attn``        attention of a request's samples over the
+                                      request's one prefix, a query per token
+  * ``bg_shared_last_token_attn``     the same with one query per sample
+    (+ ``bg_shared_attn_workspace_size``; ``bg_shared_prefill_plan``,
+    ``bg_shared_last_token_plan`` and the ``_planned`` calls split them)
+  * ``bg_token_logprobs``             log-probability of a given token, entropy
+                                      and the best tokens of rows of logits
   * ``bg_selftest_wait_timeout``, ``bg_selftest_logprobs_timeout``  diagnostics of the
                                       bounded-wait failure path
   * ``bg_status_string``
