@@ -348,6 +348,13 @@ def _fits(*sizes) -> bool:
     return True
 
 
+def _raw_stream(index: int) -> int:
+    """The current stream of device ``index``: torch's own shortcut, which makes no object, where there is one."""
+    import torch
+    short = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return short(index) if short is not None else torch.cuda.current_stream(index).cuda_stream
+
+
 def _launch(fn: str, index: int, stream, *args):
     """Calls the library's ``fn`` with device ``index`` current, on ``stream`` or that device's current one."""
     import torch
@@ -356,7 +363,7 @@ def _launch(fn: str, index: int, stream, *args):
     if index != torch.cuda.current_device():
         with torch.cuda.device(index):
             return _launch(fn, index, stream, *args)
-    st = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    st = _raw_stream(index) if stream is None else stream.cuda_stream
     _check(fn, getattr(load(), fn)(*args, st))
 
 

@@ -1,5 +1,7 @@
 """Host-side refusals of sizes that contradict each other or do not fit the C ABI's integers, in the
 shared-prefix attention and log-probability calls (no GPU)."""
+import types
+
 import pytest
 import torch
 
@@ -47,3 +49,11 @@ def test_logprobs_selftest_refusals(lib, kw, expect):  # noqa: F811
     a = {**dict(x=F, N=4, V=100, tok=2 * F, row=2, lp=3 * F, ent=4 * F, tt=5 * F, tl=6 * F, st=7 * F), **kw}
     assert lib.bg_selftest_logprobs_timeout(a["x"], a["N"], a["V"], a["tok"], a["row"], a["lp"], a["ent"], a["tt"],
                                             a["tl"], a["st"], None) == expect
+
+
+def test_current_stream_without_torchs_shortcut(monkeypatch):
+    """The current stream is found by the public call where torch has no private one."""
+    seen = []
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda i: seen.append(i) or types.SimpleNamespace(cuda_stream=77))
+    assert bg._raw_stream(3) == 77 and seen == [3]
