@@ -624,7 +624,8 @@ bg_status_t shared_check_plan(const ShProblem &pb, const void *workspace, size_t
     if (!workspace || !aligned(workspace, 256) || workspace_bytes < shared_layout(pb).total) return BG_ERR_INVALID_ARG;
     if (overlap(pb.cu_seqlens, (static_cast<size_t>(pb.num_seqs) + 1) * 4, workspace, workspace_bytes) ||
         overlap(pb.cu_prefix, (static_cast<size_t>(pb.num_groups) + 1) * 4, workspace, workspace_bytes) ||
-        overlap(pb.cu_group, (static_cast<size_t>(pb.num_groups) + 1) * 4, workspace, workspace_bytes))
+        overlap(pb.cu_group, (static_cast<size_t>(pb.num_groups) + 1) * 4, workspace, workspace_bytes) ||
+        overlap(dev_status, 4, workspace, workspace_bytes))
         return BG_ERR_INVALID_ARG;
     return BG_OK;
 }
@@ -665,10 +666,11 @@ bg_status_t shared_impl(const ShProblem &pb, const void *q, const void *k, const
     const size_t kvbytes = static_cast<size_t>(pb.total_tokens) * pb.Hkv * pb.head_dim * 2;
     const size_t pbytes = static_cast<size_t>(pb.total_prefix) * pb.Hkv * pb.head_dim * 2;
     const size_t lsebytes = lse ? rows * pb.Hq * 4 : 0;
-    const void *in[8] = {q, k, v, prefix_k, prefix_v, pb.cu_seqlens, pb.cu_prefix, pb.cu_group};
-    const size_t inb[8] = {qbytes, kvbytes, kvbytes, pbytes, pbytes, (static_cast<size_t>(pb.num_seqs) + 1) * 4,
-                           (static_cast<size_t>(pb.num_groups) + 1) * 4, (static_cast<size_t>(pb.num_groups) + 1) * 4};
-    for (int i = 0; i < 8; ++i)
+    const void *in[9] = {q, k, v, prefix_k, prefix_v, pb.cu_seqlens, pb.cu_prefix, pb.cu_group, dev_status};
+    const size_t groups = (static_cast<size_t>(pb.num_groups) + 1) * 4;
+    const size_t inb[9] = {qbytes, kvbytes, kvbytes, pbytes, pbytes, (static_cast<size_t>(pb.num_seqs) + 1) * 4,
+                           groups, groups, 4};
+    for (int i = 0; i < 9; ++i)
         if (overlap(out, qbytes, in[i], inb[i]) || overlap(lse, lsebytes, in[i], inb[i]) ||
             overlap(workspace, workspace_bytes, in[i], inb[i]))
             return BG_ERR_INVALID_ARG;
@@ -817,7 +819,8 @@ bg_status_t bg_token_logprobs(const void *logits, int32_t dtype, int64_t row_str
     const void *outs[4] = {logprob_out, entropy_out, top_token_out, top_logprob_out};
     const size_t outb[4] = {n * 4, n * 4, n * K * 4, n * K * 4};
     for (int o = 0; o < 4; ++o) {
-        if (overlap(outs[o], outb[o], logits, lbytes) || overlap(outs[o], outb[o], tokens, n * 4))
+        if (overlap(outs[o], outb[o], logits, lbytes) || overlap(outs[o], outb[o], tokens, n * 4) ||
+            overlap(outs[o], outb[o], dev_status, 4))
             return BG_ERR_INVALID_ARG;
         for (int o2 = o + 1; o2 < 4; ++o2)
             if (overlap(outs[o], outb[o], outs[o2], outb[o2])) return BG_ERR_INVALID_ARG;

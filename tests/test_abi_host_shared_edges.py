@@ -57,3 +57,15 @@ def test_current_stream_without_torchs_shortcut(monkeypatch):
     monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda i: seen.append(i) or types.SimpleNamespace(cuda_stream=77))
     assert bg._raw_stream(3) == 77 and seen == [3]
+
+
+def test_status_word_in_another_argument(lib):  # noqa: F811
+    """dev_status is an argument too: outputs and the workspace do not overlap it."""
+    for name in ("bg_shared_prefill_attn", "bg_shared_last_token_attn_planned"):
+        for kw in (dict(st=9 * F + 4), dict(st=10 * F + 512), dict(lse=11 * F, st=11 * F + 8)):
+            assert run(lib, name, **kw) == INV
+    assert plan(lib, "bg_shared_prefill_plan", st=10 * F + 512) == INV
+    lp = dict(x=F, N=4, V=100, tok=2 * F, K=3, lp=3 * F, ent=4 * F, tt=5 * F, tl=6 * F)
+    for st in (3 * F + 4, 4 * F + 12, 5 * F + 44, 6 * F):
+        assert lib.bg_token_logprobs(lp["x"], 0, 100, lp["N"], lp["V"], lp["tok"], lp["K"], lp["lp"], lp["ent"], lp["tt"],
+                                     lp["tl"], st, None) == INV
