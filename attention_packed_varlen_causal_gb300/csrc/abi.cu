@@ -647,7 +647,8 @@ bg_status_t shared_impl(const ShProblem &pb, const void *q, const void *k, const
                         const void *prefix_v, float scale, float softcap, void *out, float *lse, void *workspace,
                         size_t workspace_bytes, int32_t *dev_status, cudaStream_t stream, bool with_plan)
 {
-    if (!std::isfinite(scale) || !(scale > 0.f) || !std::isfinite(softcap) || softcap < 0.f) return BG_ERR_INVALID_ARG;
+    if (!std::isfinite(scale * 1.4426950408889634f) || !(scale > 0.f) || !std::isfinite(softcap) || softcap < 0.f)
+        return BG_ERR_INVALID_ARG;
     // scale / cap and cap * log2(e) have to be ordinary numbers
     const bool capped = softcap > 0.f;
     if (capped && (!std::isnormal(3.f * (scale / softcap)) || !std::isnormal(softcap * 1.4426950408889634f)))

@@ -466,8 +466,8 @@ bg_status_t bg_beam_select(const float *logits, const float *cum,
  *
  * Errors: BG_ERR_INVALID_ARG for NULL or misaligned pointers, negative sizes,
  * num_groups == 0 with samples or prefix rows, tokens without samples (prefill),
- * Hq % Hkv != 0, a bad scale or softcap (or one whose quotient or product with
- * log2(e) is not a normal number), a too-small workspace, or an output or the
+ * Hq % Hkv != 0, a bad scale or softcap (a scale whose product with log2(e) is
+ * not finite; a softcap whose own, or whose quotient with it, is not a normal number), a too-small workspace, or an output or the
  * workspace overlapping another argument; BG_ERR_UNSUPPORTED for head_dim not in {64, 128},
  * Hq/Hkv > 128, or max_seqlen or max_prefix_len > BG_MAX_SEQLEN.  No queries
  * (total_tokens == 0, or num_seqs == 0 for the last-token call) is a valid

@@ -69,3 +69,9 @@ def test_status_word_in_another_argument(lib):  # noqa: F811
     for st in (3 * F + 4, 4 * F + 12, 5 * F + 44, 6 * F):
         assert lib.bg_token_logprobs(lp["x"], 0, 100, lp["N"], lp["V"], lp["tok"], lp["K"], lp["lp"], lp["ent"], lp["tt"],
                                      lp["tl"], st, None) == INV
+
+
+def test_scale_past_the_range_of_base_two(lib):  # noqa: F811
+    """The kernels take scores in base 2: 3e38 log2(e) is infinite."""
+    for name in ("bg_shared_prefill_attn", "bg_shared_last_token_attn_planned"):
+        assert run(lib, name, scale=3e38) == INV
