@@ -25,8 +25,8 @@
 // first tokens that equal it.
 // Two CTAs of 16 warps per SM keep 64 KB of copies in flight; what is left to the bound is issue slots
 // (about 9 instructions per logit and lane, the K best among them): 8192 rows of 65,536 bf16 logits take
-// 198 us for the 20 best, 5.4 TB/s; 480 rows of 50,001 fp32 logits with an eighth of them banned 22.0 us,
-// 4.4 TB/s.
+// 196 us for the 20 best, 5.5 TB/s; 480 rows of 50,001 fp32 logits with an eighth of them banned 21.8 us,
+// 4.4 TB/s, and 25.6 with all but 16 neighbours banned.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <stdint.h>
@@ -70,7 +70,7 @@ struct LpShared {
     LpPart warp[kLpWarps];                       // (bound: unused)
     uint32_t top[kLpWarps][32];                  // a team's 32 lane maxima, at its first warp
     unsigned long long few[kLpWarps / 4][32];    // per team: the K best of a long list
-    int n[2][kLpWarps];                          // per team: logits gathered in this round, in the next
+    int n[2][kLpWarps];                          // per team: logits gathered in this sweep, in the next
     int total[2];                                // ... by the CTAs of the cluster
     int joined[2];                               // first CTA: ... that have a place in its list
 };
@@ -516,11 +516,11 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LpParams 
             float least = A.bound, bound = least == -INFINITY ? above(least) : least;
             int n = 0;
             unsigned long long *cand = C > 1 ? reinterpret_cast<unsigned long long *>(sh.data) : list;
-            // Every round but the last raises the bound over kCap - K logits at least, usually over nearly all.
-            const int rounds = bad ? 0 : p.V / (kCap - 32) + 2;
+            // Every sweep but the last raises the bound over kCap - K logits at least, usually over nearly all.
+            const int sweeps = bad ? 0 : p.V / (kCap - 32) + 2;
 #pragma unroll 1
-            for (int round = 0; round < rounds; ++round) {
-                int *count = &sh.n[round & 1][team];
+            for (int sweep = 0; sweep < sweeps; ++sweep) {
+                int *count = &sh.n[sweep & 1][team];
                 auto put = [&](bool in, float f, int v) {      // whole warps call it
                     const unsigned who = __ballot_sync(0xffffffffu, in);
                     if (who == 0) return;
@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LpParams 
                     for (int e = 0; e < 8; ++e) mask |= f[e] >= bound ? 1u << (8 * i + e) : 0u;
                 }
                 mask &= (1u << slot) - 1u;
-                if (sizeof(T) == 4 && round > 0) {
+                if (sizeof(T) == 4 && sweep > 0) {
                     // a bound that many logits equal: their stored maxima were rounded up to it or above
                     unsigned left = mask;
 #pragma unroll 1
@@ -564,7 +564,7 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LpParams 
                 for (;;) {
                     const unsigned who = __ballot_sync(0xffffffffu, mask != 0);
                     if (who == 0) break;
-                    // more than the list holds: this round only serves to raise the bound
+                    // more than the list holds: this sweep only serves to raise the bound
                     if (__any_sync(0xffffffffu, *static_cast<volatile int *>(count) > kCap)) break;
                     const int nth = __popc(who & ((1u << lane) - 1u));
                     if (mask != 0 && nth < 8) {
@@ -595,20 +595,20 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LpParams 
                     if (warp == 0) {
                         LpShared *lead = cluster.map_shared_rank(&sh, 0);
                         int pos = 0;
-                        if (lane == 0) pos = atomicAdd(&lead->joined[round & 1], n);
-                        if (lane < C) atomicAdd(&cluster.map_shared_rank(&sh, lane)->total[round & 1], n);
+                        if (lane == 0) pos = atomicAdd(&lead->joined[sweep & 1], n);
+                        if (lane < C) atomicAdd(&cluster.map_shared_rank(&sh, lane)->total[sweep & 1], n);
                         pos = __shfl_sync(0xffffffffu, pos, 0);
                         unsigned long long *joined = reinterpret_cast<unsigned long long *>(lead->data);
                         for (int i = lane; i < min(n, kCap) && pos + i < kCap; i += 32) joined[pos + i] = list[i];
                     }
                     cluster.sync();
-                    n = sh.total[round & 1];
+                    n = sh.total[sweep & 1];
                 }
                 if (n <= kCap) break;
-                // The list is full.  Its K-th largest is a bound too; what exceeds that goes into the next round.
+                // The list is full.  Its K-th largest is a bound too; what exceeds that goes into the next sweep.
                 if (tid == 0) {
-                    sh.n[(round + 1) & 1][team] = 0;
-                    if (C > 1) sh.total[(round + 1) & 1] = sh.joined[(round + 1) & 1] = 0;
+                    sh.n[(sweep + 1) & 1][team] = 0;
+                    if (C > 1) sh.total[(sweep + 1) & 1] = sh.joined[(sweep + 1) & 1] = 0;
                 }
                 if (c == 0 && tw == 0) {
                     auto reach = [&](uint32_t key) {

@@ -622,7 +622,7 @@ __device__ __forceinline__ void capped4_any(float *s, float cap_in, float cap_lo
 
 // How scores become weights: plain; capped, by the same running maximum; or capped by at most
 // kShCapFixed (in base 2), where 2^x of any score and any sum of them is an ordinary fp32 number, so
-// that no maximum is needed and the tile goes from S to P 32 columns at a time (a cap of 30, 112 samples of
+// that no running maximum is needed and the tile goes from S to P 32 columns at a time (a cap of 30, 112 samples of
 // 1-300 tokens over 1-500 keys: 114 us, with the running maximum 169).  2^80 of a weight and 2^17 keys leave
 // |v| < 2^30 within fp32; 2^-80 of one, where all scores of a row are near the negative cap, leaves
 // |v| >= 2^-46 among its normal numbers.
@@ -633,9 +633,9 @@ constexpr float kShCapFixed = 80.f;
 constexpr float kShNoWeight = -3.402823466e38f;
 
 // Measured, 16 / 8 heads of 128, device time with plan and join: 16 samples of 257-700 tokens over 8000
-// keys 398 us, 1380 TFLOP/s; 32 requests of 15 samples of 16-96 tokens over 200-500 keys 142.5 us (prefill)
+// keys 399 us within a graph, 418 among other calls, 1310 TFLOP/s; 32 requests of 15 samples of 16-96 tokens over 200-500 keys 142.5 us (prefill)
 // and 45 us, 3.5 TB/s (last token); 128 last tokens over 30000-32768 keys 115 us, 5.4 TB/s.  14 / 2 heads
-// of 64, scores capped at 30: 112 samples of 1-300 tokens over 1-500 keys 96 us, 744 last tokens 38 us.
+// of 64, scores capped at 30: 112 samples of 1-300 tokens over 1-500 keys 100 us, 744 last tokens 38 us.
 // What bounds it is the chain of one query tile per key tile: about 2250 cycles of softmax (tensor memory
 // to registers, maximum, 128 exponentials of a row, weights back), then 1400 of hand-overs and products.
 // Two query tiles overlap their chains; tensor memory (S and O of each) has no room for a third at D = 128.

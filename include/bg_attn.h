@@ -57,7 +57,7 @@ typedef enum {
 #define BG_DEVSTAT_SEQ_TOO_LONG 0x02  /* a sequence is longer than max_seqlen       */
 #define BG_DEVSTAT_PARENT       0x04  /* a parent index is outside [0, W)           */
 #define BG_DEVSTAT_CU_PROMPT    0x08  /* cu_prompt invalid or prompt > max_prompt   */
-#define BG_DEVSTAT_EMPTY_ROW    0x10  /* prompt length 0 with suffix_len 0          */
+#define BG_DEVSTAT_EMPTY_ROW    0x10  /* a query without any key                    */
 #define BG_DEVSTAT_PLAN         0x20  /* planned run: the workspace's work list is
                                          for another packing (nothing written)     */
 #define BG_DEVSTAT_GROUP        0x40  /* cu_group[0]!=0, decreasing, or cu_group[R]!=num_seqs */
@@ -467,8 +467,9 @@ bg_status_t bg_beam_select(const float *logits, const float *cum,
  * Errors: BG_ERR_INVALID_ARG for NULL or misaligned pointers, negative sizes,
  * num_groups == 0 with samples or prefix rows, tokens without samples (prefill),
  * Hq % Hkv != 0, a bad scale or softcap (a scale whose product with log2(e) is
- * not finite; a softcap whose own, or whose quotient with it, is not a normal number), a too-small workspace, or an output or the
- * workspace overlapping another argument; BG_ERR_UNSUPPORTED for head_dim not in {64, 128},
+ * not finite; a softcap whose own product, or the quotient of scale and softcap,
+ * is not a normal number), a too-small workspace, or an output or the workspace
+ * overlapping another argument; BG_ERR_UNSUPPORTED for head_dim not in {64, 128},
  * Hq/Hkv > 128, or max_seqlen or max_prefix_len > BG_MAX_SEQLEN.  No queries
  * (total_tokens == 0, or num_seqs == 0 for the last-token call) is a valid
  * no-op.  bg_shared_attn_workspace_size gives 0 for sizes that either call

@@ -99,7 +99,7 @@ def test_rows_about_as_long_as_the_list(V, dtype):
     check(restrict(logits(54, 64, V, dtype), None, 54), 32, f"restricted {V}")
 
 
-def test_rising_rows_of_many_rounds():
+def test_rising_rows_of_many_sweeps():
     """All live logits in one warp's lanes and rising: the worst order for a list that keeps the first ones."""
     import torch
     x = torch.full((2, 1 << 20), -float("inf"))
