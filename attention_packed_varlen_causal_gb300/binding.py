@@ -29,6 +29,8 @@ BG_DEVSTAT_PLAN = 0x20
 BG_DEVSTAT_GROUP = 0x40
 BG_DEVSTAT_TOKEN = 0x80
 BG_DEVSTAT_TIMEOUT = 0x100
+BG_DEVSTAT_BIAS = 0x200
+BG_DEVSTAT_MASK = 0x400
 BG_MAX_SUFFIX = 16
 BG_MAX_SEQLEN = 65536
 BG_NOALLOC_SCRATCH_BYTES = 1 << 20
@@ -36,12 +38,18 @@ BG_MAX_BEAM = 512
 BG_MAX_VOCAB = 1 << 22
 BG_MAX_TOP = 32
 BG_DTYPE_F32, BG_DTYPE_BF16 = 0, 1
+BG_MAX_AXES = 4
+BG_MAX_BIAS = 8191
+BG_MAX_TREE = 1024
 
 # Every symbol include/bg_attn.h declares, with its ctypes signature.
 _P, _I32, _F32, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
 _SHARED_PLAN = [_P, _I32, _I32, _I32, _P, _I32, _I32, _P, _I32, _I32, _I32, _I32, _P, _SZ, _P, _P]
 _SHARED_RUN = [_P, _P, _P, _P, _I32, _I32, _I32, _P, _P, _P, _I32, _I32, _P, _I32, _I32, _I32, _I32, _F32, _F32, _P, _P,
                _P, _SZ, _P, _P]
+_I64 = ctypes.c_int64
+_TREE_RUN = [_P, _P, _P, _P, _P, _I32, _I32, _I32, _P, _P, _P, _I32, _I32, _I32, _I32, _I32, _F32, _F32, _P, _P, _P, _SZ, _P,
+             _P]
 SIGNATURES = {
     "bg_status_string": ([ctypes.c_int], ctypes.c_char_p),
     "bg_packed_prefill_workspace_size": ([_I32] * 6, _SZ),
@@ -70,6 +78,16 @@ SIGNATURES = {
     "bg_shared_prefill_attn_planned": (_SHARED_RUN, ctypes.c_int),
     "bg_shared_last_token_attn": (_SHARED_RUN, ctypes.c_int),
     "bg_shared_last_token_attn_planned": (_SHARED_RUN, ctypes.c_int),
+    "bg_tree_attn_workspace_size": ([_I32] * 7, _SZ),
+    "bg_tree_plan": ([_P, _P, _I32, _I32, _I32, _P, _I32, _I32, _I32, _I32, _I32, _P, _SZ, _P, _P], ctypes.c_int),
+    "bg_tree_attn": (_TREE_RUN, ctypes.c_int),
+    "bg_tree_attn_planned": (_TREE_RUN, ctypes.c_int),
+    "bg_packed_qk_norm_rope": ([_P, _I64, _P, _I64, _P, _I64, _I32, _I32, _I32, _I32, _P, _P, _F32, _F32, _P, _I32, _P, _P,
+                                _I32, _I32, _F32, _P, _P, _P, _P], ctypes.c_int),
+    "bg_beam_qk_norm_rope": ([_P, _I64, _P, _I64, _P, _I64, _I32, _I32, _I32, _I32, _I32, _P, _P, _F32, _F32, _P, _I32, _P,
+                              _I32, _P, _I32, _I32, _F32, _P, _P, _P, _I32, _I32, _P], ctypes.c_int),
+    "bg_adjust_logits": ([_P, _I32, _I64, _I32, _I32, _I32, _P, _P, _I32, _P, _P, _I32, _P, _P, _P, _P, _P, _P, _I32, _P,
+                          _I64, _I32, _P, _P, _I32, _I64, _P, _P], ctypes.c_int),
     "bg_token_logprobs": ([_P, _I32, ctypes.c_int64, _I32, _I32, _P, _I32, _P, _P, _P, _P, _P, _P], ctypes.c_int),
     "bg_selftest_wait_timeout": ([_P, _P, _P], ctypes.c_int),
     "bg_selftest_logprobs_timeout": ([_P, _I32, _I32, _P, _I32, _P, _P, _P, _P, _P, _P], ctypes.c_int),
@@ -538,3 +556,236 @@ def bg_selftest_logprobs_timeout(logits, tokens, stalled_row: int, *, logprob, e
         raise BgError(fn, BG_ERR_UNSUPPORTED)
     _launch(fn, logits.get_device(), stream, logits.data_ptr(), N, V, tokens.data_ptr(), stalled_row, logprob.data_ptr(),
             entropy.data_ptr(), top_token.data_ptr(), top_logprob.data_ptr(), dev_status.data_ptr())
+
+
+def bg_tree_attn_workspace_size(num_requests: int, total_nodes: int, max_nodes: int, max_prefix_len: int, Hq: int, Hkv: int,
+                                head_dim: int) -> int:
+    if not _fits(num_requests, total_nodes, max_nodes, max_prefix_len, Hq, Hkv, head_dim):
+        return 0
+    return int(load().bg_tree_attn_workspace_size(num_requests, total_nodes, max_nodes, max_prefix_len, Hq, Hkv, head_dim))
+
+
+def _tree_workspace(fn: str, workspace, sizes, index: int):
+    if workspace is None:
+        raise ValueError(f"{fn}: workspace of {bg_tree_attn_workspace_size(*sizes)} bytes required (the library never "
+                         "allocates)")
+    if workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError(f"{fn}: workspace must be contiguous on the other tensors' device, got {workspace.device}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _tree_run(fn: str, q, k, v, parent, cu_nodes, max_nodes, prefix_k, prefix_v, cu_prefix, max_prefix_len, out, lse, scale,
+              softcap, workspace, dev_status, stream):
+    import torch
+    bf16, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    T, Hq, d = q.shape
+    kv = k.shape
+    Hkv = kv[1]
+    R = cu_nodes.numel() - 1
+    if (prefix_k is None) != (prefix_v is None):
+        raise ValueError(f"{fn}: prefix_k and prefix_v come together")
+    P = 0 if prefix_k is None else prefix_k.shape[0]
+    index = q.get_device()
+    if not (_alike(bf16, index, (q, k, v, prefix_k, prefix_v, out)) and
+            _alike(i32, index, (parent, cu_nodes, cu_prefix, dev_status)) and
+            (lse is None or (_alike(f32, index, (lse,)) and lse.shape == (T, Hq))) and
+            out.shape == q.shape and kv == (T, Hkv, d) and v.shape == kv and parent.shape == (T,) and
+            (prefix_k is None or prefix_k.shape == prefix_v.shape == (P, Hkv, d)) and
+            cu_nodes.dim() == cu_prefix.dim() == 1 and cu_prefix.numel() == R + 1):
+        _expect(fn, q.device, (
+            ("q", q, bf16, (T, Hq, d)), ("k", k, bf16, (T, Hkv, d)), ("v", v, bf16, (T, Hkv, d)),
+            ("parent", parent, i32, (T,)), ("cu_nodes", cu_nodes, i32, (R + 1,)),
+            ("prefix_k", prefix_k, bf16, (P, Hkv, d)), ("prefix_v", prefix_v, bf16, (P, Hkv, d)),
+            ("cu_prefix", cu_prefix, i32, (R + 1,)), ("out", out, bf16, (T, Hq, d)), ("lse", lse, f32, (T, Hq)),
+            ("dev_status", dev_status, i32, dev_status.shape if dev_status is not None else ())))
+    max_nodes, max_prefix_len = int(max_nodes), int(max_prefix_len)
+    if not _fits(R, T, P, max_nodes, max_prefix_len):
+        raise BgError(fn, BG_ERR_UNSUPPORTED)
+    ws, ws_bytes = _tree_workspace(fn, workspace, (R, T, max_nodes, max_prefix_len, Hq, Hkv, d), index)
+    _launch(fn, index, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), parent.data_ptr(), cu_nodes.data_ptr(), R, T,
+            max_nodes, _ptr(prefix_k), _ptr(prefix_v), cu_prefix.data_ptr(), P, max_prefix_len, Hq, Hkv, d,
+            1.0 / math.sqrt(d) if scale is None else float(scale), float(softcap), out.data_ptr(), _ptr(lse), ws,
+            ws_bytes, _ptr(dev_status))
+    return out
+
+
+def bg_tree_attn(q, k, v, parent, cu_nodes, max_nodes: int, prefix_k, prefix_v, cu_prefix, max_prefix_len: int, out, *,
+                 lse=None, scale: Optional[float] = None, softcap: float = 0.0, workspace=None, dev_status=None,
+                 stream=None):
+    """Attention of the nodes of drafted trees over their request's prefix, their ancestors and themselves.
+    q [T,Hq,d], k/v [T,Hkv,d] bf16, request r at rows cu_nodes[r] .. cu_nodes[r+1]-1 (int32 [R+1]); parent
+    int32 [T]: a lower node of the same request, counted from its first, or -1; prefix_k/prefix_v [P,Hkv,d]
+    (or None) packed by cu_prefix int32 [R+1]; out [T,Hq,d] (written); lse fp32 [T,Hq] or None; workspace a
+    uint8 CUDA tensor of bg_tree_attn_workspace_size bytes."""
+    return _tree_run("bg_tree_attn", q, k, v, parent, cu_nodes, max_nodes, prefix_k, prefix_v, cu_prefix, max_prefix_len,
+                     out, lse, scale, softcap, workspace, dev_status, stream)
+
+
+def bg_tree_attn_planned(q, k, v, parent, cu_nodes, max_nodes: int, prefix_k, prefix_v, cu_prefix, max_prefix_len: int, out,
+                         *, lse=None, scale: Optional[float] = None, softcap: float = 0.0, workspace=None,
+                         dev_status=None, stream=None):
+    """bg_tree_attn with the work list and the masks that bg_tree_plan left in workspace."""
+    return _tree_run("bg_tree_attn_planned", q, k, v, parent, cu_nodes, max_nodes, prefix_k, prefix_v, cu_prefix,
+                     max_prefix_len, out, lse, scale, softcap, workspace, dev_status, stream)
+
+
+def bg_tree_plan(parent, cu_nodes, max_nodes: int, cu_prefix, total_prefix: int, max_prefix_len: int, Hq: int, Hkv: int,
+                 head_dim: int, *, workspace=None, dev_status=None, stream=None):
+    """The work list and masks of the trees (parent int32 [T], cu_nodes int32 [R+1]) into workspace, for
+    bg_tree_attn_planned calls with them."""
+    import torch
+    fn, i32 = "bg_tree_plan", torch.int32
+    T, R = parent.numel(), cu_nodes.numel() - 1
+    index = parent.get_device()
+    _expect(fn, parent.device, (
+        ("parent", parent, i32, (T,)), ("cu_nodes", cu_nodes, i32, (R + 1,)), ("cu_prefix", cu_prefix, i32, (R + 1,)),
+        ("dev_status", dev_status, i32, dev_status.shape if dev_status is not None else ())))
+    P, max_nodes, max_prefix_len = int(total_prefix), int(max_nodes), int(max_prefix_len)
+    if not _fits(R, T, P, max_nodes, max_prefix_len, Hq, Hkv, head_dim):
+        raise BgError(fn, BG_ERR_UNSUPPORTED)
+    ws, ws_bytes = _tree_workspace(fn, workspace, (R, T, max_nodes, max_prefix_len, Hq, Hkv, head_dim), index)
+    _launch(fn, index, stream, parent.data_ptr(), cu_nodes.data_ptr(), R, T, max_nodes, cu_prefix.data_ptr(), P,
+            max_prefix_len, Hq, Hkv, head_dim, ws, ws_bytes, _ptr(dev_status))
+
+
+def _rows_of_heads(fn: str, name: str, t, lead, index: int):
+    """Row stride of ``t``, whose last two dimensions (heads, d) are side by side and whose ``lead`` leading ones step
+    through rows at one distance (a view into the fused projection's output, for instance)."""
+    import torch
+    shape, st = t.shape, t.stride()
+    ok = t.dtype is torch.bfloat16 and t.get_device() == index and st[-1] == 1 and (shape[-2] == 1 or st[-2] == shape[-1])
+    row = st[lead - 1]
+    if lead == 2 and shape[0] > 1:
+        if shape[1] == 1:
+            row = st[0]
+        else:
+            ok = ok and st[0] == shape[1] * row
+    rows = shape[0] if lead == 1 else shape[0] * shape[1]
+    if not ok:
+        raise ValueError(f"{fn}: {name} must be bfloat16 rows of heads side by side at one distance, on the other tensors' "
+                         f"device, got {t.dtype} {tuple(shape)} with strides {st} on {t.device}")
+    return row if rows > 1 else (shape[-2] * shape[-1] + 7) // 8 * 8
+
+
+def _qk_norm_rope(fn: str, q, k, v, positions, place_shape, outs, lead, q_weight, k_weight, inv_freq, axis_of):
+    """Checks of both forms; returns the row strides, the number of axes and axis_of as a ctypes array."""
+    import torch
+    bf16, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    index = q.get_device()
+    Hq, d = q.shape[-2:]
+    axes = 1 if positions.dim() == len(place_shape) else positions.shape[0]
+    if k.shape[:lead] != q.shape[:lead] or k.shape[-1] != d or (v is not None and v.shape != k.shape):
+        raise ValueError(f"{fn}: q, k and v must have the same rows and head_dim, got {tuple(q.shape)}, {tuple(k.shape)}, "
+                         f"{None if v is None else tuple(v.shape)}")
+    if not (_alike(bf16, index, (q_weight, k_weight) + tuple(t for _, t, _ in outs)) and _alike(i32, index, (positions,)) and
+            _alike(f32, index, (inv_freq,)) and positions.shape[-len(place_shape):] == place_shape and
+            positions.dim() <= len(place_shape) + 1 and inv_freq.dim() == 1 and
+            (q_weight is None or q_weight.shape == (d,)) and (k_weight is None or k_weight.shape == (d,)) and
+            all(t is None or t.shape == s for _, t, s in outs)):
+        _expect(fn, q.device, [("positions", positions, i32, (axes,) + place_shape if positions.dim() > 1 else place_shape),
+                               ("inv_freq", inv_freq, f32, (inv_freq.numel(),)), ("q_weight", q_weight, bf16, (d,)),
+                               ("k_weight", k_weight, bf16, (d,))] + [(n, t, bf16, s) for n, t, s in outs])
+    strides = tuple(0 if t is None else _rows_of_heads(fn, n, t, lead, index) for n, t in (("q", q), ("k", k), ("v", v)))
+    n_freq = inv_freq.shape[0]
+    if axis_of is not None:
+        if len(axis_of) != n_freq:
+            raise ValueError(f"{fn}: axis_of must have an axis for each of the {n_freq} frequencies, got {len(axis_of)}")
+        axis_of = (_I32 * n_freq)(*axis_of)
+    return strides, axes, axis_of, 2 * n_freq
+
+
+def bg_packed_qk_norm_rope(q, k, v, positions, q_out, k_out, v_out=None, *, inv_freq, q_weight=None, k_weight=None,
+                           eps: float = 1e-6, weight_offset: float = 0.0, axis_of=None, interleaved: bool = False,
+                           rope_scale: float = 1.0, stream=None):
+    """Norm of every head of q [T,Hq,d] and k [T,Hkv,d] (bf16; rows may be strided, as views into a fused projection
+    are) with q_weight/k_weight bf16 [d] (None: no norm), then the rotation of the first 2 * len(inv_freq) dimensions
+    by positions int32 [T] or [axes,T] times inv_freq fp32; axis_of: the axis of each frequency (a list).
+    q_out [T,Hq,d], k_out and v_out [T,Hkv,d] contiguous (written); v [T,Hkv,d] is copied to v_out, or both are None."""
+    fn = "bg_packed_qk_norm_rope"
+    T, Hq, d = q.shape
+    Hkv = k.shape[1]
+    if not _fits(T, Hq, Hkv, d):
+        raise BgError(fn, BG_ERR_UNSUPPORTED)
+    (qs, ks, vs), axes, axis_of, rot = _qk_norm_rope(
+        fn, q, k, v, positions, (T,), (("q_out", q_out, (T, Hq, d)), ("k_out", k_out, (T, Hkv, d)),
+                                       ("v_out", v_out, (T, Hkv, d))), 1, q_weight, k_weight, inv_freq, axis_of)
+    _launch(fn, q.get_device(), stream, q.data_ptr(), qs, k.data_ptr(), ks, _ptr(v), vs, T, Hq, Hkv, d, _ptr(q_weight),
+            _ptr(k_weight), float(eps), float(weight_offset), positions.data_ptr(), axes, axis_of, inv_freq.data_ptr(), rot,
+            int(interleaved), float(rope_scale), q_out.data_ptr(), k_out.data_ptr(), _ptr(v_out))
+    return q_out, k_out, v_out
+
+
+def bg_beam_qk_norm_rope(q, k, v, base_pos, step: int, q_out, suffix_k, suffix_v, slot: int, *, inv_freq, q_weight=None,
+                         k_weight=None, eps: float = 1e-6, weight_offset: float = 0.0, axis_of=None,
+                         interleaved: bool = False, rope_scale: float = 1.0, stream=None):
+    """bg_packed_qk_norm_rope for the new token of every beam: q [R,W,Hq,d], k/v [R,W,Hkv,d] bf16 (strided rows as
+    there), all beams of request r at base_pos int32 [R] or [axes,R] plus step; q_out [R,W,Hq,d] and slot ``slot`` of
+    suffix_k/suffix_v [R,W,S_max,Hkv,d] are written."""
+    fn = "bg_beam_qk_norm_rope"
+    R, W, Hq, d = q.shape
+    Hkv, S_max = k.shape[2], suffix_k.shape[2]
+    if not _fits(R, W, Hq, Hkv, d, S_max, step, slot):
+        raise BgError(fn, BG_ERR_UNSUPPORTED)
+    suffix = (R, W, S_max, Hkv, d)
+    (qs, ks, vs), axes, axis_of, rot = _qk_norm_rope(
+        fn, q, k, v, base_pos, (R,), (("q_out", q_out, (R, W, Hq, d)), ("suffix_k", suffix_k, suffix),
+                                      ("suffix_v", suffix_v, suffix)), 2, q_weight, k_weight, inv_freq, axis_of)
+    _launch(fn, q.get_device(), stream, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, R, W, Hq, Hkv, d,
+            _ptr(q_weight), _ptr(k_weight), float(eps), float(weight_offset), base_pos.data_ptr(), axes, axis_of, int(step),
+            inv_freq.data_ptr(), rot, int(interleaved), float(rope_scale), q_out.data_ptr(), suffix_k.data_ptr(),
+            suffix_v.data_ptr(), S_max, int(slot))
+    return q_out, suffix_k, suffix_v
+
+
+def bg_adjust_logits(logits, out, *, rows_per_group: int = 1, prompt_tokens=None, cu_prompt=None, own_tokens=None,
+                     own_lens=None, repetition=None, frequency=None, presence=None, bias_tokens=None, bias_values=None,
+                     cu_bias=None, mask=None, mask_index=None, dev_status=None, stream=None):
+    """Penalties, biases and masks on logits fp32 or bf16 [N,V] into out [N,V] (rows may be strided; out may be logits).
+    Groups of rows_per_group rows share prompt_tokens int32 (packed by cu_prompt int32 [G+1]), repetition/frequency/
+    presence fp32 [G] and bias_tokens int32, bias_values fp32 (packed by cu_bias int32 [G+1]); own_tokens int32 [N,S],
+    of which row i has own_lens[i] (int32 [N] or None: S); mask int32 or uint32 [M,words], bit v % 32 of word v // 32 set
+    where v is allowed, mask_index int32 [N] (-1: no mask) or None: row i has mask i."""
+    import torch
+    fn = "bg_adjust_logits"
+    N, V = logits.shape
+    kinds = {torch.float32: BG_DTYPE_F32, torch.bfloat16: BG_DTYPE_BF16}
+    index = logits.get_device()
+    for name, t in (("logits", logits), ("out", out)):
+        if t.dtype not in kinds or t.shape != (N, V) or (V > 1 and N > 0 and t.stride(1) != 1) or t.get_device() != index:
+            raise ValueError(f"{fn}: {name} must be float32 or bfloat16 with contiguous rows of shape {(N, V)} on "
+                             f"{logits.device}, got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
+    rows_per_group = int(rows_per_group)
+    if rows_per_group < 1 or N % rows_per_group:
+        raise ValueError(f"{fn}: {N} rows are no whole groups of {rows_per_group}")
+    G = N // rows_per_group
+    f32, i32 = torch.float32, torch.int32
+    if (prompt_tokens is None) != (cu_prompt is None) or (bias_tokens is None) != (cu_bias is None) or \
+            (bias_tokens is None) != (bias_values is None):
+        raise ValueError(f"{fn}: prompt_tokens and cu_prompt, and bias_tokens, bias_values and cu_bias, come together")
+    P = 0 if prompt_tokens is None else prompt_tokens.numel()
+    B = 0 if bias_tokens is None else bias_tokens.numel()
+    S = 0 if own_tokens is None else own_tokens.shape[-1]
+    M, words = (0, 0) if mask is None else (mask.shape[0], mask.shape[-1])
+    if mask is not None and mask.dtype is getattr(torch, "uint32", None):
+        mask = mask.view(i32)
+    if not (_alike(i32, index, (prompt_tokens, cu_prompt, own_tokens, own_lens, bias_tokens, cu_bias, mask, mask_index,
+                                dev_status)) and
+            _alike(f32, index, (repetition, frequency, presence, bias_values)) and
+            all(t is None or t.shape == s for t, s in (
+                (prompt_tokens, (P,)), (cu_prompt, (G + 1,)), (own_tokens, (N, S)), (own_lens, (N,)), (repetition, (G,)),
+                (frequency, (G,)), (presence, (G,)), (bias_tokens, (B,)), (bias_values, (B,)), (cu_bias, (G + 1,)),
+                (mask, (M, words)), (mask_index, (N,))))):
+        _expect(fn, logits.device, (
+            ("prompt_tokens", prompt_tokens, i32, (P,)), ("cu_prompt", cu_prompt, i32, (G + 1,)),
+            ("own_tokens", own_tokens, i32, (N, S)), ("own_lens", own_lens, i32, (N,)), ("repetition", repetition, f32, (G,)),
+            ("frequency", frequency, f32, (G,)), ("presence", presence, f32, (G,)), ("bias_tokens", bias_tokens, i32, (B,)),
+            ("bias_values", bias_values, f32, (B,)), ("cu_bias", cu_bias, i32, (G + 1,)), ("mask", mask, i32, (M, words)),
+            ("mask_index", mask_index, i32, (N,)),
+            ("dev_status", dev_status, i32, dev_status.shape if dev_status is not None else ())))
+    if not _fits(N, V, P, B, S, M):
+        raise BgError(fn, BG_ERR_UNSUPPORTED)
+    _launch(fn, index, stream, logits.data_ptr(), kinds[logits.dtype], logits.stride(0) if N > 1 else V, G, rows_per_group, V,
+            _ptr(prompt_tokens), _ptr(cu_prompt), P, _ptr(own_tokens), _ptr(own_lens), S, _ptr(repetition),
+            _ptr(frequency), _ptr(presence), _ptr(bias_tokens), _ptr(bias_values), _ptr(cu_bias), B, _ptr(mask), words, M,
+            _ptr(mask_index), out.data_ptr(), kinds[out.dtype], out.stride(0) if N > 1 else V, _ptr(dev_status))
+    return out

@@ -596,7 +596,7 @@ bg_status_t shared_check_sizes(const ShProblem &pb)
     if (pb.num_groups == 0 && (pb.num_seqs > 0 || pb.total_prefix > 0)) return BG_ERR_INVALID_ARG;
     if (!pb.last && pb.num_seqs == 0 && pb.total_tokens > 0) return BG_ERR_INVALID_ARG;
     if (!supported_head_dim(pb.head_dim) || pb.Hq / pb.Hkv > kShRows || pb.max_seqlen > BG_MAX_SEQLEN ||
-        pb.max_prefix_len > BG_MAX_SEQLEN)
+        pb.max_prefix_len > BG_MAX_SEQLEN || (pb.tree && pb.max_seqlen > BG_MAX_TREE))
         return BG_ERR_UNSUPPORTED;
     if (shared_layout(pb).max_entries * pb.Hkv >= (int64_t(1) << 31)) return BG_ERR_UNSUPPORTED;
     return BG_OK;
@@ -618,16 +618,26 @@ bool shared_is_noop(const ShProblem &pb) { return pb.last ? pb.num_seqs == 0 : p
 bg_status_t shared_check_plan(const ShProblem &pb, const void *workspace, size_t workspace_bytes,
                               const int32_t *dev_status)
 {
-    if (!pb.cu_seqlens || !pb.cu_prefix || !pb.cu_group || !aligned(pb.cu_seqlens, 4) || !aligned(pb.cu_prefix, 4) ||
-        !aligned(pb.cu_group, 4) || (dev_status && !aligned(dev_status, 4)))
+    if (!pb.cu_seqlens || !pb.cu_prefix || !(pb.tree ? pb.parent : pb.cu_group) || !aligned(pb.cu_seqlens, 4) ||
+        !aligned(pb.cu_prefix, 4) || !aligned(pb.cu_group, 4) || !aligned(pb.parent, 4) ||
+        (dev_status && !aligned(dev_status, 4)))
         return BG_ERR_INVALID_ARG;
     if (!workspace || !aligned(workspace, 256) || workspace_bytes < shared_layout(pb).total) return BG_ERR_INVALID_ARG;
     if (overlap(pb.cu_seqlens, (static_cast<size_t>(pb.num_seqs) + 1) * 4, workspace, workspace_bytes) ||
         overlap(pb.cu_prefix, (static_cast<size_t>(pb.num_groups) + 1) * 4, workspace, workspace_bytes) ||
         overlap(pb.cu_group, (static_cast<size_t>(pb.num_groups) + 1) * 4, workspace, workspace_bytes) ||
+        overlap(pb.parent, static_cast<size_t>(pb.total_tokens) * 4, workspace, workspace_bytes) ||
         overlap(dev_status, 4, workspace, workspace_bytes))
         return BG_ERR_INVALID_ARG;
     return BG_OK;
+}
+
+// The pre-pass: a tree's masks, and the work list.
+bool shared_enqueue_plan(const ShProblem &pb, const ShLayout &lay, void *workspace, int grid, int32_t *dev_status,
+                         cudaStream_t stream)
+{
+    if (pb.tree && launch_tree_masks(pb, lay, workspace, dev_status, stream) != cudaSuccess) return false;
+    return launch_shared_plan(pb, lay, workspace, grid, dev_status, stream) == cudaSuccess;
 }
 
 bg_status_t shared_plan_impl(const ShProblem &pb, void *workspace, size_t workspace_bytes, int32_t *dev_status,
@@ -640,7 +650,7 @@ bg_status_t shared_plan_impl(const ShProblem &pb, void *workspace, size_t worksp
     const ShLayout lay = shared_layout(pb);
     const int grid = shared_grid(pb, lay);
     if (grid <= 0) return BG_ERR_CUDA;
-    return launch_shared_plan(pb, lay, workspace, grid, dev_status, stream) == cudaSuccess ? BG_OK : BG_ERR_CUDA;
+    return shared_enqueue_plan(pb, lay, workspace, grid, dev_status, stream) ? BG_OK : BG_ERR_CUDA;
 }
 
 bg_status_t shared_impl(const ShProblem &pb, const void *q, const void *k, const void *v, const void *prefix_k,
@@ -667,11 +677,11 @@ bg_status_t shared_impl(const ShProblem &pb, const void *q, const void *k, const
     const size_t kvbytes = static_cast<size_t>(pb.total_tokens) * pb.Hkv * pb.head_dim * 2;
     const size_t pbytes = static_cast<size_t>(pb.total_prefix) * pb.Hkv * pb.head_dim * 2;
     const size_t lsebytes = lse ? rows * pb.Hq * 4 : 0;
-    const void *in[9] = {q, k, v, prefix_k, prefix_v, pb.cu_seqlens, pb.cu_prefix, pb.cu_group, dev_status};
+    const void *in[10] = {q, k, v, prefix_k, prefix_v, pb.cu_seqlens, pb.cu_prefix, pb.cu_group, pb.parent, dev_status};
     const size_t groups = (static_cast<size_t>(pb.num_groups) + 1) * 4;
-    const size_t inb[9] = {qbytes, kvbytes, kvbytes, pbytes, pbytes, (static_cast<size_t>(pb.num_seqs) + 1) * 4,
-                           groups, groups, 4};
-    for (int i = 0; i < 9; ++i)
+    const size_t inb[10] = {qbytes, kvbytes, kvbytes, pbytes, pbytes, (static_cast<size_t>(pb.num_seqs) + 1) * 4,
+                            groups, groups, static_cast<size_t>(pb.total_tokens) * 4, 4};
+    for (int i = 0; i < 10; ++i)
         if (overlap(out, qbytes, in[i], inb[i]) || overlap(lse, lsebytes, in[i], inb[i]) ||
             overlap(workspace, workspace_bytes, in[i], inb[i]))
             return BG_ERR_INVALID_ARG;
@@ -701,8 +711,7 @@ bg_status_t shared_impl(const ShProblem &pb, const void *q, const void *k, const
         !kv_map(&tm_pv, prefix_v, pb.total_prefix))
         return BG_ERR_CUDA;
 
-    if (with_plan && launch_shared_plan(pb, lay, workspace, grid, dev_status, stream) != cudaSuccess)
-        return BG_ERR_CUDA;
+    if (with_plan && !shared_enqueue_plan(pb, lay, workspace, grid, dev_status, stream)) return BG_ERR_CUDA;
 
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     ShParams p;
@@ -722,6 +731,8 @@ bg_status_t shared_impl(const ShProblem &pb, const void *q, const void *k, const
     p.dev_status = dev_status;
     p.key = shared_key(pb, grid);
     p.cu_seqlens = pb.cu_seqlens;
+    p.tree = pb.tree ? reinterpret_cast<const uint32_t *>(ws + lay.tree) : nullptr;
+    p.tree_words = tree_words(pb.max_seqlen);
     p.hdr = reinterpret_cast<int32_t *>(ws);
     p.entries = reinterpret_cast<const ShEntry *>(ws + lay.entries);
     p.sorted = reinterpret_cast<const ShEntry *>(ws + lay.sorted);
@@ -798,6 +809,43 @@ BG_SHARED_RUN(bg_shared_last_token_attn_planned, 1, false)
 #undef BG_SHARED_RUN
 #undef BG_SHARED_PROBLEM
 
+size_t bg_tree_attn_workspace_size(int32_t num_requests, int32_t total_nodes, int32_t max_nodes, int32_t max_prefix_len,
+                                   int32_t Hq, int32_t Hkv, int32_t head_dim)
+{
+    const ShProblem pb{nullptr, nullptr, nullptr, num_requests, total_nodes, max_nodes, num_requests, 0,
+                       max_prefix_len, Hq, Hkv, head_dim, 0, 1, nullptr};
+    return shared_check_sizes(pb) == BG_OK ? shared_layout(pb).total : 0;
+}
+
+#define BG_TREE_PROBLEM                                                                                                \
+    const ShProblem pb{cu_nodes, cu_prefix, nullptr, num_requests, total_nodes, max_nodes, num_requests, total_prefix, \
+                       max_prefix_len, Hq, Hkv, head_dim, 0, 1, parent}
+
+bg_status_t bg_tree_plan(const int32_t *parent, const int32_t *cu_nodes, int32_t num_requests, int32_t total_nodes,
+                         int32_t max_nodes, const int32_t *cu_prefix, int32_t total_prefix, int32_t max_prefix_len,
+                         int32_t Hq, int32_t Hkv, int32_t head_dim, void *workspace, size_t workspace_bytes,
+                         int32_t *dev_status, cudaStream_t stream)
+{
+    BG_TREE_PROBLEM;
+    return shared_plan_impl(pb, workspace, workspace_bytes, dev_status, stream);
+}
+
+#define BG_TREE_RUN(NAME, PLAN)                                                                                        \
+    bg_status_t NAME(const void *q, const void *k, const void *v, const int32_t *parent, const int32_t *cu_nodes,      \
+                     int32_t num_requests, int32_t total_nodes, int32_t max_nodes, const void *prefix_k,               \
+                     const void *prefix_v, const int32_t *cu_prefix, int32_t total_prefix, int32_t max_prefix_len,     \
+                     int32_t Hq, int32_t Hkv, int32_t head_dim, float scale, float softcap, void *out, float *lse,     \
+                     void *workspace, size_t workspace_bytes, int32_t *dev_status, cudaStream_t stream)                \
+    {                                                                                                                  \
+        BG_TREE_PROBLEM;                                                                                               \
+        return shared_impl(pb, q, k, v, prefix_k, prefix_v, scale, softcap, out, lse, workspace, workspace_bytes,      \
+                           dev_status, stream, PLAN);                                                                  \
+    }
+BG_TREE_RUN(bg_tree_attn, true)
+BG_TREE_RUN(bg_tree_attn_planned, false)
+#undef BG_TREE_RUN
+#undef BG_TREE_PROBLEM
+
 bg_status_t bg_token_logprobs(const void *logits, int32_t dtype, int64_t row_stride, int32_t N, int32_t V,
                               const int32_t *tokens, int32_t K, float *logprob_out, float *entropy_out,
                               int32_t *top_token_out, float *top_logprob_out, int32_t *dev_status,
@@ -850,6 +898,191 @@ bg_status_t bg_selftest_logprobs_timeout(const float *logits, int32_t N, int32_t
                                     top_logprob_out, dev_status, nsm, stream) == cudaSuccess
                ? BG_OK
                : BG_ERR_CUDA;
+}
+
+}  // extern "C"
+
+namespace {
+
+// Bytes from the first to the last element of `rows` rows of n elements of 2 bytes, `stride` elements apart.
+size_t strided_bytes(int64_t rows, int64_t stride, int64_t n)
+{
+    return rows > 0 ? (static_cast<size_t>(rows - 1) * static_cast<size_t>(stride) + static_cast<size_t>(n)) * 2 : 0;
+}
+
+// What both forms of the norm and rotation share.  p has the rows, heads, strides, pointers and scalars; a buffer for
+// K or V has kv_rows rows of Hkv heads, of which the first one written is slot.
+bg_status_t qk_rope_impl(RopeParams &p, int32_t head_dim, int32_t num_axes, const int32_t *axis_of, int32_t rot_dim,
+                         int32_t interleaved, int64_t kv_rows, int32_t slot, cudaStream_t stream)
+{
+    if (p.Hq <= 0 || p.Hkv <= 0 || head_dim <= 0 || p.Hq % p.Hkv != 0 || num_axes < 1 || rot_dim < 1 ||
+        (interleaved != 0 && interleaved != 1))
+        return BG_ERR_INVALID_ARG;
+    if (!(p.eps >= 0.f) || !std::isfinite(p.eps) || !std::isfinite(p.weight_offset) || !std::isfinite(p.rope_scale))
+        return BG_ERR_INVALID_ARG;
+    if (!supported_head_dim(head_dim) || num_axes > BG_MAX_AXES || rot_dim > head_dim || rot_dim % 16 != 0)
+        return BG_ERR_UNSUPPORTED;
+    if ((p.q_weight != nullptr) != (p.k_weight != nullptr) || (p.v != nullptr) != (p.v_out != nullptr))
+        return BG_ERR_INVALID_ARG;
+    p.rot = rot_dim;
+    std::memset(p.axis, 0, sizeof(p.axis));
+    if (num_axes > 1 && !axis_of) return BG_ERR_INVALID_ARG;
+    for (int32_t i = 0; axis_of && i < rot_dim / 2; ++i) {
+        if (axis_of[i] < 0 || axis_of[i] >= num_axes) return BG_ERR_INVALID_ARG;
+        p.axis[i] = static_cast<uint8_t>(axis_of[i]);
+    }
+    const int64_t nq = static_cast<int64_t>(p.Hq) * head_dim, nkv = static_cast<int64_t>(p.Hkv) * head_dim;
+    if (p.q_stride < nq || p.k_stride < nkv || (p.v && p.v_stride < nkv) || p.q_stride % 8 || p.k_stride % 8 ||
+        (p.v && p.v_stride % 8))
+        return BG_ERR_INVALID_ARG;
+    if (p.rows == 0) return BG_OK;
+    if (!p.q || !p.k || !p.positions || !p.inv_freq || !p.q_out || !p.k_out) return BG_ERR_INVALID_ARG;
+    for (const void *t : {static_cast<const void *>(p.q), static_cast<const void *>(p.k), static_cast<const void *>(p.v),
+                          static_cast<const void *>(p.q_out), static_cast<const void *>(p.k_out),
+                          static_cast<const void *>(p.v_out), static_cast<const void *>(p.q_weight),
+                          static_cast<const void *>(p.k_weight)})
+        if (!aligned(t, 16)) return BG_ERR_INVALID_ARG;
+    if (!aligned(p.positions, 4) || !aligned(p.inv_freq, 4)) return BG_ERR_INVALID_ARG;
+    const size_t wbytes = static_cast<size_t>(head_dim) * 2;
+    const void *in[7] = {p.q, p.k, p.v, p.q_weight, p.k_weight, p.positions, p.inv_freq};
+    const size_t inb[7] = {strided_bytes(p.rows, p.q_stride, nq), strided_bytes(p.rows, p.k_stride, nkv),
+                           p.v ? strided_bytes(p.rows, p.v_stride, nkv) : 0, wbytes, wbytes,
+                           static_cast<size_t>(num_axes) * static_cast<size_t>(p.places) * 4,
+                           static_cast<size_t>(rot_dim / 2) * 4};
+    const void *out[3] = {p.q_out, p.k_out, p.v_out};
+    const size_t kv_bytes = static_cast<size_t>(kv_rows) * nkv * 2;
+    const size_t outb[3] = {static_cast<size_t>(p.rows) * nq * 2, kv_bytes, p.v ? kv_bytes : 0};
+    p.k_out += slot * nkv;
+    if (p.v) p.v_out += slot * nkv;
+    // in place: the output is the input, row by row
+    const bool same[3] = {p.q_out == p.q && p.q_stride == nq, p.k_out == p.k && p.k_stride == p.kv_out_stride,
+                          p.v && p.v_out == p.v && p.v_stride == p.kv_out_stride};
+    for (int o = 0; o < 3; ++o) {
+        for (int i = 0; i < 7; ++i)
+            if (!(i == o && same[o]) && overlap(out[o], outb[o], in[i], inb[i])) return BG_ERR_INVALID_ARG;
+        for (int o2 = o + 1; o2 < 3; ++o2)
+            if (overlap(out[o], outb[o], out[o2], outb[o2])) return BG_ERR_INVALID_ARG;
+    }
+    const int nsm = sm_count();
+    if (nsm <= 0) return BG_ERR_CUDA;
+    return launch_qk_rope(p, head_dim, interleaved != 0, nsm, stream) == cudaSuccess ? BG_OK : BG_ERR_CUDA;
+}
+
+const __nv_bfloat16 *bf16_in(const void *p) { return static_cast<const __nv_bfloat16 *>(p); }
+__nv_bfloat16 *bf16_out(void *p) { return static_cast<__nv_bfloat16 *>(p); }
+
+}  // namespace
+
+extern "C" {
+
+bg_status_t bg_packed_qk_norm_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                                   int64_t v_stride, int32_t total_tokens, int32_t Hq, int32_t Hkv, int32_t head_dim,
+                                   const void *q_weight, const void *k_weight, float eps, float weight_offset,
+                                   const int32_t *positions, int32_t num_axes, const int32_t *axis_of,
+                                   const float *inv_freq, int32_t rot_dim, int32_t interleaved, float rope_scale,
+                                   void *q_out, void *k_out, void *v_out, cudaStream_t stream)
+{
+    if (total_tokens < 0) return BG_ERR_INVALID_ARG;
+    RopeParams p{bf16_in(q), bf16_in(k), bf16_in(v), bf16_out(q_out), bf16_out(k_out), bf16_out(v_out),
+                 bf16_in(q_weight), bf16_in(k_weight), positions, inv_freq, q_stride, k_stride, v_stride,
+                 static_cast<int64_t>(Hkv) * head_dim, total_tokens, total_tokens, 1, 0, Hq, Hkv, 0, 0, eps,
+                 weight_offset, rope_scale, {}};
+    return qk_rope_impl(p, head_dim, num_axes, axis_of, rot_dim, interleaved, total_tokens, 0, stream);
+}
+
+bg_status_t bg_beam_qk_norm_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                                 int64_t v_stride, int32_t R, int32_t W, int32_t Hq, int32_t Hkv, int32_t head_dim,
+                                 const void *q_weight, const void *k_weight, float eps, float weight_offset,
+                                 const int32_t *base_pos, int32_t num_axes, const int32_t *axis_of, int32_t step,
+                                 const float *inv_freq, int32_t rot_dim, int32_t interleaved, float rope_scale,
+                                 void *q_out, void *suffix_k, void *suffix_v, int32_t suffix_max, int32_t slot,
+                                 cudaStream_t stream)
+{
+    if (R < 0 || W <= 0 || suffix_max <= 0 || slot < 0 || slot >= suffix_max || step < 0) return BG_ERR_INVALID_ARG;
+    if (suffix_max > BG_MAX_SUFFIX) return BG_ERR_UNSUPPORTED;
+    if (R > 0 && (!v || !suffix_k || !suffix_v)) return BG_ERR_INVALID_ARG;
+    const int64_t row = static_cast<int64_t>(Hkv) * head_dim, rows = static_cast<int64_t>(R) * W;
+    RopeParams p{bf16_in(q), bf16_in(k), bf16_in(v), bf16_out(q_out), bf16_out(suffix_k), bf16_out(suffix_v),
+                 bf16_in(q_weight), bf16_in(k_weight), base_pos, inv_freq, q_stride, k_stride, v_stride,
+                 row * suffix_max, rows, R, W, step, Hq, Hkv, 0, 0, eps, weight_offset, rope_scale, {}};
+    return qk_rope_impl(p, head_dim, num_axes, axis_of, rot_dim, interleaved, rows * suffix_max, slot, stream);
+}
+
+bg_status_t bg_adjust_logits(const void *logits, int32_t in_dtype, int64_t in_stride, int32_t num_groups,
+                             int32_t rows_per_group, int32_t V, const int32_t *prompt_tokens, const int32_t *cu_prompt,
+                             int32_t total_prompt, const int32_t *own_tokens, const int32_t *own_lens, int32_t own_max,
+                             const float *repetition, const float *frequency, const float *presence,
+                             const int32_t *bias_tokens, const float *bias_values, const int32_t *cu_bias,
+                             int32_t total_bias, const uint32_t *mask, int64_t mask_stride, int32_t num_masks,
+                             const int32_t *mask_index, void *out, int32_t out_dtype, int64_t out_stride,
+                             int32_t *dev_status, cudaStream_t stream)
+{
+    if (num_groups < 0 || rows_per_group < 1 || total_prompt < 0 || own_max < 0 || total_bias < 0 || num_masks < 0)
+        return BG_ERR_INVALID_ARG;
+    if ((in_dtype != BG_DTYPE_F32 && in_dtype != BG_DTYPE_BF16) || (out_dtype != BG_DTYPE_F32 && out_dtype != BG_DTYPE_BF16))
+        return BG_ERR_INVALID_ARG;
+    if (V < 1 || V > BG_MAX_VOCAB || own_max > BG_MAX_SEQLEN || (in_dtype == BG_DTYPE_F32 && out_dtype == BG_DTYPE_BF16))
+        return BG_ERR_UNSUPPORTED;
+    const int64_t rows = static_cast<int64_t>(num_groups) * rows_per_group;
+    if (rows > INT32_MAX) return BG_ERR_UNSUPPORTED;
+    if (in_stride < V || out_stride < V) return BG_ERR_INVALID_ARG;
+    const int64_t words = (static_cast<int64_t>(V) + 31) / 32;
+    if (mask ? mask_stride < words : (mask_index || num_masks > 0)) return BG_ERR_INVALID_ARG;
+    if (mask && !mask_index && num_masks < rows) return BG_ERR_INVALID_ARG;
+    if (rows == 0) return BG_OK;
+    // an empty list may come without its tokens
+    const bool prompt = total_prompt > 0, own = own_max > 0, bias = total_bias > 0;
+    if (!logits || !out || (prompt && (!prompt_tokens || !cu_prompt)) || (own && !own_tokens) ||
+        (bias && (!bias_tokens || !bias_values || !cu_bias)))
+        return BG_ERR_INVALID_ARG;
+    const size_t ies = in_dtype == BG_DTYPE_F32 ? 4 : 2, oes = out_dtype == BG_DTYPE_F32 ? 4 : 2;
+    if (!aligned(logits, ies) || !aligned(out, oes)) return BG_ERR_INVALID_ARG;
+    const size_t n = static_cast<size_t>(rows), g = static_cast<size_t>(num_groups);
+    const size_t ibytes = ((n - 1) * static_cast<size_t>(in_stride) + V) * ies;
+    const size_t obytes = ((n - 1) * static_cast<size_t>(out_stride) + V) * oes;
+    const void *in[12] = {prompt_tokens, cu_prompt, own_tokens, own_lens, repetition, frequency, presence, bias_tokens,
+                          bias_values, cu_bias, mask, mask_index};
+    const size_t inb[12] = {static_cast<size_t>(total_prompt) * 4, (g + 1) * 4, n * own_max * 4, n * 4, g * 4, g * 4, g * 4,
+                            static_cast<size_t>(total_bias) * 4, static_cast<size_t>(total_bias) * 4, (g + 1) * 4,
+                            static_cast<size_t>(num_masks) * static_cast<size_t>(mask_stride) * 4, n * 4};
+    for (int i = 0; i < 12; ++i)
+        if (!aligned(in[i], 4) || overlap(out, obytes, in[i], inb[i])) return BG_ERR_INVALID_ARG;
+    if (!aligned(dev_status, 4) || overlap(out, obytes, dev_status, 4)) return BG_ERR_INVALID_ARG;
+    const bool in_place = out == logits && in_dtype == out_dtype && in_stride == out_stride;
+    if (!in_place && overlap(out, obytes, logits, ibytes)) return BG_ERR_INVALID_ARG;
+    LogitsParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.in = logits;
+    p.out = out;
+    p.prompt = prompt ? prompt_tokens : nullptr;
+    p.cu_prompt = cu_prompt;
+    p.own = own ? own_tokens : nullptr;
+    p.own_lens = own_lens;
+    p.repetition = repetition;
+    p.frequency = frequency;
+    p.presence = presence;
+    p.bias_tokens = bias ? bias_tokens : nullptr;
+    p.bias_values = bias_values;
+    p.cu_bias = cu_bias;
+    p.mask = mask;
+    p.mask_index = mask_index;
+    p.dev_status = dev_status;
+    p.in_stride = in_stride;
+    p.out_stride = out_stride;
+    p.own_stride = own_max;
+    p.mask_stride = mask_stride;
+    p.groups = num_groups;
+    p.per = rows_per_group;
+    p.V = V;
+    p.total_prompt = total_prompt;
+    p.own_max = own_max;
+    p.total_bias = total_bias;
+    p.num_masks = num_masks;
+    const int nsm = sm_count();
+    if (nsm <= 0) return BG_ERR_CUDA;
+    const bool vectors = aligned(logits, 16) && aligned(out, 16) &&
+                         (rows == 1 || (in_stride * ies % 16 == 0 && out_stride * oes % 16 == 0));
+    return launch_adjust_logits(p, in_dtype, out_dtype, vectors, nsm, stream) == cudaSuccess ? BG_OK : BG_ERR_CUDA;
 }
 
 }  // extern "C"

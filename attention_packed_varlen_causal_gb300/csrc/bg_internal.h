@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -65,6 +66,40 @@ cudaError_t launch_token_logprobs(const void *logits, int32_t dtype, int64_t row
 cudaError_t launch_logprobs_selftest(const float *logits, int32_t N, int32_t V, const int32_t *tokens, int32_t stalled,
                                      float *logprob, float *entropy, int32_t *top_token, float *top_logprob,
                                      int32_t *dev_status, int nsm, cudaStream_t stream);
+
+// Norm and rotation of Q and K (qk_rope.cu).  Strides in elements; positions [axes][places], place row / rows_per_pos.
+struct RopeParams {
+    const __nv_bfloat16 *q, *k, *v;                // v NULL: not copied
+    __nv_bfloat16 *q_out, *k_out, *v_out;
+    const __nv_bfloat16 *q_weight, *k_weight;      // NULL: no norm
+    const int32_t *positions;
+    const float *inv_freq;
+    int64_t q_stride, k_stride, v_stride, kv_out_stride;
+    int64_t rows, places;
+    int32_t rows_per_pos, step, Hq, Hkv, rot, parts;
+    float eps, weight_offset, rope_scale;
+    uint8_t axis[64];                              // of each frequency
+};
+cudaError_t launch_qk_rope(RopeParams p, int head_dim, bool interleaved, int nsm, cudaStream_t stream);
+
+// Penalties, biases and masks on logits (logits.cu).  Strides in elements (mask: words); row = group * per + r.
+struct LogitsParams {
+    const void *in;
+    void *out;
+    const int32_t *prompt, *cu_prompt;             // prompt tokens of the groups, or NULL
+    const int32_t *own, *own_lens;                 // [rows][own_stride], or NULL
+    const float *repetition, *frequency, *presence;      // [groups], each may be NULL
+    const int32_t *bias_tokens, *cu_bias;          // or NULL
+    const float *bias_values;
+    const uint32_t *mask;                          // [num_masks][mask_stride], or NULL
+    const int32_t *mask_index;                     // [rows], or NULL: row i has mask i
+    int32_t *dev_status;
+    int64_t in_stride, out_stride, own_stride, mask_stride;
+    int32_t groups, per, V, total_prompt, own_max, total_bias, num_masks;
+};
+// vectors: rows of `in` and `out` are 16-byte aligned.
+cudaError_t launch_adjust_logits(const LogitsParams &p, int in_dtype, int out_dtype, bool vectors, int nsm,
+                                 cudaStream_t stream);
 
 cudaError_t launch_suffix_reorder(const void *src_k, const void *src_v, void *dst_k, void *dst_v,
                                   const int32_t *parent_idx, const void *new_k, const void *new_v, int32_t R,

@@ -117,11 +117,12 @@ __global__ void __launch_bounds__(kPlanThreads)
     __syncthreads();
     if (tid < 12) hdr[kShHdrKey + tid] = key.w[tid];
     const int32_t *cu = pb.cu_seqlens, *cup = pb.cu_prefix, *cug = pb.cu_group;
+    auto group = [&](int r) { return cug ? cug[r] : r; };      // a tree: request r is sample r
     if (pb.num_seqs <= kPlanSeqs && pb.num_groups <= kPlanGroups) {
         for (int i = tid; i <= pb.num_seqs; i += kPlanThreads) s_cu[i] = cu[i];
         for (int i = tid; i <= pb.num_groups; i += kPlanThreads) {
             s_cup[i] = cup[i];
-            s_cug[i] = cug[i];
+            s_cug[i] = group(i);
         }
         cu = s_cu;
         cup = s_cup;
@@ -132,7 +133,7 @@ __global__ void __launch_bounds__(kPlanThreads)
     // ---- the offsets, before anything is read through them
     int err = 0;
     for (int i = tid; i < pb.num_groups; i += kPlanThreads) {
-        const int a = cug[i], b = cug[i + 1];
+        const int a = group(i), b = group(i + 1);
         if (a < 0 || b < a || b > pb.num_seqs || (i == 0 && a != 0) || (i == pb.num_groups - 1 && b != pb.num_seqs))
             err |= BG_DEVSTAT_GROUP;
         const int c = cup[i], d = cup[i + 1];
@@ -169,7 +170,7 @@ __global__ void __launch_bounds__(kPlanThreads)
         const int r = r0 + tid;
         int items = 0;
         if (r < pb.num_groups) {
-            const int a = cug[r], b = cug[r + 1];
+            const int a = group(r), b = group(r + 1);
             const int rows = pb.last ? b - a : cu[b] - cu[a];
             items = static_cast<int>(ceil_div(rows, per));
             // paired heads: an entry of one query tile serves both heads, the others come once for each
@@ -188,7 +189,7 @@ __global__ void __launch_bounds__(kPlanThreads)
                     if (s_base[mid] <= e) t = mid; else end = mid;
                 }
                 const int grp = r0 + t, first = ((e - s_base[t]) >> (heads - 1)) * per;
-                const int sa = cug[grp], sb = cug[grp + 1];
+                const int sa = group(grp), sb = group(grp + 1);
                 E.prow0 = cup[grp];
                 E.plen = cup[grp + 1] - E.prow0;
                 const int base = pb.last ? sa : cu[sa];
@@ -357,6 +358,44 @@ __global__ void __launch_bounds__(kPlanThreads)
         hdr[kShHdrSplits] = s_nsplit;
         hdr[kShHdrEntries] = n_entries;
         hdr[kShHdrItems] = 0;
+    }
+}
+
+// ------------------------------------------------------------------------------------ trees
+// The mask of each node of a request: its own bit and its ancestors'.  One CTA per request, a thread per node, which
+// follows the parents through shared memory; they have falling numbers, so that the words come one after the other.
+constexpr int kTreeThreads = 128;
+
+__global__ void __launch_bounds__(kTreeThreads) tree_mask_kernel(const ShProblem pb, uint32_t *masks, int32_t *dev_status)
+{
+    __shared__ int16_t s_parent[BG_MAX_TREE];
+    grid_dep_launch();
+    grid_dep_wait();
+    const int a = pb.cu_seqlens[blockIdx.x], b = pb.cu_seqlens[blockIdx.x + 1], n = b - a;
+    if (a < 0 || b < a || b > pb.total_tokens || n > pb.max_seqlen) return;      // the plan reports it
+    bool bad = false;
+    for (int i = threadIdx.x; i < n; i += kTreeThreads) {
+        int up = pb.parent[a + i];
+        if (up < -1 || up >= i) {
+            bad = true;
+            up = -1;
+        }
+        s_parent[i] = static_cast<int16_t>(up);
+    }
+    if (bad && dev_status) atomicOr(dev_status, BG_DEVSTAT_PARENT);
+    __syncthreads();
+    const int words = tree_words(pb.max_seqlen);
+    for (int i = threadIdx.x; i < n; i += kTreeThreads) {
+        uint32_t *out = masks + static_cast<int64_t>(a + i) * words;
+        int at = i;
+        for (int w = words - 1; w >= 0; --w) {
+            uint32_t bits = 0;
+            while (at >= 32 * w) {
+                bits |= 1u << (at - 32 * w);
+                at = s_parent[at];
+            }
+            out[w] = bits;
+        }
     }
 }
 
@@ -641,7 +680,7 @@ constexpr float kShNoWeight = -3.402823466e38f;
 // Two query tiles overlap their chains; tensor memory (S and O of each) has no room for a third at D = 128.
 // 128-key tiles against 64: half the hand-overs.  Items of few tiles add the start and the end of an item,
 // where nothing overlaps: about 4 us of 12 for five key tiles.
-template <int D, int MODE, bool LAST>
+template <int D, int MODE, bool LAST, bool TREE>
 __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
     shared_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_pk,
@@ -1174,6 +1213,9 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
                         lo = p.cu_seqlens[row];
                         hi = p.cu_seqlens[row + 1];
                     }
+                } else if constexpr (TREE) {
+                    lo = I.ka0;                // of these, the node's mask keeps its ancestors and itself
+                    hi = live ? row + 1 : lo;
                 } else {
                     // the last sample start that is not behind the row; 32 sample starts at a time
                     const int last_row = I.row0 + I.nrows - 1;
@@ -1198,6 +1240,7 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
             for (int j = tb; j < te; ++j) {
                 int nk = kShKeys, c0 = 0, c1 = kShKeys;    // keys of the tile; this row's columns [c0, c1)
                 bool some = warp_live, masked = false, zero_v = false;
+                uint4 path = make_uint4(~0u, ~0u, ~0u, ~0u);       // tree: the nodes of the tile that this row sees
                 if (j >= whole_end) {
                     nk = I.keys_of(h, j);
                     if (nk <= 0) continue;
@@ -1205,14 +1248,20 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
                         const int base = I.own_base(j);
                         c0 = min(max(lo - base, 0), kShKeys);
                         c1 = min(max(hi - base, 0), nk);
+                        if constexpr (TREE) {
+                            path = make_uint4(0u, 0u, 0u, 0u);
+                            if (live)
+                                path = *reinterpret_cast<const uint4 *>(p.tree + static_cast<int64_t>(row) * p.tree_words +
+                                                                        (kShKeys / 32) * (j - npt));
+                        }
                     } else {
                         c1 = nk;
                     }
                     some = __any_sync(0xffffffffu, live && c1 > c0);
-                    masked = __any_sync(0xffffffffu, live && (c0 > 0 || c1 < kShKeys));
+                    masked = (TREE && j >= npt) || __any_sync(0xffffffffu, live && (c0 > 0 || c1 < kShKeys));
                     zero_v = ((nk + 15) & ~15) > I.keys(j);
                 }
-                seen = seen || c1 > c0;
+                seen = seen || (TREE ? c1 > c0 && (path.x | path.y | path.z | path.w) != 0 : c1 > c0);
                 if (!sh_warp_wait(&s_full[h], tiles & 1, abort_flag)) { ok = false; break; }
                 tc_fence_after();
                 // Keys behind the last one that any row of the item sees (a later token, another
@@ -1253,7 +1302,9 @@ __global__ void __maxnreg__((ShCfg<D>::kRegsLaunch))
                     auto columns = [&](int c) {
                         const int a = min(max(c0 - 32 * c, 0), 32), b = min(max(c1 - 32 * c, 0), 32);
                         const uint32_t below_b = b == 32 ? ~0u : (1u << b) - 1u;
-                        return a == 32 ? 0u : below_b & ~((1u << a) - 1u);
+                        const uint32_t in = a == 32 ? 0u : below_b & ~((1u << a) - 1u);
+                        if constexpr (TREE) return in & (c < 2 ? (c == 0 ? path.x : path.y) : (c == 2 ? path.z : path.w));
+                        return in;
                     };
                     if constexpr (MODE == kShCappedFixed) {
                         float2 rs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -1575,13 +1626,13 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const ShParam
     if (p.lse && sub == 0) p.lse[orow] = (mx + __log2f(sum)) * 0.69314718055994530942f;
 }
 
-template <int D, int MODE, bool LAST>
+template <int D, int MODE, bool LAST, bool TREE>
 cudaError_t launch_one(const CUtensorMap &tm_q, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
                        const CUtensorMap &tm_pk, const CUtensorMap &tm_pv, const ShParams &p, int grid, int join,
                        cudaStream_t stream)
 {
     using C = ShCfg<D>;
-    auto kern = shared_attn_kernel<D, MODE, LAST>;
+    auto kern = shared_attn_kernel<D, MODE, LAST, TREE>;
     static std::atomic<uint64_t> smem_done{0}, split_done{0};
     cudaError_t e = ensure_smem_attribute(kern, C::kSmemBytes, smem_done);
     if (e != cudaSuccess) return e;
@@ -1650,13 +1701,21 @@ ShLayout shared_layout(const ShProblem &pb)
     L.splits = L.starts + al((kShMaxCtas + 1) * sizeof(ShStart));
     L.part_l = L.splits + al(kShMaxCtas * sizeof(ShSplit));
     L.part_o = L.part_l + al(static_cast<size_t>(L.slots) * kShTiles * kShRows * 2 * sizeof(float));
-    L.total = L.part_o + al(static_cast<size_t>(L.slots) * kShTiles * kShRows * pb.head_dim * sizeof(float));
+    L.tree = L.part_o + al(static_cast<size_t>(L.slots) * kShTiles * kShRows * pb.head_dim * sizeof(float));
+    L.total = L.tree + (pb.tree ? al(static_cast<size_t>(pb.total_tokens) * tree_words(pb.max_seqlen) * 4) : 0);
     return L;
+}
+
+cudaError_t launch_tree_masks(const ShProblem &pb, const ShLayout &lay, void *workspace, int32_t *dev_status,
+                              cudaStream_t stream)
+{
+    return launch_dependent(tree_mask_kernel, dim3(pb.num_groups), dim3(kTreeThreads), 0, stream, pb,
+                            reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(workspace) + lay.tree), dev_status);
 }
 
 ShKey shared_key(const ShProblem &pb, int grid)
 {
-    return ShKey{{pb.last, pb.num_seqs, pb.total_tokens, pb.max_seqlen, pb.num_groups, pb.total_prefix,
+    return ShKey{{pb.tree ? 2 : pb.last, pb.num_seqs, pb.total_tokens, pb.max_seqlen, pb.num_groups, pb.total_prefix,
                   pb.max_prefix_len, pb.Hq, pb.Hkv, pb.head_dim, grid, 0x5348}};
 }
 
@@ -1679,8 +1738,9 @@ cudaError_t launch_shared_attn(int head_dim, bool is_capped, const CUtensorMap &
     const int mode = !is_capped ? kShPlain : p.cap_log2 <= kShCapFixed ? kShCappedFixed : kShCapped;
 #define BG_SHARED(DD, MM)                                                                                   \
     if (head_dim == DD && mode == MM)                                                                       \
-        return p.last ? launch_one<DD, MM, true>(tm_q, tm_k, tm_v, tm_pk, tm_pv, p, grid, join, stream)      \
-                      : launch_one<DD, MM, false>(tm_q, tm_k, tm_v, tm_pk, tm_pv, p, grid, join, stream)
+        return p.tree   ? launch_one<DD, MM, false, true>(tm_q, tm_k, tm_v, tm_pk, tm_pv, p, grid, join, stream)  \
+               : p.last ? launch_one<DD, MM, true, false>(tm_q, tm_k, tm_v, tm_pk, tm_pv, p, grid, join, stream)  \
+                        : launch_one<DD, MM, false, false>(tm_q, tm_k, tm_v, tm_pk, tm_pv, p, grid, join, stream)
     BG_SHARED(128, kShPlain);
     BG_SHARED(128, kShCapped);
     BG_SHARED(128, kShCappedFixed);

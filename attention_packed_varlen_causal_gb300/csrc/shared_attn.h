@@ -62,7 +62,7 @@ struct __align__(16) ShKey {
 
 // Workspace layout (byte offsets); every part is 256-byte aligned.
 struct ShLayout {
-    size_t entries, sorted, starts, splits, part_l, part_o, total;
+    size_t entries, sorted, starts, splits, part_l, part_o, tree, total;
     int64_t max_entries;
     int64_t items, units;     // items and cost units of the work at most, by single heads
     int64_t slots;            // partial results (two per CTA), or 0: no item can be split
@@ -76,7 +76,12 @@ struct ShProblem {
     int32_t num_groups, total_prefix, max_prefix_len;
     int32_t Hq, Hkv, head_dim;
     int32_t last;             // 1: one query row per sample, 0: one per token
+    int32_t tree;             // 1: a request's nodes are its one sample (cu_group NULL), and each sees its ancestors
+    const int32_t *parent;
 };
+
+// Words of a node's mask over the nodes of its request: whole key tiles.
+__host__ __device__ inline int32_t tree_words(int32_t max_nodes) { return (max_nodes + kShKeys - 1) / kShKeys * (kShKeys / 32); }
 
 // kv heads that the work line takes at once: 2 pairs them.  In the last-token call a request has a row per
 // sample, often not enough for two query tiles; then two kv heads fill both, and the softmax of one runs
@@ -103,6 +108,8 @@ struct ShParams {
     int32_t *dev_status;
     ShKey key;
     const int32_t *cu_seqlens;
+    const uint32_t *tree;     // masks [node][tree_words], or NULL
+    int32_t tree_words;
     int32_t *hdr;
     const ShEntry *entries;
     const ShEntry *sorted;    // the same in falling order of tiles, where more items than CTAs are dealt out
@@ -117,6 +124,9 @@ enum : int { kShJoinNone = 0, kShJoinFew = 1, kShJoinMany = 2 };
 
 cudaError_t launch_shared_plan(const ShProblem &pb, const ShLayout &lay, void *workspace, int grid,
                                int32_t *dev_status, cudaStream_t stream);
+// The masks of a tree's nodes, into the workspace.
+cudaError_t launch_tree_masks(const ShProblem &pb, const ShLayout &lay, void *workspace, int32_t *dev_status,
+                              cudaStream_t stream);
 cudaError_t launch_shared_attn(int head_dim, bool capped, const CUtensorMap &tm_q, const CUtensorMap &tm_k,
                                const CUtensorMap &tm_v, const CUtensorMap &tm_pk, const CUtensorMap &tm_pv,
                                const ShParams &p, int grid, int join, cudaStream_t stream);

@@ -63,6 +63,8 @@ typedef enum {
 #define BG_DEVSTAT_GROUP        0x40  /* cu_group[0]!=0, decreasing, or cu_group[R]!=num_seqs */
 #define BG_DEVSTAT_TOKEN        0x80  /* a given token is outside [0, V)            */
 #define BG_DEVSTAT_TIMEOUT      0x100 /* an internal pipeline wait ran out          */
+#define BG_DEVSTAT_BIAS         0x200 /* cu_bias invalid or a list > BG_MAX_BIAS    */
+#define BG_DEVSTAT_MASK         0x400 /* a mask index is outside [-1, num_masks)    */
 
 /* Supported shapes: head_dim in {64, 128}; Hq % Hkv == 0; for decode
  * Hq/Hkv <= 128; suffix_max <= BG_MAX_SUFFIX; max_seqlen <= BG_MAX_SEQLEN. */
@@ -76,6 +78,12 @@ typedef enum {
 #define BG_MAX_TOP 32
 #define BG_DTYPE_F32 0
 #define BG_DTYPE_BF16 1
+/* Axes of the positions of bg_packed_qk_norm_rope and bg_beam_qk_norm_rope. */
+#define BG_MAX_AXES 4
+/* Biased tokens per group of bg_adjust_logits. */
+#define BG_MAX_BIAS 8191
+/* Nodes of a request's tree in bg_tree_attn. */
+#define BG_MAX_TREE 1024
 
 /* Human-readable name of a status code (static storage, never NULL). */
 const char *bg_status_string(bg_status_t status);
@@ -516,6 +524,178 @@ bg_status_t bg_shared_last_token_attn_planned(const void *q, const void *k, cons
                        int32_t num_groups, int32_t Hq, int32_t Hkv, int32_t head_dim, float scale,
                        float softcap, void *out, float *lse, void *workspace,
                        size_t workspace_bytes, int32_t *dev_status, cudaStream_t stream);
+
+/*
+ * Attention of a tree of drafted tokens over the request's one prefix (its
+ * cached K/V) and each token's own ancestors.  Source: section 1.2 of the page
+ * above (what sequences of a request share is kept once); a request whose next
+ * tokens are drafted in several branches and verified in one pass is a tree of
+ * samples that share more than the prefix.  Request r has prefix rows
+ * cu_prefix[r] .. cu_prefix[r+1]-1 and the nodes cu_nodes[r] .. cu_nodes[r+1]-1;
+ * node i of a request (counted from 0) has the parent parent[cu_nodes[r] + i],
+ * a lower number of the same request, or -1 where it follows the prefix.  With
+ * the softmax over
+ *     keys = [all prefix rows of r ; the node's ancestors and the node itself]
+ * and scores as for bg_shared_prefill_attn (softcap included), out is
+ * sum_j softmax_j(x) value_j.  A tree that is one chain is bg_shared_prefill_attn
+ * with one sample per request.
+ *
+ *   q            bf16 [total_nodes, Hq, head_dim]
+ *   k, v         bf16 [total_nodes, Hkv, head_dim]
+ *   parent       int32 [total_nodes], device.  A parent that is neither -1 nor a
+ *                lower number counts as -1 and raises BG_DEVSTAT_PARENT.
+ *   cu_nodes     int32 [num_requests+1], device; cu[0]=0, non-decreasing,
+ *                cu[num_requests]=total_nodes; requests without nodes are allowed
+ *   max_nodes    host upper bound of a request's nodes, at most BG_MAX_TREE
+ *                (checked on device)
+ *   prefix_k, prefix_v, cu_prefix, total_prefix, max_prefix_len, scale, softcap,
+ *   out, lse, dev_status   as in bg_shared_prefill_attn
+ *   workspace    at least bg_tree_attn_workspace_size(...) bytes, 256-byte
+ *                aligned; contents on entry do not matter; not for calls that
+ *                overlap in time
+ * Layers that share one packing and one tree plan once: bg_tree_plan, then
+ * bg_tree_attn_planned per layer with the same offsets, parents and sizes, under
+ * the rules of bg_shared_prefill_plan (the parents are read by the plan alone).
+ * Bad offsets raise BG_DEVSTAT_CU_SEQLENS, _SEQ_TOO_LONG or _CU_PROMPT, and
+ * nothing is written.  Non-finite K or V rows reach only queries of the same
+ * request; a non-finite V row of a node may reach nodes that do not descend from it.
+ * Errors: as bg_shared_prefill_attn; BG_ERR_UNSUPPORTED also for max_nodes >
+ * BG_MAX_TREE.  bg_tree_attn_workspace_size gives 0 for sizes that the call
+ * refuses.
+ */
+size_t bg_tree_attn_workspace_size(int32_t num_requests, int32_t total_nodes, int32_t max_nodes,
+                                   int32_t max_prefix_len, int32_t Hq, int32_t Hkv, int32_t head_dim);
+bg_status_t bg_tree_attn(const void *q, const void *k, const void *v, const int32_t *parent,
+                         const int32_t *cu_nodes, int32_t num_requests, int32_t total_nodes, int32_t max_nodes,
+                         const void *prefix_k, const void *prefix_v, const int32_t *cu_prefix, int32_t total_prefix,
+                         int32_t max_prefix_len, int32_t Hq, int32_t Hkv, int32_t head_dim, float scale,
+                         float softcap, void *out, float *lse, void *workspace, size_t workspace_bytes,
+                         int32_t *dev_status, cudaStream_t stream);
+bg_status_t bg_tree_plan(const int32_t *parent, const int32_t *cu_nodes, int32_t num_requests, int32_t total_nodes,
+                         int32_t max_nodes, const int32_t *cu_prefix, int32_t total_prefix, int32_t max_prefix_len,
+                         int32_t Hq, int32_t Hkv, int32_t head_dim, void *workspace, size_t workspace_bytes,
+                         int32_t *dev_status, cudaStream_t stream);
+bg_status_t bg_tree_attn_planned(const void *q, const void *k, const void *v, const int32_t *parent,
+                         const int32_t *cu_nodes, int32_t num_requests, int32_t total_nodes, int32_t max_nodes,
+                         const void *prefix_k, const void *prefix_v, const int32_t *cu_prefix, int32_t total_prefix,
+                         int32_t max_prefix_len, int32_t Hq, int32_t Hkv, int32_t head_dim, float scale,
+                         float softcap, void *out, float *lse, void *workspace, size_t workspace_bytes,
+                         int32_t *dev_status, cudaStream_t stream);
+
+/*
+ * Norm of every head of Q and K and the rotation by the token's position, out of
+ * the fused projection's rows into the packed tensors that the attention calls
+ * read.  Source: section 1.2 of the page above (packed tokens; the attention's
+ * K arrives rotated).  For a head x of head_dim elements of a token at positions
+ * pos[0 .. num_axes-1], in fp32 and rounded to bf16 once:
+ *     y     = x / sqrt(mean(x^2) + eps) * (weight_offset + w)    (y = x without weights)
+ *     angle = pos[axis_of[i]] * inv_freq[i],   c = rope_scale cos(angle),
+ *     s     = rope_scale sin(angle)            for i < rot_dim / 2
+ *     (out_a, out_b) = (y_a c - y_b s, y_b c + y_a s)
+ * over the pairs (a, b) = (i, i + rot_dim / 2), or (2 i, 2 i + 1) if interleaved;
+ * out = y from rot_dim on.  V is copied.  Angles are off by about 2^-20 for positions
+ * up to 2^24 and 2^-17 for any other (with frequencies of at most 1).
+ *   bg_packed_qk_norm_rope   any packed tokens, each with its positions
+ *   bg_beam_qk_norm_rope     the new token of every beam of a search: beam b of
+ *                            request r is at base_pos[., r] + step, and its K and V
+ *                            go to slot `slot` of its suffix (with suffix_max = 1
+ *                            and slot = 0 the new_k and new_v of bg_beam_decode_step)
+ *
+ *   q, k, v      bf16, row i at q + i * q_stride elements (k_stride, v_stride): Hq,
+ *                Hkv and Hkv heads side by side; strides are multiples of 8 and at
+ *                least a row.  v may be NULL with v_out (packed form).
+ *   q_weight, k_weight   bf16 [head_dim], or both NULL: no norm
+ *   eps          finite, >= 0;  weight_offset 0 or, for weights stored as their
+ *                difference from 1, 1 (finite)
+ *   positions    int32 [num_axes, total_tokens], device (base_pos: [num_axes, R])
+ *   axis_of      HOST int32 [rot_dim / 2]: the axis of each frequency, in
+ *                [0, num_axes); may be NULL if num_axes == 1
+ *   inv_freq     fp32 [rot_dim / 2], device, finite;  rope_scale finite
+ *   rot_dim      a multiple of 16, 16 .. head_dim
+ *   q_out        bf16 [total_tokens, Hq, head_dim] ([R, W, Hq, head_dim])
+ *   k_out, v_out bf16 [total_tokens, Hkv, head_dim]
+ *   suffix_k, suffix_v  bf16 [R, W, suffix_max, Hkv, head_dim]; the other slots
+ *                stay as they are
+ *   step         0 or more: tokens between base_pos and this one
+ * An output may be its own input (q_out == q with q_stride == Hq * head_dim, and so
+ * for K and V); outputs may not overlap anything else.
+ * One launch, no workspace.
+ * Errors: BG_ERR_INVALID_ARG for NULL or misaligned (16 bytes) pointers, bad sizes,
+ * strides, scalars or axes, Hq % Hkv != 0, one weight or one of v and v_out without the
+ * other, or overlaps; BG_ERR_UNSUPPORTED for head_dim not in {64, 128}, num_axes >
+ * BG_MAX_AXES, rot_dim not a multiple of 16 or > head_dim, or suffix_max >
+ * BG_MAX_SUFFIX.  No rows is a valid no-op.
+ */
+bg_status_t bg_packed_qk_norm_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                         int64_t v_stride, int32_t total_tokens, int32_t Hq, int32_t Hkv, int32_t head_dim,
+                         const void *q_weight, const void *k_weight, float eps, float weight_offset,
+                         const int32_t *positions, int32_t num_axes, const int32_t *axis_of,
+                         const float *inv_freq, int32_t rot_dim, int32_t interleaved, float rope_scale,
+                         void *q_out, void *k_out, void *v_out, cudaStream_t stream);
+bg_status_t bg_beam_qk_norm_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                         int64_t v_stride, int32_t R, int32_t W, int32_t Hq, int32_t Hkv, int32_t head_dim,
+                         const void *q_weight, const void *k_weight, float eps, float weight_offset,
+                         const int32_t *base_pos, int32_t num_axes, const int32_t *axis_of, int32_t step,
+                         const float *inv_freq, int32_t rot_dim, int32_t interleaved, float rope_scale,
+                         void *q_out, void *suffix_k, void *suffix_v, int32_t suffix_max, int32_t slot,
+                         cudaStream_t stream);
+
+/*
+ * Penalties for repeated tokens, biases and grammar masks on rows of logits,
+ * ahead of bg_beam_select or bg_token_logprobs.  Source: section 1.1 of the page
+ * above (the next-token logits are what a step's candidates are selected from).
+ * Rows g * rows_per_group .. (g+1) * rows_per_group - 1 are those of group g (the
+ * beams or samples of a request).  For row i of group g and token v, with p(v)
+ * whether v is in the group's prompt and c(v) how often it is among the row's own
+ * tokens, in this order, in fp32, rounded once where the output is bf16:
+ *     y = x > 0 ? x / repetition[g] : x * repetition[g]     if p(v) or c(v) > 0
+ *     y = y - (frequency[g] * c(v) + presence[g])           if c(v) > 0
+ *     y = y + bias                                          if v is in the group's biases
+ *     y = -inf                                              if the row's mask lacks bit v
+ * A token listed twice in a group's biases has its last value.  A masked logit is
+ * -inf whatever it was (NaN and +inf too); a row whose mask is empty is -inf
+ * throughout.
+ *
+ *   logits       fp32 or bf16 (in_dtype), row i at logits + i * in_stride
+ *                elements, in_stride >= V
+ *   prompt_tokens int32 [total_prompt], those of group g at cu_prompt[g] ..
+ *                cu_prompt[g+1]-1 (int32 [num_groups+1], device), or NULL with
+ *                total_prompt == 0
+ *   own_tokens   int32 [rows, own_max], of which row i has own_lens[i] (int32, device;
+ *                NULL: own_max); NULL with own_max == 0.  own_max <= BG_MAX_SEQLEN
+ *   repetition, frequency, presence   fp32 [num_groups], device, each may be NULL
+ *                (1, 0, 0); repetition is > 0
+ *   bias_tokens, bias_values   int32 and fp32 [total_bias], those of group g at
+ *                cu_bias[g] .. cu_bias[g+1]-1 (int32 [num_groups+1], device), at most
+ *                BG_MAX_BIAS; NULL with total_bias == 0
+ *   mask         uint32 [num_masks, mask_stride], device: bit v % 32 of word v / 32
+ *                of a mask is 1 where token v is allowed (bits from V on do not
+ *                matter), mask_stride >= ceil(V / 32); NULL: every token is allowed
+ *   mask_index   int32 [rows], device: the mask of each row, -1 for none; NULL: row
+ *                i has mask i
+ *   out          fp32 or bf16 (out_dtype), row i at out + i * out_stride, out_stride
+ *                >= V; bf16 only from bf16.  May be the logits themselves (same
+ *                type and stride); elements between rows are left alone.
+ *   dev_status   device int32 or NULL
+ * A listed token outside [0, V) is ignored and raises BG_DEVSTAT_TOKEN.  A group
+ * whose offsets are bad (BG_DEVSTAT_CU_PROMPT, _BIAS) and a row whose length or mask
+ * index is (BG_DEVSTAT_SEQ_TOO_LONG, _MASK) are not written.
+ * One launch, no workspace.  Logits next to which every logit of the same 16 bytes is
+ * masked are not read.
+ * Errors: BG_ERR_INVALID_ARG for negative sizes, unknown types, NULL or misaligned
+ * pointers, strides below V (mask_stride below its words), num_masks < rows without
+ * mask_index, or out overlapping another argument; BG_ERR_UNSUPPORTED unless 1 <= V
+ * <= BG_MAX_VOCAB, for own_max > BG_MAX_SEQLEN, bf16 output of fp32 logits, or 2^31 rows
+ * and more.  No rows is a valid no-op.
+ */
+bg_status_t bg_adjust_logits(const void *logits, int32_t in_dtype, int64_t in_stride, int32_t num_groups,
+                         int32_t rows_per_group, int32_t V, const int32_t *prompt_tokens, const int32_t *cu_prompt,
+                         int32_t total_prompt, const int32_t *own_tokens, const int32_t *own_lens, int32_t own_max,
+                         const float *repetition, const float *frequency, const float *presence,
+                         const int32_t *bias_tokens, const float *bias_values, const int32_t *cu_bias,
+                         int32_t total_bias, const uint32_t *mask, int64_t mask_stride, int32_t num_masks,
+                         const int32_t *mask_index, void *out, int32_t out_dtype, int64_t out_stride,
+                         int32_t *dev_status, cudaStream_t stream);
 
 /*
  * Log-probability of a given token, entropy and the best alternatives of rows
