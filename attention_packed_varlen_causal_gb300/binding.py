@@ -12,6 +12,7 @@ ctypes functions themselves for callers that manage pointers directly.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from typing import Optional
@@ -667,31 +668,40 @@ def _rows_of_heads(fn: str, name: str, t, lead, index: int):
     return row if rows > 1 else (shape[-2] * shape[-1] + 7) // 8 * 8
 
 
-def _qk_norm_rope(fn: str, q, k, v, positions, place_shape, outs, lead, q_weight, k_weight, inv_freq, axis_of):
-    """Checks of both forms; returns the row strides, the number of axes and axis_of as a ctypes array."""
+@functools.lru_cache(maxsize=64)
+def _axes(axis_of):
+    return (_I32 * len(axis_of))(*axis_of)
+
+
+def _qk_norm_rope(fn: str, q, k, v, positions, place_shape, outs, lead, q_weight, k_weight, inv_freq):
+    """Checks of both forms, with the messages; returns the row strides of q, k and v."""
     import torch
     bf16, f32, i32 = torch.bfloat16, torch.float32, torch.int32
     index = q.get_device()
-    Hq, d = q.shape[-2:]
-    axes = 1 if positions.dim() == len(place_shape) else positions.shape[0]
+    d = q.shape[-1]
     if k.shape[:lead] != q.shape[:lead] or k.shape[-1] != d or (v is not None and v.shape != k.shape):
         raise ValueError(f"{fn}: q, k and v must have the same rows and head_dim, got {tuple(q.shape)}, {tuple(k.shape)}, "
                          f"{None if v is None else tuple(v.shape)}")
-    if not (_alike(bf16, index, (q_weight, k_weight) + tuple(t for _, t, _ in outs)) and _alike(i32, index, (positions,)) and
-            _alike(f32, index, (inv_freq,)) and positions.shape[-len(place_shape):] == place_shape and
-            positions.dim() <= len(place_shape) + 1 and inv_freq.dim() == 1 and
-            (q_weight is None or q_weight.shape == (d,)) and (k_weight is None or k_weight.shape == (d,)) and
-            all(t is None or t.shape == s for _, t, s in outs)):
-        _expect(fn, q.device, [("positions", positions, i32, (axes,) + place_shape if positions.dim() > 1 else place_shape),
-                               ("inv_freq", inv_freq, f32, (inv_freq.numel(),)), ("q_weight", q_weight, bf16, (d,)),
-                               ("k_weight", k_weight, bf16, (d,))] + [(n, t, bf16, s) for n, t, s in outs])
-    strides = tuple(0 if t is None else _rows_of_heads(fn, n, t, lead, index) for n, t in (("q", q), ("k", k), ("v", v)))
-    n_freq = inv_freq.shape[0]
+    lead_axes = tuple(positions.shape[:1]) if positions.dim() > len(place_shape) else ()
+    _expect(fn, q.device, [("positions", positions, i32, lead_axes + place_shape),
+                           ("inv_freq", inv_freq, f32, (inv_freq.numel(),)), ("q_weight", q_weight, bf16, (d,)),
+                           ("k_weight", k_weight, bf16, (d,))] + [(n, t, bf16, s) for n, t, s in outs])
+    return tuple(0 if t is None else _rows_of_heads(fn, n, t, lead, index) for n, t in (("q", q), ("k", k), ("v", v)))
+
+
+def _rope_common(fn: str, d: int, index: int, positions, places: int, q_weight, k_weight, inv_freq, axis_of):
+    """Quick checks of what both forms share, (whether they pass, axes, axis_of as an array, rotated dimensions)."""
+    import torch
+    f32 = torch.float32
+    ps, n = positions.shape, inv_freq.shape[0]
+    ok = (0 < len(ps) <= 2 and ps[-1] == places and positions.dtype is torch.int32 and positions.get_device() == index and
+          positions.is_contiguous() and inv_freq.dtype is f32 and inv_freq.get_device() == index and inv_freq.is_contiguous() and
+          inv_freq.dim() == 1 and (q_weight is None or q_weight.shape == (d,)) and (k_weight is None or k_weight.shape == (d,)))
     if axis_of is not None:
-        if len(axis_of) != n_freq:
-            raise ValueError(f"{fn}: axis_of must have an axis for each of the {n_freq} frequencies, got {len(axis_of)}")
-        axis_of = (_I32 * n_freq)(*axis_of)
-    return strides, axes, axis_of, 2 * n_freq
+        if len(axis_of) != n:
+            raise ValueError(f"{fn}: axis_of must have an axis for each of the {n} frequencies, got {len(axis_of)}")
+        axis_of = _axes(tuple(axis_of))
+    return ok, ps[0] if len(ps) == 2 else 1, axis_of, 2 * n
 
 
 def bg_packed_qk_norm_rope(q, k, v, positions, q_out, k_out, v_out=None, *, inv_freq, q_weight=None, k_weight=None,
@@ -701,15 +711,28 @@ def bg_packed_qk_norm_rope(q, k, v, positions, q_out, k_out, v_out=None, *, inv_
     are) with q_weight/k_weight bf16 [d] (None: no norm), then the rotation of the first 2 * len(inv_freq) dimensions
     by positions int32 [T] or [axes,T] times inv_freq fp32; axis_of: the axis of each frequency (a list).
     q_out [T,Hq,d], k_out and v_out [T,Hkv,d] contiguous (written); v [T,Hkv,d] is copied to v_out, or both are None."""
+    import torch
     fn = "bg_packed_qk_norm_rope"
-    T, Hq, d = q.shape
-    Hkv = k.shape[1]
-    if not _fits(T, Hq, Hkv, d):
+    qs, ks = q.shape, k.shape
+    T, Hq, d = qs
+    Hkv = ks[1]
+    index = q.get_device()
+    ok, axes, axis_of, rot = _rope_common(fn, d, index, positions, T, q_weight, k_weight, inv_freq, axis_of)
+    bf16 = torch.bfloat16
+    a, b = q.stride(), k.stride()
+    c = b if v is None else v.stride()
+    # as the calls usually are: rows of heads, d apart, of more than one token
+    if not (ok and T > 1 and a[2] == b[2] == c[2] == 1 and a[1] == b[1] == c[1] == d and ks == (T, Hkv, d) and
+            q.dtype is bf16 and k.dtype is bf16 and k.get_device() == index and
+            (v is None or (v.shape == ks and v.dtype is bf16 and v.get_device() == index)) and
+            _alike(bf16, index, (q_out, k_out, v_out, q_weight, k_weight)) and q_out.shape == qs and k_out.shape == ks and
+            (v_out is None or v_out.shape == ks)):
+        a, b, c = ((n,) for n in _qk_norm_rope(fn, q, k, v, positions, (T,), (
+            ("q_out", q_out, (T, Hq, d)), ("k_out", k_out, (T, Hkv, d)), ("v_out", v_out, (T, Hkv, d))), 1, q_weight,
+            k_weight, inv_freq))
+    if T > 0x7fffffff or Hq > 0x7fffffff or Hkv > 0x7fffffff:
         raise BgError(fn, BG_ERR_UNSUPPORTED)
-    (qs, ks, vs), axes, axis_of, rot = _qk_norm_rope(
-        fn, q, k, v, positions, (T,), (("q_out", q_out, (T, Hq, d)), ("k_out", k_out, (T, Hkv, d)),
-                                       ("v_out", v_out, (T, Hkv, d))), 1, q_weight, k_weight, inv_freq, axis_of)
-    _launch(fn, q.get_device(), stream, q.data_ptr(), qs, k.data_ptr(), ks, _ptr(v), vs, T, Hq, Hkv, d, _ptr(q_weight),
+    _launch(fn, index, stream, q.data_ptr(), a[0], k.data_ptr(), b[0], _ptr(v), c[0], T, Hq, Hkv, d, _ptr(q_weight),
             _ptr(k_weight), float(eps), float(weight_offset), positions.data_ptr(), axes, axis_of, inv_freq.data_ptr(), rot,
             int(interleaved), float(rope_scale), q_out.data_ptr(), k_out.data_ptr(), _ptr(v_out))
     return q_out, k_out, v_out
@@ -721,16 +744,28 @@ def bg_beam_qk_norm_rope(q, k, v, base_pos, step: int, q_out, suffix_k, suffix_v
     """bg_packed_qk_norm_rope for the new token of every beam: q [R,W,Hq,d], k/v [R,W,Hkv,d] bf16 (strided rows as
     there), all beams of request r at base_pos int32 [R] or [axes,R] plus step; q_out [R,W,Hq,d] and slot ``slot`` of
     suffix_k/suffix_v [R,W,S_max,Hkv,d] are written."""
+    import torch
     fn = "bg_beam_qk_norm_rope"
-    R, W, Hq, d = q.shape
-    Hkv, S_max = k.shape[2], suffix_k.shape[2]
-    if not _fits(R, W, Hq, Hkv, d, S_max, step, slot):
+    qs, ks, ss = q.shape, k.shape, suffix_k.shape
+    R, W, Hq, d = qs
+    Hkv, S_max = ks[2], ss[2]
+    index = q.get_device()
+    ok, axes, axis_of, rot = _rope_common(fn, d, index, base_pos, R, q_weight, k_weight, inv_freq, axis_of)
+    bf16 = torch.bfloat16
+    a, b, c = q.stride(), k.stride(), v.stride()
+    # as the calls usually are: rows of heads, d apart, at one distance, of more than one beam
+    if not (ok and W > 1 and a[3] == b[3] == c[3] == 1 and a[2] == b[2] == c[2] == d and
+            (R == 1 or (a[0] == W * a[1] and b[0] == W * b[1] and c[0] == W * c[1])) and ks == (R, W, Hkv, d) and v.shape == ks and
+            q.dtype is bf16 and k.dtype is bf16 and v.dtype is bf16 and k.get_device() == index == v.get_device() and
+            _alike(bf16, index, (q_out, suffix_k, suffix_v, q_weight, k_weight)) and q_out.shape == qs and
+            ss == (R, W, S_max, Hkv, d) and suffix_v.shape == ss):
+        suffix = (R, W, S_max, Hkv, d)
+        a, b, c = ((0, n) for n in _qk_norm_rope(fn, q, k, v, base_pos, (R,), (
+            ("q_out", q_out, (R, W, Hq, d)), ("suffix_k", suffix_k, suffix), ("suffix_v", suffix_v, suffix)), 2, q_weight,
+            k_weight, inv_freq))
+    if not _fits(R, W, Hq, Hkv, S_max, step, slot):
         raise BgError(fn, BG_ERR_UNSUPPORTED)
-    suffix = (R, W, S_max, Hkv, d)
-    (qs, ks, vs), axes, axis_of, rot = _qk_norm_rope(
-        fn, q, k, v, base_pos, (R,), (("q_out", q_out, (R, W, Hq, d)), ("suffix_k", suffix_k, suffix),
-                                      ("suffix_v", suffix_v, suffix)), 2, q_weight, k_weight, inv_freq, axis_of)
-    _launch(fn, q.get_device(), stream, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, R, W, Hq, Hkv, d,
+    _launch(fn, index, stream, q.data_ptr(), a[1], k.data_ptr(), b[1], v.data_ptr(), c[1], R, W, Hq, Hkv, d,
             _ptr(q_weight), _ptr(k_weight), float(eps), float(weight_offset), base_pos.data_ptr(), axes, axis_of, int(step),
             inv_freq.data_ptr(), rot, int(interleaved), float(rope_scale), q_out.data_ptr(), suffix_k.data_ptr(),
             suffix_v.data_ptr(), S_max, int(slot))
@@ -771,10 +806,12 @@ def bg_adjust_logits(logits, out, *, rows_per_group: int = 1, prompt_tokens=None
     if not (_alike(i32, index, (prompt_tokens, cu_prompt, own_tokens, own_lens, bias_tokens, cu_bias, mask, mask_index,
                                 dev_status)) and
             _alike(f32, index, (repetition, frequency, presence, bias_values)) and
-            all(t is None or t.shape == s for t, s in (
-                (prompt_tokens, (P,)), (cu_prompt, (G + 1,)), (own_tokens, (N, S)), (own_lens, (N,)), (repetition, (G,)),
-                (frequency, (G,)), (presence, (G,)), (bias_tokens, (B,)), (bias_values, (B,)), (cu_bias, (G + 1,)),
-                (mask, (M, words)), (mask_index, (N,))))):
+            (prompt_tokens is None or (prompt_tokens.dim() == 1 and cu_prompt.shape == (G + 1,))) and
+            (own_tokens is None or own_tokens.shape == (N, S)) and (own_lens is None or own_lens.shape == (N,)) and
+            (repetition is None or repetition.shape == (G,)) and (frequency is None or frequency.shape == (G,)) and
+            (presence is None or presence.shape == (G,)) and
+            (bias_tokens is None or (bias_tokens.shape == bias_values.shape == (B,) and cu_bias.shape == (G + 1,))) and
+            (mask is None or mask.dim() == 2) and (mask_index is None or mask_index.shape == (N,))):
         _expect(fn, logits.device, (
             ("prompt_tokens", prompt_tokens, i32, (P,)), ("cu_prompt", cu_prompt, i32, (G + 1,)),
             ("own_tokens", own_tokens, i32, (N, S)), ("own_lens", own_lens, i32, (N,)), ("repetition", repetition, f32, (G,)),

@@ -10,11 +10,19 @@
 // in fp32, rounded once where the output is bf16.
 //
 // Memory bounds it: a logit is read (unless the mask bans it and its neighbours) and written.  A CTA takes a
-// chunk of the vocabulary for some rows of one group.  It keeps one word per token of its chunk in shared memory:
-// the bias' number, whether the prompt has the token, and the row's count, which is added before a row and
-// taken away after it.  So prompt and biases are looked at once for all rows of the CTA, histories of any
-// length cost their own reading, and integer atomics leave no order to depend on.
+// chunk of the vocabulary for some rows of one group.  In shared memory it keeps two bits per token of its chunk (the
+// prompt has it; it has a bias) and one word (the bias' number, and in the LONG form the row's count), so that
+// prompt and biases are looked at once for all rows of the CTA.
+//   Each warp copies a block of 1024 logits of a row: the mask's words with one load, the logits that they allow,
+// then the stores.  What is listed and allowed is few: the warp then reads, changes and writes those again.  (The same
+// in the copying loop: three times the instructions.)  A row's mask, lengths and words are fetched ahead.
+//   A row's own tokens are few (at most 32; beams): there is no barrier; the lanes hold the tokens and change them last.
+//   They are many (LONG): the warps take a row together.  Its counts are added to the words beside the copy and taken
+//   away after it, so that a history costs its own reading whatever its length, and integer atomics leave no
+//   order to depend on.
 #include <cuda_bf16.h>
+
+#include <type_traits>
 
 #include "bg_internal.h"
 #include "bg_ptx.cuh"
@@ -22,49 +30,72 @@
 namespace bg {
 namespace {
 
-constexpr int kLgThreads = 256;
-constexpr int kLgMaxChunk = 8192;
-constexpr int kLgMinChunk = 1024;
-constexpr int kCountBits = 18;                       // two rows' counts meet for a moment: 2 * 65536 fits
-constexpr uint32_t kCountMask = (1u << kCountBits) - 1, kPromptBit = 1u << kCountBits;
-constexpr int kBiasShift = kCountBits + 1;
+constexpr int kLgThreads = 128;
+constexpr int kLgWarps = kLgThreads / 32;
+constexpr int kLgCtas = 6;                           // per SM, at least (8 leave 64 registers, and fetched words would be spilled)
+constexpr int kChunk = 4096;                         // tokens of a CTA: a block per warp
+constexpr int kBlock = 1024;                         // logits that a warp takes at once
+constexpr int kLgShare = 32;                         // CTAs per SM that the rows are cut to
+constexpr int kBlocks = kChunk / kBlock;
+static_assert(kChunk / 32 == kLgThreads && kBlocks == kLgWarps, "a bit word per thread, a block per warp");
+constexpr int kBiasShift = 18;                       // two rows' counts meet for a moment: 2 * 65536 fits below it
+constexpr uint32_t kCountMask = (1u << kBiasShift) - 1;
 static_assert(2 * BG_MAX_SEQLEN <= static_cast<int>(kCountMask), "count bits");
 static_assert(BG_MAX_BIAS < (1 << (32 - kBiasShift)), "bias numbers");
 
-__device__ __forceinline__ float load_one(const float *p) { return *p; }
-__device__ __forceinline__ float load_one(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
 __device__ __forceinline__ void store_one(float *p, float x) { *p = x; }
 __device__ __forceinline__ void store_one(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
 
-template <int N>
-__device__ __forceinline__ void load_vec(const float *p, float *x)
-{
-#pragma unroll
-    for (int i = 0; i < N; i += 4) *reinterpret_cast<float4 *>(x + i) = *reinterpret_cast<const float4 *>(p + i);
-}
-template <int N>
-__device__ __forceinline__ void load_vec(const __nv_bfloat16 *p, float *x)
-{
-    static_assert(N == 8, "16 bytes");
-    const uint4 v = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+// N logits as they lie in memory, read where `want` is set (0 elsewhere).  The loads of a block carry predicates and are
+// converted later: in branches, each one's conversion waits for it.  64 bytes are the least that memory gives; where a mask
+// leaves few of them the usual 128 are too many (3200 rows of 65,536 fp32 logits with 2% allowed: 208 us, so 196).
+template <typename T, int N>
+struct Raw {
+    uint32_t w[N * sizeof(T) / 4 > 0 ? N * sizeof(T) / 4 : 1];
+    __device__ __forceinline__ void load(const T *p, bool want)
+    {
+        const int on = want;
+        if constexpr (N * sizeof(T) == 16) {
+            w[0] = w[1] = w[2] = w[3] = 0;
+            asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t@q ld.global.L2::64B.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+                         : "+r"(w[0]), "+r"(w[1]), "+r"(w[2]), "+r"(w[3])
+                         : "l"(p), "r"(on)
+                         : "memory");
+        } else if constexpr (sizeof(T) == 4) {
+            w[0] = 0;
+            asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t@q ld.global.b32 %0, [%1];\n\t}"
+                         : "+r"(w[0])
+                         : "l"(p), "r"(on)
+                         : "memory");
+        } else {
+            uint16_t h = 0;
+            asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t@q ld.global.b16 %0, [%1];\n\t}"
+                         : "+h"(h)
+                         : "l"(p), "r"(on)
+                         : "memory");
+            w[0] = h;
+        }
     }
-}
+    __device__ __forceinline__ float get(int e) const
+    {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[e]);
+        else return __uint_as_float((e & 1) ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
+    }
+};
 template <int N>
 __device__ __forceinline__ void store_vec(float *p, const float *x)
 {
+    if (N == 1) *p = x[0];
+    else
 #pragma unroll
     for (int i = 0; i < N; i += 4) *reinterpret_cast<float4 *>(p + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
 }
 template <int N>
 __device__ __forceinline__ void store_vec(__nv_bfloat16 *p, const float *x)
 {
-    static_assert(N == 8, "16 bytes");
-    *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+    if constexpr (N == 1) *p = __float2bfloat16_rn(x[0]);
+    else
+        *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
                                                pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
 }
 
@@ -74,20 +105,81 @@ __device__ __forceinline__ bool offsets_ok(int a, int b, int n, int g, int group
     return a >= 0 && b >= a && b <= n && (g > 0 || a == 0) && (g < groups - 1 || b == n);
 }
 
-// N logits (1, 4 or 8 side by side) per thread and step.
-template <typename TI, typename TO, int N>
-__global__ void __launch_bounds__(kLgThreads)
-    logits_kernel(const LogitsParams p, int chunk, int chunks, int rows_per_cta, int row_blocks)
+// kBlock logits (WHOLE), or the first n of them, by one warp, N side by side per lane and step: -inf where the mask has no
+// bit; lane l has the word of tokens 32 l .. 32 l + 31.
+template <typename TI, typename TO, int N, bool WHOLE>
+__device__ __forceinline__ void copy_block(const TI *in, TO *out, uint32_t words, int n, bool in_place)
 {
-    extern __shared__ uint32_t table[];              // [chunk], where there are lists
+    constexpr int kStep = 32 * N, kSteps = N == 1 ? 16 : kBlock / kStep;      // steps whose loads are under way together
+    constexpr uint32_t kFull = (1u << N) - 1u;
+    const int lane = threadIdx.x & 31;
+    in += lane * N;
+    out += lane * N;
+#pragma unroll 1
+    for (int s0 = 0; s0 < kBlock; s0 += kSteps * kStep) {
+        uint32_t keep = 0;                           // N bits per step
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k)
+            keep |= ((__shfl_sync(0xffffffffu, words, s0 / 32 + k * N + lane * N / 32) >> (lane * N % 32)) & kFull) << (k * N);
+        Raw<TI, N> raw[kSteps];
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) {
+            const uint32_t bits = (keep >> (k * N)) & kFull;
+            raw[k].load(in + s0 + k * kStep, bits != 0 && !(in_place && bits == kFull) && (WHOLE || s0 + k * kStep + lane < n));
+        }
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) {
+            const uint32_t bits = (keep >> (k * N)) & kFull;
+            if ((in_place && bits == kFull) || (!WHOLE && s0 + k * kStep + lane >= n)) continue;      // in place: they stay
+            float x[N];
+#pragma unroll
+            for (int e = 0; e < N; ++e) x[e] = (bits >> e) & 1u ? raw[k].get(e) : -INFINITY;
+            store_vec<N>(out + s0 + k * kStep, x);
+        }
+    }
+}
+
+// N logits (1, 4 or 8 side by side) per lane and step of a warp.
+template <typename TI, typename TO, int N, bool LONG>
+__global__ void __launch_bounds__(kLgThreads, kLgCtas)
+    logits_kernel(const LogitsParams p, int chunks, int rows_per_cta, int row_blocks)
+{
+    extern __shared__ uint32_t table[];              // [kChunk], where there are biases or counts
+    __shared__ uint32_t s_prompt[kChunk / 32], s_bias[kChunk / 32], s_own[LONG ? kChunk / 32 : 1];
     grid_dep_launch();
     grid_dep_wait();
-    const int tid = threadIdx.x;
-    const int block = static_cast<int>(blockIdx.x) / chunks, v0 = (static_cast<int>(blockIdx.x) - block * chunks) * chunk;
-    const int n = min(chunk, p.V - v0);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int block = static_cast<int>(blockIdx.x) / chunks, v0 = (static_cast<int>(blockIdx.x) - block * chunks) * kChunk;
+    const int n = min(kChunk, p.V - v0);
     const int g = block / row_blocks, first = (block - g * row_blocks) * rows_per_cta;
     const int last = min(first + rows_per_cta, p.per);
-    const bool lists = p.prompt || p.own || p.bias_tokens;
+    const int b0 = warp * kBlock, word0 = b0 / 32 + lane;      // this warp's block, this lane's word
+    const bool in_place = static_cast<const void *>(p.in) == p.out;
+    const bool lists = LONG || p.prompt || p.bias_tokens, words_kept = LONG || p.bias_tokens;
+
+    // what a row needs: its mask, the number of its own tokens, and the first of them
+    constexpr int kHeld = LONG ? 4 : 1;
+    struct Row {
+        int m, len, t[kHeld];
+    };
+    auto row_at = [&](int r) { return static_cast<int64_t>(g) * p.per + r; };
+    auto fetch = [&](int r) {
+        Row R = {-1, 0, {}};
+        if (r >= last) return R;
+        const int64_t row = row_at(r);
+        if (p.mask) R.m = p.mask_index ? p.mask_index[row] : static_cast<int>(row);
+        if (p.own) R.len = p.own_lens ? p.own_lens[row] : p.own_max;
+#pragma unroll
+        for (int k = 0; k < kHeld; ++k) {
+            const int i = (LONG ? tid : lane) + k * kLgThreads;
+            if (i < p.own_max) R.t[k] = p.own[row * p.own_stride + i];
+        }
+        return R;
+    };
+    auto words_of = [&](const Row &R) {              // of the mask, for tokens b0 + 32 lane ..
+        return R.m >= 0 && R.m < p.num_masks && b0 + 32 * lane < n ? p.mask[R.m * p.mask_stride + v0 / 32 + word0] : ~0u;
+    };
+    Row cur = fetch(first), next = fetch(first + 1);
     int pa = 0, pb = 0, ba = 0, bb = 0, bad = 0;
     if (p.prompt) {
         pa = p.cu_prompt[g];
@@ -105,137 +197,221 @@ __global__ void __launch_bounds__(kLgThreads)
     }
     bool outside = false;                            // a token outside the vocabulary
     if (lists) {
-        for (int i = tid; i < (n + 3) / 4; i += kLgThreads) reinterpret_cast<uint4 *>(table)[i] = make_uint4(0, 0, 0, 0);
+        s_prompt[tid] = 0;
+        s_bias[tid] = 0;
+        if (LONG) s_own[tid] = 0;
+        if (words_kept)
+            for (int i = tid; i < kChunk / 4; i += kLgThreads) reinterpret_cast<uint4 *>(table)[i] = make_uint4(0, 0, 0, 0);
         __syncthreads();
+#pragma unroll 4
         for (int i = ba + tid; i < bb; i += kLgThreads) {
-            const int t = p.bias_tokens[i];
+            int t = p.bias_tokens[i];
             outside = outside || t < 0 || t >= p.V;
-            if (t >= v0 && t < v0 + n) atomicMax(&table[t - v0], static_cast<uint32_t>(i - ba + 1) << kBiasShift);
+            t -= v0;
+            if (t >= 0 && t < n) {
+                atomicMax(&table[t], static_cast<uint32_t>(i - ba + 1) << kBiasShift);
+                atomicOr(&s_bias[t / 32], 1u << t % 32);
+            }
         }
-        if (p.bias_tokens) __syncthreads();
+#pragma unroll 8
         for (int i = pa + tid; i < pb; i += kLgThreads) {
-            const int t = p.prompt[i];
+            int t = p.prompt[i];
             outside = outside || t < 0 || t >= p.V;
-            if (t >= v0 && t < v0 + n) atomicOr(&table[t - v0], kPromptBit);
+            t -= v0;
+            if (t >= 0 && t < n) atomicOr(&s_prompt[t / 32], 1u << t % 32);
         }
         __syncthreads();
     }
-    const float rho = p.repetition ? p.repetition[g] : 1.f;
+    // one division for all (the product's second rounding is 2^-24): without penalties both factors are 1
+    const float rho = p.repetition ? p.repetition[g] : 1.f, inv = 1.f / rho;
     const float alpha = p.frequency ? p.frequency[g] : 0.f, beta = p.presence ? p.presence[g] : 0.f;
-    auto edit = [&](float x, uint32_t w) {
-        const uint32_t c = w & kCountMask;
-        if (p.repetition && (w & (kCountMask | kPromptBit))) x = x > 0.f ? x / rho : x * rho;
-        if (c) x -= fmaf(alpha, static_cast<float>(c), beta);
-        if (w >> kBiasShift) x += p.bias_values[ba + static_cast<int>(w >> kBiasShift) - 1];
-        return x;
+    // The logits of M tokens t[k] >= 0 of the chunk, c times among the row's own (LONG: as their words say): those that
+    // `ok` has are changed, and in the LONG form all counts are taken away.  Each kind of load is made for all of them
+    // together, before any store, which the next loads would not pass.
+    auto edit = [&](const TI *in, TO *out, auto &t, auto &ok, int c_own) {
+        constexpr int M = sizeof(t) / sizeof(t[0]);
+        Raw<TI, 1> x[M];
+        uint32_t w[M], said[M];
+        float bias[M];
+#pragma unroll
+        for (int k = 0; k < M; ++k) x[k].load(in + t[k], ok[k]);
+#pragma unroll
+        for (int k = 0; k < M; ++k) {
+            w[k] = words_kept && t[k] >= 0 ? table[t[k]] : 0u;
+            said[k] = lists && t[k] >= 0 ? s_prompt[t[k] / 32] >> t[k] % 32 & 1u : 0u;
+        }
+#pragma unroll
+        for (int k = 0; k < M; ++k) bias[k] = w[k] >> kBiasShift ? p.bias_values[ba + static_cast<int>(w[k] >> kBiasShift) - 1] : 0.f;
+#pragma unroll
+        for (int k = 0; k < M; ++k) {
+            const int c = LONG ? static_cast<int>(w[k] & kCountMask) : c_own;
+            float y = x[k].get(0);
+            if (c > 0 || said[k] != 0) y *= y > 0.f ? inv : rho;
+            if (c > 0) y -= fmaf(alpha, static_cast<float>(c), beta);
+            if (w[k] >> kBiasShift) y += bias[k];
+            if (ok[k]) store_one(out + t[k], y);
+            if (LONG && c > 0) table[t[k]] = w[k] & ~kCountMask;
+        }
+    };
+    // The tokens of the block whose bits are set, bit e of lane l for token b0 + 32 l + e.  Each lane goes through its own
+    // where they are few; where some lane has many (the frequent tokens often lie side by side), all lanes go through
+    // the words together.
+    auto change = [&](const TI *in, TO *out, uint32_t bits, uint32_t allowed) {
+        constexpr int kFew = 3, kWords = 8;
+        if (__any_sync(0xffffffffu, __popc(bits) > 2 * kFew)) {
+#pragma unroll 1
+            for (int l0 = 0; l0 < 32; l0 += kWords) {
+                int t[kWords];
+                bool ok[kWords];
+#pragma unroll
+                for (int k = 0; k < kWords; ++k) {
+                    const uint32_t some = __shfl_sync(0xffffffffu, bits, l0 + k), free = __shfl_sync(0xffffffffu, allowed, l0 + k);
+                    t[k] = (some >> lane) & 1u ? b0 + 32 * (l0 + k) + lane : -1;
+                    ok[k] = (some & free) >> lane & 1u;
+                }
+                edit(in, out, t, ok, 0);
+            }
+        } else {
+#pragma unroll 1
+            for (int i = 0; i < 2; ++i) {
+                int t[kFew];
+                bool ok[kFew];
+#pragma unroll
+                for (int k = 0; k < kFew; ++k) {
+                    const int e = __ffs(bits) - 1;
+                    bits &= bits - 1;
+                    t[k] = e >= 0 ? 32 * word0 + e : -1;
+                    ok[k] = e >= 0 && (allowed >> (e & 31)) & 1u;
+                }
+                edit(in, out, t, ok, 0);
+            }
+        }
+    };
+    auto copy = [&](const TI *in, TO *out, uint32_t words) {
+        if (b0 + kBlock <= n) copy_block<TI, TO, N, true>(in + b0, out + b0, words, kBlock, in_place);
+        else copy_block<TI, TO, 1, false>(in + b0, out + b0, words, n - b0, in_place);
+    };
+    // whether the row can be written
+    auto row_ok = [&](const Row &R, bool tell) {
+        const int wrong = (p.mask && (R.m < -1 || R.m >= p.num_masks) ? BG_DEVSTAT_MASK : 0) |
+                          (R.len < 0 || R.len > p.own_max ? BG_DEVSTAT_SEQ_TOO_LONG : 0);
+        if (wrong && tell && p.dev_status) atomicOr(p.dev_status, wrong);
+        return wrong == 0;
     };
 
-    for (int r = first; r < last; ++r) {
-        const int64_t row = static_cast<int64_t>(g) * p.per + r;
-        const int m = !p.mask ? -1 : p.mask_index ? p.mask_index[row] : static_cast<int>(row);
-        int len = 0;
-        if (p.own) len = p.own_lens ? p.own_lens[row] : p.own_max;
-        const int wrong = (p.mask && (m < -1 || m >= p.num_masks) ? BG_DEVSTAT_MASK : 0) |
-                          (len < 0 || len > p.own_max ? BG_DEVSTAT_SEQ_TOO_LONG : 0);
-        if (wrong) {                                 // the same for all threads
-            if (tid == 0 && p.dev_status) atomicOr(p.dev_status, wrong);
-            continue;
+    auto in_of = [&](int r) { return static_cast<const TI *>(p.in) + row_at(r) * p.in_stride + v0; };
+    auto out_of = [&](int r) { return static_cast<TO *>(p.out) + row_at(r) * p.out_stride + v0; };
+    uint32_t words = words_of(cur);
+    if constexpr (!LONG) {
+        for (int r = first; r < last; ++r) {
+            const Row R = cur;
+            const uint32_t allowed = words;
+            cur = next;
+            words = words_of(cur);
+            next = fetch(r + 2);
+            if (!row_ok(R, tid == 0)) continue;                // the same for all threads
+            int t = R.t[0];
+            if (lane < R.len && (t < 0 || t >= p.V)) outside = true;
+            if (b0 >= n) continue;
+            const TI *in = in_of(r);
+            TO *out = out_of(r);
+            copy(in, out, allowed);
+            // the lane's token lies in the block: the last lane of those with the same token changes it
+            t -= v0;
+            const bool mine = lane < R.len && t >= b0 && t < min(b0 + kBlock, n);
+            bool leads = false;
+            int c = 0;
+            uint32_t bits = lists ? allowed & (s_prompt[word0] | s_bias[word0]) : 0u;
+            if (__any_sync(0xffffffffu, mine)) {
+                const unsigned same = __match_any_sync(0xffffffffu, mine ? t : -1 - lane);
+                c = __popc(same);
+                const uint32_t w = __shfl_sync(0xffffffffu, allowed, mine ? (t - b0) / 32 : 0);
+                leads = mine && (same >> lane) == 1u && (w >> t % 32) & 1u;
+                for (unsigned l = __ballot_sync(0xffffffffu, leads); l != 0; l &= l - 1) {
+                    const int u = __shfl_sync(0xffffffffu, t, __ffs(l) - 1);
+                    if (u / 32 == word0) bits &= ~(1u << u % 32);
+                }
+            }
+            __syncwarp();                                      // what other lanes have copied is there
+            if (__any_sync(0xffffffffu, bits != 0)) change(in, out, bits, allowed);
+            if (leads) {
+                const int u[1] = {t};
+                const bool yes[1] = {true};
+                edit(in, out, u, yes, c);
+            }
         }
-        const int32_t *own = p.own ? p.own + row * p.own_stride : nullptr;
-        if (p.own) {
-            for (int i = tid; i < len; i += kLgThreads) {
-                const int t = own[i];
+    } else {
+        // counts of a row's own tokens into the words of the chunk
+        auto add = [&](int r, const Row &R) {
+            auto one = [&](int t) {
                 outside = outside || t < 0 || t >= p.V;
-                if (t >= v0 && t < v0 + n) atomicAdd(&table[t - v0], 1u);
-            }
-            __syncthreads();
+                t -= v0;
+                if (t >= 0 && t < n) {
+                    atomicAdd(&table[t], 1u);
+                    atomicOr(&s_own[t / 32], 1u << t % 32);
+                }
+            };
+#pragma unroll
+            for (int k = 0; k < kHeld; ++k)
+                if (tid + k * kLgThreads < R.len) one(R.t[k]);
+            for (int i = tid + kHeld * kLgThreads; i < R.len; i += kLgThreads) one(p.own[row_at(r) * p.own_stride + i]);
+        };
+        bool ok = row_ok(cur, tid == 0);                       // the same for all threads
+        if (ok) {
+            add(first, cur);
+            if (b0 < n) copy(in_of(first), out_of(first), words);
         }
-        const TI *in = static_cast<const TI *>(p.in) + row * p.in_stride + v0;
-        TO *out = static_cast<TO *>(p.out) + row * p.out_stride + v0;
-        const uint32_t *mask = m < 0 ? nullptr : p.mask + m * p.mask_stride + v0 / 32;
-        constexpr int kSteps = N == 1 ? 8 : 4;
-        for (int i0 = tid * N; i0 < n; i0 += kSteps * kLgThreads * N) {
-            uint32_t keep[kSteps];
-#pragma unroll
-            for (int k = 0; k < kSteps; ++k) {
-                const int i = i0 + k * kLgThreads * N;
-                keep[k] = i < n ? (mask ? mask[i / 32] >> (i % 32) : ~0u) & ((1u << N) - 1u) : 0u;
+        for (int r = first; r < last; ++r) {
+            const uint32_t allowed = words;
+            const bool changes = ok && b0 < n;
+            cur = next;
+            words = words_of(cur);
+            next = fetch(r + 2);
+            __syncthreads();                                   // row r's counts are there
+            if (changes) {
+                const uint32_t own = s_own[word0];
+                change(in_of(r), out_of(r), (allowed & (s_prompt[word0] | s_bias[word0])) | own, allowed);
+                s_own[word0] = 0;
             }
-            float x[kSteps][N];
-#pragma unroll
-            for (int k = 0; k < kSteps; ++k) {
-                const int i = i0 + k * kLgThreads * N;
-                if (!keep[k]) continue;
-                if (N > 1 && i + N <= n) {
-                    if constexpr (N > 1) load_vec<N>(in + i, x[k]);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < N; ++e) x[k][e] = i + e < n ? load_one(in + i + e) : 0.f;
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < kSteps; ++k) {
-                const int i = i0 + k * kLgThreads * N;
-                if (i >= n) break;
-                if (lists && keep[k]) {
-#pragma unroll
-                    for (int e = 0; e < N; ++e) {
-                        const uint32_t w = table[i + e];       // (past n: whatever it is)
-                        if (w && i + e < n) x[k][e] = edit(x[k][e], w);
-                    }
-                }
-#pragma unroll
-                for (int e = 0; e < N; ++e)
-                    if (!((keep[k] >> e) & 1u)) x[k][e] = -INFINITY;
-                if (N > 1 && i + N <= n) {
-                    if constexpr (N > 1) store_vec<N>(out + i, x[k]);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < N; ++e)
-                        if (i + e < n) store_one(out + i + e, x[k][e]);
-                }
-            }
-        }
-        if (p.own) {
-            __syncthreads();
-            for (int i = tid; i < len; i += kLgThreads) {
-                const int t = own[i];
-                if (t >= v0 && t < v0 + n) atomicSub(&table[t - v0], 1u);
-            }
+            ok = r + 1 < last && row_ok(cur, tid == 0);
+            if (ok && b0 < n) copy(in_of(r + 1), out_of(r + 1), words);
+            __syncthreads();                                   // ... and gone
+            if (ok) add(r + 1, cur);
         }
     }
     if (outside && p.dev_status) atomicOr(p.dev_status, BG_DEVSTAT_TOKEN);
 }
 
 template <typename TI, typename TO, int N>
-cudaError_t launch_typed(const LogitsParams &p, int chunk, int rows_per_cta, cudaStream_t stream)
+cudaError_t launch_typed(const LogitsParams &p, int rows_per_cta, cudaStream_t stream)
 {
-    const int row_blocks = (p.per + rows_per_cta - 1) / rows_per_cta, chunks = (p.V + chunk - 1) / chunk;
-    const bool lists = p.prompt || p.own || p.bias_tokens;
+    const int row_blocks = (p.per + rows_per_cta - 1) / rows_per_cta, chunks = (p.V + kChunk - 1) / kChunk;
+    const bool many = p.own && p.own_max > 32;
+    const size_t smem = many || p.bias_tokens ? kChunk * sizeof(uint32_t) : 0;
     const int64_t ctas = static_cast<int64_t>(p.groups) * row_blocks * chunks;
     if (ctas > INT32_MAX) return cudaErrorInvalidValue;
-    return launch_dependent(logits_kernel<TI, TO, N>, dim3(static_cast<unsigned>(ctas)), dim3(kLgThreads),
-                            lists ? chunk * sizeof(uint32_t) : 0, stream, p, chunk, chunks, rows_per_cta, row_blocks);
+    return launch_dependent(many ? logits_kernel<TI, TO, N, true> : logits_kernel<TI, TO, N, false>,
+                            dim3(static_cast<unsigned>(ctas)), dim3(kLgThreads), smem, stream, p, chunks, rows_per_cta,
+                            row_blocks);
 }
 
 }  // namespace
 
 cudaError_t launch_adjust_logits(const LogitsParams &p, int in_dtype, int out_dtype, bool vectors, int nsm, cudaStream_t stream)
 {
-    // Chunks as large as leaves two CTAs per SM, then rows as many as leave eight.
-    int chunk = kLgMaxChunk;
-    const int64_t rows = static_cast<int64_t>(p.groups) * p.per;
-    auto chunks = [&] { return (p.V + chunk - 1) / chunk; };
-    while (chunk > kLgMinChunk && chunks() * rows < 2 * nsm) chunk /= 2;
+    // The rows of a group are cut to kLgShare CTAs per SM, as long as a CTA has four of them, and eight logits for each
+    // token of the lists that it has to look at.
+    const int64_t chunks = (p.V + kChunk - 1) / kChunk, listed = p.total_prompt / p.groups + p.total_bias / p.groups;
     int per = p.per;
-    while (per > 1 && chunks() * static_cast<int64_t>(p.groups) * ((p.per + per - 1) / per) < 8 * nsm) per = (per + 1) / 2;
+    while (per >= 8 && per / 2 * static_cast<int64_t>(kChunk) >= 8 * listed && chunks * p.groups * ((p.per + per - 1) / per) < kLgShare * nsm)
+        per = (per + 1) / 2;
     if (in_dtype == BG_DTYPE_F32)
-        return vectors ? launch_typed<float, float, 4>(p, chunk, per, stream) : launch_typed<float, float, 1>(p, chunk, per, stream);
+        return vectors ? launch_typed<float, float, 4>(p, per, stream) : launch_typed<float, float, 1>(p, per, stream);
     if (out_dtype == BG_DTYPE_F32)
-        return vectors ? launch_typed<__nv_bfloat16, float, 8>(p, chunk, per, stream)
-                       : launch_typed<__nv_bfloat16, float, 1>(p, chunk, per, stream);
-    return vectors ? launch_typed<__nv_bfloat16, __nv_bfloat16, 8>(p, chunk, per, stream)
-                   : launch_typed<__nv_bfloat16, __nv_bfloat16, 1>(p, chunk, per, stream);
+        return vectors ? launch_typed<__nv_bfloat16, float, 8>(p, per, stream)
+                       : launch_typed<__nv_bfloat16, float, 1>(p, per, stream);
+    return vectors ? launch_typed<__nv_bfloat16, __nv_bfloat16, 8>(p, per, stream)
+                   : launch_typed<__nv_bfloat16, __nv_bfloat16, 1>(p, per, stream);
 }
 
 }  // namespace bg
