@@ -32,7 +32,6 @@ namespace {
 
 constexpr int kLgThreads = 128;
 constexpr int kLgWarps = kLgThreads / 32;
-constexpr int kLgCtas = 6;                           // per SM, at least (8 leave 64 registers, and fetched words would be spilled)
 constexpr int kChunk = 4096;                         // tokens of a CTA: a block per warp
 constexpr int kBlock = 1024;                         // logits that a warp takes at once
 constexpr int kLgShare = 32;                         // CTAs per SM that the rows are cut to
@@ -139,9 +138,10 @@ __device__ __forceinline__ void copy_block(const TI *in, TO *out, uint32_t words
     }
 }
 
-// N logits (1, 4 or 8 side by side) per lane and step of a warp.
+// N logits (1, 4 or 8 side by side) per lane and step of a warp.  As many CTAs per SM as leave the registers for what is
+// fetched ahead: spilled, it is waited for at once (eight CTAs: 3200 rows of 65,536 logits 398 us, seven 183).
 template <typename TI, typename TO, int N, bool LONG>
-__global__ void __launch_bounds__(kLgThreads, kLgCtas)
+__global__ void __launch_bounds__(kLgThreads, LONG ? 6 : 7)
     logits_kernel(const LogitsParams p, int chunks, int rows_per_cta, int row_blocks)
 {
     extern __shared__ uint32_t table[];              // [kChunk], where there are biases or counts
@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kLgThreads, kLgCtas)
     // where they are few; where some lane has many (the frequent tokens often lie side by side), all lanes go through
     // the words together.
     auto change = [&](const TI *in, TO *out, uint32_t bits, uint32_t allowed) {
-        constexpr int kFew = 3, kWords = 8;
+        constexpr int kFew = 3, kWords = 4;
         if (__any_sync(0xffffffffu, __popc(bits) > 2 * kFew)) {
 #pragma unroll 1
             for (int l0 = 0; l0 < 32; l0 += kWords) {
@@ -399,11 +399,11 @@ cudaError_t launch_typed(const LogitsParams &p, int rows_per_cta, cudaStream_t s
 
 cudaError_t launch_adjust_logits(const LogitsParams &p, int in_dtype, int out_dtype, bool vectors, int nsm, cudaStream_t stream)
 {
-    // The rows of a group are cut to kLgShare CTAs per SM, as long as a CTA has four of them, and eight logits for each
-    // token of the lists that it has to look at.
+    // The rows of a group are cut to kLgShare CTAs per SM, as long as a CTA has four of them, and four logits for each
+    // token of the lists that it has to look at (eight: 480 rows with prompts of 3000 tokens 76 us instead of 67).
     const int64_t chunks = (p.V + kChunk - 1) / kChunk, listed = p.total_prompt / p.groups + p.total_bias / p.groups;
     int per = p.per;
-    while (per >= 8 && per / 2 * static_cast<int64_t>(kChunk) >= 8 * listed && chunks * p.groups * ((p.per + per - 1) / per) < kLgShare * nsm)
+    while (per >= 8 && per / 2 * static_cast<int64_t>(kChunk) >= 4 * listed && chunks * p.groups * ((p.per + per - 1) / per) < kLgShare * nsm)
         per = (per + 1) / 2;
     if (in_dtype == BG_DTYPE_F32)
         return vectors ? launch_typed<float, float, 4>(p, per, stream) : launch_typed<float, float, 1>(p, per, stream);

@@ -8,11 +8,13 @@
 // over the pairs (a, b) = (i, i + rot / 2), or (2 i, 2 i + 1) where they are interleaved; dimensions from rot on
 // keep y.  V is copied beside them, out of the fused projection's rows.  All in fp32, rounded to bf16 once.
 //
-// Memory bounds it: every element is read once and written once, about 130 instructions of a warp for 2 KB.
-// A warp takes a token (or a part of its heads, where there are few tokens), so that its angles are computed
-// once for all heads.  Eight lanes (four at d = 64) hold a head, each 16 of its elements that make up eight
-// whole pairs with the frequencies 8 j .. 8 j + 7 in either layout: the rotation needs no exchange, the norm
-// a sum over the lanes of a head.
+// Memory bounds it: every element is read once and written once.  Eight lanes (four at d = 64) take a token, a warp
+// four (eight) of them, and go through the heads.  A lane holds 16 elements of a head that make up eight whole pairs,
+// with the frequencies 8 j .. 8 j + 7 in either layout: it computes their angles once for all heads of its token, the
+// rotation needs no exchange, and the norm a sum over the lanes of a head.  (A warp for one token, with each angle
+// computed once and shuffled to the lanes that need it, and heads left over in the last round: 70,375 tokens of 16/8
+// heads of 128 196 us, 23,041 of 14/2 heads of 64 31 us.)  Where there are few tokens, their heads are dealt out to
+// several warps.
 #include <cuda_bf16.h>
 
 #include "bg_internal.h"
@@ -22,8 +24,12 @@ namespace bg {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeCtas = 3;              // per SM
-constexpr int kRopeBatch = 2;             // head rounds whose loads are under way together
+#ifndef CTAS
+#define CTAS 2
+#define BATCH 2
+#endif
+constexpr int kRopeCtas = CTAS;              // per SM
+constexpr int kRopeBatch = BATCH;             // heads whose loads are under way together
 
 __device__ __forceinline__ void unpack(const uint4 &v, float *x)
 {
@@ -53,9 +59,8 @@ __device__ __forceinline__ float2 cos_sin(int32_t pos, float hi, float lo)
 template <int D, bool INTERLEAVED, bool NORM>
 __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_kernel(const __grid_constant__ RopeParams p)
 {
-    constexpr int kLanes = D / 16;                 // lanes of a head
-    constexpr int kHeads = 32 / kLanes;            // heads of a round
-    constexpr int kOwn = D / 64;                   // frequencies whose angle a lane computes
+    constexpr int kLanes = D / 16;                 // lanes of a token
+    constexpr int kTokens = 32 / kLanes;           // tokens of a warp
     const int lane = threadIdx.x & 31, j = lane % kLanes, sub = lane / kLanes;
     const int half = p.rot / 2;
     grid_dep_launch();
@@ -65,119 +70,111 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_kernel(const __g
     const bool turns = 8 * j < half;
     const int lo = INTERLEAVED || !turns ? 16 * j : 8 * j;
     const int hi = INTERLEAVED || !turns ? 16 * j + 8 : 8 * j + half;
-    uint4 wq[2], wk[2];
-    if (NORM) {
-        wq[0] = *reinterpret_cast<const uint4 *>(p.q_weight + lo);
-        wq[1] = *reinterpret_cast<const uint4 *>(p.q_weight + hi);
-        wk[0] = *reinterpret_cast<const uint4 *>(p.k_weight + lo);
-        wk[1] = *reinterpret_cast<const uint4 *>(p.k_weight + hi);
-    }
-    // f / (2 pi) as a sum of two numbers
-    constexpr double kTurn = 0.15915494309189533577;
-    constexpr float kTurnHi = static_cast<float>(kTurn), kTurnLo = static_cast<float>(kTurn - kTurnHi);
-    float f_hi[kOwn], f_lo[kOwn];
-    int axis[kOwn];
+    float f[8];
+    uint32_t axes = 0;                             // two bits each
 #pragma unroll
-    for (int m = 0; m < kOwn; ++m) {
-        const int i = lane * kOwn + m;
-        const float f = i < half ? p.inv_freq[i] : 0.f;
-        axis[m] = p.axis[i];
-        f_hi[m] = f * kTurnHi;
-        f_lo[m] = fmaf(f, kTurnLo, fmaf(f, kTurnHi, -f_hi[m]));
+    for (int i = 0; i < 8; ++i) {
+        f[i] = turns ? p.inv_freq[8 * j + i] : 0.f;
+        axes |= static_cast<uint32_t>(p.axis[8 * j + i]) << (2 * i);
     }
 
     const int n_heads = p.Hq + p.Hkv + (p.v ? p.Hkv : 0);
-    const int64_t units = p.rows * p.parts, stride = static_cast<int64_t>(gridDim.x) * (kRopeThreads / 32);
+    const int64_t units = (p.rows + kTokens - 1) / kTokens * p.parts;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * (kRopeThreads / 32);
     for (int64_t u = static_cast<int64_t>(blockIdx.x) * (kRopeThreads / 32) + (threadIdx.x >> 5); u < units; u += stride) {
-        const int64_t row = u / p.parts;
-        const int part = static_cast<int>(u - row * p.parts);
-        const int64_t place = row / p.rows_per_pos;
+        const int64_t first = u / p.parts * kTokens;
+        const int part = static_cast<int>(u % p.parts);
+        const int begin = part * n_heads / p.parts, end = (part + 1) * n_heads / p.parts;
+        const bool live = first + sub < p.rows;
+        const int64_t row = live ? first + sub : p.rows - 1;
         float c[8], s[8];
-        {
-            float2 cs[kOwn];
+        if (begin < p.Hq + p.Hkv) {
+            const int64_t place = row / p.rows_per_pos;
+            int32_t pos[BG_MAX_AXES];
 #pragma unroll
-            for (int m = 0; m < kOwn; ++m)
-                cs[m] = cos_sin(p.positions[axis[m] * p.places + place] + p.step, f_hi[m], f_lo[m]);
+            for (int a = 0; a < BG_MAX_AXES; ++a) pos[a] = a < p.num_axes ? p.positions[a * p.places + place] : 0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {          // frequency 8 j + i is lane (8 j + i) / kOwn's
-                const int src = (8 * j + i) / kOwn;
-                c[i] = __shfl_sync(0xffffffffu, cs[i % kOwn].x, src) * p.rope_scale;
-                s[i] = __shfl_sync(0xffffffffu, cs[i % kOwn].y, src) * p.rope_scale;
+            for (int i = 0; i < 8; ++i) {
+                int32_t at = pos[0];
+                if (p.num_axes > 1) {
+                    const uint32_t a = (axes >> (2 * i)) & 3u;
+                    at = a < 2 ? (a == 0 ? pos[0] : pos[1]) : (a == 2 ? pos[2] : pos[3]);
+                }
+                // f / (2 pi) as a sum of two numbers
+                constexpr double kTurn = 0.15915494309189533577;
+                constexpr float kTurnHi = static_cast<float>(kTurn), kTurnLo = static_cast<float>(kTurn - kTurnHi);
+                const float f_hi = f[i] * kTurnHi, f_lo = fmaf(f[i], kTurnLo, fmaf(f[i], kTurnHi, -f_hi));
+                const float2 cs = cos_sin(at + p.step, f_hi, f_lo);
+                c[i] = cs.x * p.rope_scale;
+                s[i] = cs.y * p.rope_scale;
             }
         }
-        for (int h0 = part * kHeads; h0 < n_heads; h0 += kRopeBatch * p.parts * kHeads) {
-            uint4 a[kRopeBatch], b[kRopeBatch];
-            __nv_bfloat16 *dst[kRopeBatch];
+        // heads [from, to) of q or k, kRopeBatch at a time; V: copied
+        auto heads = [&](const __nv_bfloat16 *src, __nv_bfloat16 *dst, const __nv_bfloat16 *weight, int from, int to, bool copied) {
+            float w[NORM ? 16 : 1];
+            if (NORM && !copied && from < to) {
+                unpack(*reinterpret_cast<const uint4 *>(weight + lo), w);
+                unpack(*reinterpret_cast<const uint4 *>(weight + hi), w + (NORM ? 8 : 0));
 #pragma unroll
-            for (int k = 0; k < kRopeBatch; ++k) {
-                const int h = h0 + k * p.parts * kHeads + sub;
-                const __nv_bfloat16 *src;
-                if (h < p.Hq) {
-                    src = p.q + row * p.q_stride + h * D;
-                    dst[k] = p.q_out + (row * p.Hq + h) * D;
-                } else if (h < p.Hq + p.Hkv) {
-                    src = p.k + row * p.k_stride + (h - p.Hq) * D;
-                    dst[k] = p.k_out + row * p.kv_out_stride + (h - p.Hq) * D;
-                } else {
-                    src = p.v + row * p.v_stride + (h - p.Hq - p.Hkv) * D;
-                    dst[k] = p.v_out + row * p.kv_out_stride + (h - p.Hq - p.Hkv) * D;
-                }
-                if (h < n_heads) {
-                    a[k] = *reinterpret_cast<const uint4 *>(src + lo);
-                    b[k] = *reinterpret_cast<const uint4 *>(src + hi);
-                } else {
-                    a[k] = b[k] = make_uint4(0, 0, 0, 0);
-                }
+                for (int i = 0; i < (NORM ? 16 : 1); ++i) w[i] += p.weight_offset;
             }
+#pragma unroll 1
+            for (int h0 = from; h0 < to; h0 += kRopeBatch) {
+                uint4 a[kRopeBatch], b[kRopeBatch];
 #pragma unroll
-            for (int k = 0; k < kRopeBatch; ++k) {
-                const int hr = h0 + k * p.parts * kHeads;     // the round's first head
-                const int h = hr + sub;
-                if (hr < p.Hq + p.Hkv) {
-                    float x[16];
-                    unpack(a[k], x);
-                    unpack(b[k], x + 8);
-                    if (NORM) {
-                        float sum = 0.f;
+                for (int k = 0; k < kRopeBatch; ++k) {
+                    const __nv_bfloat16 *at = src + min(h0 + k, to - 1) * D;
+                    a[k] = *reinterpret_cast<const uint4 *>(at + lo);
+                    b[k] = *reinterpret_cast<const uint4 *>(at + hi);
+                }
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) sum = fmaf(x[i], x[i], sum);
+                for (int k = 0; k < kRopeBatch; ++k) {
+                    if (h0 + k >= to) break;
+                    if (!copied) {
+                        float x[16];
+                        unpack(a[k], x);
+                        unpack(b[k], x + 8);
+                        if (NORM) {
+                            float sum = 0.f;
 #pragma unroll
-                        for (int o = 1; o < kLanes; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                        const float inv = rsqrtf(fmaf(sum, 1.f / D, p.eps));
-                        float w[16];
-                        const bool is_q = h < p.Hq;
-                        unpack(is_q ? wq[0] : wk[0], w);
-                        unpack(is_q ? wq[1] : wk[1], w + 8);
+                            for (int i = 0; i < 16; ++i) sum = fmaf(x[i], x[i], sum);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) x[i] *= inv * (w[i] + p.weight_offset);
-                    }
-                    uint32_t o[8];
-                    if (!turns) {
+                            for (int o = 1; o < kLanes; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                            const float inv = rsqrtf(fmaf(sum, 1.f / D, p.eps));
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) o[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
-                    } else if (INTERLEAVED) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            o[i] = pack_bf16x2(x[2 * i] * c[i] - x[2 * i + 1] * s[i], x[2 * i + 1] * c[i] + x[2 * i] * s[i]);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int e = 2 * i, f = 2 * i + 1;
-                            o[i] = pack_bf16x2(x[e] * c[e] - x[8 + e] * s[e], x[f] * c[f] - x[8 + f] * s[f]);
-                            o[4 + i] = pack_bf16x2(x[8 + e] * c[e] + x[e] * s[e], x[8 + f] * c[f] + x[f] * s[f]);
+                            for (int i = 0; i < 16; ++i) x[i] *= inv * w[NORM ? i : 0];
                         }
-                    }
-                    if (h < p.Hq + p.Hkv) {
+                        uint32_t o[8];
+                        if (!turns) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) o[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+                        } else if (INTERLEAVED) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                o[i] = pack_bf16x2(x[2 * i] * c[i] - x[2 * i + 1] * s[i], x[2 * i + 1] * c[i] + x[2 * i] * s[i]);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int e = 2 * i, g = 2 * i + 1;
+                                o[i] = pack_bf16x2(x[e] * c[e] - x[8 + e] * s[e], x[g] * c[g] - x[8 + g] * s[g]);
+                                o[4 + i] = pack_bf16x2(x[8 + e] * c[e] + x[e] * s[e], x[8 + g] * c[g] + x[g] * s[g]);
+                            }
+                        }
                         a[k] = make_uint4(o[0], o[1], o[2], o[3]);
                         b[k] = make_uint4(o[4], o[5], o[6], o[7]);
                     }
-                }
-                if (h < n_heads) {
-                    *reinterpret_cast<uint4 *>(dst[k] + lo) = a[k];
-                    *reinterpret_cast<uint4 *>(dst[k] + hi) = b[k];
+                    if (live) {
+                        __nv_bfloat16 *at = dst + (h0 + k) * D;
+                        *reinterpret_cast<uint4 *>(at + lo) = a[k];
+                        *reinterpret_cast<uint4 *>(at + hi) = b[k];
+                    }
                 }
             }
-        }
+        };
+        const int k0 = p.Hq, v0 = p.Hq + p.Hkv;
+        heads(p.q + row * p.q_stride, p.q_out + row * p.Hq * D, p.q_weight, begin, min(end, k0), false);
+        heads(p.k + row * p.k_stride, p.k_out + row * p.kv_out_stride, p.k_weight, max(begin, k0) - k0, min(end, v0) - k0, false);
+        heads(p.v + row * p.v_stride, p.v_out + row * p.kv_out_stride, nullptr, max(begin, v0) - v0, end - v0, true);
     }
 }
 
@@ -194,11 +191,12 @@ cudaError_t launch_d(const RopeParams &p, bool interleaved, int grid, cudaStream
 
 cudaError_t launch_qk_rope(RopeParams p, int head_dim, bool interleaved, int nsm, cudaStream_t stream)
 {
-    const int rounds = (p.Hq + 2 * p.Hkv) * head_dim / 512;      // of a token; one at least
-    // Few tokens: the heads of a token over several warps, as long as a warp per SM sub-partition and more is free.
+    const int heads = p.Hq + p.Hkv + (p.v ? p.Hkv : 0);
+    const int64_t tokens = 512 / head_dim, groups = (p.rows + tokens - 1) / tokens;      // of a warp
+    // Few tokens: their heads over several warps, two heads to each at least, as long as the card has room for them.
     p.parts = 1;
-    while (2 * p.parts <= rounds && 2 * p.parts * p.rows <= nsm * 32) p.parts *= 2;
-    const int64_t warps = kRopeThreads / 32, ctas = (p.rows * p.parts + warps - 1) / warps;
+    while (4 * p.parts <= heads && 2 * p.parts * groups <= nsm * kRopeCtas * (kRopeThreads / 32)) p.parts *= 2;
+    const int64_t warps = kRopeThreads / 32, ctas = (groups * p.parts + warps - 1) / warps;
     const int grid = static_cast<int>(ctas < nsm * kRopeCtas ? ctas : nsm * kRopeCtas);
     return head_dim == 128 ? launch_d<128>(p, interleaved, grid, stream) : launch_d<64>(p, interleaved, grid, stream);
 }
