@@ -632,14 +632,6 @@ bg_status_t shared_check_plan(const ShProblem &pb, const void *workspace, size_t
     return BG_OK;
 }
 
-// The pre-pass: a tree's masks, and the work list.
-bool shared_enqueue_plan(const ShProblem &pb, const ShLayout &lay, void *workspace, int grid, int32_t *dev_status,
-                         cudaStream_t stream)
-{
-    if (pb.tree && launch_tree_masks(pb, lay, workspace, dev_status, stream) != cudaSuccess) return false;
-    return launch_shared_plan(pb, lay, workspace, grid, dev_status, stream) == cudaSuccess;
-}
-
 bg_status_t shared_plan_impl(const ShProblem &pb, void *workspace, size_t workspace_bytes, int32_t *dev_status,
                              cudaStream_t stream)
 {
@@ -650,7 +642,7 @@ bg_status_t shared_plan_impl(const ShProblem &pb, void *workspace, size_t worksp
     const ShLayout lay = shared_layout(pb);
     const int grid = shared_grid(pb, lay);
     if (grid <= 0) return BG_ERR_CUDA;
-    return shared_enqueue_plan(pb, lay, workspace, grid, dev_status, stream) ? BG_OK : BG_ERR_CUDA;
+    return launch_shared_plan(pb, lay, workspace, grid, dev_status, stream) == cudaSuccess ? BG_OK : BG_ERR_CUDA;
 }
 
 bg_status_t shared_impl(const ShProblem &pb, const void *q, const void *k, const void *v, const void *prefix_k,
@@ -711,7 +703,8 @@ bg_status_t shared_impl(const ShProblem &pb, const void *q, const void *k, const
         !kv_map(&tm_pv, prefix_v, pb.total_prefix))
         return BG_ERR_CUDA;
 
-    if (with_plan && !shared_enqueue_plan(pb, lay, workspace, grid, dev_status, stream)) return BG_ERR_CUDA;
+    if (with_plan && launch_shared_plan(pb, lay, workspace, grid, dev_status, stream) != cudaSuccess)
+        return BG_ERR_CUDA;
 
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     ShParams p;

@@ -90,14 +90,47 @@ __device__ int sample_of(const int32_t *cu, int s, int end, int row)
 constexpr int kItemUnits = 2;
 __device__ __forceinline__ int entry_units(const ShEntry &E) { return E.tiles > 0 ? E.tiles + kItemUnits : 0; }
 
+// Masks of a tree's nodes: of each one its own bit and its ancestors'.  One CTA per request, a thread per node, which
+// follows the parents through shared memory; they have falling numbers, so that the words come one after the other.
+__device__ void tree_masks(const ShProblem &pb, int request, int32_t *s_parent, uint32_t *masks, int32_t *dev_status)
+{
+    const int a = pb.cu_seqlens[request], b = pb.cu_seqlens[request + 1], n = b - a;
+    if (a < 0 || b < a || b > pb.total_tokens || n > pb.max_seqlen) return;      // the plan reports it
+    bool bad = false;
+    for (int i = threadIdx.x; i < n; i += kPlanThreads) {
+        int up = pb.parent[a + i];
+        if (up < -1 || up >= i) {
+            bad = true;
+            up = -1;
+        }
+        s_parent[i] = up;
+    }
+    if (bad && dev_status) atomicOr(dev_status, BG_DEVSTAT_PARENT);
+    __syncthreads();
+    const int words = tree_words(pb.max_seqlen);
+    for (int i = threadIdx.x; i < n; i += kPlanThreads) {
+        uint32_t *out = masks + static_cast<int64_t>(a + i) * words;
+        int at = i;
+        for (int w = words - 1; w >= 0; --w) {
+            uint32_t bits = 0;
+            while (at >= 32 * w) {
+                bits |= 1u << (at - 32 * w);
+                at = s_parent[at];
+            }
+            out[w] = bits;
+        }
+    }
+}
+
 // Latency alone bounds it: a few loads of the offsets in a row and about ten barriers of one CTA, 3.3 us for
 // one request, 4.5 where ranges are cut, with 512 threads (4.9 with 1024; 256 are 0.1 faster for a few
 // requests and 0.7 slower for 500 entries); the sort of 500 entries adds 2.5.
-// The offsets are held in shared memory because the searches read them many times.
+// The offsets are held in shared memory because the searches read them many times.  For trees CTA 1 + r makes the masks of
+// request r beside it (in a launch of their own: 2 us more).
 __global__ void __launch_bounds__(kPlanThreads)
     shared_plan_kernel(const ShProblem pb, const ShKey key, int bt, int32_t *hdr, ShEntry *entries, ShEntry *sorted,
                        ShStart *__restrict__ starts, ShSplit *__restrict__ splits, int grid, int can_split, int tiles_per, int heads,
-                       int32_t *dev_status)
+                       uint32_t *masks, int32_t *dev_status)
 {
     __shared__ int s_err, s_nsplit, s_empty;
     __shared__ int s_warp[32];
@@ -115,6 +148,11 @@ __global__ void __launch_bounds__(kPlanThreads)
     }
     grid_dep_wait();
     __syncthreads();
+    if (blockIdx.x > 0) {
+        static_assert(kPlanSeqs >= BG_MAX_TREE, "a request's parents");
+        tree_masks(pb, static_cast<int>(blockIdx.x) - 1, s_cu, masks, dev_status);
+        return;
+    }
     if (tid < 12) hdr[kShHdrKey + tid] = key.w[tid];
     const int32_t *cu = pb.cu_seqlens, *cup = pb.cu_prefix, *cug = pb.cu_group;
     auto group = [&](int r) { return cug ? cug[r] : r; };      // a tree: request r is sample r
@@ -358,44 +396,6 @@ __global__ void __launch_bounds__(kPlanThreads)
         hdr[kShHdrSplits] = s_nsplit;
         hdr[kShHdrEntries] = n_entries;
         hdr[kShHdrItems] = 0;
-    }
-}
-
-// ------------------------------------------------------------------------------------ trees
-// The mask of each node of a request: its own bit and its ancestors'.  One CTA per request, a thread per node, which
-// follows the parents through shared memory; they have falling numbers, so that the words come one after the other.
-constexpr int kTreeThreads = 128;
-
-__global__ void __launch_bounds__(kTreeThreads) tree_mask_kernel(const ShProblem pb, uint32_t *masks, int32_t *dev_status)
-{
-    __shared__ int16_t s_parent[BG_MAX_TREE];
-    grid_dep_launch();
-    grid_dep_wait();
-    const int a = pb.cu_seqlens[blockIdx.x], b = pb.cu_seqlens[blockIdx.x + 1], n = b - a;
-    if (a < 0 || b < a || b > pb.total_tokens || n > pb.max_seqlen) return;      // the plan reports it
-    bool bad = false;
-    for (int i = threadIdx.x; i < n; i += kTreeThreads) {
-        int up = pb.parent[a + i];
-        if (up < -1 || up >= i) {
-            bad = true;
-            up = -1;
-        }
-        s_parent[i] = static_cast<int16_t>(up);
-    }
-    if (bad && dev_status) atomicOr(dev_status, BG_DEVSTAT_PARENT);
-    __syncthreads();
-    const int words = tree_words(pb.max_seqlen);
-    for (int i = threadIdx.x; i < n; i += kTreeThreads) {
-        uint32_t *out = masks + static_cast<int64_t>(a + i) * words;
-        int at = i;
-        for (int w = words - 1; w >= 0; --w) {
-            uint32_t bits = 0;
-            while (at >= 32 * w) {
-                bits |= 1u << (at - 32 * w);
-                at = s_parent[at];
-            }
-            out[w] = bits;
-        }
     }
 }
 
@@ -1706,13 +1706,6 @@ ShLayout shared_layout(const ShProblem &pb)
     return L;
 }
 
-cudaError_t launch_tree_masks(const ShProblem &pb, const ShLayout &lay, void *workspace, int32_t *dev_status,
-                              cudaStream_t stream)
-{
-    return launch_dependent(tree_mask_kernel, dim3(pb.num_groups), dim3(kTreeThreads), 0, stream, pb,
-                            reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(workspace) + lay.tree), dev_status);
-}
-
 ShKey shared_key(const ShProblem &pb, int grid)
 {
     return ShKey{{pb.tree ? 2 : pb.last, pb.num_seqs, pb.total_tokens, pb.max_seqlen, pb.num_groups, pb.total_prefix,
@@ -1723,12 +1716,12 @@ cudaError_t launch_shared_plan(const ShProblem &pb, const ShLayout &lay, void *w
                                int32_t *dev_status, cudaStream_t stream)
 {
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    return launch_dependent(shared_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, pb, shared_key(pb, grid),
+    return launch_dependent(shared_plan_kernel, dim3(pb.tree ? 1 + pb.num_groups : 1), dim3(kPlanThreads), 0, stream, pb, shared_key(pb, grid),
                             kShRows / (pb.Hq / pb.Hkv), reinterpret_cast<int32_t *>(ws),
                             reinterpret_cast<ShEntry *>(ws + lay.entries), reinterpret_cast<ShEntry *>(ws + lay.sorted),
                             reinterpret_cast<ShStart *>(ws + lay.starts),
                             reinterpret_cast<ShSplit *>(ws + lay.splits), grid, lay.slots > 0 ? 1 : 0, shared_tiles(pb), shared_heads(pb),
-                            dev_status);
+                            pb.tree ? reinterpret_cast<uint32_t *>(ws + lay.tree) : nullptr, dev_status);
 }
 
 cudaError_t launch_shared_attn(int head_dim, bool is_capped, const CUtensorMap &tm_q, const CUtensorMap &tm_k,

@@ -124,9 +124,6 @@ enum : int { kShJoinNone = 0, kShJoinFew = 1, kShJoinMany = 2 };
 
 cudaError_t launch_shared_plan(const ShProblem &pb, const ShLayout &lay, void *workspace, int grid,
                                int32_t *dev_status, cudaStream_t stream);
-// The masks of a tree's nodes, into the workspace.
-cudaError_t launch_tree_masks(const ShProblem &pb, const ShLayout &lay, void *workspace, int32_t *dev_status,
-                              cudaStream_t stream);
 cudaError_t launch_shared_attn(int head_dim, bool capped, const CUtensorMap &tm_q, const CUtensorMap &tm_k,
                                const CUtensorMap &tm_v, const CUtensorMap &tm_pk, const CUtensorMap &tm_pv,
                                const ShParams &p, int grid, int join, cudaStream_t stream);
