@@ -8,14 +8,17 @@
 // over the pairs (a, b) = (i, i + rot / 2), or (2 i, 2 i + 1) where they are interleaved; dimensions from rot on
 // keep y.  V is copied beside them, out of the fused projection's rows.  All in fp32, rounded to bf16 once.
 //
-// Memory bounds it: every element is read once and written once.  Eight lanes (four at d = 64) take a token, a warp
-// four (eight) of them, and go through the heads.  A lane holds 16 elements of a head that make up eight whole pairs,
-// with the frequencies 8 j .. 8 j + 7 in either layout: it computes their angles once for all heads of its token, the
-// rotation needs no exchange, and the norm a sum over the lanes of a head.  (A warp for one token, with each angle
-// computed once and shuffled to the lanes that need it, and heads left over in the last round: 70,375 tokens of 16/8
-// heads of 128 196 us, 23,041 of 14/2 heads of 64 31 us.)  Where there are few tokens, their heads are dealt out to
-// several warps.
+// Memory bounds it: every element is read once and written once.  A warp takes a token (or a part of its heads, where
+// there are few tokens) in rounds of 1 KB, whole rows one after the other: four tokens at a time, 256 bytes of each, reach
+// 0.63 of the copy rate on rows of 12 KB, this 0.96.  Eight lanes (four at d = 64) hold a head, each 16 of its elements
+// that make up eight whole pairs in either layout, so that the rotation needs no exchange and the norm a sum over the
+// lanes of a head.  The angles of a token are computed once, two (one) per lane, and shuffled to the lanes that need them.
+// Each lane's elements come through shared memory by copies of its own, kRopeAhead rounds ahead, without a barrier.
+// Measured: 70,375 tokens of 16/8 heads of 128 183 us, 6.3 TB/s; 32,768 of 32/8 heads without a norm 124 us, 6.5 TB/s;
+// 23,041 of 14/2 heads of 64 27 us, 3.9 TB/s (the latency of a token's three rounds, the last of which holds two heads).
 #include <cuda_bf16.h>
+
+#include <atomic>
 
 #include "bg_internal.h"
 #include "bg_ptx.cuh"
@@ -24,12 +27,11 @@ namespace bg {
 namespace {
 
 constexpr int kRopeThreads = 256;
-#ifndef CTAS
-#define CTAS 2
-#define BATCH 2
-#endif
-constexpr int kRopeCtas = CTAS;              // per SM
-constexpr int kRopeBatch = BATCH;             // heads whose loads are under way together
+constexpr int kRopeCtas = 2;              // per SM (three leave 80 registers, with spills: 229 us instead of 183)
+// Rounds whose copies are under way, per warp.  Not more: with three the second case below takes 134 us, with four the
+// first one 200.
+constexpr int kRopeAhead = 2;
+constexpr int kRopeSmem = kRopeThreads / 32 * kRopeAhead * 1024;
 
 __device__ __forceinline__ void unpack(const uint4 &v, float *x)
 {
@@ -56,149 +58,242 @@ __device__ __forceinline__ float2 cos_sin(int32_t pos, float hi, float lo)
     return make_float2(__cosf(r), __sinf(r));
 }
 
+// The two runs of 8 elements of a head, at a and b, that lane j of the head's D / 16 lanes holds, whether they turn, and
+// the first of the four frequencies of each.  The lanes' runs lie side by side in memory.  Halves: the runs are the two
+// sides of pairs i .. i + 7 (where they turn).  Interleaved: each holds four pairs.
+template <int D, bool INTERLEAVED>
+struct Share {
+    int a, b, fa, fb;
+    bool ta, tb;
+    __device__ Share(int j, int half)
+    {
+        constexpr int kLanes = D / 16;
+        if (INTERLEAVED) {
+            a = 8 * j;
+            b = 8 * (j + kLanes);
+            ta = a < 2 * half;
+            tb = b < 2 * half;
+            fa = 4 * j;
+            fb = 4 * (j + kLanes);
+        } else {
+            const int n = half / 8;                // lanes that turn
+            ta = tb = j < n;
+            a = 8 * (j < n ? j : j + n);
+            b = 8 * (j < n ? j + n : j + kLanes);
+            fa = 8 * j;
+            fb = 8 * j + 4;
+        }
+    }
+};
+
+// Norm over the lanes of a head, then the rotation of the pairs that this lane holds.  All lanes of the warp call it.
+template <int D, bool INTERLEAVED, bool NORM>
+__device__ __forceinline__ void turn_head(uint4 &a, uint4 &b, const float *w, const float *c, const float *s,
+                                          const Share<D, INTERLEAVED> &at, float eps)
+{
+    float x[16];
+    unpack(a, x);
+    unpack(b, x + 8);
+    if (NORM) {
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sum = fmaf(x[i], x[i], sum);
+#pragma unroll
+        for (int o = 1; o < D / 16; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        const float inv = rsqrtf(fmaf(sum, 1.f / D, eps));
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] *= inv * w[i];
+    }
+    if (INTERLEAVED) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float u = x[2 * i], v = x[2 * i + 1];
+            if (i < 4 ? at.ta : at.tb) {
+                x[2 * i] = u * c[i] - v * s[i];
+                x[2 * i + 1] = v * c[i] + u * s[i];
+            }
+        }
+    } else if (at.ta) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float u = x[i], v = x[8 + i];
+            x[i] = u * c[i] - v * s[i];
+            x[8 + i] = v * c[i] + u * s[i];
+        }
+    }
+    a = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+    b = make_uint4(pack_bf16x2(x[8], x[9]), pack_bf16x2(x[10], x[11]), pack_bf16x2(x[12], x[13]), pack_bf16x2(x[14], x[15]));
+}
+
+// f / (2 pi) as a sum of two numbers.
+__device__ __forceinline__ float2 per_turn(float f)
+{
+    constexpr double kTurn = 0.15915494309189533577;
+    constexpr float kHi = static_cast<float>(kTurn), kLo = static_cast<float>(kTurn - kHi);
+    const float hi = f * kHi;
+    return make_float2(hi, fmaf(f, kLo, fmaf(f, kHi, -hi)));
+}
+
+__device__ __forceinline__ void copy_async(void *smem, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(smem)), "l"(src) : "memory");
+}
+
 template <int D, bool INTERLEAVED, bool NORM>
 __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_kernel(const __grid_constant__ RopeParams p)
 {
-    constexpr int kLanes = D / 16;                 // lanes of a token
-    constexpr int kTokens = 32 / kLanes;           // tokens of a warp
+    constexpr int kLanes = D / 16;                 // lanes of a head
+    constexpr int kHeads = 32 / kLanes;            // heads of a round
+    constexpr int kOwn = D / 64;                   // frequencies whose angle a lane computes
+    extern __shared__ uint4 s_ring[];              // [warp][slot][2][lane]: what a lane copies, it alone reads
     const int lane = threadIdx.x & 31, j = lane % kLanes, sub = lane / kLanes;
+    uint4 *ring = s_ring + (threadIdx.x >> 5) * (kRopeAhead * 64) + lane;
     const int half = p.rot / 2;
     grid_dep_launch();
     grid_dep_wait();
 
-    // elements lo .. lo + 7 and hi .. hi + 7 of a head are this lane's
-    const bool turns = 8 * j < half;
-    const int lo = INTERLEAVED || !turns ? 16 * j : 8 * j;
-    const int hi = INTERLEAVED || !turns ? 16 * j + 8 : 8 * j + half;
-    float f[8];
-    uint32_t axes = 0;                             // two bits each
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        f[i] = turns ? p.inv_freq[8 * j + i] : 0.f;
-        axes |= static_cast<uint32_t>(p.axis[8 * j + i]) << (2 * i);
-    }
+    const Share<D, INTERLEAVED> share(j, half);
+    const int lo = share.a, hi = share.b;
+    const int k0 = p.Hq, v0 = p.Hq + p.Hkv, n_heads = v0 + (p.v ? p.Hkv : 0);
+    // unit u: token u / parts, and its rounds u % parts, + parts, ...
+    const int rounds = (n_heads + kHeads - 1) / kHeads;
+    const int64_t units = p.rows * p.parts, stride = static_cast<int64_t>(gridDim.x) * (kRopeThreads / 32);
+    const int64_t u0 = static_cast<int64_t>(blockIdx.x) * (kRopeThreads / 32) + (threadIdx.x >> 5);
 
-    const int n_heads = p.Hq + p.Hkv + (p.v ? p.Hkv : 0);
-    const int64_t units = (p.rows + kTokens - 1) / kTokens * p.parts;
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * (kRopeThreads / 32);
-    for (int64_t u = static_cast<int64_t>(blockIdx.x) * (kRopeThreads / 32) + (threadIdx.x >> 5); u < units; u += stride) {
-        const int64_t first = u / p.parts * kTokens;
-        const int part = static_cast<int>(u % p.parts);
-        const int begin = part * n_heads / p.parts, end = (part + 1) * n_heads / p.parts;
-        const bool live = first + sub < p.rows;
-        const int64_t row = live ? first + sub : p.rows - 1;
-        float c[8], s[8];
-        if (begin < p.Hq + p.Hkv) {
-            const int64_t place = row / p.rows_per_pos;
-            int32_t pos[BG_MAX_AXES];
-#pragma unroll
-            for (int a = 0; a < BG_MAX_AXES; ++a) pos[a] = a < p.num_axes ? p.positions[a * p.places + place] : 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                int32_t at = pos[0];
-                if (p.num_axes > 1) {
-                    const uint32_t a = (axes >> (2 * i)) & 3u;
-                    at = a < 2 ? (a == 0 ? pos[0] : pos[1]) : (a == 2 ? pos[2] : pos[3]);
-                }
-                // f / (2 pi) as a sum of two numbers
-                constexpr double kTurn = 0.15915494309189533577;
-                constexpr float kTurnHi = static_cast<float>(kTurn), kTurnLo = static_cast<float>(kTurn - kTurnHi);
-                const float f_hi = f[i] * kTurnHi, f_lo = fmaf(f[i], kTurnLo, fmaf(f[i], kTurnHi, -f_hi));
-                const float2 cs = cos_sin(at + p.step, f_hi, f_lo);
-                c[i] = cs.x * p.rope_scale;
-                s[i] = cs.y * p.rope_scale;
+    // ---- copies, kRopeAhead rounds ahead; a group for each round, also behind the last one
+    int64_t u_in = u0;
+    int round_in = 0, slot_in = 0;
+    const __nv_bfloat16 *src_q = nullptr, *src_k = nullptr, *src_v = nullptr;
+    auto start_in = [&] {
+        if (u_in >= units) return;
+        const int64_t row = u_in / p.parts;
+        round_in = static_cast<int>(u_in - row * p.parts);
+        src_q = p.q + row * p.q_stride;
+        src_k = p.k + row * p.k_stride - k0 * D;
+        src_v = p.v + row * p.v_stride - v0 * D;
+    };
+    auto fetch = [&] {
+        if (u_in < units) {
+            const int h = round_in * kHeads + sub;
+            if (h < n_heads) {
+                const __nv_bfloat16 *at = (h < k0 ? src_q : h < v0 ? src_k : src_v) + h * D;
+                copy_async(ring + slot_in * 64, at + lo);
+                copy_async(ring + slot_in * 64 + 32, at + hi);
+            }
+            round_in += p.parts;
+            if (round_in >= rounds) {
+                u_in += stride;
+                start_in();
             }
         }
-        // heads [from, to) of q or k, kRopeBatch at a time; V: copied
-        auto heads = [&](const __nv_bfloat16 *src, __nv_bfloat16 *dst, const __nv_bfloat16 *weight, int from, int to, bool copied) {
-            float w[NORM ? 16 : 1];
-            if (NORM && !copied && from < to) {
-                unpack(*reinterpret_cast<const uint4 *>(weight + lo), w);
-                unpack(*reinterpret_cast<const uint4 *>(weight + hi), w + (NORM ? 8 : 0));
-#pragma unroll
-                for (int i = 0; i < (NORM ? 16 : 1); ++i) w[i] += p.weight_offset;
-            }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (++slot_in == kRopeAhead) slot_in = 0;
+    };
+    start_in();
 #pragma unroll 1
-            for (int h0 = from; h0 < to; h0 += kRopeBatch) {
-                uint4 a[kRopeBatch], b[kRopeBatch];
+    for (int i = 0; i < kRopeAhead; ++i) fetch();
+
+    float2 f[kOwn];
+    int axis[kOwn];
 #pragma unroll
-                for (int k = 0; k < kRopeBatch; ++k) {
-                    const __nv_bfloat16 *at = src + min(h0 + k, to - 1) * D;
-                    a[k] = *reinterpret_cast<const uint4 *>(at + lo);
-                    b[k] = *reinterpret_cast<const uint4 *>(at + hi);
+    for (int m = 0; m < kOwn; ++m) {
+        const int i = lane * kOwn + m;
+        f[m] = per_turn(i < half ? p.inv_freq[i] : 0.f);
+        axis[m] = p.axis[i];
+    }
+    uint4 wq[2], wk[2];
+    if (NORM) {
+        wq[0] = *reinterpret_cast<const uint4 *>(p.q_weight + lo);
+        wq[1] = *reinterpret_cast<const uint4 *>(p.q_weight + hi);
+        wk[0] = *reinterpret_cast<const uint4 *>(p.k_weight + lo);
+        wk[1] = *reinterpret_cast<const uint4 *>(p.k_weight + hi);
+    }
+    int32_t next[kOwn];                            // positions, fetched a unit ahead
+    auto places = [&](int64_t u) {
+        if (u >= units) return;
+        const int64_t place = u / p.parts / p.rows_per_pos;
+#pragma unroll
+        for (int m = 0; m < kOwn; ++m) next[m] = p.positions[axis[m] * p.places + place];
+    };
+    places(u0);
+    int slot = 0;
+    for (int64_t u = u0; u < units; u += stride) {
+        const int64_t row = u / p.parts;
+        float c[8], s[8];
+        {
+            float2 cs[kOwn];
+#pragma unroll
+            for (int m = 0; m < kOwn; ++m) cs[m] = cos_sin(next[m] + p.step, f[m].x, f[m].y);
+            places(u + stride);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {          // frequency e is lane e / kOwn's
+                const int src = ((i < 4 ? share.fa : share.fb) + i % 4) / kOwn;
+                c[i] = __shfl_sync(0xffffffffu, cs[i % kOwn].x, src) * p.rope_scale;
+                s[i] = __shfl_sync(0xffffffffu, cs[i % kOwn].y, src) * p.rope_scale;
+            }
+        }
+        __nv_bfloat16 *dst_q = p.q_out + row * k0 * D, *dst_k = p.k_out + row * p.kv_out_stride - k0 * D;
+        __nv_bfloat16 *dst_v = p.v_out + row * p.kv_out_stride - v0 * D;
+#pragma unroll 1
+        for (int r = static_cast<int>(u - row * p.parts); r < rounds; r += p.parts) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kRopeAhead - 1) : "memory");
+            uint4 a = ring[slot * 64], b = ring[slot * 64 + 32];
+            if (++slot == kRopeAhead) slot = 0;
+            const int h = r * kHeads + sub;
+            if (r * kHeads < v0) {                 // (V's heads of this round keep what they are)
+                float w[16];
+                if (NORM) {
+                    unpack(h < k0 ? wq[0] : wk[0], w);
+                    unpack(h < k0 ? wq[1] : wk[1], w + 8);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) w[i] += p.weight_offset;
                 }
-#pragma unroll
-                for (int k = 0; k < kRopeBatch; ++k) {
-                    if (h0 + k >= to) break;
-                    if (!copied) {
-                        float x[16];
-                        unpack(a[k], x);
-                        unpack(b[k], x + 8);
-                        if (NORM) {
-                            float sum = 0.f;
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) sum = fmaf(x[i], x[i], sum);
-#pragma unroll
-                            for (int o = 1; o < kLanes; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                            const float inv = rsqrtf(fmaf(sum, 1.f / D, p.eps));
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) x[i] *= inv * w[NORM ? i : 0];
-                        }
-                        uint32_t o[8];
-                        if (!turns) {
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) o[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
-                        } else if (INTERLEAVED) {
-#pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                o[i] = pack_bf16x2(x[2 * i] * c[i] - x[2 * i + 1] * s[i], x[2 * i + 1] * c[i] + x[2 * i] * s[i]);
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const int e = 2 * i, g = 2 * i + 1;
-                                o[i] = pack_bf16x2(x[e] * c[e] - x[8 + e] * s[e], x[g] * c[g] - x[8 + g] * s[g]);
-                                o[4 + i] = pack_bf16x2(x[8 + e] * c[e] + x[e] * s[e], x[8 + g] * c[g] + x[g] * s[g]);
-                            }
-                        }
-                        a[k] = make_uint4(o[0], o[1], o[2], o[3]);
-                        b[k] = make_uint4(o[4], o[5], o[6], o[7]);
-                    }
-                    if (live) {
-                        __nv_bfloat16 *at = dst + (h0 + k) * D;
-                        *reinterpret_cast<uint4 *>(at + lo) = a[k];
-                        *reinterpret_cast<uint4 *>(at + hi) = b[k];
-                    }
+                uint4 ta = a, tb = b;
+                turn_head<D, INTERLEAVED, NORM>(ta, tb, w, c, s, share, p.eps);
+                if (h < v0) {
+                    a = ta;
+                    b = tb;
                 }
             }
-        };
-        const int k0 = p.Hq, v0 = p.Hq + p.Hkv;
-        heads(p.q + row * p.q_stride, p.q_out + row * p.Hq * D, p.q_weight, begin, min(end, k0), false);
-        heads(p.k + row * p.k_stride, p.k_out + row * p.kv_out_stride, p.k_weight, max(begin, k0) - k0, min(end, v0) - k0, false);
-        heads(p.v + row * p.v_stride, p.v_out + row * p.kv_out_stride, nullptr, max(begin, v0) - v0, end - v0, true);
+            if (h < n_heads) {
+                __nv_bfloat16 *at = (h < k0 ? dst_q : h < v0 ? dst_k : dst_v) + h * D;
+                *reinterpret_cast<uint4 *>(at + lo) = a;
+                *reinterpret_cast<uint4 *>(at + hi) = b;
+            }
+            fetch();                               // into the slot that has been read
+        }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-template <int D>
-cudaError_t launch_d(const RopeParams &p, bool interleaved, int grid, cudaStream_t stream)
+template <int D, bool INTERLEAVED, bool NORM>
+cudaError_t launch_one(RopeParams &p, int nsm, cudaStream_t stream)
 {
-    const bool norm = p.q_weight != nullptr;
-    auto kern = interleaved ? (norm ? rope_kernel<D, true, true> : rope_kernel<D, true, false>)
-                            : (norm ? rope_kernel<D, false, true> : rope_kernel<D, false, false>);
-    return launch_dependent(kern, dim3(grid), dim3(kRopeThreads), 0, stream, p);
+    const int heads = p.Hq + p.Hkv + (p.v ? p.Hkv : 0);
+    // Few tokens: their heads over several warps, two heads to each at least, as long as the card has room for them.
+    const int64_t warps = kRopeThreads / 32;
+    const int rounds = (heads * D + 511) / 512;
+    p.parts = 1;
+    while (2 * p.parts <= rounds && 2 * p.parts * p.rows <= nsm * kRopeCtas * warps) p.parts *= 2;
+    const int64_t ctas = (p.rows * p.parts + warps - 1) / warps;
+    const int grid = static_cast<int>(ctas < nsm * kRopeCtas ? ctas : nsm * kRopeCtas);
+    static std::atomic<uint64_t> done{0};
+    auto kern = rope_kernel<D, INTERLEAVED, NORM>;
+    const cudaError_t e = ensure_smem_attribute(kern, kRopeSmem, done);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(kern, dim3(grid), dim3(kRopeThreads), kRopeSmem, stream, p);
 }
 
 }  // namespace
 
 cudaError_t launch_qk_rope(RopeParams p, int head_dim, bool interleaved, int nsm, cudaStream_t stream)
 {
-    const int heads = p.Hq + p.Hkv + (p.v ? p.Hkv : 0);
-    const int64_t tokens = 512 / head_dim, groups = (p.rows + tokens - 1) / tokens;      // of a warp
-    // Few tokens: their heads over several warps, two heads to each at least, as long as the card has room for them.
-    p.parts = 1;
-    while (4 * p.parts <= heads && 2 * p.parts * groups <= nsm * kRopeCtas * (kRopeThreads / 32)) p.parts *= 2;
-    const int64_t warps = kRopeThreads / 32, ctas = (groups * p.parts + warps - 1) / warps;
-    const int grid = static_cast<int>(ctas < nsm * kRopeCtas ? ctas : nsm * kRopeCtas);
-    return head_dim == 128 ? launch_d<128>(p, interleaved, grid, stream) : launch_d<64>(p, interleaved, grid, stream);
+    const bool norm = p.q_weight != nullptr;
+    if (head_dim == 128)
+        return interleaved ? (norm ? launch_one<128, true, true>(p, nsm, stream) : launch_one<128, true, false>(p, nsm, stream))
+                           : (norm ? launch_one<128, false, true>(p, nsm, stream) : launch_one<128, false, false>(p, nsm, stream));
+    return interleaved ? (norm ? launch_one<64, true, true>(p, nsm, stream) : launch_one<64, true, false>(p, nsm, stream))
+                       : (norm ? launch_one<64, false, true>(p, nsm, stream) : launch_one<64, false, false>(p, nsm, stream));
 }
 
 }  // namespace bg
