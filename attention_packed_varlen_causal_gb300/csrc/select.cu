@@ -553,7 +553,7 @@ __global__ void __launch_bounds__(kSelThreads)
                 M = mn;
             }
         }
-        row_lse[row] = M + __logf(S);
+        row_lse[row] = M > -INFINITY ? M + __logf(S) : 0.f;   // nothing but -inf: all scores are -inf, not NaN
         sh.above = 0;
     }
     __syncthreads();

@@ -396,7 +396,8 @@ bg_status_t bg_beam_decode_step(const void *q, const void *prompt_k, const void 
  * on `stream` (per-beam selection, then a merge: one level when W * W <= 16384,
  * else two); the logits come from HBM
  * once (a second pass over each beam's row reads back from L2 only the 16-byte
- * groups that can hold one of its W best).  NaN logits are
+ * groups that can hold one of its W best).  A beam all of whose logits are -inf (a
+ * mask that leaves nothing) has the scores -inf, as a dead beam has.  NaN logits are
  * not supported (the result is then unspecified).
  * Errors: BG_ERR_INVALID_ARG for NULL/misaligned pointers, R < 0, a too small
  * workspace or overlaps; BG_ERR_UNSUPPORTED unless 1 <= W <= BG_MAX_BEAM and
