@@ -40,6 +40,7 @@ BG_MAX_VOCAB = 1 << 22
 BG_MAX_TOP = 32
 BG_DTYPE_F32, BG_DTYPE_BF16 = 0, 1
 BG_MAX_AXES = 4
+BG_MAX_HEADS = 65536
 BG_MAX_BIAS = 8191
 BG_MAX_TREE = 1024
 

@@ -897,6 +897,9 @@ bg_status_t bg_selftest_logprobs_timeout(const float *logits, int32_t N, int32_t
 
 namespace {
 
+// Row strides past any memory, whose product with a number of rows could wrap.
+constexpr int64_t kMostStride = int64_t(1) << 31;
+
 // Bytes from the first to the last element of `rows` rows of n elements of 2 bytes, `stride` elements apart.
 size_t strided_bytes(int64_t rows, int64_t stride, int64_t n)
 {
@@ -913,7 +916,8 @@ bg_status_t qk_rope_impl(RopeParams &p, int32_t head_dim, int32_t num_axes, cons
         return BG_ERR_INVALID_ARG;
     if (!(p.eps >= 0.f) || !std::isfinite(p.eps) || !std::isfinite(p.weight_offset) || !std::isfinite(p.rope_scale))
         return BG_ERR_INVALID_ARG;
-    if (!supported_head_dim(head_dim) || num_axes > BG_MAX_AXES || rot_dim > head_dim || rot_dim % 16 != 0)
+    if (!supported_head_dim(head_dim) || num_axes > BG_MAX_AXES || rot_dim > head_dim || rot_dim % 16 != 0 ||
+        p.Hq > BG_MAX_HEADS)
         return BG_ERR_UNSUPPORTED;
     if ((p.q_weight != nullptr) != (p.k_weight != nullptr) || (p.v != nullptr) != (p.v_out != nullptr))
         return BG_ERR_INVALID_ARG;
@@ -926,7 +930,7 @@ bg_status_t qk_rope_impl(RopeParams &p, int32_t head_dim, int32_t num_axes, cons
     }
     const int64_t nq = static_cast<int64_t>(p.Hq) * head_dim, nkv = static_cast<int64_t>(p.Hkv) * head_dim;
     if (p.q_stride < nq || p.k_stride < nkv || (p.v && p.v_stride < nkv) || p.q_stride % 8 || p.k_stride % 8 ||
-        (p.v && p.v_stride % 8))
+        (p.v && p.v_stride % 8) || p.q_stride > kMostStride || p.k_stride > kMostStride || (p.v && p.v_stride > kMostStride))
         return BG_ERR_INVALID_ARG;
     if (p.rows == 0) return BG_OK;
     if (!p.q || !p.k || !p.positions || !p.inv_freq || !p.q_out || !p.k_out) return BG_ERR_INVALID_ARG;
@@ -995,6 +999,7 @@ bg_status_t bg_beam_qk_norm_rope(const void *q, int64_t q_stride, const void *k,
     if (suffix_max > BG_MAX_SUFFIX) return BG_ERR_UNSUPPORTED;
     if (R > 0 && (!v || !suffix_k || !suffix_v)) return BG_ERR_INVALID_ARG;
     const int64_t row = static_cast<int64_t>(Hkv) * head_dim, rows = static_cast<int64_t>(R) * W;
+    if (rows > INT32_MAX) return BG_ERR_UNSUPPORTED;
     RopeParams p{bf16_in(q), bf16_in(k), bf16_in(v), bf16_out(q_out), bf16_out(suffix_k), bf16_out(suffix_v),
                  bf16_in(q_weight), bf16_in(k_weight), base_pos, inv_freq, q_stride, k_stride, v_stride,
                  row * suffix_max, rows, R, W, num_axes, step, Hq, Hkv, 0, 0, eps, weight_offset, rope_scale, {}};
@@ -1018,7 +1023,8 @@ bg_status_t bg_adjust_logits(const void *logits, int32_t in_dtype, int64_t in_st
         return BG_ERR_UNSUPPORTED;
     const int64_t rows = static_cast<int64_t>(num_groups) * rows_per_group;
     if (rows > INT32_MAX) return BG_ERR_UNSUPPORTED;
-    if (in_stride < V || out_stride < V) return BG_ERR_INVALID_ARG;
+    if (in_stride < V || out_stride < V || in_stride > kMostStride || out_stride > kMostStride || mask_stride > kMostStride)
+        return BG_ERR_INVALID_ARG;
     const int64_t words = (static_cast<int64_t>(V) + 31) / 32;
     if (mask ? mask_stride < words : (mask_index || num_masks > 0)) return BG_ERR_INVALID_ARG;
     if (mask && !mask_index && num_masks < rows) return BG_ERR_INVALID_ARG;

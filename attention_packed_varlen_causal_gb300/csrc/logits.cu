@@ -149,7 +149,9 @@ __global__ void __launch_bounds__(kLgThreads, LONG ? 6 : 7)
     grid_dep_launch();
     grid_dep_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int block = static_cast<int>(blockIdx.x) / chunks, v0 = (static_cast<int>(blockIdx.x) - block * chunks) * kChunk;
+    // the first chunks first: vocabularies begin with the frequent tokens, which have the most to change
+    const int all = static_cast<int>(gridDim.x) / chunks, v0 = static_cast<int>(blockIdx.x) / all * kChunk;
+    const int block = static_cast<int>(blockIdx.x) % all;
     const int n = min(kChunk, p.V - v0);
     const int g = block / row_blocks, first = (block - g * row_blocks) * rows_per_cta;
     const int last = min(first + rows_per_cta, p.per);

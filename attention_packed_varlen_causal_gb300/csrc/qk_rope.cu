@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_kernel(const __g
         {
             float2 cs[kOwn];
 #pragma unroll
-            for (int m = 0; m < kOwn; ++m) cs[m] = cos_sin(next[m] + p.step, f[m].x, f[m].y);
+            for (int m = 0; m < kOwn; ++m) cs[m] = cos_sin(static_cast<int32_t>(static_cast<uint32_t>(next[m]) + p.step), f[m].x, f[m].y);
             places(u + stride);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {          // frequency e is lane e / kOwn's

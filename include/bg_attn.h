@@ -80,6 +80,8 @@ typedef enum {
 #define BG_DTYPE_BF16 1
 /* Axes of the positions of bg_packed_qk_norm_rope and bg_beam_qk_norm_rope. */
 #define BG_MAX_AXES 4
+/* Query heads of those calls. */
+#define BG_MAX_HEADS 65536
 /* Biased tokens per group of bg_adjust_logits. */
 #define BG_MAX_BIAS 8191
 /* Nodes of a request's tree in bg_tree_attn. */
@@ -603,8 +605,8 @@ bg_status_t bg_tree_attn_planned(const void *q, const void *k, const void *v, co
  *                            and slot = 0 the new_k and new_v of bg_beam_decode_step)
  *
  *   q, k, v      bf16, row i at q + i * q_stride elements (k_stride, v_stride): Hq,
- *                Hkv and Hkv heads side by side; strides are multiples of 8 and at
- *                least a row.  v may be NULL with v_out (packed form).
+ *                Hkv and Hkv heads side by side; strides are multiples of 8, at least
+ *                a row and at most 2^31.  v may be NULL with v_out (packed form).
  *   q_weight, k_weight   bf16 [head_dim], or both NULL: no norm
  *   eps          finite, >= 0;  weight_offset 0 or, for weights stored as their
  *                difference from 1, 1 (finite)
@@ -617,15 +619,16 @@ bg_status_t bg_tree_attn_planned(const void *q, const void *k, const void *v, co
  *   k_out, v_out bf16 [total_tokens, Hkv, head_dim]
  *   suffix_k, suffix_v  bf16 [R, W, suffix_max, Hkv, head_dim]; the other slots
  *                stay as they are
- *   step         0 or more: tokens between base_pos and this one
+ *   step         0 or more: tokens between base_pos and this one (the sum wraps
+ *                as int32 does)
  * An output may be its own input (q_out == q with q_stride == Hq * head_dim, and so
  * for K and V); outputs may not overlap anything else.
  * One launch, no workspace.
  * Errors: BG_ERR_INVALID_ARG for NULL or misaligned (16 bytes) pointers, bad sizes,
  * strides, scalars or axes, Hq % Hkv != 0, one weight or one of v and v_out without the
  * other, or overlaps; BG_ERR_UNSUPPORTED for head_dim not in {64, 128}, num_axes >
- * BG_MAX_AXES, rot_dim not a multiple of 16 or > head_dim, or suffix_max >
- * BG_MAX_SUFFIX.  No rows is a valid no-op.
+ * BG_MAX_AXES, Hq > BG_MAX_HEADS, rot_dim not a multiple of 16 or > head_dim,
+ * suffix_max > BG_MAX_SUFFIX, or R * W of 2^31 and more.  No rows is a valid no-op.
  */
 bg_status_t bg_packed_qk_norm_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
                          int64_t v_stride, int32_t total_tokens, int32_t Hq, int32_t Hkv, int32_t head_dim,
@@ -684,7 +687,7 @@ bg_status_t bg_beam_qk_norm_rope(const void *q, int64_t q_stride, const void *k,
  * One launch, no workspace.  Logits next to which every logit of the same 16 bytes is
  * masked are not read.
  * Errors: BG_ERR_INVALID_ARG for negative sizes, unknown types, NULL or misaligned
- * pointers, strides below V (mask_stride below its words), num_masks < rows without
+ * pointers, strides below V (mask_stride below its words) or above 2^31, num_masks < rows without
  * mask_index, or out overlapping another argument; BG_ERR_UNSUPPORTED unless 1 <= V
  * <= BG_MAX_VOCAB, for own_max > BG_MAX_SEQLEN, bf16 output of fp32 logits, or 2^31 rows
  * and more.  No rows is a valid no-op.

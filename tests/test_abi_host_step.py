@@ -55,6 +55,7 @@ BOTH = [
     (dict(pos=None), INV), (dict(f=None), INV), (dict(qo=None), INV), (dict(ko=None), INV), (dict(q=F + 8), INV),
     (dict(v=3 * F + 2), INV), (dict(qo=8 * F + 8), INV), (dict(qw=4 * F + 8), INV), (dict(pos=6 * F + 2), INV),
     (dict(f=7 * F + 1), INV), (dict(qo=2 * F), INV), (dict(ko=F + 4096), INV), (dict(vo=9 * F), INV), (dict(ko=6 * F), INV),
+    (dict(Hq=1 << 17, qs=1 << 24), UNS), (dict(qs=1 << 40), INV), (dict(vs=(1 << 31) + 8), INV),
     (dict(qo=F, qs=520), INV), (dict(qo=F + 1024), INV), (dict(vo=2 * F), INV), (dict(qo=4 * F - 512), INV)]
 
 
@@ -96,7 +97,8 @@ def adjust(lib, **kw):
 @pytest.mark.parametrize("kw,expect", [
     (dict(G=-1), INV), (dict(per=0), INV), (dict(P=-1), INV), (dict(S=-1), INV), (dict(B=-1), INV), (dict(M=-1), INV),
     (dict(idt=2), INV), (dict(odt=-1), INV), (dict(V=0), UNS), (dict(V=bg.BG_MAX_VOCAB + 1, istr=1 << 23, ostr=1 << 23), UNS),
-    (dict(S=bg.BG_MAX_SEQLEN + 1), UNS), (dict(odt=1), UNS), (dict(istr=99), INV), (dict(ostr=99), INV), (dict(ms=3), INV),
+    (dict(S=bg.BG_MAX_SEQLEN + 1), UNS), (dict(odt=1), UNS), (dict(istr=99), INV), (dict(ostr=99), INV), (dict(ms=3), INV), (dict(istr=1 << 50), INV),
+    (dict(ostr=1 << 32), INV), (dict(ms=1 << 62), INV),
     (dict(mask=None), INV), (dict(mask=None, mi=None), INV), (dict(mi=None), INV), (dict(G=1 << 20, per=1 << 12), UNS),
     (dict(x=None), INV), (dict(out=None), INV), (dict(pt=None), INV), (dict(cup=None), INV), (dict(own=None), INV),
     (dict(bt=None), INV), (dict(bv=None), INV), (dict(cub=None), INV), (dict(x=F + 2), INV), (dict(out=14 * F + 2), INV),
