@@ -8,6 +8,9 @@
     python profile_case.py shared_prefill --iters 3
     python profile_case.py shared_last --iters 3
     python profile_case.py logprobs --iters 3
+    python profile_case.py rope --iters 3
+    python profile_case.py adjust --iters 3
+    python profile_case.py tree --iters 3
 
 Prefill workloads (tiny, prefill_only, skewed) call bg_packed_prefill_attn
 ``iters`` times on one layer of inputs; decode workloads (beam_short,
@@ -20,7 +23,10 @@ configurations' shapes with fp32 logits N(0, 3) over 65,536 tokens;
 shared_prefill and shared_last call bg_shared_prefill_attn and
 bg_shared_last_token_attn on 32 requests of 15 samples of 56 tokens after a
 prefix of 350 (16/8 heads, d 128); logprobs calls bg_token_logprobs on 8192 rows of
-65,536 bf16 logits.  Inputs are drawn on the device with a seeded generator,
+65,536 bf16 logits; rope calls bg_packed_qk_norm_rope on prefill_only's tokens out of
+a fused projection; adjust calls bg_adjust_logits on 8 searches of 100 beams over
+65,536 fp32 logits, prompts of 500 tokens, 2% of the tokens allowed; tree calls
+bg_tree_attn on 8 drafts of 52 nodes over 8,000 keys (32/8 heads, d 128).  Inputs are drawn on the device with a seeded generator,
 shaped as in ``workloads``.  Nothing is
 timed here: use ncu (or bench.py for timings).
 """
@@ -47,7 +53,8 @@ def main(argv=None):
     ap = argparse.ArgumentParser()
     select = {"select_short": "beam_short", "select_long": "beam_long"}
     scoring = ["shared_prefill", "shared_last", "logprobs"]
-    ap.add_argument("workload", choices=sorted(list(wl.PREFILL_CONFIGS) + list(wl.DECODE_CONFIGS) + list(select) + scoring))
+    steps = ["rope", "adjust", "tree"]
+    ap.add_argument("workload", choices=sorted(list(wl.PREFILL_CONFIGS) + list(wl.DECODE_CONFIGS) + list(select) + scoring + steps))
     ap.add_argument("--iters", type=int, default=3)
     ap.add_argument("--two-call", action="store_true", help="decode: separate reorder and attention calls")
     ap.add_argument("--fp8", action="store_true", help="prefill: E4M3 Q and K (bg_packed_prefill_attn_fp8)")
@@ -78,6 +85,44 @@ def main(argv=None):
         tl = torch.empty((N, K), dtype=torch.float32, device=dev)
         for _ in range(args.iters):
             bg.bg_token_logprobs(logits, tok, logprob=lp, entropy=ent, top_token=tt, top_logprob=tl)
+    elif args.workload == "rope":
+        cfg = wl.PREFILL_CONFIGS["prefill_only"]
+        T, Hq, Hkv, d = sum(wl.prefill_lengths(cfg)), cfg.Hq, cfg.Hkv, cfg.head_dim
+        x = torch.randn((T, (Hq + 2 * Hkv) * d), generator=g, device=dev).to(bf)
+        q, k, v = (t.unflatten(-1, (-1, d)) for t in x.split((Hq * d, Hkv * d, Hkv * d), -1))
+        pos = torch.randint(cfg.hi, (T,), generator=g, device=dev, dtype=torch.int32)
+        w = torch.ones(d, dtype=bf, device=dev)
+        f = (1e6 ** (-torch.arange(d // 2, device=dev) * 2 / d)).float()
+        out = [torch.empty((T, h, d), dtype=bf, device=dev) for h in (Hq, Hkv, Hkv)]
+        for _ in range(args.iters):
+            bg.bg_packed_qk_norm_rope(q, k, v, pos, *out, inv_freq=f, q_weight=w, k_weight=w)
+    elif args.workload == "adjust":
+        G, W, V, P, M = 8, 100, 65536, 500, 512
+        x = torch.randn((G * W, V), generator=g, device=dev) * 2.5
+        out = torch.empty_like(x)
+
+        def tokens(*shape):
+            return (torch.rand(shape, generator=g, device=dev) ** 3 * V).to(torch.int32)
+
+        bits = torch.rand((M, V // 32, 32), generator=g, device=dev) < 0.02
+        mask = (bits.long() << torch.arange(32, device=dev)).sum(-1).to(torch.uint32).view(torch.int32)
+        kw = dict(rows_per_group=W, prompt_tokens=tokens(G * P), cu_prompt=torch.arange(G + 1, dtype=torch.int32, device=dev) * P,
+                  own_tokens=tokens(G * W, 4), repetition=torch.full((G,), 1.2, device=dev), mask=mask,
+                  mask_index=torch.randint(M, (G * W,), generator=g, device=dev, dtype=torch.int32))
+        for _ in range(args.iters):
+            bg.bg_adjust_logits(x, out, **kw)
+    elif args.workload == "tree":
+        R, n, plen, Hq, Hkv, d = 8, 52, 8000, 32, 8, 128
+        q = torch.randn((R * n, Hq, d), generator=g, device=dev).to(bf)
+        k, v = (torch.randn((R * n, Hkv, d), generator=g, device=dev).to(bf) for _ in range(2))
+        pk, pv = (torch.randn((R * plen, Hkv, d), generator=g, device=dev).to(bf) for _ in range(2))
+        parent = torch.arange(R * n, dtype=torch.int32, device=dev) % n // 2 - 1
+        cu = torch.arange(R + 1, dtype=torch.int32, device=dev) * n
+        cup = torch.arange(R + 1, dtype=torch.int32, device=dev) * plen
+        out = torch.empty_like(q)
+        ws = torch.empty(bg.bg_tree_attn_workspace_size(R, R * n, n, plen, Hq, Hkv, d), dtype=torch.uint8, device=dev)
+        for _ in range(args.iters):
+            bg.bg_tree_attn(q, k, v, parent, cu, n, pk, pv, cup, plen, out, workspace=ws)
     elif args.workload in scoring:
         R, S, n, plen, Hq, Hkv, d = 32, 15, 56, 350, 16, 8, 128
         last = args.workload == "shared_last"
