@@ -1022,7 +1022,7 @@ bg_status_t bg_adjust_logits(const void *logits, int32_t in_dtype, int64_t in_st
     if (V < 1 || V > BG_MAX_VOCAB || own_max > BG_MAX_SEQLEN || (in_dtype == BG_DTYPE_F32 && out_dtype == BG_DTYPE_BF16))
         return BG_ERR_UNSUPPORTED;
     const int64_t rows = static_cast<int64_t>(num_groups) * rows_per_group;
-    if (rows > INT32_MAX) return BG_ERR_UNSUPPORTED;
+    if (rows > (1 << 30)) return BG_ERR_UNSUPPORTED;
     if (in_stride < V || out_stride < V || in_stride > kMostStride || out_stride > kMostStride || mask_stride > kMostStride)
         return BG_ERR_INVALID_ARG;
     const int64_t words = (static_cast<int64_t>(V) + 31) / 32;

@@ -689,8 +689,8 @@ bg_status_t bg_beam_qk_norm_rope(const void *q, int64_t q_stride, const void *k,
  * Errors: BG_ERR_INVALID_ARG for negative sizes, unknown types, NULL or misaligned
  * pointers, strides below V (mask_stride below its words) or above 2^31, num_masks < rows without
  * mask_index, or out overlapping another argument; BG_ERR_UNSUPPORTED unless 1 <= V
- * <= BG_MAX_VOCAB, for own_max > BG_MAX_SEQLEN, bf16 output of fp32 logits, or 2^31 rows
- * and more.  No rows is a valid no-op.
+ * <= BG_MAX_VOCAB, for own_max > BG_MAX_SEQLEN, bf16 output of fp32 logits, or more than
+ * 2^30 rows.  No rows is a valid no-op.
  */
 bg_status_t bg_adjust_logits(const void *logits, int32_t in_dtype, int64_t in_stride, int32_t num_groups,
                          int32_t rows_per_group, int32_t V, const int32_t *prompt_tokens, const int32_t *cu_prompt,

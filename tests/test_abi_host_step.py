@@ -99,7 +99,7 @@ def adjust(lib, **kw):
     (dict(idt=2), INV), (dict(odt=-1), INV), (dict(V=0), UNS), (dict(V=bg.BG_MAX_VOCAB + 1, istr=1 << 23, ostr=1 << 23), UNS),
     (dict(S=bg.BG_MAX_SEQLEN + 1), UNS), (dict(odt=1), UNS), (dict(istr=99), INV), (dict(ostr=99), INV), (dict(ms=3), INV), (dict(istr=1 << 50), INV),
     (dict(ostr=1 << 32), INV), (dict(ms=1 << 62), INV),
-    (dict(mask=None), INV), (dict(mask=None, mi=None), INV), (dict(mi=None), INV), (dict(G=1 << 20, per=1 << 12), UNS),
+    (dict(mask=None), INV), (dict(mask=None, mi=None), INV), (dict(mi=None), INV), (dict(G=1 << 20, per=1 << 12), UNS), (dict(G=1, per=(1 << 30) + 1), UNS),
     (dict(x=None), INV), (dict(out=None), INV), (dict(pt=None), INV), (dict(cup=None), INV), (dict(own=None), INV),
     (dict(bt=None), INV), (dict(bv=None), INV), (dict(cub=None), INV), (dict(x=F + 2), INV), (dict(out=14 * F + 2), INV),
     (dict(x=F + 1, idt=1), INV), (dict(pt=2 * F + 2), INV), (dict(lens=5 * F + 1), INV), (dict(mask=12 * F + 2), INV),

@@ -389,3 +389,41 @@ def test_element_offsets_past_31_bits():
     own = torch.full((rows, 1), V - 1, dtype=torch.int32, device="cuda")
     bg.bg_adjust_logits(x, x, rows_per_group=rows, own_tokens=own, presence=torch.tensor([3.0], device="cuda"))
     assert x[-1, -9:].tolist() == [0.0] + [1.0] * 7 + [-2.0] and (x[:-1, -1] == -3).all() and (x[:, :-8] == 0).all()
+
+
+@pytest.mark.parametrize("own", [3, 40], ids=["few", "many"])
+@pytest.mark.parametrize("V", [70, 5000, 4096 * 3 + 5])
+def test_more_rows_than_a_cta_takes(V, own):
+    """Groups of many rows, each with a mask, list and history of its own, and rows that are refused among them."""
+    import torch
+    h, x, t = make(20, 3, 67, V, own=own, prompt=30, bias=9, masks=7)
+    want = check(h, x, t)
+    bad = t["own_lens"].clone()
+    bad[[0, 1, 65, 66, 67, 200]] = own + 1
+    out, st = torch.full_like(x, GUARD), i32([0])
+    bg.bg_adjust_logits(x, out, dev_status=st, **dict(t, own_lens=bad))
+    assert int(st.item()) == bg.BG_DEVSTAT_SEQ_TOO_LONG
+    ok = (bad <= own).nonzero()[:, 0]
+    assert torch.equal(out[ok], want[ok]) and (out[bad > own] == GUARD).all()
+
+
+@pytest.mark.parametrize("types", TYPES, ids="-".join)
+def test_dense_lists(types):
+    """Nearly every token of the first blocks is listed, as a vocabulary's frequent tokens are."""
+    import torch
+    rng = np.random.default_rng(21)
+    V, N = 9000, 6
+    h, x, t = make(21, 2, 3, V, dtype=types[0], prompt=0, own=0, bias=0, masks=3, allowed=0.9)
+    h["prompts"] = [rng.integers(0, 1500, 6000).tolist() for _ in range(2)]
+    t["prompt_tokens"], t["cu_prompt"] = packed(h["prompts"])
+    tokens = rng.integers(0, 2500, (N, 3000))
+    h["own"], t["own_tokens"] = tokens.tolist(), i32(tokens.tolist())
+    h["biases"] = [[(int(k), np.float32(rng.normal())) for k in rng.integers(0, 1200, 2000)] for _ in range(2)]
+    t["bias_tokens"], t["cu_bias"] = packed([[b[0] for b in g] for g in h["biases"]])
+    t["bias_values"] = torch.tensor([float(b[1]) for g in h["biases"] for b in g], device="cuda")
+    check(h, x, t, out_dtype=types[1])
+    if types[0] == types[1]:
+        want = torch.empty_like(x)
+        bg.bg_adjust_logits(x, want, **t)
+        bg.bg_adjust_logits(x, x, **t)
+        assert torch.equal(x, want)

@@ -305,6 +305,22 @@ def test_streams_and_graphs_that_share_a_workspace():
     assert torch.equal(outs[0], want[0])
 
 
+@pytest.mark.parametrize("heads", HEADS[:2], ids=lambda h: "h%d_%d_d%d" % h)
+def test_without_any_prefix(heads):
+    """prefix_k and prefix_v are None: nodes see their paths alone."""
+    import torch
+    x = make(18, [0, 0, 0], [40, 1, 200], *heads)
+    t = device(x)
+    out = torch.empty_like(t["q"])
+    bg.bg_tree_attn(t["q"], t["k"], t["v"], t["parent"], t["cu"], 200, None, None, t["cup"], 0, out, scale=x["scale"],
+                    workspace=workspace(x))
+    assert_close(from_dev(out), None, reference(x), "no prefix")
+    roots = x["parent"] == -1
+    same = out[torch.from_numpy(np.flatnonzero(roots)).cuda()]
+    v = t["v"][torch.from_numpy(np.flatnonzero(roots)).cuda()].repeat_interleave(heads[0] // heads[1], 1)
+    assert torch.equal(same, v)                       # a root's only key is its own
+
+
 def test_no_nodes():
     import torch
     e = torch.empty((0, 4, 64), dtype=torch.bfloat16, device="cuda")
