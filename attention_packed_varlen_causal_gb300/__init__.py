@@ -26,6 +26,16 @@ sm_103a CUDA kernels:
     ``bg_shared_last_token_plan`` and the ``_planned`` calls split them)
   * ``bg_token_logprobs``             log-probability of a given token, entropy
                                       and the best tokens of rows of logits
+  * ``bg_packed_qk_norm_rope``        norm of the heads of Q and K and their
+                                      rotation by position, out of a fused
+                                      projection's rows
+  * ``bg_beam_qk_norm_rope``          the same for every beam's new token, into
+                                      its suffix slot
+  * ``bg_adjust_logits``              penalties, biases and masks on logits
+  * ``bg_tree_attn``                  attention of drafted trees over the
+                                      request's prefix and each node's ancestors
+    (+ ``bg_tree_attn_workspace_size``; ``bg_tree_plan`` and
+    ``bg_tree_attn_planned`` split it)
   * ``bg_selftest_wait_timeout``, ``bg_selftest_logprobs_timeout``  diagnostics of the
                                       bounded-wait failure path
   * ``bg_status_string``

@@ -8,6 +8,8 @@
 //     out   = sum_j softmax_j(x) v_j,kvh
 // Prefill has a query row per token, which sees its sample's rows up to itself; the last-token
 // form has one per sample, which sees the whole sample.
+// A tree of drafted tokens (TREE) is a prefill with one sample per request, of whose rows a query sees its ancestors
+// and itself: each has a mask over them, one word per 32, which the plan makes from the parents.
 //
 // A query tile is dense over the rows of the REQUEST, not of one sample: its 128 rows are
 // (row, head of the kv head) pairs of consecutive packed rows, whatever samples they belong to.
@@ -126,7 +128,7 @@ __device__ void tree_masks(const ShProblem &pb, int request, int32_t *s_parent, 
 // one request, 4.5 where ranges are cut, with 512 threads (4.9 with 1024; 256 are 0.1 faster for a few
 // requests and 0.7 slower for 500 entries); the sort of 500 entries adds 2.5.
 // The offsets are held in shared memory because the searches read them many times.  For trees CTA 1 + r makes the masks of
-// request r beside it (in a launch of their own: 2 us more).
+// request r beside it (in a launch of their own: 1 to 2 us more).
 __global__ void __launch_bounds__(kPlanThreads)
     shared_plan_kernel(const ShProblem pb, const ShKey key, int bt, int32_t *hdr, ShEntry *entries, ShEntry *sorted,
                        ShStart *__restrict__ starts, ShSplit *__restrict__ splits, int grid, int can_split, int tiles_per, int heads,
