@@ -36,7 +36,7 @@ constexpr int kLgThreads = 128;
 constexpr int kLgWarps = kLgThreads / 32;
 constexpr int kChunk = 4096;                         // tokens of a CTA: a block per warp
 constexpr int kBlock = 1024;                         // logits that a warp takes at once
-constexpr int kLgShare = 32;                         // CTAs per SM that the rows are cut to
+constexpr int kLgShare = 16;                         // CTAs per SM that the rows are cut to
 constexpr int kBlocks = kChunk / kBlock;
 static_assert(kChunk / 32 == kLgThreads && kBlocks == kLgWarps, "a bit word per thread, a block per warp");
 constexpr int kBiasShift = 18;                       // two rows' counts meet for a moment: 2 * 65536 fits below it

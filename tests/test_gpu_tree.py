@@ -328,3 +328,25 @@ def test_no_nodes():
     z = i32_dev(np.zeros(3))
     ws = torch.empty(max(256, bg.bg_tree_attn_workspace_size(2, 0, 0, 10, 4, 2, 64)), dtype=torch.uint8, device="cuda")
     bg.bg_tree_attn(e, k, k, i32_dev(np.zeros(0)), z, 0, None, None, z, 10, e, workspace=ws)
+
+
+@pytest.mark.parametrize("heads", [(128, 1, 64), (48, 24, 128), (7, 1, 128)], ids=lambda h: "h%d_%d_d%d" % h)
+def test_other_head_counts(heads):
+    for softcap in (0.0, 30.0):
+        check(make(19, [140, 0, 1100], [9, 33, 5], *heads), softcap, f"heads {heads}")
+
+
+def test_bounds_above_the_lengths():
+    """max_nodes and max_prefix_len are upper bounds: the same bits as with the lengths themselves."""
+    import torch
+    x = make(20, [900, 33], [45, 12], 16, 8, 128)
+    t = device(x)
+    want, out = torch.empty_like(t["q"]), torch.empty_like(t["q"])
+    call(x, t, want)
+    assert_close(from_dev(want), None, reference(x), "exact bounds")
+    y = dict(x, max_nodes=bg.BG_MAX_TREE)
+    call(y, t, out)
+    assert torch.equal(out, want)
+    y["max_prefix"] = 4000
+    call(y, t, out)
+    assert_close(from_dev(out), None, reference(x), "loose bounds")
