@@ -21,7 +21,7 @@
 //   They are many (LONG): the warps take a row together.  Its counts are added to the words beside the copy and taken
 //   away after it, so that a history costs its own reading whatever its length, and integer atomics leave no
 //   order to depend on.
-// Measured: 3200 rows of 65,536 fp32 logits in groups of 100, 2% allowed, 183 us (the writes alone 138); 480 rows of 50,001
+// Measured: 3200 rows of 65,536 fp32 logits in groups of 100, 2% allowed, 180 us (the writes alone 138); 480 rows of 50,001
 // bf16 logits, prompts of 2000-4000 tokens, histories of 350-700, 300 biases, 56 us, a row's chain of counts, barrier,
 // logits, changes and barrier; one row of 65,536 6.9 us.
 #include <cuda_bf16.h>

@@ -14,11 +14,9 @@
 // that make up eight whole pairs in either layout, so that the rotation needs no exchange and the norm a sum over the
 // lanes of a head.  The angles of a token are computed once, two (one) per lane, and shuffled to the lanes that need them.
 // Each lane's elements come through shared memory by copies of its own, kRopeAhead rounds ahead, without a barrier.
-// Measured: 70,375 tokens of 16/8 heads of 128 183 us, 6.3 TB/s; 32,768 of 32/8 heads without a norm 124 us, 6.5 TB/s;
+// Measured: 70,375 tokens of 16/8 heads of 128 175 us, 6.6 TB/s; 32,768 of 32/8 heads without a norm 124 us, 6.5 TB/s;
 // 23,041 of 14/2 heads of 64 27 us, 3.9 TB/s (the latency of a token's three rounds, the last of which holds two heads).
 #include <cuda_bf16.h>
-
-#include <atomic>
 
 #include "bg_internal.h"
 #include "bg_ptx.cuh"
@@ -26,12 +24,13 @@
 namespace bg {
 namespace {
 
-constexpr int kRopeThreads = 256;
-constexpr int kRopeCtas = 2;              // per SM (three leave 80 registers, with spills: 229 us instead of 183)
-// Rounds whose copies are under way, per warp.  Not more: with three the second case below takes 134 us, with four the
-// first one 200.
+// Warps of a CTA: ten where many tokens are normed, which need issue slots (the first case below 175 us; with eight 181);
+// eight where memory alone counts (the second one 124; with ten 134) or few tokens (392 tokens 4.7; with ten 5.5).
+constexpr int kRopeFew = 8, kRopeMany = 10;
+constexpr int kRopeCtas = 2;              // per SM (three leave 80 registers, with spills: 192 us instead of 181)
+// Rounds whose copies are under way, per warp.  Not more: with three the second case takes 134 us, the first (with eight
+// warps) 191, with four 200.
 constexpr int kRopeAhead = 2;
-constexpr int kRopeSmem = kRopeThreads / 32 * kRopeAhead * 1024;
 
 __device__ __forceinline__ void unpack(const uint4 &v, float *x)
 {
@@ -139,8 +138,8 @@ __device__ __forceinline__ void copy_async(void *smem, const void *src)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(smem)), "l"(src) : "memory");
 }
 
-template <int D, bool INTERLEAVED, bool NORM>
-__global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_kernel(const __grid_constant__ RopeParams p)
+template <int D, bool INTERLEAVED, bool NORM, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, kRopeCtas) rope_kernel(const __grid_constant__ RopeParams p)
 {
     constexpr int kLanes = D / 16;                 // lanes of a head
     constexpr int kHeads = 32 / kLanes;            // heads of a round
@@ -157,8 +156,8 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_kernel(const __g
     const int k0 = p.Hq, v0 = p.Hq + p.Hkv, n_heads = v0 + (p.v ? p.Hkv : 0);
     // unit u: token u / parts, and its rounds u % parts, + parts, ...
     const int rounds = (n_heads + kHeads - 1) / kHeads;
-    const int64_t units = p.rows * p.parts, stride = static_cast<int64_t>(gridDim.x) * (kRopeThreads / 32);
-    const int64_t u0 = static_cast<int64_t>(blockIdx.x) * (kRopeThreads / 32) + (threadIdx.x >> 5);
+    const int64_t units = p.rows * p.parts, stride = static_cast<int64_t>(gridDim.x) * WARPS;
+    const int64_t u0 = static_cast<int64_t>(blockIdx.x) * WARPS + (threadIdx.x >> 5);
 
     // ---- copies, kRopeAhead rounds ahead; a group for each round, also behind the last one
     int64_t u_in = u0;
@@ -201,12 +200,22 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_kernel(const __g
         f[m] = per_turn(i < half ? p.inv_freq[i] : 0.f);
         axis[m] = p.axis[i];
     }
-    uint4 wq[2], wk[2];
+    // offset + weight of the elements that lane j of a head holds, four at (part * kLanes + j)
+    __shared__ float4 s_weight[NORM ? 2 : 1][NORM ? 4 * kLanes : 1];
     if (NORM) {
-        wq[0] = *reinterpret_cast<const uint4 *>(p.q_weight + lo);
-        wq[1] = *reinterpret_cast<const uint4 *>(p.q_weight + hi);
-        wk[0] = *reinterpret_cast<const uint4 *>(p.k_weight + lo);
-        wk[1] = *reinterpret_cast<const uint4 *>(p.k_weight + hi);
+        if (threadIdx.x < 2 * kLanes) {
+            const int t = threadIdx.x % kLanes, k = threadIdx.x / kLanes;
+            const Share<D, INTERLEAVED> of(t, half);
+            const __nv_bfloat16 *weight = k == 0 ? p.q_weight : p.k_weight;
+            float w[16];
+            unpack(*reinterpret_cast<const uint4 *>(weight + of.a), w);
+            unpack(*reinterpret_cast<const uint4 *>(weight + of.b), w + 8);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] += p.weight_offset;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s_weight[k][i * kLanes + t] = make_float4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        }
+        __syncthreads();
     }
     int32_t next[kOwn];                            // positions, fetched a unit ahead
     auto places = [&](int64_t u) {
@@ -243,10 +252,15 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_kernel(const __g
             if (r * kHeads < v0) {                 // (V's heads of this round keep what they are)
                 float w[16];
                 if (NORM) {
-                    unpack(h < k0 ? wq[0] : wk[0], w);
-                    unpack(h < k0 ? wq[1] : wk[1], w + 8);
+                    const float4 *from = s_weight[h < k0 ? 0 : 1] + j;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) w[i] += p.weight_offset;
+                    for (int i = 0; i < 4; ++i) {
+                        const float4 v = from[i * kLanes];
+                        w[4 * i] = v.x;
+                        w[4 * i + 1] = v.y;
+                        w[4 * i + 2] = v.z;
+                        w[4 * i + 3] = v.w;
+                    }
                 }
                 uint4 ta = a, tb = b;
                 turn_head<D, INTERLEAVED, NORM>(ta, tb, w, c, s, share, p.eps);
@@ -266,22 +280,28 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_kernel(const __g
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
+template <int D, bool INTERLEAVED, bool NORM, int WARPS>
+cudaError_t launch_warps(RopeParams &p, int nsm, cudaStream_t stream)
+{
+    // Few tokens: their heads over several warps, a round to each at least, as long as the card has room for them.
+    const int64_t room = static_cast<int64_t>(nsm) * kRopeCtas * WARPS;
+    const int heads = p.Hq + p.Hkv + (p.v ? p.Hkv : 0), rounds = (heads * D + 511) / 512;
+    p.parts = 1;
+    while (2 * p.parts <= rounds && 2 * p.parts * p.rows <= room) p.parts *= 2;
+    const int64_t ctas = (p.rows * p.parts + WARPS - 1) / WARPS;
+    const int grid = static_cast<int>(ctas < nsm * kRopeCtas ? ctas : nsm * kRopeCtas);
+    constexpr int kSmem = WARPS * kRopeAhead * 1024;
+    static_assert(kSmem <= 48 * 1024, "no larger limit to be asked for");
+    return launch_dependent(rope_kernel<D, INTERLEAVED, NORM, WARPS>, dim3(grid), dim3(32 * WARPS), kSmem, stream, p);
+}
+
 template <int D, bool INTERLEAVED, bool NORM>
 cudaError_t launch_one(RopeParams &p, int nsm, cudaStream_t stream)
 {
-    const int heads = p.Hq + p.Hkv + (p.v ? p.Hkv : 0);
-    // Few tokens: their heads over several warps, two heads to each at least, as long as the card has room for them.
-    const int64_t warps = kRopeThreads / 32;
-    const int rounds = (heads * D + 511) / 512;
-    p.parts = 1;
-    while (2 * p.parts <= rounds && 2 * p.parts * p.rows <= nsm * kRopeCtas * warps) p.parts *= 2;
-    const int64_t ctas = (p.rows * p.parts + warps - 1) / warps;
-    const int grid = static_cast<int>(ctas < nsm * kRopeCtas ? ctas : nsm * kRopeCtas);
-    static std::atomic<uint64_t> done{0};
-    auto kern = rope_kernel<D, INTERLEAVED, NORM>;
-    const cudaError_t e = ensure_smem_attribute(kern, kRopeSmem, done);
-    if (e != cudaSuccess) return e;
-    return launch_dependent(kern, dim3(grid), dim3(kRopeThreads), kRopeSmem, stream, p);
+    // many: eight tokens and more for each warp
+    if (NORM && p.rows >= static_cast<int64_t>(8) * nsm * kRopeCtas * kRopeMany)
+        return launch_warps<D, INTERLEAVED, NORM, NORM ? kRopeMany : kRopeFew>(p, nsm, stream);
+    return launch_warps<D, INTERLEAVED, NORM, kRopeFew>(p, nsm, stream);
 }
 
 }  // namespace

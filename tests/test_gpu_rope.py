@@ -116,6 +116,20 @@ def test_many_rows():
     check(inputs(2, 20011, 14, 2, 64))
 
 
+@pytest.mark.parametrize("norm", [True, False], ids=["norm", "plain"])
+@pytest.mark.parametrize("interleaved", [False, True], ids=["halves", "pairs"])
+@pytest.mark.parametrize("heads", [(4, 2, 128), (7, 1, 64)], ids=lambda h: "h%d_%d_d%d" % h)
+def test_a_large_batch_is_its_parts(heads, interleaved, norm):
+    """Launches of many and of few tokens give the same bits."""
+    import torch
+    x = inputs(19, 26001, *heads, norm=norm, axes=2)
+    x["kw"]["interleaved"] = interleaved
+    whole = run(x)
+    for a, b in ((0, 900), (12000, 12700), (25500, 26001)):
+        part = run(dict(x, qkv=x["qkv"][a:b], positions=x["positions"][:, a:b].contiguous()))
+        assert all(torch.equal(w[a:b], t) for w, t in zip(whole, part))
+
+
 @pytest.mark.parametrize("interleaved", [False, True], ids=["halves", "pairs"])
 @pytest.mark.parametrize("d,rot", [(128, 16), (128, 64), (128, 112), (64, 16), (64, 32), (64, 48)])
 def test_partly_rotated(d, rot, interleaved):
