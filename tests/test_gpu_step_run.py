@@ -168,6 +168,34 @@ def test_beams_with_nothing_left_are_dead():
         assert all((0 <= t).all() and (t < n).all() for t, n in ((tok, V), (par, W)))
 
 
+@pytest.mark.parametrize("heads", [(16, 8, 128), (14, 2, 64)], ids=lambda h: "h%d_%d_d%d" % h)
+def test_new_tokens_straight_into_the_suffix(heads):
+    """Reorder without an append, K and V of the new tokens into their slot, attention: what bg_beam_decode_step gives
+    with new_k and new_v, bit for bit."""
+    import torch
+    m = Model(*heads, seed=6)
+    Hq, Hkv, d = heads
+    R, W, slots = 3, 33, 4
+    lengths = [40, 0, 129]
+    cup = i32_dev(np.concatenate(([0], np.cumsum(lengths))))
+    pk, pv = m.prompt(lengths)
+    base = i32_dev(np.array(lengths))
+    src = [torch.randn((R, W, slots, Hkv, d), generator=m.gen, device="cuda").bfloat16() for _ in range(2)]
+    for t in (1, 3):
+        parent = torch.randint(W, (R, W), generator=m.gen, device="cuda", dtype=torch.int32)
+        x = m.embed[torch.randint(VOCAB, (R, W), generator=m.gen, device="cuda")]
+        q, k, v = m.split(x)
+        nk, nv = (torch.empty((R, W, 1, Hkv, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        q1, q2, o1, o2 = (torch.empty((R, W, Hq, d), dtype=torch.bfloat16, device="cuda") for _ in range(4))
+        a, b = ([torch.zeros_like(s) for s in src] for _ in range(2))
+        bg.bg_beam_qk_norm_rope(q, k, v, base, t - 1, q1, nk, nv, 0, **m.kw)
+        bg.bg_beam_decode_step(q1, pk, pv, cup, max(lengths), *src, parent, nk[:, :, 0], nv[:, :, 0], *a, t, o1)
+        bg.bg_beam_suffix_reorder(*src, *b, parent, t - 1)
+        bg.bg_beam_qk_norm_rope(q, k, v, base, t - 1, q2, *b, t - 1, **m.kw)
+        bg.bg_beam_decode_attn(q2, pk, pv, cup, max(lengths), *b, t, o2)
+        assert torch.equal(q1, q2) and torch.equal(o1, o2) and all(torch.equal(s, u) for s, u in zip(a, b))
+
+
 class Verify:
     """Two layers of a verify step; the buffers stay, so that the whole step can be captured."""
 
