@@ -22,8 +22,8 @@
 //   away after it, so that a history costs its own reading whatever its length, and integer atomics leave no
 //   order to depend on.
 // Measured: 3200 rows of 65,536 fp32 logits in groups of 100, 2% allowed, 180 us (the writes alone 138); 480 rows of 50,001
-// bf16 logits, prompts of 2000-4000 tokens, histories of 350-700, 300 biases, 56 us, a row's chain of counts, barrier,
-// logits, changes and barrier; one row of 65,536 6.9 us.
+// bf16 logits, prompts of 2000-4000 tokens, histories of 350-700, 300 biases, 54 us, a row's chain of counts, barrier,
+// logits, changes and barrier; one row of 65,536 7 us.
 #include <cuda_bf16.h>
 
 #include "bg_internal.h"
@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(kLgThreads, LONG ? 6 : 7)
     // the words together.
     auto change = [&](const TI *in, TO *out, uint32_t bits, uint32_t allowed) {
         constexpr int kFew = 3, kWords = 4;
-        if (__any_sync(0xffffffffu, __popc(bits) > 2 * kFew)) {
+        if (__any_sync(0xffffffffu, __popc(bits) > 3 * kFew)) {
 #pragma unroll 1
             for (int l0 = 0; l0 < 32; l0 += kWords) {
                 int t[kWords];
@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(kLgThreads, LONG ? 6 : 7)
             }
         } else {
 #pragma unroll 1
-            for (int i = 0; i < 2; ++i) {
+            while (__any_sync(0xffffffffu, bits != 0)) {
                 int t[kFew];
                 bool ok[kFew];
 #pragma unroll
@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(kLgThreads, LONG ? 6 : 7)
                 }
             }
             __syncwarp();                                      // what other lanes have copied is there
-            if (__any_sync(0xffffffffu, bits != 0)) change(in, out, bits, allowed);
+            change(in, out, bits, allowed);
             if (leads) {
                 const int u[1] = {t};
                 const bool yes[1] = {true};
