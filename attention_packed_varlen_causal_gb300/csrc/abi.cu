@@ -951,9 +951,11 @@ bg_status_t qk_rope_impl(RopeParams &p, int32_t head_dim, int32_t num_axes, cons
     const size_t outb[3] = {static_cast<size_t>(p.rows) * nq * 2, kv_bytes, p.v ? kv_bytes : 0};
     p.k_out += slot * nkv;
     if (p.v) p.v_out += slot * nkv;
-    // in place: the output is the input, row by row
-    const bool same[3] = {p.q_out == p.q && p.q_stride == nq, p.k_out == p.k && p.k_stride == p.kv_out_stride,
-                          p.v && p.v_out == p.v && p.v_stride == p.kv_out_stride};
+    // in place: the output is the input, row by row (of one row the strides do not matter)
+    const bool one = p.rows == 1;
+    const bool same[3] = {p.q_out == p.q && (one || p.q_stride == nq),
+                          p.k_out == p.k && (one || p.k_stride == p.kv_out_stride),
+                          p.v && p.v_out == p.v && (one || p.v_stride == p.kv_out_stride)};
     for (int o = 0; o < 3; ++o) {
         for (int i = 0; i < 7; ++i)
             if (!(i == o && same[o]) && overlap(out[o], outb[o], in[i], inb[i])) return BG_ERR_INVALID_ARG;

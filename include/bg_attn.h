@@ -621,8 +621,9 @@ bg_status_t bg_tree_attn_planned(const void *q, const void *k, const void *v, co
  *                stay as they are
  *   step         0 or more: tokens between base_pos and this one (the sum wraps
  *                as int32 does)
- * An output may be its own input (q_out == q with q_stride == Hq * head_dim, and so
- * for K and V); outputs may not overlap anything else.
+ * An output may be its own input: q_out == q with q_stride == Hq * head_dim, and so
+ * for K and V (beam form: the slot itself, with k_stride == suffix_max * Hkv * head_dim);
+ * the stride of a single row does not matter.  Outputs may not overlap anything else.
  * One launch, no workspace.
  * Errors: BG_ERR_INVALID_ARG for NULL or misaligned (16 bytes) pointers, bad sizes,
  * strides, scalars or axes, Hq % Hkv != 0, one weight or one of v and v_out without the
