@@ -42,16 +42,17 @@ __device__ __forceinline__ void unpack(const uint4 &v, float *x)
     }
 }
 
-// cos and sin of 2 pi * pos * (hi + lo).  The products with the upper and the lower bits of pos are held exactly as a
-// rounded value and its error (both factors have few enough bits), and whole turns are dropped exactly, so that the
-// angle is off by about 2^-20 for positions up to 2^24, and 2^-17 for all others (of frequencies up to 1).
+// cos and sin of 2 pi * pos * (hi + lo).  Whole turns are taken from the products with the upper and the lower bits of pos
+// before these are rounded (a far position's first one is exact then, and may hold some more).  What is left: the three
+// fractions and the last one's sum round by 2^-25 or 2^-26 of a turn, their sum by 2^-25 and 2^-24, 11 * 2^-26 together; lo
+// rounds by 2^-52 (times pos); 2 pi and its product by 2^-22.  For frequencies up to 1 the angle is off by less than 2^-19
+// for positions up to 2^24 and 2^-17 for all others.
 __device__ __forceinline__ float2 cos_sin(int32_t pos, float hi, float lo)
 {
     const float up = static_cast<float>(pos & ~0xfff), low = static_cast<float>(pos & 0xfff);
-    const float t1 = up * hi, t2 = low * hi, t3 = static_cast<float>(pos) * lo;
-    const float e1 = fmaf(up, hi, -t1), e2 = fmaf(low, hi, -t2);
-    float r = (t1 - rintf(t1)) + (t2 - rintf(t2));
-    r += (e1 - rintf(e1)) + e2 + (t3 - rintf(t3));
+    const float f1 = fmaf(up, hi, -rintf(up * hi)), f2 = fmaf(low, hi, -rintf(low * hi));
+    const float f3 = fmaf(up, lo, -rintf(up * lo));
+    float r = ((f1 - rintf(f1)) + f2) + fmaf(low, lo, f3);
     r = (r - rintf(r)) * 6.2831853071795864769f;
     // [-pi, pi], where the fast forms are off by at most 2^-21; outputs are rounded to 2^-9 of theirs
     return make_float2(__cosf(r), __sinf(r));
@@ -124,13 +125,18 @@ __device__ __forceinline__ void turn_head(uint4 &a, uint4 &b, const float *w, co
     b = make_uint4(pack_bf16x2(x[8], x[9]), pack_bf16x2(x[10], x[11]), pack_bf16x2(x[12], x[13]), pack_bf16x2(x[14], x[15]));
 }
 
-// f / (2 pi) as a sum of two numbers.
+// f / (2 pi) as a sum of two numbers, the lower one at most half a step of the upper one: otherwise its own rounding,
+// times a far position, would be four times as large.
 __device__ __forceinline__ float2 per_turn(float f)
 {
     constexpr double kTurn = 0.15915494309189533577;
     constexpr float kHi = static_cast<float>(kTurn), kLo = static_cast<float>(kTurn - kHi);
-    const float hi = f * kHi;
-    return make_float2(hi, fmaf(f, kLo, fmaf(f, kHi, -hi)));
+    constexpr float kRest = static_cast<float>(kTurn - kHi - kLo);
+    const float h = f * kHi, e = fmaf(f, kHi, -h);            // h + e is f * kHi
+    const float p = f * kLo, pe = fmaf(f, kRest, fmaf(f, kLo, -p));
+    const float s = e + p, b = s - e, se = (e - (s - b)) + (p - b);      // s + se is e + p
+    const float hi = h + s;
+    return make_float2(hi, (s - (hi - h)) + (se + pe));
 }
 
 __device__ __forceinline__ void copy_async(void *smem, const void *src)

@@ -596,8 +596,9 @@ bg_status_t bg_tree_attn_planned(const void *q, const void *k, const void *v, co
  *     s     = rope_scale sin(angle)            for i < rot_dim / 2
  *     (out_a, out_b) = (y_a c - y_b s, y_b c + y_a s)
  * over the pairs (a, b) = (i, i + rot_dim / 2), or (2 i, 2 i + 1) if interleaved;
- * out = y from rot_dim on.  V is copied.  Angles are off by about 2^-20 for positions
- * up to 2^24 and 2^-17 for any other (with frequencies of at most 1).
+ * out = y from rot_dim on.  V is copied.  Angles are off by less than 2^-19 for positions
+ * up to 2^24 and 2^-17 for any other (with frequencies of at most 1), their cosines and
+ * sines by 2^-21 more.
  *   bg_packed_qk_norm_rope   any packed tokens, each with its positions
  *   bg_beam_qk_norm_rope     the new token of every beam of a search: beam b of
  *                            request r is at base_pos[., r] + step, and its K and V
