@@ -32,6 +32,7 @@ BG_DEVSTAT_TOKEN = 0x80
 BG_DEVSTAT_TIMEOUT = 0x100
 BG_DEVSTAT_BIAS = 0x200
 BG_DEVSTAT_MASK = 0x400
+BG_DEVSTAT_PENALTY = 0x800
 BG_MAX_SUFFIX = 16
 BG_MAX_SEQLEN = 65536
 BG_NOALLOC_SCRATCH_BYTES = 1 << 20

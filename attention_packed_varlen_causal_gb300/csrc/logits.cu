@@ -195,6 +195,8 @@ __global__ void __launch_bounds__(kLgThreads, LONG ? 6 : 7)
         bb = p.cu_bias[g + 1];
         if (!offsets_ok(ba, bb, p.total_bias, g, p.groups) || bb - ba > BG_MAX_BIAS) bad |= BG_DEVSTAT_BIAS;
     }
+    // the quotient comes by the reciprocal (below), which is a normal number for these factors alone
+    if (p.repetition && !(p.repetition[g] >= 0x1p-126f && p.repetition[g] <= 0x1p126f)) bad |= BG_DEVSTAT_PENALTY;
     if (bad) {                                       // the same for all threads
         if (tid == 0 && p.dev_status) atomicOr(p.dev_status, bad);
         return;

@@ -65,6 +65,7 @@ typedef enum {
 #define BG_DEVSTAT_TIMEOUT      0x100 /* an internal pipeline wait ran out          */
 #define BG_DEVSTAT_BIAS         0x200 /* cu_bias invalid or a list > BG_MAX_BIAS    */
 #define BG_DEVSTAT_MASK         0x400 /* a mask index is outside [-1, num_masks)    */
+#define BG_DEVSTAT_PENALTY      0x800 /* a repetition penalty outside [2^-126, 2^126] */
 
 /* Supported shapes: head_dim in {64, 128}; Hq % Hkv == 0; for decode
  * Hq/Hkv <= 128; suffix_max <= BG_MAX_SUFFIX; max_seqlen <= BG_MAX_SEQLEN. */
@@ -670,7 +671,8 @@ bg_status_t bg_beam_qk_norm_rope(const void *q, int64_t q_stride, const void *k,
  *   own_tokens   int32 [rows, own_max], of which row i has own_lens[i] (int32, device;
  *                NULL: own_max); NULL with own_max == 0.  own_max <= BG_MAX_SEQLEN
  *   repetition, frequency, presence   fp32 [num_groups], device, each may be NULL
- *                (1, 0, 0); repetition is > 0
+ *                (1, 0, 0); repetition is between 2^-126 and 2^126, and x / repetition
+ *                is x times its reciprocal (both round)
  *   bias_tokens, bias_values   int32 and fp32 [total_bias], those of group g at
  *                cu_bias[g] .. cu_bias[g+1]-1 (int32 [num_groups+1], device), at most
  *                BG_MAX_BIAS; NULL with total_bias == 0
@@ -684,8 +686,8 @@ bg_status_t bg_beam_qk_norm_rope(const void *q, int64_t q_stride, const void *k,
  *                type and stride); elements between rows are left alone.
  *   dev_status   device int32 or NULL
  * A listed token outside [0, V) is ignored and raises BG_DEVSTAT_TOKEN.  A group
- * whose offsets are bad (BG_DEVSTAT_CU_PROMPT, _BIAS) and a row whose length or mask
- * index is (BG_DEVSTAT_SEQ_TOO_LONG, _MASK) are not written.
+ * whose offsets or repetition are bad (BG_DEVSTAT_CU_PROMPT, _BIAS, _PENALTY) and a row
+ * whose length or mask index is (BG_DEVSTAT_SEQ_TOO_LONG, _MASK) are not written.
  * One launch, no workspace.  Logits next to which every logit of the same 16 bytes is
  * masked are not read.
  * Errors: BG_ERR_INVALID_ARG for negative sizes, unknown types, NULL or misaligned
