@@ -1028,7 +1028,8 @@ bg_status_t bg_adjust_logits(const void *logits, int32_t in_dtype, int64_t in_st
     if (in_stride < V || out_stride < V || in_stride > kMostStride || out_stride > kMostStride || mask_stride > kMostStride)
         return BG_ERR_INVALID_ARG;
     const int64_t words = (static_cast<int64_t>(V) + 31) / 32;
-    if (mask ? mask_stride < words : (mask_index || num_masks > 0)) return BG_ERR_INVALID_ARG;
+    // an index may come without masks, of which there are none then: each row's is -1
+    if (mask ? mask_stride < words : num_masks > 0) return BG_ERR_INVALID_ARG;
     if (mask && !mask_index && num_masks < rows) return BG_ERR_INVALID_ARG;
     if (rows == 0) return BG_OK;
     // an empty list may come without its tokens

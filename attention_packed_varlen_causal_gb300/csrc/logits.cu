@@ -171,7 +171,8 @@ __global__ void __launch_bounds__(kLgThreads, LONG ? 6 : 7)
         Row R = {-1, 0, {}};
         if (r >= last) return R;
         const int64_t row = row_at(r);
-        if (p.mask) R.m = p.mask_index ? p.mask_index[row] : static_cast<int>(row);
+        if (p.mask_index) R.m = p.mask_index[row];
+        else if (p.mask) R.m = static_cast<int>(row);
         if (p.own) R.len = p.own_lens ? p.own_lens[row] : p.own_max;
 #pragma unroll
         for (int k = 0; k < kHeld; ++k) {
@@ -299,7 +300,7 @@ __global__ void __launch_bounds__(kLgThreads, LONG ? 6 : 7)
     };
     // whether the row can be written
     auto row_ok = [&](const Row &R, bool tell) {
-        const int wrong = (p.mask && (R.m < -1 || R.m >= p.num_masks) ? BG_DEVSTAT_MASK : 0) |
+        const int wrong = (R.m < -1 || R.m >= p.num_masks ? BG_DEVSTAT_MASK : 0) |
                           (R.len < 0 || R.len > p.own_max ? BG_DEVSTAT_SEQ_TOO_LONG : 0);
         if (wrong && tell && p.dev_status) atomicOr(p.dev_status, wrong);
         return wrong == 0;

@@ -679,8 +679,8 @@ bg_status_t bg_beam_qk_norm_rope(const void *q, int64_t q_stride, const void *k,
  *   mask         uint32 [num_masks, mask_stride], device: bit v % 32 of word v / 32
  *                of a mask is 1 where token v is allowed (bits from V on do not
  *                matter), mask_stride >= ceil(V / 32); NULL: every token is allowed
- *   mask_index   int32 [rows], device: the mask of each row, -1 for none; NULL: row
- *                i has mask i
+ *   mask_index   int32 [rows], device: the mask of each row, -1 for none (of every row
+ *                where num_masks is 0, with mask NULL or not); NULL: row i has mask i
  *   out          fp32 or bf16 (out_dtype), row i at out + i * out_stride, out_stride
  *                >= V; bf16 only from bf16.  May be the logits themselves (same
  *                type and stride); elements between rows are left alone.

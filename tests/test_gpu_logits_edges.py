@@ -1,4 +1,4 @@
-"""GPU edges of bg_adjust_logits: penalties at and past the ends of their range."""
+"""GPU edges of bg_adjust_logits: penalties at and past the ends of their range, an index of no masks."""
 import math
 
 import numpy as np
@@ -71,3 +71,29 @@ def test_penalties_at_the_ends_of_their_range(types, own_room):
     bg.bg_adjust_logits(x, out, rows_per_group=per, repetition=torch.from_numpy(rep).cuda(), dev_status=st, **t)
     assert int(st.item()) == 0
     tl.assert_close(out, olg.adjust(x.double().cpu().numpy(), per, repetition=rep, **h), types[1] == "bfloat16")
+
+
+@pytest.mark.parametrize("own_room", [3, 60])
+@pytest.mark.parametrize("V", [70, 4500])
+def test_no_masks_at_all(V, own_room):
+    """A step none of whose rows has a grammar: an empty set of masks (or none) and an index of -1 change nothing; any other
+    index is reported and its row left as it was."""
+    import torch
+    G, per = 3, 2
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn((G * per, V), generator=gen, device="cuda")
+    h, t = lists(own_room, V, G * per, G)
+    kw = dict(t, rows_per_group=per, repetition=torch.full((G,), 1.25, device="cuda"))
+    want = torch.empty_like(x)
+    bg.bg_adjust_logits(x, want, **kw)
+    for mask in (torch.empty((0, (V + 31) // 32), dtype=torch.int32, device="cuda"), None):
+        index = tl.i32([-1] * (G * per))
+        out, st = torch.full_like(x, tl.GUARD), tl.i32([0])
+        bg.bg_adjust_logits(x, out, mask=mask, mask_index=index, dev_status=st, **kw)
+        assert int(st.item()) == 0 and torch.equal(out, want)
+        for bad in (0, -2, 1 << 30):
+            index[3] = bad
+            out, st = torch.full_like(x, tl.GUARD), tl.i32([0])
+            bg.bg_adjust_logits(x, out, mask=mask, mask_index=index, dev_status=st, **kw)
+            rest = [0, 1, 2, 4, 5]
+            assert int(st.item()) == bg.BG_DEVSTAT_MASK and (out[3] == tl.GUARD).all() and torch.equal(out[rest], want[rest])
