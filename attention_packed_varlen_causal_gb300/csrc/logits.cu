@@ -146,7 +146,7 @@ template <typename TI, typename TO, int N, bool LONG>
 __global__ void __launch_bounds__(kLgThreads, LONG ? 6 : 7)
     logits_kernel(const LogitsParams p, int chunks, int rows_per_cta, int row_blocks)
 {
-    extern __shared__ uint32_t table[];              // [kChunk], where there are biases or counts
+    extern __shared__ __align__(16) uint32_t table[];      // [kChunk], where there are biases or counts; cleared as uint4
     __shared__ uint32_t s_prompt[kChunk / 32], s_bias[kChunk / 32], s_own[LONG ? kChunk / 32 : 1];
     grid_dep_launch();
     grid_dep_wait();
