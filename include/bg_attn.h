@@ -557,6 +557,12 @@ bg_status_t bg_shared_last_token_attn_planned(const void *q, const void *k, cons
  *   workspace    at least bg_tree_attn_workspace_size(...) bytes, 256-byte
  *                aligned; contents on entry do not matter; not for calls that
  *                overlap in time
+ * Prefixes lie side by side without gaps.  Caches that grow where they lie (accepted
+ * nodes are appended to every request's) leave room behind each: the free rows between
+ * two prefixes are the prefix of a request without nodes, which nobody reads.  2 R
+ * requests with cu_nodes 0, n0, n0, n0 + n1, n0 + n1, .. and cu_prefix 0, l0, c, c + l1,
+ * 2 c, .. are R requests with room for c rows each; max_prefix_len bounds the free rows
+ * as well.  total_prefix then stays, and a captured step replays on the next offsets.
  * Layers that share one packing and one tree plan once: bg_tree_plan, then
  * bg_tree_attn_planned per layer with the same offsets, parents and sizes, under
  * the rules of bg_shared_prefill_plan (the parents are read by the plan alone).
