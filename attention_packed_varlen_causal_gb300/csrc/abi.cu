@@ -984,7 +984,7 @@ bg_status_t bg_packed_qk_norm_rope(const void *q, int64_t q_stride, const void *
     if (total_tokens < 0) return BG_ERR_INVALID_ARG;
     RopeParams p{bf16_in(q), bf16_in(k), bf16_in(v), bf16_out(q_out), bf16_out(k_out), bf16_out(v_out),
                  bf16_in(q_weight), bf16_in(k_weight), positions, inv_freq, q_stride, k_stride, v_stride,
-                 static_cast<int64_t>(Hkv) * head_dim, total_tokens, total_tokens, 1, num_axes, 0, Hq, Hkv, 0, 0, eps,
+                 static_cast<int64_t>(Hkv) * head_dim, total_tokens, total_tokens, 1, 0, Hq, Hkv, 0, 0, eps,
                  weight_offset, rope_scale, {}};
     return qk_rope_impl(p, head_dim, num_axes, axis_of, rot_dim, interleaved, total_tokens, 0, stream);
 }
@@ -1004,7 +1004,7 @@ bg_status_t bg_beam_qk_norm_rope(const void *q, int64_t q_stride, const void *k,
     if (rows > INT32_MAX) return BG_ERR_UNSUPPORTED;
     RopeParams p{bf16_in(q), bf16_in(k), bf16_in(v), bf16_out(q_out), bf16_out(suffix_k), bf16_out(suffix_v),
                  bf16_in(q_weight), bf16_in(k_weight), base_pos, inv_freq, q_stride, k_stride, v_stride,
-                 row * suffix_max, rows, R, W, num_axes, step, Hq, Hkv, 0, 0, eps, weight_offset, rope_scale, {}};
+                 row * suffix_max, rows, R, W, step, Hq, Hkv, 0, 0, eps, weight_offset, rope_scale, {}};
     return qk_rope_impl(p, head_dim, num_axes, axis_of, rot_dim, interleaved, rows * suffix_max, slot, stream);
 }
 

@@ -76,7 +76,7 @@ struct RopeParams {
     const float *inv_freq;
     int64_t q_stride, k_stride, v_stride, kv_out_stride;
     int64_t rows, places;
-    int32_t rows_per_pos, num_axes, step, Hq, Hkv, rot, parts;
+    int32_t rows_per_pos, step, Hq, Hkv, rot, parts;
     float eps, weight_offset, rope_scale;
     uint8_t axis[64];                              // of each frequency
 };

@@ -19,11 +19,13 @@
 // A row's mask, lengths and words are fetched ahead.
 //   A row's own tokens are few (at most 32; beams): there is no barrier; the lanes hold the tokens and change them last.
 //   They are many (LONG): the warps take a row together.  Its counts are added to the words beside the copy and taken
-//   away after it, so that a history costs its own reading whatever its length, and integer atomics leave no
-//   order to depend on.
-// Measured: 3200 rows of 65,536 fp32 logits in groups of 100, 2% allowed, 180 us (the writes alone 138); 480 rows of 50,001
-// bf16 logits, prompts of 2000-4000 tokens, histories of 350-700, 300 biases, 54 us, a row's chain of counts, barrier,
-// logits, changes and barrier; one row of 65,536 7 us.
+//   away after it, so that a history costs its reading, once per chunk of the vocabulary, and integer atomics leave no
+//   order to depend on.  Room for more tokens than a row has costs nothing (480 rows of 50,001 with at most 20: 46 to
+//   47 us with room for 20, 33 or 2048).
+// Measured: 3200 rows of 65,536 fp32 logits in groups of 100, 2% allowed, 180 us (the writes alone 138), in place 172; 480
+// rows of 50,001 bf16 logits, prompts of 2000-4000 tokens, histories of 350-700, 300 biases, 54 us, a row's chain of counts,
+// barrier, logits, changes and barrier (to bf16 55, in place 54; with 50,000, which gives vectors, 50, 44 and 43); one row of
+// 65,536 7 us.
 #include <cuda_bf16.h>
 
 #include "bg_internal.h"
@@ -36,12 +38,14 @@ constexpr int kLgThreads = 128;
 constexpr int kLgWarps = kLgThreads / 32;
 constexpr int kChunk = 4096;                         // tokens of a CTA: a block per warp
 constexpr int kBlock = 1024;                         // logits that a warp takes at once
-constexpr int kLgShare = 16;                         // CTAs per SM that the rows are cut to
+// CTAs per SM that the rows are cut to (8: 64 groups of 8 rows of 100,000 bf16 logits 81 us instead of 72; 32: the first case
+// above 183 instead of 180).
+constexpr int kLgShare = 16;
 constexpr int kBlocks = kChunk / kBlock;
 static_assert(kChunk / 32 == kLgThreads && kBlocks == kLgWarps, "a bit word per thread, a block per warp");
-constexpr int kBiasShift = 18;                       // two rows' counts meet for a moment: 2 * 65536 fits below it
+constexpr int kBiasShift = 18;                       // a row's count, at most 2^16, fits below it
 constexpr uint32_t kCountMask = (1u << kBiasShift) - 1;
-static_assert(2 * BG_MAX_SEQLEN <= static_cast<int>(kCountMask), "count bits");
+static_assert(BG_MAX_SEQLEN <= static_cast<int>(kCountMask), "count bits");
 static_assert(BG_MAX_BIAS < (1 << (32 - kBiasShift)), "bias numbers");
 
 __device__ __forceinline__ void store_one(float *p, float x) { *p = x; }
@@ -141,7 +145,8 @@ __device__ __forceinline__ void copy_block(const TI *in, TO *out, uint32_t words
 }
 
 // N logits (1, 4 or 8 side by side) per lane and step of a warp.  As many CTAs per SM as leave the registers for what is
-// fetched ahead: spilled, it is waited for at once (eight CTAs: 3200 rows of 65,536 logits 398 us, seven 183).
+// fetched ahead: spilled, it is waited for at once (eight CTAs: 3200 rows of 65,536 logits 398 us, seven 180; seven leave
+// 72 registers, with two words spilled in <float, float, 4, few> and six in <bf16, bf16, 1, few>).
 template <typename TI, typename TO, int N, bool LONG>
 __global__ void __launch_bounds__(kLgThreads, LONG ? 6 : 7)
     logits_kernel(const LogitsParams p, int chunks, int rows_per_cta, int row_blocks)
@@ -229,7 +234,8 @@ __global__ void __launch_bounds__(kLgThreads, LONG ? 6 : 7)
         }
         __syncthreads();
     }
-    // one division for all (the product's second rounding is 2^-24): without penalties both factors are 1
+    // one division for all (the product's second rounding is 2^-24; a division for each logit needs registers: 279 us instead
+    // of 180): without penalties both factors are 1
     const float rho = p.repetition ? p.repetition[g] : 1.f, inv = 1.f / rho;
     const float alpha = p.frequency ? p.frequency[g] : 0.f, beta = p.presence ? p.presence[g] : 0.f;
     // The logits of M tokens t[k] >= 0 of the chunk, c times among the row's own (LONG: as their words say): those that
@@ -407,7 +413,8 @@ cudaError_t launch_typed(const LogitsParams &p, int rows_per_cta, cudaStream_t s
 cudaError_t launch_adjust_logits(const LogitsParams &p, int in_dtype, int out_dtype, bool vectors, int nsm, cudaStream_t stream)
 {
     // The rows of a group are cut to kLgShare CTAs per SM, as long as a CTA has four of them, and four logits for each
-    // token of the lists that it has to look at (eight: 480 rows with prompts of 3000 tokens 76 us instead of 67).
+    // token of the lists that it has to look at (eight: 480 rows with prompts of 3000 tokens 69 us instead of 54; two: the same
+    // 54, and one group of 480 rows of 50,000 with a prompt of 8000 55 instead of 91).
     const int64_t chunks = (p.V + kChunk - 1) / kChunk, listed = p.total_prompt / p.groups + p.total_bias / p.groups;
     int per = p.per;
     while (per >= 8 && per / 2 * static_cast<int64_t>(kChunk) >= 4 * listed && chunks * p.groups * ((p.per + per - 1) / per) < kLgShare * nsm)

@@ -14,8 +14,8 @@
 // that make up eight whole pairs in either layout, so that the rotation needs no exchange and the norm a sum over the
 // lanes of a head.  The angles of a token are computed once, two (one) per lane, and shuffled to the lanes that need them.
 // Each lane's elements come through shared memory by copies of its own, kRopeAhead rounds ahead, without a barrier.
-// Measured: 70,375 tokens of 16/8 heads of 128 175 us, 6.6 TB/s; 32,768 of 32/8 heads without a norm 124 us, 6.5 TB/s;
-// 23,041 of 14/2 heads of 64 27 us, 3.9 TB/s (the latency of a token's three rounds, the last of which holds two heads).
+// Measured: 70,375 tokens of 16/8 heads of 128 176 us, 6.5 TB/s; 32,768 of 32/8 heads without a norm 124 us, 6.5 TB/s;
+// 23,041 of 14/2 heads of 64 26 us, 4.0 TB/s (the latency of a token's three rounds, the last of which holds two heads).
 #include <cuda_bf16.h>
 
 #include "bg_internal.h"
@@ -24,12 +24,15 @@
 namespace bg {
 namespace {
 
-// Warps of a CTA: ten where many tokens are normed, which need issue slots (the first case below 175 us; with eight 181);
-// eight where memory alone counts (the second one 124; with ten 134) or few tokens (392 tokens 4.7; with ten 5.5).
+// Warps of a CTA: ten where many tokens are normed, which need issue slots (the first case above 176 us; with eight 183);
+// eight where memory alone counts (the second one 124; with ten 134) or few tokens (392 tokens 4.6; with ten 5.4).  Around the
+// border, 24,320 tokens, eight and ten take: 16/8 heads of 128 46.6 and 48.1 us for 16,001 tokens, 57.5 and 56.7 for 20,001,
+// 68.3 and 66.7 for 24,400, 77.1 and 74.8 for 28,001; 14/2 heads of 64 22.5 and 24.0 for 20,001, 27.2 and 27.8 for 24,400,
+// 38.0 and 38.6 for 36,001.
 constexpr int kRopeFew = 8, kRopeMany = 10;
-constexpr int kRopeCtas = 2;              // per SM (three leave 80 registers, with spills: 192 us instead of 181)
-// Rounds whose copies are under way, per warp.  Not more: with three the second case takes 134 us, the first (with eight
-// warps) 191, with four 200.
+constexpr int kRopeCtas = 2;              // per SM (three of eight warps leave 80 registers, with spills: 195 us instead of 183)
+// Rounds whose copies are under way, per warp.  Not more: with three the second case takes 134 us, the first 200 (with eight
+// warps 192).
 constexpr int kRopeAhead = 2;
 
 __device__ __forceinline__ void unpack(const uint4 &v, float *x)
@@ -54,7 +57,7 @@ __device__ __forceinline__ float2 cos_sin(int32_t pos, float hi, float lo)
     const float f3 = fmaf(up, lo, -rintf(up * lo));
     float r = ((f1 - rintf(f1)) + f2) + fmaf(low, lo, f3);
     r = (r - rintf(r)) * 6.2831853071795864769f;
-    // [-pi, pi], where the fast forms are off by at most 2^-21; outputs are rounded to 2^-9 of theirs
+    // [-pi, pi], where the fast forms are off by at most 2^-21; outputs are rounded to 2^-8 of theirs
     return make_float2(__cosf(r), __sinf(r));
 }
 

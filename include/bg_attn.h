@@ -603,9 +603,10 @@ bg_status_t bg_tree_attn_planned(const void *q, const void *k, const void *v, co
  *     s     = rope_scale sin(angle)            for i < rot_dim / 2
  *     (out_a, out_b) = (y_a c - y_b s, y_b c + y_a s)
  * over the pairs (a, b) = (i, i + rot_dim / 2), or (2 i, 2 i + 1) if interleaved;
- * out = y from rot_dim on.  V is copied.  Angles are off by less than 2^-19 for positions
- * up to 2^24 and 2^-17 for any other (with frequencies of at most 1), their cosines and
- * sines by 2^-21 more.
+ * out = y from rot_dim on.  V is copied.  The sum of x^2 is held in fp32: heads with
+ * elements past 2^60 (with eps = 0 also below 2^-60 throughout) are out of its range.
+ * Angles are off by less than 2^-19 for positions up to 2^24 and 2^-17 for any other
+ * (with frequencies of at most 1), their cosines and sines by 2^-21 more.
  *   bg_packed_qk_norm_rope   any packed tokens, each with its positions
  *   bg_beam_qk_norm_rope     the new token of every beam of a search: beam b of
  *                            request r is at base_pos[., r] + step, and its K and V
@@ -695,7 +696,7 @@ bg_status_t bg_beam_qk_norm_rope(const void *q, int64_t q_stride, const void *k,
  * whose offsets or repetition are bad (BG_DEVSTAT_CU_PROMPT, _BIAS, _PENALTY) and a row
  * whose length or mask index is (BG_DEVSTAT_SEQ_TOO_LONG, _MASK) are not written.
  * One launch, no workspace.  Logits next to which every logit of the same 16 bytes is
- * masked are not read.
+ * masked are not read; the lists are read again for every 4096 tokens of the vocabulary.
  * Errors: BG_ERR_INVALID_ARG for negative sizes, unknown types, NULL or misaligned
  * pointers, strides below V (mask_stride below its words) or above 2^31, num_masks < rows without
  * mask_index, or out overlapping another argument; BG_ERR_UNSUPPORTED unless 1 <= V
